@@ -58,8 +58,13 @@ typedef enum okls_status {
   OKLS_ERR_NO_DEVICE = 6     /* no CUDA device / wrong architecture          */
 } okls_status;
 
-/* Element types of W and G. */
-typedef enum okls_dtype { OKLS_F32 = 0, OKLS_BF16 = 1 } okls_dtype;
+/* Element types of W and G, and of the language-model operators' tensors
+ * (8-bit values only where an operator names them). */
+typedef enum okls_dtype {
+  OKLS_F32 = 0,
+  OKLS_BF16 = 1,
+  OKLS_E4M3 = 2 /* 8-bit floating point: 4 exponent, 3 mantissa bits */
+} okls_dtype;
 
 /* Preconditioner step computed by okls_step. */
 typedef enum okls_method {
@@ -99,6 +104,7 @@ typedef enum okls_state_part {
 #define OKLS_DEV_NONFINITE_ITER 0x2u   /* a Newton-Schulz iterate overflowed */
 #define OKLS_DEV_NONFINITE_UPDATE 0x4u /* the new W holds a non-finite value */
 #define OKLS_DEV_TIMEOUT 0x8u          /* a bounded pipeline wait expired   */
+#define OKLS_DEV_BAD_TOKEN 0x10u       /* a token id at or past the vocabulary */
 
 /*
  * Hyperparameters of one same-shape batch.  Defaults (okls_config_default)
@@ -447,6 +453,201 @@ okls_status okls_inv_root_noalloc(const float *S_dev, float *P_dev, int64_t d,
                                   int64_t count, int32_t iters,
                                   int32_t split_iters, float lo, float ridge,
                                   void *stream);
+
+/* ======================================================================
+ * Language-model operators: the token embedding, the RMS norm, the 8-bit
+ * matrix product and the token log probabilities of a transformer trained
+ * with the steps above, with the gradients that feed them.
+ *
+ * Conventions of this section
+ *   - Matrices are row-major with a row pitch `ld*` in elements (ld >= the
+ *     number of columns); columns are contiguous.  Pointers are device
+ *     pointers aligned to their element; rows that start on 16-byte
+ *     boundaries are read and written in 16-byte accesses, others element by
+ *     element.  Inputs and outputs do not overlap unless an operator says so.
+ *   - Calls are stateless, allocate nothing and are asynchronous on `stream`;
+ *     scratch comes from the caller (the *_workspace_bytes functions), may be
+ *     uninitialised and is free again when the call's work has run.  Calls
+ *     that run at the same time need workspaces of their own.
+ *   - Sums are taken in fp32 in an order fixed by the sizes and the device,
+ *     without floating-point atomics: the same inputs give the same bits.
+ *   - A size of zero rows or tokens is valid and writes nothing that has no
+ *     elements.
+ *   - `status_dev` is a device word of the caller, zeroed before its first
+ *     use, into which a launch ORs OKLS_DEV_* bits (okls_status_word_read).
+ *   - Token ids are int32 (ids_i64 = 0) or int64 (ids_i64 = 1).  A negative
+ *     id is padding: it has no embedding, no loss and no gradient.  An id
+ *     at or past the vocabulary is treated the same and raises
+ *     OKLS_DEV_BAD_TOKEN.
+ * ====================================================================== */
+
+/* Synchronise `stream`, read the status word into *dev_status (may be NULL)
+ * and clear it.  Returns OKLS_ERR_TIMEOUT / OKLS_ERR_INVALID_ARG when
+ * OKLS_DEV_TIMEOUT / OKLS_DEV_BAD_TOKEN was set, OKLS_OK otherwise. */
+okls_status okls_status_word_read(uint32_t *status_dev, void *stream,
+                                  uint32_t *dev_status);
+
+/*
+ * Token embedding: out[t] = scale * weight[ids[t]], zeros for padding.
+ *   weight  vocab x dim, fp32 or bf16;  out  tokens x dim, fp32 or bf16.
+ * The product is formed in fp32 and rounded once.
+ */
+okls_status okls_embedding(const void *weight, int32_t weight_dtype,
+                           int64_t ldw, int64_t vocab, int64_t dim,
+                           const void *ids, int32_t ids_i64, int64_t tokens,
+                           float scale, void *out, int32_t out_dtype,
+                           int64_t ldo, uint32_t *status_dev, void *stream);
+
+/*
+ * Gradient of the embedding by sorted tokens:
+ *   out[v] = base[v] + scale * sum over t with ids[t] = v of dy[t].
+ *   dy    tokens x dim, fp32 or bf16.
+ *   base  vocab x dim of out's type, or NULL for zeros.  base == out (with
+ *         ldbase == ldo) adds in place and touches only rows with a token.
+ *   out   vocab x dim, fp32 or bf16; every row is written otherwise.
+ * The token positions are sorted by id (stably), so each row is one fp32 sum
+ * over its tokens in their order, split at fixed places and joined in order.
+ * vocab and tokens are below 2^31.
+ */
+okls_status okls_embedding_grad_workspace_bytes(int64_t tokens, int64_t vocab,
+                                                int64_t dim,
+                                                size_t *workspace_bytes);
+okls_status okls_embedding_grad(const void *dy, int32_t dy_dtype, int64_t lddy,
+                                const void *ids, int32_t ids_i64,
+                                int64_t tokens, int64_t vocab, int64_t dim,
+                                float scale, const void *base, int64_t ldbase,
+                                void *out, int32_t out_dtype, int64_t ldo,
+                                void *workspace, size_t workspace_bytes,
+                                uint32_t *status_dev, void *stream);
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   s = x + residual, rounded to their type (s = x without a residual);
+ *   rstd = 1 / sqrt(mean(s^2) + eps);  y = s * rstd * weight.
+ *   x, residual, res_out  rows x dim, fp32 or bf16 (one type); residual and
+ *          res_out are both given or both NULL; res_out may be x or residual.
+ *   weight dim, fp32 or bf16 (weight_dtype).
+ *   out    rows x dim, fp32, bf16 or e4m3.  For e4m3 each group of 128
+ *          columns of a row has one scale (see okls_fp8_quantize, row
+ *          groups): out_scale[row * lds_row + group * lds_group]; out_scale
+ *          is NULL for the other types.
+ *   rstd   rows fp32, or NULL.
+ * dim <= 32768.
+ */
+okls_status okls_rms_norm(const void *x, int32_t dtype, int64_t ldx,
+                          const void *residual, int64_t ldr,
+                          const void *weight, int32_t weight_dtype,
+                          int64_t rows, int64_t dim, float eps, void *out,
+                          int32_t out_dtype, int64_t ldo, float *out_scale,
+                          int64_t lds_row, int64_t lds_group, void *res_out,
+                          int64_t ldro, float *rstd, void *stream);
+
+/*
+ * Gradient of the norm: with xhat = s * rstd and g = dy * weight,
+ *   ds = rstd * (g - xhat * mean(g * xhat)) + dres   (dx and dresidual both)
+ *   dweight = sum over rows of dy * xhat             (fp32; NULL to skip)
+ *   dy    rows x dim, fp32 or bf16 (dy_dtype).
+ *   s     rows x dim, the sum that was normed (res_out, or x without a
+ *         residual); dres (NULL: none) and ds have its type (s_dtype).
+ *   ds may be dres or (of the same type) dy.
+ */
+okls_status okls_rms_norm_grad_workspace_bytes(int64_t rows, int64_t dim,
+                                               size_t *workspace_bytes);
+okls_status okls_rms_norm_grad(const void *dy, int32_t dy_dtype, int64_t lddy,
+                               const void *s, int32_t s_dtype, int64_t lds,
+                               const void *weight, int32_t weight_dtype,
+                               const float *rstd, const void *dres,
+                               int64_t lddres, int64_t rows, int64_t dim,
+                               void *ds, int64_t ldds, float *dweight,
+                               void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
+ * Quantisation to e4m3 with a scale for each group of 128:
+ *   a = max(largest |x| of the group, 2^-100), q = e4m3(x * (448 / a)),
+ *   scale = a / 448; q * scale stands for x.  448 / a and a / 448 are fp32
+ *   quotients rounded to nearest, as are the product and the code.  A group
+ *   that holds an infinity or a NaN stands for NaN.
+ *   block  OKLS_FP8_ROW: groups of 128 consecutive columns of one row;
+ *          OKLS_FP8_SQUARE: blocks of 128 rows x 128 columns.
+ *   x      rows x cols, fp32 or bf16.
+ *   q      rows x cols e4m3, row pitch ldq, or NULL; scale of element (i, j):
+ *          scale[(row block or row i) * lds_row + (j / 128) * lds_group].
+ *   qt     the same of the transposed matrix (cols x rows, groups along its
+ *          rows, i.e. along x's columns), or NULL; at least one is given.
+ *          For square blocks its values are q's, transposed.
+ */
+typedef enum okls_fp8_block {
+  OKLS_FP8_ROW = 0,
+  OKLS_FP8_SQUARE = 1
+} okls_fp8_block;
+okls_status okls_fp8_quantize(const void *x, int32_t dtype, int64_t ldx,
+                              int64_t rows, int64_t cols, int32_t block,
+                              void *q, int64_t ldq, float *scale,
+                              int64_t lds_row, int64_t lds_group, void *qt,
+                              int64_t ldqt, float *scale_t, int64_t ldst_row,
+                              int64_t ldst_group, void *stream);
+
+/*
+ * 8-bit matrix product:  out = A B^T (+ out when accumulate = 1), with
+ *   A  m x k e4m3, row groups: value a * a_scale[i * lda_row + (p / 128) * lda_group];
+ *   B  n x k e4m3, row groups or square blocks (b_block):
+ *      value b * b_scale[(j or j / 128) * ldb_row + (p / 128) * ldb_group];
+ *   out  m x n fp32 or bf16.
+ * Each 128-deep partial product is formed exactly enough in the tensor
+ * core's fp32 accumulator, scaled and added to the running sum in fp32.
+ * Row pitches lda and ldb are multiples of 16 bytes and the bases 16-byte
+ * aligned (OKLS_ERR_UNSUPPORTED otherwise); m, n, k are any size.
+ */
+okls_status okls_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k,
+                                            size_t *workspace_bytes);
+okls_status okls_fp8_matmul(const void *a, int64_t lda, const float *a_scale,
+                            int64_t lda_row, int64_t lda_group, const void *b,
+                            int64_t ldb, const float *b_scale, int64_t ldb_row,
+                            int64_t ldb_group, int32_t b_block, int64_t m,
+                            int64_t n, int64_t k, void *out,
+                            int32_t out_dtype, int64_t ldo, int32_t accumulate,
+                            void *workspace, size_t workspace_bytes,
+                            uint32_t *status_dev, void *stream);
+
+/*
+ * Log probabilities of given tokens, entropy and best alternatives, with
+ * z = scale * logits (scale > 0, an inverse temperature):
+ *   lse[r] = log sum_j exp z_rj;  logp[r] = z_r,ids[r] - lse[r] (0 for
+ *   padding);  entropy[r] = -sum_j p_rj log p_rj;  top_ids / top_logp
+ *   [r * top_k + i]: the i-th largest logit's column and its log
+ *   probability, equal logits in the order of their columns.
+ *   logits   rows x vocab, fp32 or bf16, pitch ldl.
+ *   logp, entropy, lse  rows fp32, each may be NULL; top_* may be NULL when
+ *            top_k = 0; 0 <= top_k <= min(vocab, 32).
+ * Logits of -inf are impossible tokens.  A row of nothing else has lse,
+ * logp and top_logp -inf and entropy 0.  A row with a NaN or +inf has NaN for
+ * these; a NaN logit ranks with -inf.
+ */
+okls_status okls_token_logprobs(const void *logits, int32_t dtype, int64_t ldl,
+                                const void *ids, int32_t ids_i64, int64_t rows,
+                                int64_t vocab, float scale, int32_t top_k,
+                                float *logp, float *entropy, float *lse,
+                                int32_t *top_ids, float *top_logp,
+                                uint32_t *status_dev, void *stream);
+
+/*
+ * Gradient with respect to the logits of sum_r dlogp[r] logp[r] +
+ * dentropy[r] entropy[r], with p = exp(z - lse):
+ *   dlogits_rj = scale * (dlogp[r] ([j = ids[r]] - p_rj)
+ *                         - dentropy[r] p_rj (log p_rj + entropy[r])).
+ * Padding has no dlogp term.  A row without a possible token has gradient 0.
+ *   lse, entropy  as okls_token_logprobs wrote them (entropy may be NULL when
+ *                 dentropy is NULL).
+ *   dlogits       rows x vocab of logits' type; may be logits (in place).
+ */
+okls_status okls_token_logprobs_grad(const void *logits, int32_t dtype,
+                                     int64_t ldl, const void *ids,
+                                     int32_t ids_i64, int64_t rows,
+                                     int64_t vocab, float scale,
+                                     const float *lse, const float *entropy,
+                                     const float *dlogp, const float *dentropy,
+                                     void *dlogits, int64_t ldd, void *stream);
 
 #ifdef __cplusplus
 }

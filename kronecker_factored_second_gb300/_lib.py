@@ -25,6 +25,10 @@ OKLS_ERR_NO_DEVICE = 6
 
 OKLS_F32 = 0
 OKLS_BF16 = 1
+OKLS_E4M3 = 2
+
+FP8_ROW = 0
+FP8_SQUARE = 1
 
 METHOD_OKLS = 0
 METHOD_SHAMPOO = 1
@@ -38,6 +42,7 @@ DEV_NONFINITE_INPUT = 0x1
 DEV_NONFINITE_ITER = 0x2
 DEV_NONFINITE_UPDATE = 0x4
 DEV_TIMEOUT = 0x8
+DEV_BAD_TOKEN = 0x10
 
 
 class okls_config(ctypes.Structure):
@@ -122,6 +127,23 @@ _SIGS = {
     "okls_inv_root": (_I32, [_P, _P, _P, _P, _I64, _I64, _I32, _I32, _F, _F, _P, _SZ, _P]),
     "okls_inv_root_noalloc_capacity": (_SZ, []),
     "okls_inv_root_noalloc": (_I32, [_P, _P, _I64, _I64, _I32, _I32, _F, _F, _P]),
+    "okls_status_word_read": (_I32, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
+    "okls_embedding": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _I32, _I64, _F, _P, _I32, _I64, _P, _P]),
+    "okls_embedding_grad_workspace_bytes": (_I32, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
+    "okls_embedding_grad": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _I64, _I64, _F, _P, _I64, _P, _I32, _I64,
+                                   _P, _SZ, _P, _P]),
+    "okls_rms_norm": (_I32, [_P, _I32, _I64, _P, _I64, _P, _I32, _I64, _I64, _F, _P, _I32, _I64, _P, _I64, _I64,
+                             _P, _I64, _P, _P]),
+    "okls_rms_norm_grad_workspace_bytes": (_I32, [_I64, _I64, ctypes.POINTER(_SZ)]),
+    "okls_rms_norm_grad": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _P, _I32, _P, _P, _I64, _I64, _I64, _P, _I64,
+                                  _P, _P, _SZ, _P]),
+    "okls_fp8_quantize": (_I32, [_P, _I32, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64,
+                                 _I64, _P]),
+    "okls_fp8_matmul_workspace_bytes": (_I32, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
+    "okls_fp8_matmul": (_I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _I32, _I64, _I64, _I64, _P,
+                               _I32, _I64, _I32, _P, _SZ, _P, _P]),
+    "okls_token_logprobs": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _I64, _F, _I32, _P, _P, _P, _P, _P, _P, _P]),
+    "okls_token_logprobs_grad": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _I64, _F, _P, _P, _P, _P, _P, _I64, _P]),
 }
 
 

@@ -26,6 +26,7 @@
 #include <vector>
 
 #include "../../include/okls.h"
+#include "okls_host.h"
 #include "okls_internal.h"
 #include "okls_kernels.h"
 
@@ -1560,6 +1561,25 @@ okls_status build_chains(okls_handle_s* h) {
 }
 
 }  // namespace
+
+// Error message, device check and TMA encoder shared with the other entry
+// files (okls_host.h).
+namespace okls {
+
+okls_status host_fail(okls_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(s, "%s", buf);
+}
+
+okls_status host_device_sms(int* sms) { return device_sms(sms); }
+
+PFN_cuTensorMapEncodeTiled_v12000 host_encode_fn() { return encode_fn(); }
+
+}  // namespace okls
 
 // ================================================================== C entries
 extern "C" {

@@ -1,0 +1,442 @@
+// 8-bit matrix product with a scale for each block of 128 along the sum
+// (sm_103a):
+//
+//   out[i, j] = sum_kb sa[i, kb] sb[j, kb] sum_{p in kb} a[i, p] b[j, p].
+//
+// The inner sums run on the tensor cores (tcgen05 kind::f8f6f4, both operands
+// e4m3, fp32 accumulators in TMEM); the scales change with every 128 of the
+// sum, so each partial product is taken out of TMEM, scaled and added to a
+// running sum in fp32 registers.  A persistent CTA per SM:
+//   warp 0 / lane 0  TMA producer: 128 x 128 A and BN x 128 B boxes (one
+//                    128-byte swizzle row per matrix row) into a ring;
+//   warp 1 / lane 0  MMA issuer: four K32 MMAs per stage into one of two TMEM
+//                    buffers, overwriting it;
+//   warps 2-9        scale and add: a thread owns one output row and BN / 2
+//                    columns, so a row's scale is one register and a square
+//                    block's scale one multiplication per 128-deep step.
+// The two buffers let the additions of one step overlap the MMAs of the next.
+//
+// Every wait is bounded; when one expires the kernel raises kStTimeout and
+// runs to its end without further waits, apart from the bounded ones for its
+// own copies and MMAs.
+#include <cuda_fp16.h>
+
+#include "okls_internal.h"
+#include "okls_lm.cuh"
+#include "okls_ptx.cuh"
+
+namespace okls {
+namespace {
+
+constexpr int kTM = 128;         // output rows of a tile
+constexpr int kTK = 128;         // depth of a stage: one scale group
+constexpr int kThreads = 320;
+constexpr int kABytes = kTM * kTK;
+
+template <int BN>
+struct Tile {
+  static constexpr int kBBytes = BN * kTK;
+  static constexpr int kBytes = kABytes + kBBytes;
+  static constexpr int kRing = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  static constexpr int kCols = 2 * BN;  // TMEM columns
+  static constexpr int kSmem = kRing * kBytes + 1024 + 256;
+};
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// The four K32 MMAs of one 128-deep step (32 bytes apart in each operand's
+// swizzled rows); the first one overwrites the accumulator.
+__device__ __forceinline__ void umma_f8_step(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %3, %3;\n\t"
+      "setp.eq.b32 q, %3, %3;\n\t"
+      "add.s64 a1, %1, 2;\n\t"
+      "add.s64 b1, %2, 2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 a2, %1, 4;\n\t"
+      "add.s64 b2, %2, 4;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, q;\n\t"
+      "add.s64 a3, %1, 6;\n\t"
+      "add.s64 b3, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, q;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc)
+      : "memory");
+}
+
+struct TileAt {
+  int tm, tn;
+};
+
+// Tiles in groups of kGroup row blocks, column by column inside a group, so
+// that the A panels of a group and the B panel in turn stay in L2.
+constexpr int kGroup = 16;
+__device__ __forceinline__ TileAt tile_at(int t, int tiles_m, int tiles_n) {
+  const int per = kGroup * tiles_n;
+  const int g = t / per, in = t - g * per;
+  const int h = min(kGroup, tiles_m - g * kGroup);
+  return {g * kGroup + in % h, in / h};
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant__ Fp8GemmArgs A) {
+  using C = Tile<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing * C::kBytes);
+  uint64_t* empty = full + C::kRing;
+  uint64_t* acc_full = empty + C::kRing;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kRing; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 256);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int tiles_m = (A.m + kTM - 1) / kTM, tiles_n = (A.n + BN - 1) / BN;
+  const int tiles = tiles_m * tiles_n;
+  const int nkb = (A.k + kTK - 1) / kTK;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tmap(&A.amap);
+      prefetch_tmap(&A.bmap);
+      uint32_t stage = 0, phase = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const TileAt at = tile_at(t, tiles_m, tiles_n);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, A.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + stage * C::kBytes;
+          mbar_expect_tx(&full[stage], C::kBytes);
+          tma_load_2d(sa, &A.amap, &full[stage], kb * kTK, at.tm * kTM);
+          tma_load_2d(sa + kABytes, &A.bmap, &full[stage], kb * kTK, at.tn * BN);
+          ++issued;
+          if (++stage == C::kRing) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // no copy may still be landing in shared memory at exit
+      const int64_t back = issued < C::kRing ? issued : C::kRing;
+      for (int64_t q = 1; q <= back; ++q) {
+        const int64_t idx = issued - q;
+        if (!mbar_wait_own(&full[idx % C::kRing], static_cast<uint32_t>((idx / C::kRing) & 1), A.status)) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16_f32(kTM, BN);  // fp32 accumulators; format code 0 is e4m3 here
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t adesc0 = sw128_desc(s0), bdesc0 = sw128_desc(s0 + kABytes);
+      constexpr uint64_t kStep = C::kBytes >> 4;
+      uint32_t stage = 0, phase = 0, it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const uint32_t buf = it & 1u;
+          if (!mbar_wait(&acc_empty[buf], ((it >> 1) & 1u) ^ 1u, A.status) ||
+              !mbar_wait(&full[stage], phase, A.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          umma_f8_step(tmem + buf * BN, adesc0 + stage * kStep, bdesc0 + stage * kStep, idesc);
+          umma_commit(&empty[stage]);
+          umma_commit(&acc_full[buf]);
+          if (++stage == C::kRing) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      umma_commit(drain);
+      mbar_wait_own(drain, 0, A.status);
+    }
+    __syncwarp();
+  } else {
+    constexpr int kCols = BN / 2;             // columns of a thread
+    const int q = warp & 3;                   // TMEM lane quarter of this warp
+    const int half = (warp - 2) >> 2;
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kCols;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const TileAt at = tile_at(t, tiles_m, tiles_n);
+      const int row = at.tm * kTM + q * 32 + lane;
+      const int col0 = at.tn * BN + half * kCols;
+      const float* sa = A.a_scale + static_cast<int64_t>(row < A.m ? row : 0) * A.lda_row;
+      // square blocks: kCols divides 128, so one scale covers the columns
+      const float* sb = A.b_scale + static_cast<int64_t>(A.b_square ? min(col0, A.n - 1) / kFp8Group : 0) * A.ldb_row;
+      float acc[kCols];
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const uint32_t buf = it & 1u;
+        float s = sa[kb * A.lda_group];
+        const float* sbk = sb + kb * A.ldb_group;
+        if (A.b_square) s *= *sbk;
+        ok = ok && mbar_wait(&acc_full[buf], (it >> 1) & 1u, A.status);
+        __syncwarp();
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          float v[32];
+          tmem_ld32(tbase + buf * BN + c, v);
+          if (A.b_square) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(v[j], s, acc[c + j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              acc[c + j] = fmaf(v[j] * sbk[static_cast<int64_t>(min(col0 + c + j, A.n - 1)) * A.ldb_row], s, acc[c + j]);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&acc_empty[buf]);
+      }
+      if (row >= A.m) continue;
+      const int eb = A.out_dtype == kDtBf16 ? 2 : 4;
+      char* o = static_cast<char*>(A.out) + (static_cast<int64_t>(row) * A.ldo + col0) * eb;
+      const bool vec = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
+#pragma unroll
+      for (int c = 0; c < kCols; c += 8) {
+        if (A.out_dtype == kDtBf16) {
+          __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(o) + c;
+          if (vec && col0 + c + 8 <= A.n) {
+            float v[8], old[8];
+            if (A.accumulate) load8(p, old);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = A.accumulate ? acc[c + j] + old[j] : acc[c + j];
+            store8(p, v);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (col0 + c + j < A.n)
+                p[j] = __float2bfloat16_rn(A.accumulate ? acc[c + j] + __bfloat162float(p[j]) : acc[c + j]);
+          }
+        } else {
+          float* p = reinterpret_cast<float*>(o) + c;
+          if (vec && col0 + c + 8 <= A.n) {
+            float v[8], old[8];
+            if (A.accumulate) load8(p, old);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = A.accumulate ? acc[c + j] + old[j] : acc[c + j];
+            store8(p, v);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (col0 + c + j < A.n) p[j] = A.accumulate ? acc[c + j] + p[j] : acc[c + j];
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::kCols);
+}
+
+// ------------------------------------------------------------ a few tokens
+// Up to 32 rows of A: the bytes of B bound the product, and a 128-row tile
+// would be mostly padding.  A CTA takes 16 rows of B (output columns); its 8
+// warps split the sum's groups of 128 and join through shared memory.  Codes
+// become binary16 (exact), and mma.sync m16n8k16 multiplies them with fp32
+// sums: B's rows are its 16-row operand, A's rows its 8 columns.  Within a
+// group the order of the sum is free, so a lane's operand values are 16
+// consecutive bytes of its row on both sides.
+constexpr int kSkinnyMax = 32;
+constexpr int kSkinnyWarps = 8;
+
+__device__ __forceinline__ uint32_t f16x2_of(uint32_t two_codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two_codes)));
+  return r;
+}
+
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 bytes of a row at offset p, zeros at and past k (rows are 16-byte
+// aligned; a row's last bytes are read one by one)
+__device__ __forceinline__ uint4 load16(const uint8_t* row, bool valid, int p, int k) {
+  uint4 r = make_uint4(0, 0, 0, 0);
+  if (!valid || p >= k) return r;
+  if (p + 16 <= k) return *reinterpret_cast<const uint4*>(row + p);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (p + j < k) w[j >> 2] |= static_cast<uint32_t>(row[p + j]) << (8 * (j & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int MT>
+__global__ void __launch_bounds__(kSkinnyWarps * 32) k_fp8_skinny(const __grid_constant__ Fp8GemmArgs A) {
+  __shared__ float part[kSkinnyWarps][16][MT * 8 + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * 16;
+  const int nkb = (A.k + kFp8Group - 1) / kFp8Group;
+  const bool ok0 = n0 + g < A.n, ok1 = n0 + g + 8 < A.n;
+  const uint8_t* w0 = A.b + static_cast<int64_t>(n0 + g) * A.ldb;
+  const uint8_t* w1 = w0 + 8 * A.ldb;
+  const int r0 = min(n0 + g, A.n - 1), r1 = min(n0 + g + 8, A.n - 1);
+  const float* sb0 = A.b_scale + static_cast<int64_t>(A.b_square ? r0 / kFp8Group : r0) * A.ldb_row;
+  const float* sb1 = A.b_scale + static_cast<int64_t>(A.b_square ? r1 / kFp8Group : r1) * A.ldb_row;
+  float acc[MT][4] = {};
+  for (int kb = warp; kb < nkb; kb += kSkinnyWarps) {
+    uint4 wa[2], wb[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int p = kb * kFp8Group + h * 64 + t * 16;
+      wa[h] = load16(w0, ok0, p, A.k);
+      wb[h] = load16(w1, ok1, p, A.k);
+    }
+    const float s0 = sb0[kb * A.ldb_group], s1 = sb1[kb * A.ldb_group];
+    float c[MT][4] = {};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int p = kb * kFp8Group + h * 64 + t * 16;
+      const uint32_t a0[4] = {wa[h].x, wa[h].y, wa[h].z, wa[h].w};
+      const uint32_t a1[4] = {wb[h].x, wb[h].y, wb[h].z, wb[h].w};
+      uint4 x[MT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int tok = i * 8 + g;
+        x[i] = load16(A.a + static_cast<int64_t>(tok) * A.lda, tok < A.m, p, A.k);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t f0 = f16x2_of(a0[u]), f1 = f16x2_of(a1[u]);
+        const uint32_t f2 = f16x2_of(a0[u] >> 16), f3 = f16x2_of(a1[u] >> 16);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const uint32_t xw = u == 0 ? x[i].x : u == 1 ? x[i].y : u == 2 ? x[i].z : x[i].w;
+          mma_16x8x16(c[i], f0, f1, f2, f3, f16x2_of(xw), f16x2_of(xw >> 16));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int tok = i * 8 + t * 2;
+      const float x0 = A.a_scale[static_cast<int64_t>(min(tok, A.m - 1)) * A.lda_row + kb * A.lda_group];
+      const float x1 = A.a_scale[static_cast<int64_t>(min(tok + 1, A.m - 1)) * A.lda_row + kb * A.lda_group];
+      acc[i][0] = fmaf(c[i][0], s0 * x0, acc[i][0]);
+      acc[i][1] = fmaf(c[i][1], s0 * x1, acc[i][1]);
+      acc[i][2] = fmaf(c[i][2], s1 * x0, acc[i][2]);
+      acc[i][3] = fmaf(c[i][3], s1 * x1, acc[i][3]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int tok = i * 8 + t * 2;
+    part[warp][g][tok] = acc[i][0];
+    part[warp][g][tok + 1] = acc[i][1];
+    part[warp][g + 8][tok] = acc[i][2];
+    part[warp][g + 8][tok + 1] = acc[i][3];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < 16 * A.m; e += kSkinnyWarps * 32) {
+    const int tok = e >> 4, col = n0 + (e & 15);
+    if (col >= A.n) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kSkinnyWarps; ++w) v += part[w][e & 15][tok];
+    const int64_t at = static_cast<int64_t>(tok) * A.ldo + col;
+    if (A.out_dtype == kDtBf16) {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(A.out) + at;
+      *o = __float2bfloat16_rn(A.accumulate ? v + __bfloat162float(*o) : v);
+    } else {
+      float* o = static_cast<float*>(A.out) + at;
+      *o = A.accumulate ? v + *o : v;
+    }
+  }
+}
+
+template <int BN>
+cudaError_t run_gemm(const Fp8GemmArgs& A, int num_sms, cudaStream_t st) {
+  static PerDevice pd;
+  const cudaError_t e = once_per_device(pd, [](int) {
+    return cudaFuncSetAttribute(k_fp8_gemm<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<BN>::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = lm_div_up(A.m, kTM) * lm_div_up(A.n, BN);
+  k_fp8_gemm<BN><<<static_cast<int>(tiles < num_sms ? tiles : num_sms), kThreads, Tile<BN>::kSmem, st>>>(A);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k, int num_sms) {
+  (void)k;
+  Fp8Plan P = {};
+  P.skinny = m <= kSkinnyMax;
+  P.box_a = kTM;
+  P.box_b = 256;
+  while (P.box_b > 64 && lm_div_up(m, kTM) * lm_div_up(n, P.box_b) < num_sms) P.box_b /= 2;
+  return P;
+}
+
+size_t fp8_workspace(int64_t m, int64_t n, int64_t k, int num_sms) {
+  (void)m, (void)n, (void)k, (void)num_sms;
+  return 0;
+}
+
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& A, const Fp8Plan& P, void* workspace, int num_sms, cudaStream_t st) {
+  (void)workspace;
+  if (P.skinny) {
+    const int grid = static_cast<int>(lm_div_up(A.n, 16)), threads = kSkinnyWarps * 32;
+    if (A.m <= 8)
+      k_fp8_skinny<1><<<grid, threads, 0, st>>>(A);
+    else if (A.m <= 16)
+      k_fp8_skinny<2><<<grid, threads, 0, st>>>(A);
+    else
+      k_fp8_skinny<4><<<grid, threads, 0, st>>>(A);
+    return cudaGetLastError();
+  }
+  if (P.box_b == 256) return run_gemm<256>(A, num_sms, st);
+  if (P.box_b == 128) return run_gemm<128>(A, num_sms, st);
+  return run_gemm<64>(A, num_sms, st);
+}
+
+}  // namespace okls
