@@ -11,10 +11,14 @@
 //                    128-byte swizzle row per matrix row) into a ring;
 //   warp 1 / lane 0  MMA issuer: four K32 MMAs per stage into one of two TMEM
 //                    buffers, overwriting it;
-//   warps 2-9        scale and add: a thread owns one output row and BN / 2
+//   warp 2           copies each step's scales into a ring of their own, with
+//                    4-byte asynchronous copies that take any layout;
+//   warps 4-11       scale and add: a thread owns one output row and BN / 2
 //                    columns, so a row's scale is one register and a square
 //                    block's scale one multiplication per 128-deep step.
-// The two buffers let the additions of one step overlap the MMAs of the next.
+// The two TMEM buffers let the additions of one step overlap the MMAs of the
+// next.  The running sums of a 128 x 256 tile take half of the SM's
+// registers, so the first four warps hand theirs to the other eight.
 //
 // Every wait is bounded; when one expires the kernel raises kStTimeout and
 // runs to its end without further waits, apart from the bounded ones for its
@@ -30,7 +34,9 @@ namespace {
 
 constexpr int kTM = 128;         // output rows of a tile
 constexpr int kTK = 128;         // depth of a stage: one scale group
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;    // 4 control warps, 8 that scale and add
+constexpr int kCtlRegs = 40, kAddRegs = 232;
+static_assert(128 * kCtlRegs + 256 * kAddRegs <= kThreads * 168, "more registers than the launch holds");
 constexpr int kABytes = kTM * kTK;
 
 template <int BN>
@@ -39,7 +45,9 @@ struct Tile {
   static constexpr int kBytes = kABytes + kBBytes;
   static constexpr int kRing = BN == 256 ? 4 : BN == 128 ? 6 : 8;
   static constexpr int kCols = 2 * BN;  // TMEM columns
-  static constexpr int kSmem = kRing * kBytes + 1024 + 256;
+  static constexpr int kSlots = 8;                             // scale ring
+  static constexpr int kScaleBytes = (kTM + BN) * 4;           // of one step
+  static constexpr int kSmem = kRing * kBytes + kSlots * kScaleBytes + 1024 + 256;
 };
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1) {
@@ -71,6 +79,71 @@ __device__ __forceinline__ void umma_f8_step(uint32_t d, uint64_t adesc, uint64_
       : "memory");
 }
 
+// 4 bytes into shared memory without registers, zeros where !valid.
+__device__ __forceinline__ void copy4(float* dst, const float* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 4 : 0)
+               : "memory");
+}
+// One arrival on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// 32 fp32 columns of this thread's TMEM lane on their way into v; usable
+// after tmem_ld_wait(v), which waits for every load of this thread.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
+  // the registers are operands so that no use of them moves above the wait
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                 "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+
+// Two fp32 values in a 64-bit register, with one instruction for both.
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ void fma_pair(uint64_t& acc, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 32 consecutive bytes (32-byte aligned) in one access
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 struct TileAt {
   int tm, tn;
 };
@@ -90,9 +163,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
   using C = Tile<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing * C::kBytes);
+  uint8_t* scales = smem + C::kRing * C::kBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + C::kSlots * C::kScaleBytes);
   uint64_t* empty = full + C::kRing;
-  uint64_t* acc_full = empty + C::kRing;
+  uint64_t* sfull = empty + C::kRing;
+  uint64_t* sempty = sfull + C::kSlots;
+  uint64_t* acc_full = sempty + C::kSlots;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -102,6 +178,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
     for (int s = 0; s < C::kRing; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&sfull[s], 32);
+      mbar_init(&sempty[s], 8);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
@@ -123,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
   const int tiles = tiles_m * tiles_n;
   const int nkb = (A.k + kTK - 1) / kTK;
 
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
   if (warp == 0) {
     if (lane == 0) {
       prefetch_tmap(&A.amap);
@@ -186,79 +268,155 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       mbar_wait_own(drain, 0, A.status);
     }
     __syncwarp();
+  } else if (warp == 2) {
+    // scales of one step: the tile's rows of A, then its rows of B, or the
+    // one or two square blocks its columns meet; zeros outside
+    const int nb = A.b_square ? (BN + kFp8Group - 1) / kFp8Group : BN;
+    const int b_rows = A.b_square ? (A.n + kFp8Group - 1) / kFp8Group : A.n;
+    uint32_t slot = 0, phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const TileAt at = tile_at(t, tiles_m, tiles_n);
+      const int a0 = at.tm * kTM, b0 = A.b_square ? at.tn * BN / kFp8Group : at.tn * BN;
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = mbar_wait(&sempty[slot], phase ^ 1u, A.status);
+        if (__any_sync(0xffffffffu, !ok)) {
+          ok = false;
+          break;
+        }
+        float* sc = reinterpret_cast<float*>(scales + slot * C::kScaleBytes);
+        const float* sa = A.a_scale + kb * A.lda_group;
+        const float* sb = A.b_scale + kb * A.ldb_group;
+#pragma unroll
+        for (int i = 0; i < kTM / 32; ++i) {
+          const int r = i * 32 + lane;
+          copy4(sc + r, sa + static_cast<int64_t>(min(a0 + r, A.m - 1)) * A.lda_row, a0 + r < A.m);
+        }
+        for (int r = lane; r < nb; r += 32)
+          copy4(sc + kTM + r, sb + static_cast<int64_t>(min(b0 + r, b_rows - 1)) * A.ldb_row, b0 + r < b_rows);
+        copy_arrive(&sfull[slot]);
+        if (++slot == C::kSlots) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
     constexpr int kCols = BN / 2;             // columns of a thread
     const int q = warp & 3;                   // TMEM lane quarter of this warp
-    const int half = (warp - 2) >> 2;
+    const int half = (warp - 4) >> 2;
     const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kCols;
-    uint32_t it = 0;
+    uint32_t it = 0, slot = 0, sphase = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
       const TileAt at = tile_at(t, tiles_m, tiles_n);
       const int row = at.tm * kTM + q * 32 + lane;
       const int col0 = at.tn * BN + half * kCols;
-      const float* sa = A.a_scale + static_cast<int64_t>(row < A.m ? row : 0) * A.lda_row;
-      // square blocks: kCols divides 128, so one scale covers the columns
-      const float* sb = A.b_scale + static_cast<int64_t>(A.b_square ? min(col0, A.n - 1) / kFp8Group : 0) * A.ldb_row;
-      float acc[kCols];
+      uint64_t acc[kCols / 2];  // pairs of fp32 sums
 #pragma unroll
-      for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
+      for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const uint32_t buf = it & 1u;
-        float s = sa[kb * A.lda_group];
-        const float* sbk = sb + kb * A.ldb_group;
-        if (A.b_square) s *= *sbk;
+        const float* sc = reinterpret_cast<const float*>(scales + slot * C::kScaleBytes);
+        ok = ok && mbar_wait(&sfull[slot], sphase, A.status);
+        float s = sc[q * 32 + lane];
+        // kCols divides 128, so one square block covers the thread's columns
+        if (A.b_square) s *= sc[kTM + (half * kCols) / kFp8Group];
+        const uint64_t ss = pair_of(s, s);
         ok = ok && mbar_wait(&acc_full[buf], (it >> 1) & 1u, A.status);
         __syncwarp();
         tc_fence_after();
+        const ulonglong2* sbc = reinterpret_cast<const ulonglong2*>(sc + kTM + half * kCols);
+        // 32 columns are loaded while the 32 before them are added
+        uint32_t v[2][32];
+        tmem_ld32_start(tbase + buf * BN, v[0]);
 #pragma unroll
         for (int c = 0; c < kCols; c += 32) {
-          float v[32];
-          tmem_ld32(tbase + buf * BN + c, v);
+          uint32_t(&x)[32] = v[(c / 32) & 1];
+          tmem_ld_wait(x);
+          if (c + 32 < kCols) {
+            tmem_ld32_start(tbase + buf * BN + c + 32, v[(c / 32 + 1) & 1]);
+          } else {
+            tc_fence_before();
+            mbar_arrive(&acc_empty[buf]);
+          }
           if (A.b_square) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(v[j], s, acc[c + j]);
+            for (int j = 0; j < 16; ++j) fma_pair(acc[c / 2 + j], pair_of(x[2 * j], x[2 * j + 1]), ss);
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              acc[c + j] = fmaf(v[j] * sbk[static_cast<int64_t>(min(col0 + c + j, A.n - 1)) * A.ldb_row], s, acc[c + j]);
+            for (int j = 0; j < 8; ++j) {
+              const ulonglong2 w = sbc[c / 4 + j];
+              fma_pair(acc[c / 2 + 2 * j], mul_pair(pair_of(x[4 * j], x[4 * j + 1]), w.x), ss);
+              fma_pair(acc[c / 2 + 2 * j + 1], mul_pair(pair_of(x[4 * j + 2], x[4 * j + 3]), w.y), ss);
+            }
           }
         }
-        tc_fence_before();
-        mbar_arrive(&acc_empty[buf]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[slot]);
+        if (++slot == C::kSlots) {
+          slot = 0;
+          sphase ^= 1u;
+        }
       }
       if (row >= A.m) continue;
       const int eb = A.out_dtype == kDtBf16 ? 2 : 4;
       char* o = static_cast<char*>(A.out) + (static_cast<int64_t>(row) * A.ldo + col0) * eb;
-      const bool vec = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
+      // 32 bytes a store: whole memory sectors, although neighbouring lanes
+      // write different rows
+      const bool vec = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
+      if (A.out_dtype == kDtBf16) {
+        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(o);
 #pragma unroll
-      for (int c = 0; c < kCols; c += 8) {
-        if (A.out_dtype == kDtBf16) {
-          __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(o) + c;
-          if (vec && col0 + c + 8 <= A.n) {
-            float v[8], old[8];
-            if (A.accumulate) load8(p, old);
+        for (int c = 0; c < kCols; c += 16) {
+          float v[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = A.accumulate ? acc[c + j] + old[j] : acc[c + j];
-            store8(p, v);
+          for (int j = 0; j < 8; ++j) unpair(acc[c / 2 + j], v[2 * j], v[2 * j + 1]);
+          if (vec && col0 + c + 16 <= A.n) {
+            if (A.accumulate) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float old[8];
+                load8(p + c + 8 * h, old);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[8 * h + j] += old[j];
+              }
+            }
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+            store32(p + c, w);
           } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (col0 + c + j < A.n)
-                p[j] = __float2bfloat16_rn(A.accumulate ? acc[c + j] + __bfloat162float(p[j]) : acc[c + j]);
+            for (int j = 0; j < 16; ++j)
+              if (col0 + c + j < A.n) p[c + j] = __float2bfloat16_rn(A.accumulate ? v[j] + __bfloat162float(p[c + j]) : v[j]);
           }
-        } else {
-          float* p = reinterpret_cast<float*>(o) + c;
-          if (vec && col0 + c + 8 <= A.n) {
-            float v[8], old[8];
-            if (A.accumulate) load8(p, old);
+        }
+      } else {
+        float* p = reinterpret_cast<float*>(o);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = A.accumulate ? acc[c + j] + old[j] : acc[c + j];
-            store8(p, v);
+        for (int c = 0; c < kCols; c += 8) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) unpair(acc[c / 2 + j], v[2 * j], v[2 * j + 1]);
+          if (vec && col0 + c + 8 <= A.n) {
+            if (A.accumulate) {
+              float old[8];
+              load8(p + c, old);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] += old[j];
+            }
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[j]);
+            store32(p + c, w);
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              if (col0 + c + j < A.n) p[j] = A.accumulate ? acc[c + j] + p[j] : acc[c + j];
+              if (col0 + c + j < A.n) p[c + j] = A.accumulate ? v[j] + p[c + j] : v[j];
           }
         }
       }

@@ -60,13 +60,16 @@ def _out_dtype(dtype: torch.dtype) -> int:
 
 def _matrix(t: torch.Tensor, name: str) -> torch.Tensor:
     """`t` as rows x columns without a copy."""
+    if t.dim() == 2:
+        if t.stride(1) == 1 or t.shape[1] <= 1 or t.numel() == 0:
+            return t
+        _fail(f"the last dimension of {name} must be contiguous")
     if t.dim() == 0:
         _fail(f"{name} needs at least one dimension")
-    if t.dim() != 2:
-        try:
-            t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(t.shape[:-1].numel(), t.shape[-1])
-        except RuntimeError:
-            _fail(f"the leading dimensions of {name} do not fold into rows without a copy")
+    try:
+        t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(t.shape[:-1].numel(), t.shape[-1])
+    except RuntimeError:
+        _fail(f"the leading dimensions of {name} do not fold into rows without a copy")
     if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
         _fail(f"the last dimension of {name} must be contiguous")
     return t
@@ -130,8 +133,11 @@ def _on(stream, *tensors):
     return _other(device, stream)
 
 
-def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+def _stream(t: torch.Tensor) -> int:
+    """Handle of the current stream of t's device (the current device)."""
+    # the same handle as torch.cuda.current_stream().cuda_stream, without building a Stream object, which
+    # costs more than a launch
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _ptr(t: torch.Tensor | None) -> int:
@@ -157,7 +163,7 @@ def query_status(device=None, stream=None) -> int:
     with _other(dev, stream):
         w = _status_word(dev)
         v = ctypes.c_uint32(0)
-        L.check(L.lib().okls_status_word_read(w.data_ptr(), _stream(), ctypes.byref(v)))
+        L.check(L.lib().okls_status_word_read(w.data_ptr(), _stream(w), ctypes.byref(v)))
     return v.value
 
 
@@ -177,7 +183,7 @@ def embedding(weight: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, ou
     with _on(stream, weight, ids):
         out = torch.empty(*ids.shape, w.shape[1], dtype=out_dtype or w.dtype, device=w.device)
         L.check(L.lib().okls_embedding(_ptr(w), dt, _ld(w), w.shape[0], w.shape[1], _ptr(ids), i64, ids.numel(),
-                                       scale, _ptr(out), od, w.shape[1], _ptr(_status_word(w.device)), _stream()))
+                                       scale, _ptr(out), od, w.shape[1], _ptr(_status_word(w.device)), _stream(w)))
     return out
 
 
@@ -206,7 +212,7 @@ def embedding_grad(dy: torch.Tensor, ids: torch.Tensor, vocab: int, *, scale: fl
         ws = _workspace(need.value, d.device)
         L.check(lib.okls_embedding_grad(_ptr(d), dt, _ld(d), _ptr(ids), i64, d.shape[0], vocab, d.shape[1], scale,
                                         _ptr(base), 0 if base is None else _ld(base), _ptr(out), od, _ld(out),
-                                        _ptr(ws), need.value, _ptr(_status_word(d.device)), _stream()))
+                                        _ptr(ws), need.value, _ptr(_status_word(d.device)), _stream(d)))
     return out
 
 
@@ -239,19 +245,24 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | 
     rows, dim = m.shape
     with _on(stream, x, weight, residual):
         dev = m.device
-        s = None if r is None else r if inplace else torch.empty(rows, dim, dtype=m.dtype, device=dev)
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        r_ptr = ldr = s_ptr = lds = sc_ptr = sc_row = sc_group = 0
+        total = x
+        if r is not None:
+            r_ptr, ldr = r.data_ptr(), _ld(r)
+            total = residual if inplace else torch.empty(x.shape, dtype=x.dtype, device=dev)
+            s_ptr, lds = (r_ptr, ldr) if inplace else (total.data_ptr(), dim)
         if fp8:
-            q = _fp8_empty(rows, dim, "row", dev)
-            y, sc = q.data, q.scale
+            y = _fp8_empty(rows, dim, "row", dev)
+            y_ptr, ldy, sc_ptr = y.data.data_ptr(), y.data.stride(0), y.scale.data_ptr()
+            sc_row, sc_group = y.scale.stride()
         else:
-            y, sc = torch.empty(rows, dim, dtype=out_dtype, device=dev), None
-        L.check(L.lib().okls_rms_norm(_ptr(m), dt, _ld(m), _ptr(r), 0 if r is None else _ld(r), _ptr(weight), wd, rows,
-                                      dim, eps, _ptr(y), od, _ld(y), _ptr(sc), 0 if sc is None else sc.stride(0),
-                                      0 if sc is None else sc.stride(1), _ptr(s), 0 if s is None else _ld(s),
-                                      _ptr(rstd), _stream()))
-    total = x if s is None else residual if inplace else s.view(x.shape)
-    return NormOutput(q if fp8 else y.view(x.shape), total, rstd)
+            y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+            y_ptr, ldy = y.data_ptr(), dim
+        L.check(L.lib().okls_rms_norm(m.data_ptr(), dt, _ld(m), r_ptr, ldr, weight.data_ptr(), wd, rows, dim, eps,
+                                      y_ptr, od, ldy, sc_ptr, sc_row, sc_group, s_ptr, lds, rstd.data_ptr(),
+                                      _stream(m)))
+    return NormOutput(y, total, rstd)
 
 
 def rms_norm_grad(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, *,
@@ -271,7 +282,7 @@ def rms_norm_grad(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd:
         e = _matrix(dresidual, "dresidual")
         _same(dresidual, s, "dresidual")
     with _on(stream, dy, s, weight, rstd, dresidual):
-        ds = torch.empty(rows, dim, dtype=m.dtype, device=m.device)
+        ds = torch.empty(s.shape, dtype=m.dtype, device=m.device)
         dw = torch.empty(dim, dtype=torch.float32, device=m.device) if need_dweight else None
         need = ctypes.c_size_t()
         lib = L.lib()
@@ -280,8 +291,8 @@ def rms_norm_grad(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd:
         ws = _workspace(need.value, m.device)
         L.check(lib.okls_rms_norm_grad(_ptr(g), gd, _ld(g), _ptr(m), sd, _ld(m), _ptr(weight), wd, _ptr(rstd), _ptr(e),
                                        0 if e is None else _ld(e), rows, dim, _ptr(ds), dim, _ptr(dw), _ptr(ws),
-                                       need.value, _stream()))
-    return ds.view(s.shape), dw
+                                       need.value, _stream(m)))
+    return ds, dw
 
 
 # -------------------------------------------------------------------- 8 bits
@@ -321,13 +332,13 @@ class Fp8Tensor:
 def _fp8_empty(rows: int, cols: int, block: str, device) -> Fp8Tensor:
     """Rows start at multiples of 128 bytes (the product's copies need 16); the
     scales lie group by group, so that neighbouring rows' scales are neighbours."""
-    pitch = max(FP8_GROUP, -(-cols // FP8_GROUP) * FP8_GROUP)
-    data = torch.empty(rows, pitch, dtype=torch.float8_e4m3fn, device=device)[:, :cols]
     groups = -(-cols // FP8_GROUP)
-    if block == "square":
-        return Fp8Tensor(data, torch.empty(-(-rows // FP8_GROUP), groups, dtype=torch.float32, device=device), block)
-    pitch = -(-rows // 4) * 4
-    return Fp8Tensor(data, torch.empty(groups, pitch, dtype=torch.float32, device=device)[:, :rows].t(), block)
+    data = torch.empty_strided((rows, cols), (max(groups, 1) * FP8_GROUP, 1), dtype=torch.float8_e4m3fn, device=device)
+    lines = rows if block == "row" else -(-rows // FP8_GROUP)
+    scale = torch.empty_strided((lines, groups), (1, max(-(-lines // 4) * 4, 1)), dtype=torch.float32, device=device)
+    q = object.__new__(Fp8Tensor)  # right by construction: __post_init__ has nothing to check
+    q.data, q.scale, q.block = data, scale, block
+    return q
 
 
 def fp8_quantize(x: torch.Tensor, *, block: str = "row", transpose: bool = False, both: bool = False, stream=None):
@@ -343,11 +354,9 @@ def fp8_quantize(x: torch.Tensor, *, block: str = "row", transpose: bool = False
         t = _fp8_empty(cols, rows, block, m.device) if both or transpose else None
         args = []
         for f in (q, t):
-            args += [0, 0, 0, 0, 0] if f is None else [_ptr(f.data), _ld(f.data), _ptr(f.scale), f.scale.stride(0),
-                                                       f.scale.stride(1)]
-        args[1] = args[1] if q is None else q.data.stride(0)
-        args[6] = args[6] if t is None else t.data.stride(0)
-        L.check(L.lib().okls_fp8_quantize(_ptr(m), dt, _ld(m), rows, cols, _BLOCKS[block], *args, _stream()))
+            args += (0, 0, 0, 0, 0) if f is None else (f.data.data_ptr(), f.data.stride(0), f.scale.data_ptr(),
+                                                       *f.scale.stride())
+        L.check(L.lib().okls_fp8_quantize(m.data_ptr(), dt, _ld(m), rows, cols, _BLOCKS[block], *args, _stream(m)))
     return (q, t) if both else t if transpose else q
 
 
@@ -368,17 +377,17 @@ def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, *, out_dtype: torch.dtype = torch.bfl
         out_dtype = out.dtype
     od = _out_dtype(out_dtype)
     with _on(stream, a.data, a.scale, b.data, b.scale, out):
+        dev = a.data.device
         if out is None:
-            out = torch.empty(m, n, dtype=out_dtype, device=a.data.device)
+            out = torch.empty((m, n), dtype=out_dtype, device=dev)
         lib = L.lib()
         need = ctypes.c_size_t()
         L.check(lib.okls_fp8_matmul_workspace_bytes(m, n, k, ctypes.byref(need)))
-        ws = _workspace(need.value, a.data.device)
-        sa, sb = a.scale.stride(), b.scale.stride()
-        L.check(lib.okls_fp8_matmul(_ptr(a.data), a.data.stride(0), _ptr(a.scale), sa[0], sa[1], _ptr(b.data),
-                                    b.data.stride(0), _ptr(b.scale), sb[0], sb[1], _BLOCKS[b.block], m, n, k,
-                                    _ptr(out), od, _ld(out), int(accumulate), _ptr(ws), need.value,
-                                    _ptr(_status_word(a.data.device)), _stream()))
+        ws = _workspace(need.value, dev)
+        L.check(lib.okls_fp8_matmul(a.data.data_ptr(), a.data.stride(0), a.scale.data_ptr(), *a.scale.stride(),
+                                    b.data.data_ptr(), b.data.stride(0), b.scale.data_ptr(), *b.scale.stride(),
+                                    _BLOCKS[b.block], m, n, k, out.data_ptr(), od, _ld(out), int(accumulate), _ptr(ws),
+                                    need.value, _status_word(dev).data_ptr(), _stream(out)))
     return out
 
 
@@ -403,17 +412,18 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, *, top_k: int = 0, s
     dt, i64 = _dtype(z, "logits"), _ids(ids, rows)
     lead = logits.shape[:-1]
     with _on(stream, logits, ids):
-        logp, entropy, lse = torch.empty(3, rows, dtype=torch.float32, device=z.device).unbind(0)
+        dev = z.device
+        logp = torch.empty(lead, dtype=torch.float32, device=dev)
+        entropy = torch.empty(lead, dtype=torch.float32, device=dev)
+        lse = torch.empty(lead, dtype=torch.float32, device=dev)
         top_ids = top_logp = None
         if top_k > 0:
-            top_ids = torch.empty(rows, top_k, dtype=torch.int32, device=z.device)
-            top_logp = torch.empty(rows, top_k, dtype=torch.float32, device=z.device)
-        L.check(L.lib().okls_token_logprobs(_ptr(z), dt, _ld(z), _ptr(ids), i64, rows, vocab, scale, top_k, _ptr(logp),
-                                            _ptr(entropy), _ptr(lse), _ptr(top_ids), _ptr(top_logp),
-                                            _ptr(_status_word(z.device)), _stream()))
-        if top_k > 0:
-            top_ids, top_logp = top_ids.view(*lead, top_k), top_logp.view(*lead, top_k)
-    return TokenLogprobs(logp.view(lead), entropy.view(lead), lse.view(lead), top_ids, top_logp)
+            top_ids = torch.empty((*lead, top_k), dtype=torch.int32, device=dev)
+            top_logp = torch.empty((*lead, top_k), dtype=torch.float32, device=dev)
+        L.check(L.lib().okls_token_logprobs(z.data_ptr(), dt, _ld(z), ids.data_ptr(), i64, rows, vocab, scale, top_k,
+                                            logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _ptr(top_ids),
+                                            _ptr(top_logp), _status_word(dev).data_ptr(), _stream(z)))
+    return TokenLogprobs(logp, entropy, lse, top_ids, top_logp)
 
 
 def token_logprobs_grad(logits: torch.Tensor, ids: torch.Tensor, result: TokenLogprobs, dlogp: torch.Tensor, *,
@@ -430,11 +440,12 @@ def token_logprobs_grad(logits: torch.Tensor, ids: torch.Tensor, result: TokenLo
         _vector(dentropy, "dentropy", torch.float32, rows)
         _vector(result.entropy, "entropy", torch.float32, rows)
     with _on(stream, logits, ids, result.lse, dlogp, dentropy):
-        d = z if inplace else torch.empty(rows, vocab, dtype=z.dtype, device=z.device)
+        d = z if inplace else torch.empty(logits.shape, dtype=z.dtype, device=z.device)
         L.check(L.lib().okls_token_logprobs_grad(_ptr(z), dt, _ld(z), _ptr(ids), i64, rows, vocab, scale,
                                                  _ptr(result.lse), _ptr(result.entropy if dentropy is not None else None),
-                                                 _ptr(dlogp), _ptr(dentropy), _ptr(d), _ld(d), _stream()))
-    return logits if inplace else d.view(logits.shape)
+                                                 _ptr(dlogp), _ptr(dentropy), _ptr(d),
+                                                 _ld(d) if inplace else vocab, _stream(z)))
+    return logits if inplace else d
 
 
 # ------------------------------------------------------------------ autograd
