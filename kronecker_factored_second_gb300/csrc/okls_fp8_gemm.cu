@@ -115,28 +115,6 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
                : "memory");
 }
 
-// Two fp32 values in a 64-bit register, with one instruction for both.
-__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
-}
-__device__ __forceinline__ void fma_pair(uint64_t& acc, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // 32 consecutive bytes (32-byte aligned) in one access
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
@@ -184,8 +162,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       mbar_init(&sempty[s], 8);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 256);
+      mbar_init(&acc_full[b], 2);   // the MMAs, and the issuer, which has seen the step's scales
+      mbar_init(&acc_empty[b], 8);
+
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -244,23 +223,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       const uint32_t s0 = smem_u32(smem);
       const uint64_t adesc0 = sw128_desc(s0), bdesc0 = sw128_desc(s0 + kABytes);
       constexpr uint64_t kStep = C::kBytes >> 4;
-      uint32_t stage = 0, phase = 0, it = 0;
+      uint32_t stage = 0, phase = 0, slot = 0, sphase = 0, it = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const uint32_t buf = it & 1u;
-          if (!mbar_wait(&acc_empty[buf], ((it >> 1) & 1u) ^ 1u, A.status) ||
-              !mbar_wait(&full[stage], phase, A.status)) {
+          if (!mbar_wait(&full[stage], phase, A.status) || !mbar_wait(&sfull[slot], sphase, A.status) ||
+              !mbar_wait(&acc_empty[buf], ((it >> 1) & 1u) ^ 1u, A.status)) {
             ok = false;
             break;
           }
+          mbar_arrive(&acc_full[buf]);
           tc_fence_after();
           umma_f8_step(tmem + buf * BN, adesc0 + stage * kStep, bdesc0 + stage * kStep, idesc);
-          umma_commit(&empty[stage]);
           umma_commit(&acc_full[buf]);
+          umma_commit(&empty[stage]);
           if (++stage == C::kRing) {
             stage = 0;
             phase ^= 1u;
+          }
+          if (++slot == C::kSlots) {
+            slot = 0;
+            sphase ^= 1u;
           }
         }
       }
@@ -309,30 +293,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
     const int q = warp & 3;                   // TMEM lane quarter of this warp
     const int half = (warp - 4) >> 2;
     const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kCols;
-    uint32_t it = 0, slot = 0, sphase = 0;
+    uint32_t it = 0, slot = 0;
     bool ok = true;
+    // the first look at a step's barrier is taken before the last additions
+    // of the step before, so that its latency passes under them
+    bool ready = mbar_try_wait(&acc_full[0], 0);
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
       const TileAt at = tile_at(t, tiles_m, tiles_n);
       const int row = at.tm * kTM + q * 32 + lane;
       const int col0 = at.tn * BN + half * kCols;
-      uint64_t acc[kCols / 2];  // pairs of fp32 sums
+      float acc[kCols];
 #pragma unroll
-      for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
+      for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const uint32_t buf = it & 1u;
         const float* sc = reinterpret_cast<const float*>(scales + slot * C::kScaleBytes);
-        ok = ok && mbar_wait(&sfull[slot], sphase, A.status);
-        float s = sc[q * 32 + lane];
-        // kCols divides 128, so one square block covers the thread's columns
-        if (A.b_square) s *= sc[kTM + (half * kCols) / kFp8Group];
-        const uint64_t ss = pair_of(s, s);
-        ok = ok && mbar_wait(&acc_full[buf], (it >> 1) & 1u, A.status);
+        if (!ready) ok = ok && mbar_wait(&acc_full[buf], (it >> 1) & 1u, A.status);
         __syncwarp();
         tc_fence_after();
-        const ulonglong2* sbc = reinterpret_cast<const ulonglong2*>(sc + kTM + half * kCols);
         // 32 columns are loaded while the 32 before them are added
         uint32_t v[2][32];
         tmem_ld32_start(tbase + buf * BN, v[0]);
+        float s = sc[q * 32 + lane];
+        // kCols divides 128, so one square block covers the thread's columns
+        if (A.b_square) s *= sc[kTM + (half * kCols) / kFp8Group];
+        const float4* sbc = reinterpret_cast<const float4*>(sc + kTM + half * kCols);
 #pragma unroll
         for (int c = 0; c < kCols; c += 32) {
           uint32_t(&x)[32] = v[(c / 32) & 1];
@@ -341,26 +326,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
             tmem_ld32_start(tbase + buf * BN + c + 32, v[(c / 32 + 1) & 1]);
           } else {
             tc_fence_before();
-            mbar_arrive(&acc_empty[buf]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            ready = mbar_try_wait(&acc_full[buf ^ 1u], ((it + 1) >> 1) & 1u);
           }
           if (A.b_square) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) fma_pair(acc[c / 2 + j], pair_of(x[2 * j], x[2 * j + 1]), ss);
+            for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(x[j]), s, acc[c + j]);
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const ulonglong2 w = sbc[c / 4 + j];
-              fma_pair(acc[c / 2 + 2 * j], mul_pair(pair_of(x[4 * j], x[4 * j + 1]), w.x), ss);
-              fma_pair(acc[c / 2 + 2 * j + 1], mul_pair(pair_of(x[4 * j + 2], x[4 * j + 3]), w.y), ss);
+              const float4 w = sbc[c / 4 + j];
+              acc[c + 4 * j] = fmaf(__uint_as_float(x[4 * j]) * w.x, s, acc[c + 4 * j]);
+              acc[c + 4 * j + 1] = fmaf(__uint_as_float(x[4 * j + 1]) * w.y, s, acc[c + 4 * j + 1]);
+              acc[c + 4 * j + 2] = fmaf(__uint_as_float(x[4 * j + 2]) * w.z, s, acc[c + 4 * j + 2]);
+              acc[c + 4 * j + 3] = fmaf(__uint_as_float(x[4 * j + 3]) * w.w, s, acc[c + 4 * j + 3]);
             }
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty[slot]);
-        if (++slot == C::kSlots) {
-          slot = 0;
-          sphase ^= 1u;
-        }
+        if (++slot == C::kSlots) slot = 0;
       }
       if (row >= A.m) continue;
       const int eb = A.out_dtype == kDtBf16 ? 2 : 4;
@@ -374,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         for (int c = 0; c < kCols; c += 16) {
           float v[16];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) unpair(acc[c / 2 + j], v[2 * j], v[2 * j + 1]);
+          for (int j = 0; j < 16; ++j) v[j] = acc[c + j];
           if (vec && col0 + c + 16 <= A.n) {
             if (A.accumulate) {
 #pragma unroll
@@ -401,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         for (int c = 0; c < kCols; c += 8) {
           float v[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) unpair(acc[c / 2 + j], v[2 * j], v[2 * j + 1]);
+          for (int j = 0; j < 8; ++j) v[j] = acc[c + j];
           if (vec && col0 + c + 8 <= A.n) {
             if (A.accumulate) {
               float old[8];

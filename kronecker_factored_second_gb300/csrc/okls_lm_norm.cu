@@ -5,12 +5,17 @@
 //   y = s rstd w;   with xhat = s rstd, g = dy w:
 //   ds = rstd (g - xhat mean(g xhat)) + dres,   dw = sum_rows dy xhat.
 //
-// Both are bound by memory: a row is read once into registers, reduced by
-// one CTA, and written from the same registers.  A warp covers 256 columns
-// with 8 elements a lane, so a row of D columns takes ceil(D / 256) warp
-// chunks, NV of them per warp.  A group of 128 columns with one 8-bit scale
-// lies inside a warp chunk: its largest magnitude is a shuffle maximum, and
-// the codes leave from the registers that hold y.
+// Both are bound by memory: a row is read once into registers, reduced by one
+// CTA, and written from the same registers.  A warp chunk is 256 columns, 8
+// elements a lane; a warp takes NV chunks and a row as many warps as it needs.
+// Rows are held in their own type (packed), so that a CTA is small (2 warps
+// for 4096 bf16 columns) and many rows are in flight on an SM.  The gradient
+// keeps the weight's sums of its columns in registers over all rows of a CTA
+// and loads a row ahead.
+//
+// A group of 128 columns with one 8-bit scale lies inside a warp chunk: its
+// largest magnitude is two warp reductions, each lane divides for one group
+// of the warp's, and the codes leave from the registers that hold y.
 #include "okls_internal.h"
 #include "okls_lm.cuh"
 
@@ -19,6 +24,34 @@ namespace {
 
 constexpr int kChunk = 256;  // columns of one warp chunk: 32 lanes x 8
 
+// 8 elements of one lane in their own type.
+template <class T>
+struct Pack;
+template <>
+struct Pack<float> {
+  float v[8];
+  __device__ __forceinline__ void unpack(float (&o)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = v[j];
+  }
+  __device__ __forceinline__ void pack(const float (&o)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = o[j];
+  }
+  __device__ __forceinline__ void load(const float* p) { load8(p, v); }
+  __device__ __forceinline__ void store(float* p) const { store8(p, v); }
+};
+template <>
+struct Pack<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void unpack(float (&o)[8]) const { unpack8(u, o); }
+  __device__ __forceinline__ void pack(const float (&o)[8]) {
+    u = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+  }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
+};
+
 // Column of element j of warp chunk c for this lane: 8 consecutive columns a
 // lane for 16-byte accesses, or 32 consecutive columns an access otherwise.
 template <bool VEC>
@@ -26,24 +59,28 @@ __device__ __forceinline__ int col_of(int c, int lane, int j) {
   return VEC ? c * kChunk + lane * 8 + j : c * kChunk + j * 32 + lane;
 }
 
-template <class T, bool VEC>
-__device__ __forceinline__ void load_chunk(const T* row, int c, int lane, int dim, float (&v)[8]) {
+template <bool VEC, class T>
+__device__ __forceinline__ void load_chunk(const T* row, int c, int lane, int dim, Pack<T>& p) {
   if (VEC && c * kChunk + lane * 8 + 8 <= dim) {
-    load8(row + c * kChunk + lane * 8, v);
+    p.load(row + c * kChunk + lane * 8);
   } else {
+    float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int e = col_of<VEC>(c, lane, j);
       v[j] = e < dim ? to_f32(row[e]) : 0.0f;
     }
+    p.pack(v);
   }
 }
 
-template <class T, bool VEC>
-__device__ __forceinline__ void store_chunk(T* row, int c, int lane, int dim, const float (&v)[8]) {
+template <bool VEC, class T>
+__device__ __forceinline__ void store_chunk(T* row, int c, int lane, int dim, const Pack<T>& p) {
   if (VEC && c * kChunk + lane * 8 + 8 <= dim) {
-    store8(row + c * kChunk + lane * 8, v);
+    p.store(row + c * kChunk + lane * 8);
   } else {
+    float v[8];
+    p.unpack(v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int e = col_of<VEC>(c, lane, j);
@@ -52,13 +89,32 @@ __device__ __forceinline__ void store_chunk(T* row, int c, int lane, int dim, co
   }
 }
 
+// The same for a tensor whose type is known at run time only.
 template <bool VEC>
-__device__ __forceinline__ void load_chunk_dt(const void* base, int dt, int64_t off, int c, int lane, int dim,
-                                              float (&v)[8]) {
-  if (dt == kDtBf16)
-    load_chunk<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(base) + off, c, lane, dim, v);
-  else
-    load_chunk<float, VEC>(static_cast<const float*>(base) + off, c, lane, dim, v);
+__device__ __forceinline__ void load_any(const void* base, int dt, int64_t off, int c, int lane, int dim,
+                                         float (&v)[8]) {
+  if (dt == kDtBf16) {
+    Pack<__nv_bfloat16> p;
+    load_chunk<VEC>(static_cast<const __nv_bfloat16*>(base) + off, c, lane, dim, p);
+    p.unpack(v);
+  } else {
+    Pack<float> p;
+    load_chunk<VEC>(static_cast<const float*>(base) + off, c, lane, dim, p);
+    p.unpack(v);
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_any(void* base, int dt, int64_t off, int c, int lane, int dim,
+                                          const float (&v)[8]) {
+  if (dt == kDtBf16) {
+    Pack<__nv_bfloat16> p;
+    p.pack(v);
+    store_chunk<VEC>(static_cast<__nv_bfloat16*>(base) + off, c, lane, dim, p);
+  } else {
+    Pack<float> p;
+    p.pack(v);
+    store_chunk<VEC>(static_cast<float*>(base) + off, c, lane, dim, p);
+  }
 }
 
 // Sum over the CTA's warps; `slots` holds 2 x 32 floats, used in turn so that
@@ -75,143 +131,180 @@ __device__ __forceinline__ float cta_sum(float v, float* slots, int& turn) {
   return warp_sum(lane < nw ? s[lane] : 0.0f);
 }
 
-// Codes and scales of one warp chunk (two groups of 128 columns).
-template <bool VEC>
-__device__ __forceinline__ void store_chunk_fp8(const NormArgs& A, int64_t row, int c, int lane, const float (&y)[8]) {
-  uint8_t* q = static_cast<uint8_t*>(A.out) + row * A.ldo;
-  float* sc = A.out_scale + row * A.lds_row;
-  if (VEC) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, mag_bits(y[j]));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float mul, scale;
-    fp8_scales(m, &mul, &scale);
-    const int e0 = c * kChunk + lane * 8;
-    const uint2 code = e4m3x8(y, mul);
-    if (e0 + 8 <= A.dim) {
-      *reinterpret_cast<uint2*>(q + e0) = code;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (e0 + j < A.dim) q[e0 + j] = static_cast<uint8_t>((j < 4 ? code.x : code.y) >> (8 * (j & 3)));
-    }
-    const int g = c * 2 + (lane >> 4);
-    if ((lane & 15) == 0 && g * kFp8Group < A.dim) sc[g * A.lds_group] = scale;
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) m = max(m, mag_bits(y[4 * h + j]));
-      m = __reduce_max_sync(0xffffffffu, m);
-      float mul, scale;
-      fp8_scales(m, &mul, &scale);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = col_of<false>(c, lane, 4 * h + j);
-        if (e < A.dim) q[e] = static_cast<uint8_t>(e4m3x2(y[4 * h + j] * mul, 0.0f));
-      }
-      const int g = c * 2 + h;
-      if (lane == 0 && g * kFp8Group < A.dim) sc[g * A.lds_group] = scale;
-    }
-  }
-}
-
 template <class T, int NV, bool VEC>
 __global__ void __launch_bounds__(512) k_rms_norm(const NormArgs A) {
   __shared__ float slots[64];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   int turn = 0;
-  float w[NV][8];
+  const int64_t row = blockIdx.x;
+  Pack<T> s[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) load_chunk_dt<VEC>(A.weight, A.weight_dtype, 0, warp + i * nw, lane, A.dim, w[i]);
-  const float inv_dim = 1.0f / static_cast<float>(A.dim);
-  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
-    float s[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      load_chunk<T, VEC>(static_cast<const T*>(A.x) + row * A.ldx, warp + i * nw, lane, A.dim, s[i]);
-    if (A.residual) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float r[8];
-        load_chunk<T, VEC>(static_cast<const T*>(A.residual) + row * A.ldr, warp + i * nw, lane, A.dim, r);
-        // the stream is held in its own type: what is normed is what is kept
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[i][j] = to_f32(from_f32<T>(s[i][j] + r[j]));
-        store_chunk<T, VEC>(static_cast<T*>(A.res_out) + row * A.ldro, warp + i * nw, lane, A.dim, s[i]);
-      }
-    }
-    float q = 0.0f;
+  for (int i = 0; i < NV; ++i) load_chunk<VEC>(static_cast<const T*>(A.x) + row * A.ldx, warp + i * nw, lane, A.dim, s[i]);
+  if (A.residual) {
+    Pack<T> r[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q = fmaf(s[i][j], s[i][j], q);
-    const float rstd = rsqrtf(cta_sum(q, slots, turn) * inv_dim + A.eps);
-    if (A.rstd && threadIdx.x == 0) A.rstd[row] = rstd;
+      load_chunk<VEC>(static_cast<const T*>(A.residual) + row * A.ldr, warp + i * nw, lane, A.dim, r[i]);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = warp + i * nw;
-      float y[8];
+      float a[8], b[8];
+      s[i].unpack(a);
+      r[i].unpack(b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = s[i][j] * rstd * w[i][j];
-      if (A.out_dtype == kDtE4m3)
-        store_chunk_fp8<VEC>(A, row, c, lane, y);
-      else if (A.out_dtype == kDtBf16)
-        store_chunk<__nv_bfloat16, VEC>(static_cast<__nv_bfloat16*>(A.out) + row * A.ldo, c, lane, A.dim, y);
+      for (int j = 0; j < 8; ++j) a[j] += b[j];
+      // the stream is held in its own type: what is normed is what is kept
+      s[i].pack(a);
+      store_chunk<VEC>(static_cast<T*>(A.res_out) + row * A.ldro, warp + i * nw, lane, A.dim, s[i]);
+    }
+  }
+  float q = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float a[8];
+    s[i].unpack(a);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q = fmaf(a[j], a[j], q);
+  }
+  const float rstd = rsqrtf(cta_sum(q, slots, turn) * (1.0f / static_cast<float>(A.dim)) + A.eps);
+  if (A.rstd && threadIdx.x == 0) A.rstd[row] = rstd;
+
+  auto y_of = [&](int i, float(&y)[8]) {
+    float w[8];
+    load_any<VEC>(A.weight, A.weight_dtype, 0, warp + i * nw, lane, A.dim, w);
+    s[i].unpack(y);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = y[j] * rstd * w[j];
+  };
+  if (A.out_dtype != kDtE4m3) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float y[8];
+      y_of(i, y);
+      store_any<VEC>(A.out, A.out_dtype, row * A.ldo, warp + i * nw, lane, A.dim, y);
+    }
+    return;
+  }
+  // 8 bits: lane 2 i + h divides for group h of the warp's chunk i
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float y[8];
+    y_of(i, y);
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t m = mag_bits(y[j]);
+      if (VEC ? lane < 16 : j < 4)
+        lo = max(lo, m);
       else
-        store_chunk<float, VEC>(static_cast<float*>(A.out) + row * A.ldo, c, lane, A.dim, y);
+        hi = max(hi, m);
+    }
+    lo = __reduce_max_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if ((lane >> 1) == i) amax = lane & 1 ? hi : lo;
+  }
+  float mul, scale;
+  fp8_scales(amax, &mul, &scale);
+  if (lane < 2 * NV) {
+    const int g = (warp + (lane >> 1) * nw) * 2 + (lane & 1);
+    if (g * kFp8Group < A.dim) A.out_scale[row * A.lds_row + g * A.lds_group] = scale;
+  }
+  uint8_t* o = static_cast<uint8_t*>(A.out) + row * A.ldo;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = warp + i * nw;
+    float y[8];
+    y_of(i, y);
+    if (VEC) {
+      const float m = __shfl_sync(0xffffffffu, mul, 2 * i + (lane >> 4));
+      const uint2 code = e4m3x8(y, m);
+      const int e0 = c * kChunk + lane * 8;
+      if (e0 + 8 <= A.dim) {
+        *reinterpret_cast<uint2*>(o + e0) = code;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (e0 + j < A.dim) o[e0 + j] = static_cast<uint8_t>((j < 4 ? code.x : code.y) >> (8 * (j & 3)));
+      }
+    } else {
+      const float m0 = __shfl_sync(0xffffffffu, mul, 2 * i), m1 = __shfl_sync(0xffffffffu, mul, 2 * i + 1);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e = col_of<false>(c, lane, j);
+        if (e < A.dim) o[e] = static_cast<uint8_t>(e4m3x2(y[j] * (j < 4 ? m0 : m1), 0.0f));
+      }
     }
   }
 }
 
-template <class T, int NV, bool VEC>
-__global__ void __launch_bounds__(512) k_rms_norm_grad(const NormGradArgs A) {
+// D: type of dy.  PRE: the next row's loads are in flight over this row's
+// reduction and stores, at the price of twice the row's registers.
+template <class T, class D, int NV, bool VEC, bool PRE, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_rms_norm_grad(const NormGradArgs A) {
   __shared__ float slots[64];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   int turn = 0;
-  float w[NV][8], dw[NV][8];
+  float dw[NV][8];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    load_chunk_dt<VEC>(A.weight, A.weight_dtype, 0, warp + i * nw, lane, A.dim, w[i]);
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-  }
   const float inv_dim = 1.0f / static_cast<float>(A.dim);
+  Pack<T> s[NV], e[NV];
+  Pack<D> dy[NV];
+  float rstd = 0.0f;
+  auto fetch = [&](int64_t row) {
+    rstd = A.rstd[row];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      load_chunk<VEC>(static_cast<const T*>(A.s) + row * A.lds, warp + i * nw, lane, A.dim, s[i]);
+      load_chunk<VEC>(static_cast<const D*>(A.dy) + row * A.lddy, warp + i * nw, lane, A.dim, dy[i]);
+      if (PRE && A.dres) load_chunk<VEC>(static_cast<const T*>(A.dres) + row * A.lddres, warp + i * nw, lane, A.dim, e[i]);
+    }
+  };
+  if (PRE && blockIdx.x < A.rows) fetch(blockIdx.x);
   for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
-    float xh[NV][8], g[NV][8];
-    const float rstd = A.rstd[row];
+    if (!PRE) fetch(row);
+    Pack<T> s0[NV], e0[NV];
+    Pack<D> dy0[NV];
+    const float r = rstd;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s0[i] = s[i], e0[i] = e[i], dy0[i] = dy[i];
+    if (PRE && row + gridDim.x < A.rows) fetch(row + gridDim.x);
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      load_chunk<T, VEC>(static_cast<const T*>(A.s) + row * A.lds, warp + i * nw, lane, A.dim, xh[i]);
-      load_chunk_dt<VEC>(A.dy, A.dy_dtype, row * A.lddy, warp + i * nw, lane, A.dim, g[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
+      float w[8], a[8], g[8];
+      load_any<VEC>(A.weight, A.weight_dtype, 0, warp + i * nw, lane, A.dim, w);
+      s0[i].unpack(a);
+      dy0[i].unpack(g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        xh[i][j] *= rstd;
-        dw[i][j] = fmaf(g[i][j], xh[i][j], dw[i][j]);
-        g[i][j] *= w[i][j];
-        dot = fmaf(g[i][j], xh[i][j], dot);
+        const float xh = a[j] * r, p = g[j] * xh;
+        dw[i][j] += p;
+        dot = fmaf(p, w[j], dot);
       }
+    }
     const float mean = cta_sum(dot, slots, turn) * inv_dim;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = warp + i * nw;
-      float d[8];
-      if (A.dres)
-        load_chunk<T, VEC>(static_cast<const T*>(A.dres) + row * A.lddres, c, lane, A.dim, d);
-      else {
+      float w[8], a[8], g[8], d[8];
+      load_any<VEC>(A.weight, A.weight_dtype, 0, c, lane, A.dim, w);
+      s0[i].unpack(a);
+      dy0[i].unpack(g);
+      if (A.dres) {
+        if (!PRE) load_chunk<VEC>(static_cast<const T*>(A.dres) + row * A.lddres, c, lane, A.dim, e0[i]);
+        e0[i].unpack(d);
+      } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] = 0.0f;
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, g[i][j] - xh[i][j] * mean, d[j]);
-      store_chunk<T, VEC>(static_cast<T*>(A.ds) + row * A.ldds, c, lane, A.dim, d);
+      for (int j = 0; j < 8; ++j) d[j] = fmaf(r, g[j] * w[j] - a[j] * r * mean, d[j]);
+      Pack<T> o;
+      o.pack(d);
+      store_chunk<VEC>(static_cast<T*>(A.ds) + row * A.ldds, c, lane, A.dim, o);
     }
   }
   if (A.part) {
@@ -221,8 +314,8 @@ __global__ void __launch_bounds__(512) k_rms_norm_grad(const NormGradArgs A) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int e = col_of<VEC>(warp + i * nw, lane, j);
-        if (e < A.dim) p[e] = dw[i][j];
+        const int col = col_of<VEC>(warp + i * nw, lane, j);
+        if (col < A.dim) p[col] = dw[i][j];
       }
   }
 }
@@ -246,28 +339,36 @@ struct Shape {
   int nv, warps;
 };
 
-// Two chunks a warp; one when there are too few rows to fill the SMs (a row
-// then takes the most threads it can); four or eight past 16 warps.
-Shape norm_shape(int64_t rows, int dim, int num_sms) {
+// Chunks per warp: as many as `most` (small CTAs, many rows in flight) when
+// there are rows for every SM, else as few as leave at most 16 warps (the
+// shortest time for one row).
+Shape norm_shape(int64_t rows, int dim, int num_sms, int most) {
   const int chunks = static_cast<int>(lm_div_up(dim, kChunk));
-  int nv = (rows < num_sms || chunks == 1) ? 1 : 2;
+  int nv = 1;
+  if (rows >= 2 * num_sms)
+    while (nv < most && nv < chunks) nv *= 2;
   while (lm_div_up(chunks, nv) > 16) nv *= 2;
   return {nv, static_cast<int>(lm_div_up(chunks, nv))};
 }
 
-int norm_grid(int64_t rows, int warps, int num_sms) {
-  const int per_sm = 48 / warps > 16 ? 16 : (48 / warps < 1 ? 1 : 48 / warps);
-  return static_cast<int>(rows < int64_t(num_sms) * per_sm ? rows : int64_t(num_sms) * per_sm);
+// The gradient of a row of up to 8192 columns loads a row ahead: 4 chunks a
+// warp in bf16, 2 when something is fp32 (or one, as above).  Longer rows
+// need the registers for themselves.
+constexpr int kPreChunks = 32;
+Shape grad_shape(int64_t rows, int dim, bool all_bf16, int num_sms) {
+  return norm_shape(rows, dim, num_sms, all_bf16 && dim <= kPreChunks * kChunk ? 4 : 2);
 }
 
-int grad_grid(int64_t rows, int warps, int num_sms) {
-  const int per_sm = 24 / warps > 8 ? 8 : (24 / warps < 1 ? 1 : 24 / warps);
+// CTAs of the gradient: what the registers of an SM hold
+int grad_grid(int64_t rows, Shape sh, int num_sms) {
+  const int warps = sh.nv == 4 ? 12 : sh.nv == 1 ? 20 : 16;
+  const int per_sm = warps / sh.warps < 1 ? 1 : warps / sh.warps > 12 ? 12 : warps / sh.warps;
   return static_cast<int>(rows < int64_t(num_sms) * per_sm ? rows : int64_t(num_sms) * per_sm);
 }
 
 template <class T, bool VEC>
-void run_norm(const NormArgs& A, Shape sh, int grid, cudaStream_t st) {
-  const int threads = sh.warps * 32;
+void run_norm(const NormArgs& A, Shape sh, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>(A.rows), threads = sh.warps * 32;
   switch (sh.nv) {
     case 1: k_rms_norm<T, 1, VEC><<<grid, threads, 0, st>>>(A); break;
     case 2: k_rms_norm<T, 2, VEC><<<grid, threads, 0, st>>>(A); break;
@@ -276,15 +377,27 @@ void run_norm(const NormArgs& A, Shape sh, int grid, cudaStream_t st) {
   }
 }
 
-template <class T, bool VEC>
+template <class T, class D, bool VEC>
 void run_grad(const NormGradArgs& A, Shape sh, int grid, cudaStream_t st) {
   const int threads = sh.warps * 32;
-  switch (sh.nv) {
-    case 1: k_rms_norm_grad<T, 1, VEC><<<grid, threads, 0, st>>>(A); break;
-    case 2: k_rms_norm_grad<T, 2, VEC><<<grid, threads, 0, st>>>(A); break;
-    case 4: k_rms_norm_grad<T, 4, VEC><<<grid, threads, 0, st>>>(A); break;
-    default: k_rms_norm_grad<T, 8, VEC><<<grid, threads, 0, st>>>(A); break;
+  const bool pre = A.dim <= kPreChunks * kChunk;
+  constexpr bool kBf16 = sizeof(T) == 2 && sizeof(D) == 2;
+  if constexpr (kBf16) {
+    // at most 8 warps; the bound of 384 threads caps the registers at 168, so
+    // that an SM holds 12 warps
+    if (sh.nv == 4 && pre) {
+      k_rms_norm_grad<T, D, 4, VEC, true, 384><<<grid, threads, 0, st>>>(A);
+      return;
+    }
   }
+  if (sh.nv == 1)
+    k_rms_norm_grad<T, D, 1, VEC, true, 512><<<grid, threads, 0, st>>>(A);
+  else if (sh.nv == 2)
+    k_rms_norm_grad<T, D, 2, VEC, true, 512><<<grid, threads, 0, st>>>(A);
+  else if (sh.nv == 4)
+    k_rms_norm_grad<T, D, 4, VEC, false, 512><<<grid, threads, 0, st>>>(A);
+  else
+    k_rms_norm_grad<T, D, 8, VEC, false, 512><<<grid, threads, 0, st>>>(A);
 }
 
 int elem_bytes(int dt) { return dt == kDtF32 ? 4 : dt == kDtBf16 ? 2 : 1; }
@@ -293,37 +406,50 @@ int elem_bytes(int dt) { return dt == kDtF32 ? 4 : dt == kDtBf16 ? 2 : 1; }
 
 cudaError_t launch_rms_norm(const NormArgs& A, int dtype, int num_sms, cudaStream_t st) {
   if (A.rows <= 0) return cudaSuccess;
-  const Shape sh = norm_shape(A.rows, A.dim, num_sms);
-  const int grid = norm_grid(A.rows, sh.warps, num_sms), eb = elem_bytes(dtype);
+  const int eb = elem_bytes(dtype);
+  const Shape sh = norm_shape(A.rows, A.dim, num_sms, dtype == kDtBf16 ? 8 : 4);
   const bool vec = lm_aligned(A.x, A.ldx, A.rows, eb, 16) &&
                    (!A.residual || (lm_aligned(A.residual, A.ldr, A.rows, eb, 16) &&
                                     lm_aligned(A.res_out, A.ldro, A.rows, eb, 16))) &&
                    lm_aligned(A.weight, 0, 1, 1, 16) &&
                    lm_aligned(A.out, A.ldo, A.rows, elem_bytes(A.out_dtype), A.out_dtype == kDtE4m3 ? 8 : 16);
   if (dtype == kDtBf16)
-    vec ? run_norm<__nv_bfloat16, true>(A, sh, grid, st) : run_norm<__nv_bfloat16, false>(A, sh, grid, st);
+    vec ? run_norm<__nv_bfloat16, true>(A, sh, st) : run_norm<__nv_bfloat16, false>(A, sh, st);
   else
-    vec ? run_norm<float, true>(A, sh, grid, st) : run_norm<float, false>(A, sh, grid, st);
+    vec ? run_norm<float, true>(A, sh, st) : run_norm<float, false>(A, sh, st);
   return cudaGetLastError();
 }
 
 size_t rms_norm_grad_workspace(int64_t rows, int64_t dim, int num_sms) {
-  const Shape sh = norm_shape(rows, static_cast<int>(dim), num_sms);
-  return static_cast<size_t>(grad_grid(rows, sh.warps, num_sms)) * static_cast<size_t>(dim) * sizeof(float);
+  // the larger grid of the two types' shapes
+  int grid = 0;
+  for (int b = 0; b < 2; ++b) {
+    const int g = grad_grid(rows, grad_shape(rows, static_cast<int>(dim), b != 0, num_sms), num_sms);
+    grid = g > grid ? g : grid;
+  }
+  return static_cast<size_t>(grid) * static_cast<size_t>(dim) * sizeof(float);
 }
 
 cudaError_t launch_rms_norm_grad(const NormGradArgs& A, int s_dtype, float* dweight, int num_sms, cudaStream_t st) {
   if (A.rows <= 0) return dweight ? cudaMemsetAsync(dweight, 0, sizeof(float) * A.dim, st) : cudaSuccess;
-  const Shape sh = norm_shape(A.rows, A.dim, num_sms);
-  const int grid = grad_grid(A.rows, sh.warps, num_sms), eb = elem_bytes(s_dtype);
+  const Shape sh = grad_shape(A.rows, A.dim, s_dtype == kDtBf16 && A.dy_dtype == kDtBf16, num_sms);
+  const int grid = grad_grid(A.rows, sh, num_sms), eb = elem_bytes(s_dtype);
   const bool vec = lm_aligned(A.s, A.lds, A.rows, eb, 16) && lm_aligned(A.ds, A.ldds, A.rows, eb, 16) &&
                    (!A.dres || lm_aligned(A.dres, A.lddres, A.rows, eb, 16)) &&
                    lm_aligned(A.dy, A.lddy, A.rows, elem_bytes(A.dy_dtype), 16) &&
                    lm_aligned(A.weight, 0, 1, 1, 16);
-  if (s_dtype == kDtBf16)
-    vec ? run_grad<__nv_bfloat16, true>(A, sh, grid, st) : run_grad<__nv_bfloat16, false>(A, sh, grid, st);
-  else
-    vec ? run_grad<float, true>(A, sh, grid, st) : run_grad<float, false>(A, sh, grid, st);
+  typedef __nv_bfloat16 B;
+  if (s_dtype == kDtBf16) {
+    if (A.dy_dtype == kDtBf16)
+      vec ? run_grad<B, B, true>(A, sh, grid, st) : run_grad<B, B, false>(A, sh, grid, st);
+    else
+      vec ? run_grad<B, float, true>(A, sh, grid, st) : run_grad<B, float, false>(A, sh, grid, st);
+  } else {
+    if (A.dy_dtype == kDtBf16)
+      vec ? run_grad<float, B, true>(A, sh, grid, st) : run_grad<float, B, false>(A, sh, grid, st);
+    else
+      vec ? run_grad<float, float, true>(A, sh, grid, st) : run_grad<float, float, false>(A, sh, grid, st);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !dweight) return e;
   k_rms_norm_dweight<<<static_cast<int>(lm_div_up(A.dim, 32)), dim3(32, 32), 0, st>>>(A.part, grid, A.dim, dweight);
