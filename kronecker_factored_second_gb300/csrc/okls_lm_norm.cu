@@ -9,9 +9,10 @@
 // CTA, and written from the same registers.  A warp chunk is 256 columns, 8
 // elements a lane; a warp takes NV chunks and a row as many warps as it needs.
 // Rows are held in their own type (packed), so that a CTA is small (2 warps
-// for 4096 bf16 columns) and many rows are in flight on an SM.  The gradient
-// keeps the weight's sums of its columns in registers over all rows of a CTA
-// and loads a row ahead.
+// for 2048 bf16 columns) and many rows are in flight on an SM.  The gradient
+// keeps the weight's sums of its columns in registers over all rows of a CTA,
+// and loads rows ahead through a ring in shared memory: each thread copies
+// and later reads its own elements, so the ring needs no barrier.
 //
 // A group of 128 columns with one 8-bit scale lies inside a warp chunk: its
 // largest magnitude is two warp reductions, each lane divides for one group
@@ -237,10 +238,145 @@ __global__ void __launch_bounds__(512) k_rms_norm(const NormArgs A) {
   }
 }
 
-// D: type of dy.  PRE: the next row's loads are in flight over this row's
-// reduction and stores, at the price of twice the row's registers.
-template <class T, class D, int NV, bool VEC, bool PRE, int MAXT>
-__global__ void __launch_bounds__(MAXT) k_rms_norm_grad(const NormGradArgs A) {
+// 16 bytes into shared memory without registers; the first `bytes` of them
+// from global memory, zeros after that.
+__device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the latest `pending` groups of this thread have landed.
+__device__ __forceinline__ void copy_wait(int pending) {
+  switch (pending) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+  }
+}
+constexpr int kMaxAhead = 4;
+
+// Copies one lane's 8 elements of chunk c into its slot.
+template <class T>
+__device__ __forceinline__ void copy_chunk(Pack<T>* dst, const T* row, int c, int lane, int dim) {
+  const int e0 = c * kChunk + lane * 8;
+  constexpr int per = 16 / sizeof(T);
+#pragma unroll
+  for (int h = 0; h < static_cast<int>(sizeof(Pack<T>) / 16); ++h) {
+    const int e = e0 + h * per;
+    const int n = e >= dim ? 0 : e + per <= dim ? per : dim - e;
+    copy16(reinterpret_cast<char*>(dst) + h * 16, row + (n ? e : 0), n * static_cast<int>(sizeof(T)));
+  }
+}
+
+// Rows ahead in a ring of `ring` rows (shared memory: per row and thread NV
+// packs of s, dy and dres).  Needs 16-byte aligned rows.
+template <class T, class D, int NV>
+__global__ void __launch_bounds__(512) k_rms_norm_grad_ring(const NormGradArgs A, int ring) {
+  extern __shared__ __align__(16) char ring_mem[];
+  __shared__ float slots[64];
+  __shared__ float rstds[16][kMaxAhead];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = blockDim.x >> 5, nt = blockDim.x;
+  // [stage][tensor][chunk][thread]
+  const int s_bytes = nt * NV * static_cast<int>(sizeof(Pack<T>)), d_bytes = nt * NV * static_cast<int>(sizeof(Pack<D>));
+  const int stage_bytes = s_bytes * 2 + d_bytes;
+  auto s_at = [&](int st, int i) { return reinterpret_cast<Pack<T>*>(ring_mem + st * stage_bytes) + i * nt + tid; };
+  auto e_at = [&](int st, int i) { return reinterpret_cast<Pack<T>*>(ring_mem + st * stage_bytes + s_bytes) + i * nt + tid; };
+  auto d_at = [&](int st, int i) {
+    return reinterpret_cast<Pack<D>*>(ring_mem + st * stage_bytes + 2 * s_bytes) + i * nt + tid;
+  };
+  auto fetch = [&](int64_t row, int st) {
+    if (row < A.rows) {
+      if (lane == 0)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                         static_cast<uint32_t>(__cvta_generic_to_shared(&rstds[warp][st]))),
+                     "l"(A.rstd + row)
+                     : "memory");
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        copy_chunk(s_at(st, i), static_cast<const T*>(A.s) + row * A.lds, warp + i * nw, lane, A.dim);
+        copy_chunk(d_at(st, i), static_cast<const D*>(A.dy) + row * A.lddy, warp + i * nw, lane, A.dim);
+        if (A.dres) copy_chunk(e_at(st, i), static_cast<const T*>(A.dres) + row * A.lddres, warp + i * nw, lane, A.dim);
+      }
+    }
+    copy_commit();
+  };
+  for (int st = 0; st < ring; ++st) fetch(blockIdx.x + static_cast<int64_t>(st) * gridDim.x, st);
+
+  int turn = 0, st = 0;
+  float w[NV][8], dw[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    load_any<true>(A.weight, A.weight_dtype, 0, warp + i * nw, lane, A.dim, w[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  }
+  const float inv_dim = 1.0f / static_cast<float>(A.dim);
+  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
+    copy_wait(ring - 1);
+    __syncwarp();  // lane 0's copy of rstd
+    const float r = rstds[warp][st];
+    Pack<T> s[NV], e[NV];
+    Pack<D> dy[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      s[i] = *s_at(st, i);
+      dy[i] = *d_at(st, i);
+      if (A.dres) e[i] = *e_at(st, i);
+    }
+    __syncwarp();
+    fetch(row + static_cast<int64_t>(ring) * gridDim.x, st);
+    if (++st == ring) st = 0;
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float a[8], g[8];
+      s[i].unpack(a);
+      dy[i].unpack(g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float p = g[j] * (a[j] * r);
+        dw[i][j] += p;
+        dot = fmaf(p, w[i][j], dot);
+      }
+    }
+    const float mean = cta_sum(dot, slots, turn) * inv_dim;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float a[8], g[8], d[8];
+      s[i].unpack(a);
+      dy[i].unpack(g);
+      if (A.dres) {
+        e[i].unpack(d);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = fmaf(r, g[j] * w[i][j] - a[j] * r * mean, d[j]);
+      Pack<T> o;
+      o.pack(d);
+      store_chunk<true>(static_cast<T*>(A.ds) + row * A.ldds, warp + i * nw, lane, A.dim, o);
+    }
+  }
+  copy_wait(0);
+  if (A.part) {
+    float* p = A.part + static_cast<int64_t>(blockIdx.x) * A.dim;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int col = col_of<true>(warp + i * nw, lane, j);
+        if (col < A.dim) p[col] = dw[i][j];
+      }
+  }
+}
+
+// The same with the rows loaded straight into registers: for rows that are
+// not 16-byte aligned, or too long for the ring.
+template <class T, class D, int NV, bool VEC>
+__global__ void __launch_bounds__(512) k_rms_norm_grad(const NormGradArgs A) {
   __shared__ float slots[64];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   int turn = 0;
@@ -250,37 +386,25 @@ __global__ void __launch_bounds__(MAXT) k_rms_norm_grad(const NormGradArgs A) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   const float inv_dim = 1.0f / static_cast<float>(A.dim);
-  Pack<T> s[NV], e[NV];
-  Pack<D> dy[NV];
-  float rstd = 0.0f;
-  auto fetch = [&](int64_t row) {
-    rstd = A.rstd[row];
+  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
+    const float r = A.rstd[row];
+    Pack<T> s[NV];
+    Pack<D> dy[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       load_chunk<VEC>(static_cast<const T*>(A.s) + row * A.lds, warp + i * nw, lane, A.dim, s[i]);
       load_chunk<VEC>(static_cast<const D*>(A.dy) + row * A.lddy, warp + i * nw, lane, A.dim, dy[i]);
-      if (PRE && A.dres) load_chunk<VEC>(static_cast<const T*>(A.dres) + row * A.lddres, warp + i * nw, lane, A.dim, e[i]);
     }
-  };
-  if (PRE && blockIdx.x < A.rows) fetch(blockIdx.x);
-  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
-    if (!PRE) fetch(row);
-    Pack<T> s0[NV], e0[NV];
-    Pack<D> dy0[NV];
-    const float r = rstd;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s0[i] = s[i], e0[i] = e[i], dy0[i] = dy[i];
-    if (PRE && row + gridDim.x < A.rows) fetch(row + gridDim.x);
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float w[8], a[8], g[8];
       load_any<VEC>(A.weight, A.weight_dtype, 0, warp + i * nw, lane, A.dim, w);
-      s0[i].unpack(a);
-      dy0[i].unpack(g);
+      s[i].unpack(a);
+      dy[i].unpack(g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float xh = a[j] * r, p = g[j] * xh;
+        const float p = g[j] * (a[j] * r);
         dw[i][j] += p;
         dot = fmaf(p, w[j], dot);
       }
@@ -291,18 +415,18 @@ __global__ void __launch_bounds__(MAXT) k_rms_norm_grad(const NormGradArgs A) {
       const int c = warp + i * nw;
       float w[8], a[8], g[8], d[8];
       load_any<VEC>(A.weight, A.weight_dtype, 0, c, lane, A.dim, w);
-      s0[i].unpack(a);
-      dy0[i].unpack(g);
+      s[i].unpack(a);
+      dy[i].unpack(g);
+      Pack<T> o;
       if (A.dres) {
-        if (!PRE) load_chunk<VEC>(static_cast<const T*>(A.dres) + row * A.lddres, c, lane, A.dim, e0[i]);
-        e0[i].unpack(d);
+        load_chunk<VEC>(static_cast<const T*>(A.dres) + row * A.lddres, c, lane, A.dim, o);
+        o.unpack(d);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] = 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) d[j] = fmaf(r, g[j] * w[j] - a[j] * r * mean, d[j]);
-      Pack<T> o;
       o.pack(d);
       store_chunk<VEC>(static_cast<T*>(A.ds) + row * A.ldds, c, lane, A.dim, o);
     }
@@ -327,6 +451,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm_dweight(const float* part, in
   const int col = blockIdx.x * 32 + threadIdx.x;
   float v = 0.0f;
   if (col < dim)
+#pragma unroll 8
     for (int p = threadIdx.y; p < nparts; p += 32) v += part[static_cast<int64_t>(p) * dim + col];
   t[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
@@ -351,19 +476,13 @@ Shape norm_shape(int64_t rows, int dim, int num_sms, int most) {
   return {nv, static_cast<int>(lm_div_up(chunks, nv))};
 }
 
-// The gradient of a row of up to 8192 columns loads a row ahead: 4 chunks a
-// warp in bf16, 2 when something is fp32 (or one, as above).  Longer rows
-// need the registers for themselves.
-constexpr int kPreChunks = 32;
-Shape grad_shape(int64_t rows, int dim, bool all_bf16, int num_sms) {
-  return norm_shape(rows, dim, num_sms, all_bf16 && dim <= kPreChunks * kChunk ? 4 : 2);
-}
+Shape grad_shape(int64_t rows, int dim, int num_sms) { return norm_shape(rows, dim, num_sms, 2); }
 
-// CTAs of the gradient: what the registers of an SM hold
+// CTAs of the gradient: about 20 warps an SM
 int grad_grid(int64_t rows, Shape sh, int num_sms) {
-  const int warps = sh.nv == 4 ? 12 : sh.nv == 1 ? 20 : 16;
-  const int per_sm = warps / sh.warps < 1 ? 1 : warps / sh.warps > 12 ? 12 : warps / sh.warps;
-  return static_cast<int>(rows < int64_t(num_sms) * per_sm ? rows : int64_t(num_sms) * per_sm);
+  const int per_sm = (20 + sh.warps / 2) / sh.warps;
+  const int64_t most = int64_t(num_sms) * (per_sm < 1 ? 1 : per_sm > 10 ? 10 : per_sm);
+  return static_cast<int>(rows < most ? rows : most);
 }
 
 template <class T, bool VEC>
@@ -377,27 +496,37 @@ void run_norm(const NormArgs& A, Shape sh, cudaStream_t st) {
   }
 }
 
-template <class T, class D, bool VEC>
-void run_grad(const NormGradArgs& A, Shape sh, int grid, cudaStream_t st) {
+template <class T, class D, int NV>
+cudaError_t run_grad_nv(const NormGradArgs& A, Shape sh, int grid, int num_sms, bool vec, cudaStream_t st) {
   const int threads = sh.warps * 32;
-  const bool pre = A.dim <= kPreChunks * kChunk;
-  constexpr bool kBf16 = sizeof(T) == 2 && sizeof(D) == 2;
-  if constexpr (kBf16) {
-    // at most 8 warps; the bound of 384 threads caps the registers at 168, so
-    // that an SM holds 12 warps
-    if (sh.nv == 4 && pre) {
-      k_rms_norm_grad<T, D, 4, VEC, true, 384><<<grid, threads, 0, st>>>(A);
-      return;
-    }
+  const int row_bytes = threads * NV * static_cast<int>(2 * sizeof(Pack<T>) + sizeof(Pack<D>));
+  const int per_sm = static_cast<int>(lm_div_up(grid, num_sms));
+  constexpr int kSmemPerSm = 216 * 1024;
+  int ring = kSmemPerSm / (per_sm * (row_bytes + 2048));
+  if (ring > kMaxAhead) ring = kMaxAhead;
+  if (vec && ring >= 1) {
+    static PerDevice pd;
+    const cudaError_t e = once_per_device(pd, [](int) {
+      return cudaFuncSetAttribute(k_rms_norm_grad_ring<T, D, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
+    });
+    if (e != cudaSuccess) return e;
+    k_rms_norm_grad_ring<T, D, NV><<<grid, threads, ring * row_bytes, st>>>(A, ring);
+  } else if (vec) {
+    k_rms_norm_grad<T, D, NV, true><<<grid, threads, 0, st>>>(A);
+  } else {
+    k_rms_norm_grad<T, D, NV, false><<<grid, threads, 0, st>>>(A);
   }
-  if (sh.nv == 1)
-    k_rms_norm_grad<T, D, 1, VEC, true, 512><<<grid, threads, 0, st>>>(A);
-  else if (sh.nv == 2)
-    k_rms_norm_grad<T, D, 2, VEC, true, 512><<<grid, threads, 0, st>>>(A);
-  else if (sh.nv == 4)
-    k_rms_norm_grad<T, D, 4, VEC, false, 512><<<grid, threads, 0, st>>>(A);
-  else
-    k_rms_norm_grad<T, D, 8, VEC, false, 512><<<grid, threads, 0, st>>>(A);
+  return cudaGetLastError();
+}
+
+template <class T, class D>
+cudaError_t run_grad(const NormGradArgs& A, Shape sh, int grid, int num_sms, bool vec, cudaStream_t st) {
+  switch (sh.nv) {
+    case 1: return run_grad_nv<T, D, 1>(A, sh, grid, num_sms, vec, st);
+    case 2: return run_grad_nv<T, D, 2>(A, sh, grid, num_sms, vec, st);
+    case 4: return run_grad_nv<T, D, 4>(A, sh, grid, num_sms, vec, st);
+    default: return run_grad_nv<T, D, 8>(A, sh, grid, num_sms, vec, st);
+  }
 }
 
 int elem_bytes(int dt) { return dt == kDtF32 ? 4 : dt == kDtBf16 ? 2 : 1; }
@@ -407,7 +536,7 @@ int elem_bytes(int dt) { return dt == kDtF32 ? 4 : dt == kDtBf16 ? 2 : 1; }
 cudaError_t launch_rms_norm(const NormArgs& A, int dtype, int num_sms, cudaStream_t st) {
   if (A.rows <= 0) return cudaSuccess;
   const int eb = elem_bytes(dtype);
-  const Shape sh = norm_shape(A.rows, A.dim, num_sms, dtype == kDtBf16 ? 8 : 4);
+  const Shape sh = norm_shape(A.rows, A.dim, num_sms, 4);
   const bool vec = lm_aligned(A.x, A.ldx, A.rows, eb, 16) &&
                    (!A.residual || (lm_aligned(A.residual, A.ldr, A.rows, eb, 16) &&
                                     lm_aligned(A.res_out, A.ldro, A.rows, eb, 16))) &&
@@ -421,36 +550,24 @@ cudaError_t launch_rms_norm(const NormArgs& A, int dtype, int num_sms, cudaStrea
 }
 
 size_t rms_norm_grad_workspace(int64_t rows, int64_t dim, int num_sms) {
-  // the larger grid of the two types' shapes
-  int grid = 0;
-  for (int b = 0; b < 2; ++b) {
-    const int g = grad_grid(rows, grad_shape(rows, static_cast<int>(dim), b != 0, num_sms), num_sms);
-    grid = g > grid ? g : grid;
-  }
-  return static_cast<size_t>(grid) * static_cast<size_t>(dim) * sizeof(float);
+  const Shape sh = grad_shape(rows, static_cast<int>(dim), num_sms);
+  return static_cast<size_t>(grad_grid(rows, sh, num_sms)) * static_cast<size_t>(dim) * sizeof(float);
 }
 
 cudaError_t launch_rms_norm_grad(const NormGradArgs& A, int s_dtype, float* dweight, int num_sms, cudaStream_t st) {
   if (A.rows <= 0) return dweight ? cudaMemsetAsync(dweight, 0, sizeof(float) * A.dim, st) : cudaSuccess;
-  const Shape sh = grad_shape(A.rows, A.dim, s_dtype == kDtBf16 && A.dy_dtype == kDtBf16, num_sms);
+  const Shape sh = grad_shape(A.rows, A.dim, num_sms);
   const int grid = grad_grid(A.rows, sh, num_sms), eb = elem_bytes(s_dtype);
   const bool vec = lm_aligned(A.s, A.lds, A.rows, eb, 16) && lm_aligned(A.ds, A.ldds, A.rows, eb, 16) &&
                    (!A.dres || lm_aligned(A.dres, A.lddres, A.rows, eb, 16)) &&
                    lm_aligned(A.dy, A.lddy, A.rows, elem_bytes(A.dy_dtype), 16) &&
                    lm_aligned(A.weight, 0, 1, 1, 16);
   typedef __nv_bfloat16 B;
-  if (s_dtype == kDtBf16) {
-    if (A.dy_dtype == kDtBf16)
-      vec ? run_grad<B, B, true>(A, sh, grid, st) : run_grad<B, B, false>(A, sh, grid, st);
-    else
-      vec ? run_grad<B, float, true>(A, sh, grid, st) : run_grad<B, float, false>(A, sh, grid, st);
-  } else {
-    if (A.dy_dtype == kDtBf16)
-      vec ? run_grad<float, B, true>(A, sh, grid, st) : run_grad<float, B, false>(A, sh, grid, st);
-    else
-      vec ? run_grad<float, float, true>(A, sh, grid, st) : run_grad<float, float, false>(A, sh, grid, st);
-  }
-  cudaError_t e = cudaGetLastError();
+  const bool b = A.dy_dtype == kDtBf16;
+  const cudaError_t e = s_dtype == kDtBf16
+                            ? (b ? run_grad<B, B>(A, sh, grid, num_sms, vec, st) : run_grad<B, float>(A, sh, grid, num_sms, vec, st))
+                            : (b ? run_grad<float, B>(A, sh, grid, num_sms, vec, st)
+                                 : run_grad<float, float>(A, sh, grid, num_sms, vec, st));
   if (e != cudaSuccess || !dweight) return e;
   k_rms_norm_dweight<<<static_cast<int>(lm_div_up(A.dim, 32)), dim3(32, 32), 0, st>>>(A.part, grid, A.dim, dweight);
   return cudaGetLastError();
