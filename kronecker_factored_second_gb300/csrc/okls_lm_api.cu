@@ -147,7 +147,7 @@ okls_status okls_rms_norm(const void* x, int32_t dtype, int64_t ldx, const void*
   const char* op = "okls_rms_norm";
   if (!float_dtype(dtype) || !float_dtype(weight_dtype)) return bad(op, "input dtypes must be fp32 or bf16");
   if (!float_dtype(out_dtype) && out_dtype != OKLS_E4M3) return bad(op, "out_dtype must be fp32, bf16 or e4m3");
-  if (rows < 0 || dim < 1) return bad(op, "rows must be non-negative, dim positive");
+  if (rows < 0 || rows > kMaxGrid || dim < 1) return bad(op, "rows must be in [0, 2^31), dim positive");
   if (dim > kNormMaxDim)
     return host_fail(OKLS_ERR_UNSUPPORTED, "%s: dim %lld is above %d", op, static_cast<ll>(dim), kNormMaxDim);
   if (!(eps >= 0.0f) || std::isinf(eps)) return bad(op, "eps must be finite and non-negative");
@@ -330,6 +330,7 @@ okls_status okls_token_logprobs(const void* logits, int32_t dtype, int64_t ldl, 
   const char* op = "okls_token_logprobs";
   if (!float_dtype(dtype)) return bad(op, "dtype must be fp32 or bf16");
   if (rows < 0 || vocab < 1 || vocab > kMaxSide) return bad(op, "rows must be non-negative, vocab in [1, 2^31)");
+  if (rows > kMaxGrid / 8) return bad(op, "rows must be below 2^28");
   if (!(scale > 0.0f) || std::isinf(scale)) return bad(op, "scale must be positive and finite");
   if (top_k < 0 || top_k > 32 || top_k > vocab) return bad(op, "top_k must be in [0, min(vocab, 32)]");
   if (!status_dev) return bad(op, "status_dev is NULL");
