@@ -16,14 +16,16 @@
 // products are left per value (two values an instruction where the hardware
 // has it), which a bf16 row just hides under its loads.
 //
-// Best alternatives ride along: each warp keeps the 32 best (logit, column)
-// keys sorted across its lanes.  A key is 64 bits, the order-preserving image
-// of the logit above the complement of the column, so equal logits rank by
-// column and no two keys are equal.  A warp's first 1024 values give a first
-// bound, the k-th largest of its lanes' maxima; a CTA-wide bound (the best of
-// its warps' k-th keys) then rejects almost every group of 32 values with the
-// maximum that the sums need anyway, and about k ln(vocab / k) insertions a
-// row are left.
+// Best alternatives are found from maxima.  A key is 64 bits, the
+// order-preserving image of the logit above the complement of the column, so
+// equal logits rank by column and no two keys are equal.  Each thread keeps
+// the maximum of every 32 values it has read.  If k threads have seen a value
+// of at least b, the k best are at least b; such a bound is taken from the
+// threads' maxima, few values reach it, and these are read once more, where a
+// maximum says so, and ranked by counting.  If more values reach the bound
+// than the list holds (many equal logits), the row is read again and each
+// warp keeps a sorted list of its 32 best keys, into which it inserts one at a
+// time.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -86,12 +88,13 @@ __device__ __forceinline__ void list_insert(Key& mine, Key cand, int lane) {
 
 // The 32 best of two sorted lists, sorted: the larger of a[i] and b[31 - i]
 // form a bitonic list of them, which five compare-exchange steps sort.
-__device__ __forceinline__ Key list_merge(Key a, Key b, int lane) {
-  const Key rb = __shfl_sync(0xffffffffu, b, 31 - lane);
-  Key v = a > rb ? a : rb;
+template <class V>
+__device__ __forceinline__ V list_merge(V a, V b, int lane) {
+  const V rb = __shfl_sync(0xffffffffu, b, 31 - lane);
+  V v = a > rb ? a : rb;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const Key w = __shfl_xor_sync(0xffffffffu, v, o);
+    const V w = __shfl_xor_sync(0xffffffffu, v, o);
     const bool keep_max = (lane & o) == 0;
     v = keep_max ? (v > w ? v : w) : (v > w ? w : v);
   }
@@ -101,6 +104,10 @@ __device__ __forceinline__ Key list_merge(Key a, Key b, int lane) {
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kVecs = 4;  // vectors of 8 values a thread loads at a time
+// A row goes to one warp when it is short, or when there are rows for 16
+// warps on every SM (8192 x 8000 bf16: 47 us with a CTA a row, 28 with a warp;
+// 8192 x 16000: 68 and 49); longer rows leave the SMs unevenly filled.
+constexpr int kWarpRow = 16384, kWarpRowFew = 4096;
 
 __device__ __forceinline__ float ex2(float v) {
   float r;
@@ -144,18 +151,19 @@ struct Best {
   float bound_v;
 };
 
-// k-th largest of the lanes' values.
-__device__ __forceinline__ uint32_t kth_of_lanes(uint32_t v, int k, int lane) {
+// The lanes' values in descending order (bitonic).
+template <class V>
+__device__ __forceinline__ V sort_lanes(V v, int lane) {
 #pragma unroll
   for (int w = 2; w <= 32; w <<= 1)
 #pragma unroll
     for (int o = w >> 1; o > 0; o >>= 1) {
-      const uint32_t x = __shfl_xor_sync(0xffffffffu, v, o);
+      const V x = __shfl_xor_sync(0xffffffffu, v, o);
       // descending in even blocks of w lanes, ascending in odd ones
       const bool keep_max = ((lane & o) == 0) == ((lane & w) == 0);
-      v = keep_max ? max(v, x) : min(v, x);
+      v = keep_max ? (v > x ? v : x) : (v > x ? x : v);
     }
-  return __shfl_sync(0xffffffffu, v, k - 1);
+  return v;
 }
 
 // Offers the warp's values to its list: lane values z[j], j < count, whose
@@ -172,7 +180,7 @@ __device__ __forceinline__ void offer(Best& B, const float (&z)[N], float vm, in
   if (!__any_sync(0xffffffffu, count > 0 && !(vm < B.bound_v))) return;
   if (N > 1 && B.bound == 0) {
     // the k-th best of 32 of the warp's values, one a lane
-    const uint32_t kth = kth_of_lanes(count > 0 ? ord_bits(vm) : 0u, k, lane);
+    const uint32_t kth = __shfl_sync(0xffffffffu, sort_lanes(count > 0 ? ord_bits(vm) : 0u, lane), k - 1);
     if (kth > 0) B.bound = (static_cast<Key>(kth) << 32) - 1;
     B.bound_v = kth > 0 ? ord_value(kth - 1) : -CUDART_INF_F;
   }
@@ -215,7 +223,9 @@ __device__ __forceinline__ float take(Stat& L, const float (&z)[N], float scale)
   // would leave the rounding error of a huge masked logit
   const float top = SCALED ? __fmul_rn(vm, scale) : vm;
   if (top != top) {
-    L.s = top;  // the row's sums are NaN from here on
+    L.s = top;  // the row's sums are NaN from here on; the others still rank
+#pragma unroll
+    for (int j = 0; j < N; ++j) vm = fmaxf(vm, z[j]);
     return vm;
   }
   if (top > L.m) {
@@ -259,67 +269,265 @@ __device__ __forceinline__ float take(Stat& L, const float (&z)[N], float scale)
   return vm;
 }
 
-template <class T, bool TOP, bool SCALED>
-__global__ void __launch_bounds__(kScoreThreads) k_token_logprobs(const ScoreArgs A) {
-  __shared__ Stat stats[kScoreWarps];
-  __shared__ Stat cta_stat;
-  __shared__ Key lists[TOP ? kScoreWarps : 1][32];
-  __shared__ Key cta_bound;
-  cg::cluster_group cluster = cg::this_cluster();
-  const uint32_t rank = cluster.block_rank(), nct = cluster.num_blocks();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int k = TOP ? A.top_k : 1;
-  const int64_t vocab = A.vocab;
-  const int64_t row = blockIdx.x / nct;
-  if (TOP) {
-    if (threadIdx.x == 0) cta_bound = 0;
-    __syncthreads();
-  }
-  const T* z = static_cast<const T*>(A.logits) + row * A.ldl;
-  Stat L = {-CUDART_INF_F, 0.0f, 0.0f};
-  Best B = {0, 0, -CUDART_INF_F};
-  // 16-byte aligned body; the columns before and after it one by one
-  const int64_t mis = (reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T);
-  const int64_t head = min(vocab, mis ? static_cast<int64_t>(16 / sizeof(T)) - mis : int64_t(0));
-  const int64_t nvec = (vocab - head) / 8;
-  const int64_t tail0 = head + nvec * 8;
-  const int64_t step = int64_t(nct) * kScoreThreads;  // vectors between a thread's vectors
-  for (int64_t v0 = int64_t(rank) * kScoreThreads + warp * 32; v0 < nvec; v0 += step * kVecs) {
-    const int64_t i = v0 + lane;
-    float v[kVecs * 8];
-    int count = 0;
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      float t[8];
-      if (i + u * step < nvec) {
-        load8(z + head + (i + u * step) * 8, t);
-        count += 8;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] = -CUDART_INF_F;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[u * 8 + j] = t[j];
+// Results of a row from the sums L (the same in all lanes) and the list.
+template <class T, bool TOP>
+__device__ __forceinline__ void write_row(const ScoreArgs& A, int64_t row, const T* z, const Stat& L, Key best, int lane,
+                                          int k) {
+  const bool none = L.m == -CUDART_INF_F && L.s == 0.0f;  // no possible token
+  // a sum that is NaN (a NaN logit) makes everything NaN, and so does an
+  // infinite maximum, whose sum is 0
+  const float logs = logf(L.s);
+  const float lse = none ? -CUDART_INF_F : (L.s != L.s ? L.s : L.m + logs);
+  if (lane == 0) {
+    if (A.lse) A.lse[row] = lse;
+    if (A.entropy) A.entropy[row] = none ? 0.0f : logs - L.q / L.s;
+    if (A.logp) {
+      const int64_t id = token_at(A.ids, A.ids_i64, row);
+      if (id >= A.vocab) atomicOr(A.status, kStBadToken);
+      float lp = 0.0f;
+      if (id >= 0 && id < A.vocab) lp = none ? -CUDART_INF_F : __fsub_rn(__fmul_rn(to_f32(z[id]), A.scale), lse);
+      A.logp[row] = lp;
     }
-    const float vm = take<kVecs * 8, SCALED>(L, v, A.scale);
-    if (TOP)
-      offer<T, kVecs * 8, 8>(B, v, vm, count, z, static_cast<uint32_t>(head + i * 8), static_cast<uint32_t>(step * 8),
-                             lane, k, &cta_bound);
   }
-  if (rank == 0 && warp == 0) {
-    const int64_t edge = head + (vocab - tail0);  // < 16 columns
-    const int64_t col = lane < head ? lane : tail0 + (lane - head);
-    float v[1] = {lane < edge ? to_f32(z[col]) : -CUDART_INF_F};
-    const float vm = take<1, SCALED>(L, v, A.scale);
-    if (TOP)
-      offer<T, 1, 1>(B, v, vm, lane < edge ? 1 : 0, z, static_cast<uint32_t>(col), 0u, lane, k, &cta_bound);
+  if (TOP && lane < k) {
+    const uint32_t col = ~static_cast<uint32_t>(best);
+    A.top_ids[row * k + lane] = static_cast<int32_t>(col);
+    A.top_logp[row * k + lane] =
+        none ? -CUDART_INF_F : __fsub_rn(__fmul_rn(ord_value(static_cast<uint32_t>(best >> 32)), A.scale), lse);
   }
+}
 
-  // join: lanes, warps, CTAs
+// How a row lies in memory: a 16-byte aligned body of vectors of 8 columns,
+// and fewer than 16 columns before and after it, taken one by one.
+struct Layout {
+  int64_t head, nvec, tail0, edge;
+};
+template <class T>
+__device__ __forceinline__ Layout layout_of(const T* z, int64_t vocab) {
+  Layout Y;
+  const int64_t mis = (reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T);
+  Y.head = min(vocab, mis ? static_cast<int64_t>(16 / sizeof(T)) - mis : int64_t(0));
+  Y.nvec = (vocab - Y.head) / 8;
+  Y.tail0 = Y.head + Y.nvec * 8;
+  Y.edge = Y.head + (vocab - Y.tail0);
+  return Y;
+}
+
+// Values of kVecs vectors i, i + step, ... of this lane (-inf where there are
+// none); returns how many there are.
+template <class T>
+__device__ __forceinline__ int load_block(const T* z, const Layout& Y, int64_t i, int64_t step, float (&v)[kVecs * 8]) {
+  int count = 0;
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    float t[8];
+    if (i + u * step < Y.nvec) {
+      load8(z + Y.head + (i + u * step) * 8, t);
+      count += 8;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = -CUDART_INF_F;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[u * 8 + j] = t[j];
+  }
+  return count;
+}
+
+// Sums of a warp's share of a row: vectors first + lane, + step, ... and, for
+// the first share, the columns outside the body.  With TOP, block b's maximum
+// goes to maxima[b * stride], and `most` is the thread's maximum (order bits,
+// 0 where it has read nothing).
+template <class T, bool TOP, bool SCALED>
+__device__ __forceinline__ void read_row(const ScoreArgs& A, const T* z, const Layout& Y, int64_t first, int64_t step,
+                                         Stat& L, int lane, float* maxima, int stride, uint32_t& most, float& edge_v) {
+  int b = 0;
+  most = 0;
+  for (int64_t v0 = first; v0 < Y.nvec; v0 += step * kVecs, ++b) {
+    float v[kVecs * 8];
+    const int count = load_block(z, Y, v0 + lane, step, v);
+    const float vm = take<kVecs * 8, SCALED>(L, v, A.scale);
+    if (TOP) {
+      maxima[b * stride] = vm;
+      if (count > 0) most = max(most, ord_bits(vm));
+    }
+  }
+  edge_v = 0.0f;
+  if (first == 0 && Y.edge > 0) {
+    const int64_t col = lane < Y.head ? lane : Y.tail0 + (lane - Y.head);
+    edge_v = lane < Y.edge ? to_f32(z[col]) : -CUDART_INF_F;
+    float v[1] = {edge_v};
+    take<1, SCALED>(L, v, A.scale);
+    if (TOP && lane < Y.edge) most = max(most, ord_bits(edge_v));
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) L = stat_join(L, stat_shfl_xor(L, o));
+}
+
+constexpr uint32_t kOrdNegInf = 0x007FFFFFu;  // ord_bits(-inf)
+
+// Appends a key to list[0 .. cap); the count goes on past cap.
+__device__ __forceinline__ void push_key(float v, uint32_t col, Key* list, int cap, int* count) {
+  const int at = atomicAdd(count, 1);
+  if (at < cap) list[at] = make_key(v, col);
+}
+
+// The least possible value that `bound` (order bits) lets through.
+__device__ __forceinline__ float least_value(uint32_t bound) {
+  return ord_value(bound > kOrdNegInf ? bound : kOrdNegInf + 1);
+}
+
+// When fewer than k threads have seen a possible value, impossible ones are
+// among the best; their first k columns are enough of them.
+template <class T>
+__device__ __forceinline__ void collect_impossible(const T* z, int64_t vocab, int t, int k, Key* list, int cap, int* count) {
+  if (t >= k || t >= vocab) return;
+  const float v = to_f32(z[t]);
+  if (ord_bits(v) == kOrdNegInf) push_key(v, static_cast<uint32_t>(t), list, cap, count);
+}
+
+// Rank of thread t's key among list[0 .. n).
+__device__ __forceinline__ int rank_of(Key mine, const Key* list, int n) {
+  int r = 0;
+#pragma unroll 8
+  for (int j = 0; j < n; ++j) r += list[j] > mine ? 1 : 0;
+  return r;
+}
+
+// The list by insertion, for any row.
+template <class T>
+__device__ __forceinline__ Key insert_row(const T* z, const Layout& Y, int64_t first, int64_t step, int lane, int k,
+                                          Key* bound) {
+  Best B = {0, 0, -CUDART_INF_F};
+  for (int64_t v0 = first; v0 < Y.nvec; v0 += step * kVecs) {
+    float v[kVecs * 8];
+    const int count = load_block(z, Y, v0 + lane, step, v);
+    float vm = v[0];
+#pragma unroll
+    for (int j = 1; j < kVecs * 8; ++j) vm = fmaxf(vm, v[j]);
+    offer<T, kVecs * 8, 8>(B, v, vm, count, z, static_cast<uint32_t>(Y.head + (v0 + lane) * 8),
+                           static_cast<uint32_t>(step * 8), lane, k, bound);
+  }
+  if (first == 0 && Y.edge > 0) {
+    const int64_t col = lane < Y.head ? lane : Y.tail0 + (lane - Y.head);
+    float v[1] = {lane < Y.edge ? to_f32(z[col]) : -CUDART_INF_F};
+    offer<T, 1, 1>(B, v, v[0], lane < Y.edge ? 1 : 0, z, static_cast<uint32_t>(col), 0u, lane, k, bound);
+  }
+  return B.list;
+}
+
+// Short rows: a warp each.
+constexpr int kWarpList = 256;  // keys; a row whose bound is 0 has fewer columns
+constexpr int kWarpBlocks = static_cast<int>((kWarpRow + 32 * 8 * kVecs - 1) / (32 * 8 * kVecs));
+template <class T, bool TOP, bool SCALED>
+__global__ void __launch_bounds__(kScoreThreads) k_token_logprobs_warp(const ScoreArgs A) {
+  __shared__ Key lists[TOP ? kScoreWarps : 1][TOP ? kWarpList : 1];
+  __shared__ float maxima[TOP ? kScoreWarps : 1][TOP ? kWarpBlocks : 1][32];
+  __shared__ Key bounds[kScoreWarps];
+  __shared__ int counts[kScoreWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int k = TOP ? A.top_k : 1;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kScoreWarps + warp;
+  if (row >= A.rows) return;
+  const T* z = static_cast<const T*>(A.logits) + row * A.ldl;
+  const Layout Y = layout_of(z, A.vocab);
+  Stat L = {-CUDART_INF_F, 0.0f, 0.0f};
+  uint32_t most;
+  float edge_v;
+  float* mine = TOP ? &maxima[warp][0][lane] : nullptr;
+  read_row<T, TOP, SCALED>(A, z, Y, 0, 32, L, lane, mine, 32, most, edge_v);
+  Key best = 0;
+  if (TOP) {
+    Key* list = lists[warp];
+    if (lane == 0) counts[warp] = 0, bounds[warp] = 0;
+    // the k-th largest of the lanes' maxima
+    const uint32_t bound = __shfl_sync(0xffffffffu, sort_lanes(most, lane), k - 1);
+    const float least = least_value(bound);
+    __syncwarp();
+    int b = 0;
+    for (int64_t v0 = 0; v0 < Y.nvec; v0 += 32 * kVecs, ++b) {
+      if (!(mine[b * 32] >= least)) continue;
+      float v[kVecs * 8];
+      load_block(z, Y, v0 + lane, 32, v);
+      const uint32_t col = static_cast<uint32_t>(Y.head + (v0 + lane) * 8);
+#pragma unroll
+      for (int j = 0; j < kVecs * 8; ++j)
+        if (v[j] >= least) push_key(v[j], col + (j / 8) * 256 + j % 8, list, kWarpList, &counts[warp]);
+    }
+    if (lane < Y.edge && edge_v >= least)
+      push_key(edge_v, static_cast<uint32_t>(lane < Y.head ? lane : Y.tail0 + (lane - Y.head)), list, kWarpList, &counts[warp]);
+    if (bound <= kOrdNegInf) collect_impossible(z, A.vocab, lane, k, list, kWarpList, &counts[warp]);
+    __syncwarp();
+    const int n = counts[warp];
+    if (n <= kWarpList) {
+      // every lane ranks up to 8 keys before any is moved
+      Key key[kWarpList / 32];
+      int at[kWarpList / 32];
+#pragma unroll
+      for (int i = 0; i < kWarpList / 32; ++i) {
+        at[i] = 32;
+        if (i * 32 < n && i * 32 + lane < n) {
+          key[i] = list[i * 32 + lane];
+          at[i] = rank_of(key[i], list, n);
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kWarpList / 32; ++i)
+        if (at[i] < 32) list[at[i]] = key[i];
+      __syncwarp();
+      best = list[lane];
+    } else {
+      best = insert_row(z, Y, 0, 32, lane, k, &bounds[warp]);
+    }
+  }
+  write_row<T, TOP>(A, row, z, L, best, lane, k);
+}
+
+// Longer rows: a cluster of CTAs each.
+constexpr int kCtaBlocks = 16;  // maxima a thread keeps: 131072 columns a CTA
+constexpr int kHits = 512;
+template <class T, bool TOP, bool SCALED>
+__global__ void __launch_bounds__(kScoreThreads) k_token_logprobs(const ScoreArgs A, int keep_maxima) {
+  __shared__ Stat stats[kScoreWarps];
+  __shared__ Stat cta_stat;
+  __shared__ Key lists[TOP ? kScoreWarps : 1][32];  // kScoreThreads keys, or the warps' lists
+  __shared__ Key sorted[32];                        // the CTA's best
+  __shared__ uint16_t hits[TOP ? kHits : 1];        // (thread, block) whose maximum reaches the bound
+  __shared__ uint32_t tops[kScoreWarps];
+  __shared__ float maxima[TOP ? kCtaBlocks : 1][kScoreThreads];
+  __shared__ Key cta_bound;
+  __shared__ int count, nhits;
+  cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t rank = cluster.block_rank(), nct = cluster.num_blocks();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int k = TOP ? A.top_k : 1;
+  const int64_t row = blockIdx.x / nct;
+  const T* z = static_cast<const T*>(A.logits) + row * A.ldl;
+  const Layout Y = layout_of(z, A.vocab);
+  const int64_t first = int64_t(rank) * kScoreThreads + warp * 32, step = int64_t(nct) * kScoreThreads;
+  Stat L = {-CUDART_INF_F, 0.0f, 0.0f};
+  uint32_t most;
+  float edge_v;
+  // a row too long for the maxima overwrites one and is read again
+  const int stride = TOP && keep_maxima ? kScoreThreads : 0;
+  read_row<T, TOP, SCALED>(A, z, Y, first, step, L, lane, &maxima[0][tid], stride, most, edge_v);
+
+  // join: warps, CTAs
   if (lane == 0) stats[warp] = L;
-  if (TOP) lists[warp][lane] = B.list;
+  if (TOP) {
+    // the m-th largest maximum of each warp, m = ceil(k / warps): the least
+    // of these is reached by k threads
+    uint32_t left = most, mth = 0;
+    for (int i = 0; i < (k + kScoreWarps - 1) / kScoreWarps; ++i) {
+      mth = __reduce_max_sync(0xffffffffu, left);
+      const unsigned who = __ballot_sync(0xffffffffu, left == mth);
+      if (lane == __ffs(who) - 1) left = 0;
+    }
+    if (lane == 0) tops[warp] = mth;
+    if (tid == 0) count = 0, nhits = 0, cta_bound = 0;
+    if (tid < 32) sorted[tid] = 0;
+  }
   __syncthreads();
   if (warp == 0) {
     L = stats[lane & (kScoreWarps - 1)];  // every 8 lanes form the same sum
@@ -328,41 +536,68 @@ __global__ void __launch_bounds__(kScoreThreads) k_token_logprobs(const ScoreArg
     if (lane == 0) cta_stat = L;
   }
   if (TOP) {
-#pragma unroll 1
-    for (int o = kScoreWarps / 2; o > 0; o >>= 1) {
-      if (warp < o) lists[warp][lane] = list_merge(lists[warp][lane], lists[warp + o][lane], lane);
+    uint32_t bound = 0xFFFFFFFFu;
+#pragma unroll
+    for (int w = 0; w < kScoreWarps; ++w) bound = min(bound, tops[w]);
+    const float least = least_value(bound);
+    Key* list = &lists[0][0];
+    if (keep_maxima) {
+      const int blocks = static_cast<int>((Y.nvec - first + step * kVecs - 1) / (step * kVecs));
+      for (int b = 0; b < blocks; ++b)
+        if (maxima[b][tid] >= least) {
+          const int at = atomicAdd(&nhits, 1);
+          if (at < kHits) hits[at] = static_cast<uint16_t>(b * kScoreThreads + tid);
+        }
+      if (first == 0 && lane < Y.edge && edge_v >= least)
+        push_key(edge_v, static_cast<uint32_t>(lane < Y.head ? lane : Y.tail0 + (lane - Y.head)), list, kScoreThreads, &count);
+      if (rank == 0 && bound <= kOrdNegInf) collect_impossible(z, A.vocab, tid, k, list, kScoreThreads, &count);
       __syncthreads();
+      // a warp reads the 32 values of a hit, one a lane
+      const int nh = nhits <= kHits ? nhits : 0;
+#pragma unroll 4
+      for (int h = warp; h < nh; h += kScoreWarps) {
+        const int64_t i = int64_t(rank) * kScoreThreads + hits[h] % kScoreThreads +
+                          ((hits[h] / kScoreThreads) * kVecs + lane / 8) * step;
+        const int64_t col = Y.head + i * 8 + lane % 8;
+        const float v = i < Y.nvec ? to_f32(z[col]) : -CUDART_INF_F;
+        if (v >= least) push_key(v, static_cast<uint32_t>(col), list, kScoreThreads, &count);
+      }
+      if (tid == 0 && nhits > kHits) count = kScoreThreads + 1;
+    } else if (tid == 0) {
+      count = kScoreThreads + 1;
     }
-  }
-  if (nct > 1) cluster.sync();
-  if (rank == 0 && warp == 0) {
-    Key best = TOP ? lists[0][lane] : 0;
-    for (uint32_t r = 1; r < nct; ++r) {
-      L = stat_join(L, *cluster.map_shared_rank(&cta_stat, r));
-      if (TOP) best = list_merge(best, cluster.map_shared_rank(&lists[0][0], r)[lane], lane);
-    }
-    const bool none = L.m == -CUDART_INF_F && L.s == 0.0f;  // no possible token
-    // a sum that is NaN (a NaN logit) makes everything NaN, and so does an
-    // infinite maximum, whose sum is 0
-    const float logs = logf(L.s);
-    const float lse = none ? -CUDART_INF_F : (L.s != L.s ? L.s : L.m + logs);
-    if (lane == 0) {
-      if (A.lse) A.lse[row] = lse;
-      if (A.entropy) A.entropy[row] = none ? 0.0f : logs - L.q / L.s;
-      if (A.logp) {
-        const int64_t id = token_at(A.ids, A.ids_i64, row);
-        if (id >= vocab) atomicOr(A.status, kStBadToken);
-        float lp = 0.0f;
-        if (id >= 0 && id < vocab) lp = none ? -CUDART_INF_F : __fsub_rn(__fmul_rn(to_f32(z[id]), A.scale), lse);
-        A.logp[row] = lp;
+    __syncthreads();
+    const int n = count;
+    if (n <= kScoreThreads) {
+      if (tid < n) {
+        const Key mine = list[tid];
+        const int at = rank_of(mine, list, n);
+        if (at < 32) sorted[at] = mine;
+      }
+      __syncthreads();
+    } else {
+      const Key mine = insert_row(z, Y, first, step, lane, k, &cta_bound);
+      __syncthreads();
+      lists[warp][lane] = mine;
+      __syncthreads();
+      if (warp == 0) {
+        Key best = mine;
+        for (int w = 1; w < kScoreWarps; ++w) best = list_merge(best, lists[w][lane], lane);
+        sorted[lane] = best;
       }
     }
-    if (TOP && lane < k) {
-      const uint32_t col = ~static_cast<uint32_t>(best);
-      A.top_ids[row * k + lane] = static_cast<int32_t>(col);
-      A.top_logp[row * k + lane] =
-          none ? -CUDART_INF_F : __fsub_rn(__fmul_rn(ord_value(static_cast<uint32_t>(best >> 32)), A.scale), lse);
+  }
+  if (nct > 1)
+    cluster.sync();
+  else
+    __syncwarp();
+  if (rank == 0 && warp == 0) {
+    Key best = TOP ? sorted[lane] : 0;
+    for (uint32_t r = 1; r < nct; ++r) {
+      L = stat_join(L, *cluster.map_shared_rank(&cta_stat, r));
+      if (TOP) best = list_merge(best, cluster.map_shared_rank(sorted, r)[lane], lane);
     }
+    write_row<T, TOP>(A, row, z, L, best, lane, k);
   }
   // the other CTAs stay until rank 0 has read their shared memory
   if (nct > 1) cluster.sync();
@@ -449,10 +684,18 @@ __global__ void __launch_bounds__(kGradThreads) k_token_logprobs_grad(const Scor
 
 template <class T, bool TOP, bool SCALED>
 cudaError_t run_score(const ScoreArgs& A, int num_sms, cudaStream_t st) {
+  if (A.vocab <= kWarpRowFew || (A.vocab <= kWarpRow && A.rows >= 16 * num_sms)) {
+    k_token_logprobs_warp<T, TOP, SCALED>
+        <<<static_cast<unsigned>(lm_div_up(A.rows, kScoreWarps)), kScoreThreads, 0, st>>>(A);
+    return cudaGetLastError();
+  }
   // CTAs per row: enough to fill the SMs four times while each still has a
   // few vectors per thread
   int nct = 1;
   while (nct < 8 && A.rows * nct < 4 * num_sms && A.vocab / (nct * 2) >= kScoreThreads * 8) nct *= 2;
+  // and enough to keep the maxima of a long row
+  constexpr int64_t kept = int64_t(kCtaBlocks) * kScoreThreads * 8 * kVecs;
+  while (TOP && nct < 8 && A.vocab > kept * nct) nct *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(A.rows * nct));
   cfg.blockDim = dim3(kScoreThreads);
@@ -464,7 +707,7 @@ cudaError_t run_score(const ScoreArgs& A, int num_sms, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_token_logprobs<T, TOP, SCALED>, A);
+  return cudaLaunchKernelEx(&cfg, k_token_logprobs<T, TOP, SCALED>, A, static_cast<int>(A.vocab <= kept * nct));
 }
 
 template <class T>
