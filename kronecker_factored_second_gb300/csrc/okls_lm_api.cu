@@ -104,7 +104,7 @@ static okls_status check_grad_sizes(const char* op, int64_t tokens, int64_t voca
   if (vocab < 1 || dim < 1 || tokens < 0) return bad(op, "vocab and dim must be positive, tokens non-negative");
   if (vocab > kMaxSide || dim > kMaxSide || tokens > kMaxSide) return bad(op, "sizes must be below 2^31");
   // one CTA per row and slice of 2048 columns
-  if (lm_div_up(dim, 2048) > kMaxGrid / vocab || dim > 65535 * int64_t(512))
+  if (lm_div_up(dim, 2048) > kMaxGrid / vocab || dim > 65535 * int64_t(128))
     return host_fail(OKLS_ERR_UNSUPPORTED, "%s: vocab x dim is too large for one launch", op);
   if (tokens > 0 && lm_div_up(dim, 2048) > kMaxGrid / tokens)
     return host_fail(OKLS_ERR_UNSUPPORTED, "%s: tokens x dim is too large for one launch", op);

@@ -5,11 +5,12 @@
 // Both are bound by memory.  The gradient is a sum by key: the token
 // positions are sorted by id in one cluster (radix passes whose counters the
 // CTAs exchange through distributed shared memory), then the sorted list is
-// cut into chunks of kRun positions, one CTA per chunk and column slice.  A
+// cut into chunks of 16 to 64 positions, one CTA per chunk and column slice.  A
 // CTA writes the rows that begin and end inside its chunk; a row that spans
 // chunks leaves one partial sum per chunk, which a last launch joins in
 // order.  So a frequent token is spread over many CTAs, no sum depends on
-// the order in which CTAs run, and no row needs an atomic.
+// the order in which CTAs run, and no row needs an atomic.  The rest of the
+// launch that sums writes the rows without a token.
 #include <cooperative_groups.h>
 
 #include "okls_internal.h"
@@ -87,11 +88,15 @@ cudaError_t run_embedding(const EmbedArgs& A, cudaStream_t st) {
 // digits per warp, turns the counts into offsets (prefix over warps within
 // the CTA, over CTAs through distributed shared memory, then over digits),
 // and moves the pairs, 32 at a time in order, with __match_any_sync ranks.
+// It is bound by latency (a handful of dependent trips to L2 and to the other
+// CTAs a pass), so a span is loaded kHeld steps of 32 at once.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxBins = 1 << kMaxDigitBits;
 constexpr int kSortSmem = (kSortWarps * kMaxBins + 2 * kMaxBins + 32) * 4;
+constexpr int kMaxSortCtas = 8;
+constexpr int kHeld = 8;
 
 struct SortArgs {
   const void* ids;
@@ -100,7 +105,7 @@ struct SortArgs {
   uint32_t vocab;
   int32_t digit_bits, passes;
   uint32_t *key[2], *pos[2];
-  uint8_t* present;  // [vocab]: 1 where a row has a token
+  uint8_t* present;  // [vocab, rounded up to 16]: 1 where a row has a token
   uint32_t* status;
 };
 
@@ -116,12 +121,14 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs A) {
   const int bins = 1 << A.digit_bits;
   const uint32_t dmask = bins - 1;
 
-  for (int64_t v = rank * kSortThreads + tid; v < A.vocab; v += int64_t(nct) * kSortThreads) A.present[v] = 0;
+  for (int64_t v = rank * kSortThreads + tid; v < (int64_t(A.vocab) + 15) / 16; v += int64_t(nct) * kSortThreads)
+    reinterpret_cast<uint4*>(A.present)[v] = make_uint4(0, 0, 0, 0);
 
   const int64_t nwarps = int64_t(nct) * kSortWarps;
   const int64_t span = lm_div_up(lm_div_up(A.tokens, nwarps), 32) * 32;
   const int64_t lo = (int64_t(rank) * kSortWarps + warp) * span;
   const int64_t hi = min(A.tokens, lo + span);
+  uint32_t* mine = wcnt + warp * kMaxBins;
 
   for (int p = 0; p < A.passes; ++p) {
     const uint32_t* sk = A.key[(p + 1) & 1];
@@ -129,24 +136,38 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs A) {
     uint32_t* dk = A.key[p & 1];
     uint32_t* dp = A.pos[p & 1];
     const int shift = p * A.digit_bits;
-    uint32_t* mine = wcnt + warp * kMaxBins;
+    uint32_t key[kHeld], pos[kHeld];
+    // the pairs of steps i0, i0 + 32, ... (key 0xFFFFFFFF past the end)
+    auto load = [&](int64_t i0) {
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) {
+        const int64_t i = i0 + u * 32 + lane;
+        key[u] = 0xFFFFFFFFu;
+        pos[u] = static_cast<uint32_t>(i);
+        if (i < hi) {
+          if (p == 0) {
+            const int64_t id = token_at(A.ids, A.ids_i64, i);
+            if (id >= A.vocab) atomicOr(A.status, kStBadToken);
+            key[u] = id >= 0 && id < A.vocab ? static_cast<uint32_t>(id) : A.vocab;
+          } else {
+            key[u] = sk[i];
+            pos[u] = sp[i];
+          }
+        }
+      }
+    };
     for (int b = lane; b < bins; b += 32) mine[b] = 0;
     __syncwarp();
-    for (int64_t i = lo + lane; i < hi; i += 32) {
-      uint32_t k;
-      if (p == 0) {
-        const int64_t id = token_at(A.ids, A.ids_i64, i);
-        if (id >= A.vocab) atomicOr(A.status, kStBadToken);
-        k = id >= 0 && id < A.vocab ? static_cast<uint32_t>(id) : A.vocab;
-      } else {
-        k = sk[i];
-      }
-      atomicAdd(&mine[(k >> shift) & dmask], 1u);
+    for (int64_t i0 = lo; i0 < hi; i0 += kHeld * 32) {
+      load(i0);
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        if (key[u] != 0xFFFFFFFFu) atomicAdd(&mine[(key[u] >> shift) & dmask], 1u);
     }
     __syncthreads();
     for (int b = tid; b < bins; b += kSortThreads) {
       uint32_t run = 0;
-#pragma unroll 8
+#pragma unroll 16
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t c = wcnt[w * kMaxBins + b];
         wcnt[w * kMaxBins + b] = run;
@@ -157,12 +178,15 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs A) {
     cluster.sync();
     // bins <= 512 < threads: one bin a thread
     uint32_t total = 0, before = 0;
-    if (tid < bins)
-      for (uint32_t r = 0; r < nct; ++r) {
-        const uint32_t c = cluster.map_shared_rank(hist, r)[tid];
-        before += r < rank ? c : 0u;
-        total += c;
-      }
+    if (tid < bins) {
+#pragma unroll
+      for (uint32_t r = 0; r < kMaxSortCtas; ++r)
+        if (r < nct) {
+          const uint32_t c = cluster.map_shared_rank(hist, r)[tid];
+          before += r < rank ? c : 0u;
+          total += c;
+        }
+    }
     uint32_t inc = total;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -171,36 +195,30 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs A) {
     }
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    uint32_t basew = 0;
-    for (int w = 0; w < warp; ++w) basew += wsum[w];
+    const uint32_t ws = lane < warp ? wsum[lane] : 0u;
+    const uint32_t basew = __reduce_add_sync(0xffffffffu, ws);
     if (tid < bins) offs[tid] = basew + inc - total + before;
     __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const bool in = i < hi;
-      uint32_t k = 0, q = 0;
-      if (in) {
-        if (p == 0) {
-          const int64_t id = token_at(A.ids, A.ids_i64, i);
-          k = id >= 0 && id < A.vocab ? static_cast<uint32_t>(id) : A.vocab;
-          q = static_cast<uint32_t>(i);
-          if (k < A.vocab) A.present[k] = 1;
-        } else {
-          k = sk[i];
-          q = sp[i];
+    for (int64_t i0 = lo; i0 < hi; i0 += kHeld * 32) {
+      // a span of one load is still in the registers
+      if (span > kHeld * 32) load(i0);
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) {
+        if (i0 + u * 32 >= hi) break;
+        const bool in = key[u] != 0xFFFFFFFFu;
+        if (p == 0 && in && key[u] < A.vocab) A.present[key[u]] = 1;
+        const uint32_t d = in ? (key[u] >> shift) & dmask : 0xFFFFFFFFu;
+        const uint32_t peers = __match_any_sync(0xffffffffu, d);
+        const uint32_t below = __popc(peers & ((1u << lane) - 1u));
+        uint32_t at = 0;
+        if (in) at = offs[d] + mine[d] + below;
+        __syncwarp();
+        if (in && below == 0) mine[d] += __popc(peers);
+        __syncwarp();
+        if (in) {
+          dk[at] = key[u];
+          dp[at] = pos[u];
         }
-      }
-      const uint32_t d = in ? (k >> shift) & dmask : 0xFFFFFFFFu;
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
-      const uint32_t below = __popc(peers & ((1u << lane) - 1u));
-      uint32_t at = 0;
-      if (in) at = offs[d] + mine[d] + below;
-      __syncwarp();
-      if (in && below == 0) mine[d] += __popc(peers);
-      __syncwarp();
-      if (in) {
-        dk[at] = k;
-        dp[at] = q;
       }
     }
     // the pairs reach the cluster's other CTAs; hist may be rewritten
@@ -209,7 +227,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs A) {
 }
 
 // ------------------------------------------------------------- sum by key
-constexpr int kRun = 32;      // sorted positions of one chunk
+constexpr int kMaxRun = 64;   // sorted positions of one chunk: see run_of
 constexpr int kSlice = 2048;  // columns of one CTA: 256 threads x 8
 
 struct ReduceArgs {
@@ -225,7 +243,9 @@ struct ReduceArgs {
   int64_t ldo;
   float* part;  // [chunk][head, tail][dim]: sums of rows that span chunks
   int64_t chunks;
+  int32_t run;  // positions of one chunk
   int32_t slices;
+  int32_t sum_ctas;  // chunks * slices; the launch's other CTAs fill
 };
 
 template <class O, bool VEC>
@@ -250,24 +270,26 @@ __device__ __forceinline__ void write_row(const ReduceArgs& A, int64_t v, int64_
   }
 }
 
-template <class T, bool VEC>
-__device__ __forceinline__ void load_row8(const T* row, int64_t e0, int64_t dim, float (&v)[8]) {
+template <bool VEC, class T>
+__device__ __forceinline__ void load_pack(const T* row, int64_t e0, int64_t dim, Pack<T>& p) {
   if (VEC && e0 + 8 <= dim) {
-    load8(row + e0, v);
+    p.load(row + e0);
   } else {
+    float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = e0 + j < dim ? to_f32(row[e0 + j]) : 0.0f;
+    p.pack(v);
   }
 }
 
+// CTA b < sum_ctas: the sums of one chunk in one slice of columns.
 template <class T, class O, bool VEC>
-__global__ void __launch_bounds__(256) k_embed_reduce(const ReduceArgs A) {
-  __shared__ uint32_t sk[kRun], sp[kRun];
-  const int64_t b = blockIdx.x;
+__device__ __forceinline__ void sum_chunk(const ReduceArgs& A, int64_t b) {
+  __shared__ uint32_t sk[kMaxRun], sp[kMaxRun];
   const int64_t chunk = b / A.slices;
   const int64_t e0 = (b - chunk * A.slices) * kSlice + threadIdx.x * 8;
-  const int64_t i0 = chunk * kRun;
-  const int n = static_cast<int>(min(static_cast<int64_t>(kRun), A.tokens - i0));
+  const int64_t i0 = chunk * A.run;
+  const int n = static_cast<int>(min(static_cast<int64_t>(A.run), A.tokens - i0));
   if (threadIdx.x < n) {
     sk[threadIdx.x] = A.key[i0 + threadIdx.x];
     sp[threadIdx.x] = A.pos[i0 + threadIdx.x];
@@ -282,96 +304,177 @@ __global__ void __launch_bounds__(256) k_embed_reduce(const ReduceArgs A) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
   bool from_before = sk[0] == prev;
-  constexpr int U = 4;  // rows in flight
+  constexpr int U = sizeof(T) == 2 ? 8 : 4;  // rows in flight
   for (int i = 0; i < n; i += U) {
-    float v[U][8];
+    Pack<T> v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i + u < n && sk[i + u] < vocab) load_row8<T, VEC>(dy + int64_t(sp[i + u]) * A.lddy, e0, A.dim, v[u]);
+      if (i + u < n && sk[i + u] < vocab) load_pack<VEC>(dy + int64_t(sp[i + u]) * A.lddy, e0, A.dim, v[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i + u >= n) break;
       const uint32_t k = sk[i + u];
       if (k >= vocab) return;  // padding fills the rest of the list
+      float x[8];
+      v[u].unpack(x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += v[u][j];
+      for (int j = 0; j < 8; ++j) acc[j] += x[j];
       const bool last = i + u + 1 == n;
-      if (last ? k != next : k != sk[i + u + 1]) {
-        if (from_before) {
-          float* p = A.part + (chunk * 2) * A.dim;
+      const bool ends = last ? k != next : k != sk[i + u + 1];
+      if (ends && !from_before) {
+        write_row<O, VEC>(A, k, e0, acc);
+      } else if (ends || last) {
+        // a row of several chunks: the sum goes to this chunk's head slot when
+        // the row came from the chunk before, to its tail slot otherwise
+        float* p = A.part + (chunk * 2 + (from_before ? 0 : 1)) * A.dim + e0;
+        if (VEC && e0 + 8 <= A.dim && A.dim % 4 == 0) {
+          store8(p, acc);
+        } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (e0 + j < A.dim) p[e0 + j] = acc[j];
-        } else {
-          write_row<O, VEC>(A, k, e0, acc);
+            if (e0 + j < A.dim) p[j] = acc[j];
         }
+      }
+      if (ends) {
         from_before = false;
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-      } else if (last) {
-        // the row goes on in the next chunk: a head slot when it also came
-        // from the previous one, this chunk's tail slot otherwise
-        float* p = A.part + (chunk * 2 + (from_before ? 0 : 1)) * A.dim;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (e0 + j < A.dim) p[e0 + j] = acc[j];
       }
     }
   }
 }
 
-// Rows without a token: base, or zeros.
+// The other CTAs: rows without a token become base, or zeros.  A CTA takes 32
+// consecutive rows, so that which of them are absent is one look.
+constexpr int kFillRows = 32;
 template <class O, bool VEC>
-__global__ void __launch_bounds__(256) k_embed_fill(const ReduceArgs A) {
-  const int64_t b = blockIdx.x;
-  const int64_t v = b / A.slices;
-  const int64_t e0 = (b - v * A.slices) * kSlice + threadIdx.x * 8;
-  if (e0 >= A.dim || A.present[v]) return;
+__device__ __forceinline__ void fill_rows(const ReduceArgs& A, int64_t b) {
+  const int64_t v0 = b * kFillRows, v = v0 + (threadIdx.x & 31);
+  unsigned absent = __ballot_sync(0xffffffffu, v < A.vocab && !A.present[v]);
   const float zero[8] = {};
-  write_row<O, VEC>(A, v, e0, zero);
+  while (absent) {
+    const int64_t row = v0 + __ffs(absent) - 1;
+    absent &= absent - 1;
+    for (int64_t e0 = threadIdx.x * 8; e0 < A.dim; e0 += kSlice) write_row<O, VEC>(A, row, e0, zero);
+  }
+}
+
+template <class T, class O, bool VEC>
+__global__ void __launch_bounds__(256) k_embed_rows(const ReduceArgs A) {
+  if (blockIdx.x < A.sum_ctas)
+    sum_chunk<T, O, VEC>(A, blockIdx.x);
+  else
+    fill_rows<O, VEC>(A, blockIdx.x - A.sum_ctas);
 }
 
 // Rows that span chunks.  The owner is the chunk in which the row begins; it
-// adds its tail and the head slots of the chunks that follow: 4 groups of
-// threads take every fourth slot, then the groups' sums are added in order.
-constexpr int kJoinCols = 512;
-template <class O>
-__global__ void __launch_bounds__(512) k_embed_join(const ReduceArgs A) {
-  __shared__ float sum[4][kJoinCols];
-  const int64_t chunk = blockIdx.x;
-  const int64_t i0 = chunk * kRun, end = i0 + kRun;
-  if (end >= A.tokens) return;  // the last chunk has no successor
-  const uint32_t k = A.key[end - 1];
-  if (k >= A.vocab || A.key[end] != k) return;               // nothing spans the boundary
-  if (A.key[i0] == k && i0 > 0 && A.key[i0 - 1] == k) return;  // began in an earlier chunk
-  // end of the run: first position past `end` with another key
-  int64_t lo = end, hi = A.tokens;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (A.key[mid] == k)
-      lo = mid + 1;
-    else
-      hi = mid;
-  }
-  const int64_t last = (lo - 1) / kRun;  // last chunk of the row
-  const int grp = threadIdx.x >> 7, t = threadIdx.x & 127;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * kJoinCols + t * 4;
-  float acc[4] = {};
-  for (int64_t c = chunk + grp; c <= last; c += 4) {
-    const float* p = A.part + (c * 2 + (c == chunk ? 1 : 0)) * A.dim;
+// adds its tail and the head slots of the chunks that follow.  A warp takes
+// one chunk and 128 columns; the rows of more than kLongRow chunks are left to
+// the whole CTA, whose warps add an eighth of the slots each.
+constexpr int kJoinCols = 128;
+constexpr int kJoinWarps = 8;
+constexpr int kLongRow = 64;
+
+// Sum of the row's slots of chunks c0 .. c1 - 1 (c0 its first chunk or
+// later), 8 loads at a time.
+__device__ __forceinline__ void sum_slots(const ReduceArgs& A, int64_t owner, int64_t c0, int64_t c1, int64_t col,
+                                          float (&acc)[4]) {
+  constexpr int U = 8;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (c0 + j < A.dim) acc[j] += p[c0 + j];
-  }
+  for (int j = 0; j < 4; ++j) acc[j] = 0.0f;
+  if (A.dim % 4 == 0) {
+    if (col >= A.dim) return;
+    for (int64_t c = c0; c < c1; c += U) {
+      float4 v[U];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) sum[grp][t * 4 + j] = acc[j];
-  __syncthreads();
-  const int64_t col = static_cast<int64_t>(blockIdx.y) * kJoinCols + threadIdx.x;
-  if (col >= A.dim) return;
-  const float s = (sum[0][threadIdx.x] + sum[1][threadIdx.x]) + (sum[2][threadIdx.x] + sum[3][threadIdx.x]);
-  const float b0 = A.base ? to_f32(static_cast<const O*>(A.base)[k * A.ldbase + col]) : 0.0f;
-  static_cast<O*>(A.out)[k * A.ldo + col] = from_f32<O>(fmaf(s, A.scale, b0));
+      for (int u = 0; u < U; ++u)
+        v[u] = c + u < c1 ? *reinterpret_cast<const float4*>(A.part + ((c + u) * 2 + (c + u == owner ? 1 : 0)) * A.dim + col)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int u = 0; u < U; ++u) acc[0] += v[u].x, acc[1] += v[u].y, acc[2] += v[u].z, acc[3] += v[u].w;
+    }
+  } else {
+    for (int64_t c = c0; c < c1; c += U) {
+      float v[U][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[u][j] = c + u < c1 && col + j < A.dim ? A.part[((c + u) * 2 + (c + u == owner ? 1 : 0)) * A.dim + col + j] : 0.0f;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += v[u][j];
+    }
+  }
 }
+
+template <class O>
+__device__ __forceinline__ void write_sum(const ReduceArgs& A, uint32_t k, int64_t col, const float (&acc)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (col + j >= A.dim) continue;
+    const float b0 = A.base ? to_f32(static_cast<const O*>(A.base)[k * A.ldbase + col + j]) : 0.0f;
+    static_cast<O*>(A.out)[k * A.ldo + col + j] = from_f32<O>(fmaf(acc[j], A.scale, b0));
+  }
+}
+
+template <class O>
+__global__ void __launch_bounds__(kJoinWarps * 32) k_embed_join(const ReduceArgs A) {
+  __shared__ int64_t long_last[kJoinWarps];
+  __shared__ float part[kJoinWarps][kJoinCols];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t chunk = static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp;
+  const int64_t i0 = chunk * A.run, end = i0 + A.run;
+  const int64_t col = static_cast<int64_t>(blockIdx.y) * kJoinCols + lane * 4;
+  if (lane == 0) long_last[warp] = 0;
+  if (end < A.tokens) {  // the last chunk has no successor
+    const uint32_t k = A.key[end - 1], after = A.key[end], at0 = A.key[i0], before = i0 > 0 ? A.key[i0 - 1] : 0xFFFFFFFFu;
+    // something spans the boundary, and it did not begin in an earlier chunk
+    if (k < A.vocab && after == k && !(at0 == k && before == k)) {
+      // the row's last chunk: the last one that begins with its key (the keys
+      // are sorted), looked for 32 chunks at a time
+      int64_t last = chunk + 1;
+      for (;;) {
+        const int64_t c = last + 1 + lane;
+        const unsigned same = __ballot_sync(0xffffffffu, c * A.run < A.tokens && A.key[c * A.run] == k);
+        last += __popc(same);
+        if (same != 0xffffffffu) break;
+      }
+      if (last - chunk < kLongRow) {
+        float acc[4];
+        sum_slots(A, chunk, chunk, last + 1, col, acc);
+        write_sum<O>(A, k, col, acc);
+      } else if (lane == 0) {
+        long_last[warp] = last;
+      }
+    }
+  }
+  __syncthreads();
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const int64_t last = long_last[w];
+    if (last == 0) continue;
+    const int64_t owner = static_cast<int64_t>(blockIdx.x) * kJoinWarps + w;
+    const int64_t share = lm_div_up(last + 1 - owner, kJoinWarps);
+    const int64_t c0 = owner + warp * share, c1 = min(last + 1, c0 + share);
+    float acc[4];
+    sum_slots(A, owner, c0, c1, col, acc);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[warp][lane * 4 + j] = acc[j];
+    __syncthreads();
+    if (warp == 0) {
+      for (int u = 1; u < kJoinWarps; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += part[u][lane * 4 + j];
+      write_sum<O>(A, A.key[(owner + 1) * A.run - 1], col, acc);
+    }
+    __syncthreads();
+  }
+}
+
+// Positions of a chunk: short chunks for short lists, to have CTAs for every
+// SM; long ones leave fewer partial sums to write and join.
+int run_of(int64_t tokens) { return tokens <= 8192 ? 16 : tokens <= 24576 ? 32 : kMaxRun; }
 
 struct GradPlan {
   size_t key[2], pos[2], present, part, total;
@@ -386,30 +489,28 @@ GradPlan plan_grad(int64_t tokens, int64_t vocab, int64_t dim) {
     at += (bytes + 255) / 256 * 256;
     return p;
   };
-  g.chunks = lm_div_up(tokens, kRun);
+  g.chunks = lm_div_up(tokens, run_of(tokens));
   for (int i = 0; i < 2; ++i) {
     g.key[i] = take(static_cast<size_t>(tokens) * 4);
     g.pos[i] = take(static_cast<size_t>(tokens) * 4);
   }
-  g.present = take(static_cast<size_t>(vocab));
+  g.present = take(static_cast<size_t>(vocab) + 16);
   g.part = take(static_cast<size_t>(g.chunks) * 2 * dim * 4);
   g.total = at;
   return g;
 }
 
 template <class T, class O>
-cudaError_t run_reduce(const ReduceArgs& R, bool in_place, bool vec, cudaStream_t st) {
-  if (!in_place && R.vocab > 0) {
-    const unsigned grid = static_cast<unsigned>(R.vocab * R.slices);
-    vec ? k_embed_fill<O, true><<<grid, 256, 0, st>>>(R) : k_embed_fill<O, false><<<grid, 256, 0, st>>>(R);
-  }
-  if (R.tokens > 0) {
-    const unsigned grid = static_cast<unsigned>(R.chunks * R.slices);
-    vec ? k_embed_reduce<T, O, true><<<grid, 256, 0, st>>>(R) : k_embed_reduce<T, O, false><<<grid, 256, 0, st>>>(R);
-    if (R.chunks > 1)
-      k_embed_join<O><<<dim3(static_cast<unsigned>(R.chunks), static_cast<unsigned>(lm_div_up(R.dim, kJoinCols))),
-                        512, 0, st>>>(R);
-  }
+cudaError_t run_reduce(ReduceArgs R, bool in_place, bool vec, cudaStream_t st) {
+  R.sum_ctas = static_cast<int32_t>(R.chunks * R.slices);
+  const int64_t fill = in_place ? 0 : lm_div_up(R.vocab, kFillRows);
+  const unsigned grid = static_cast<unsigned>(R.sum_ctas + fill);
+  if (grid > 0)
+    vec ? k_embed_rows<T, O, true><<<grid, 256, 0, st>>>(R) : k_embed_rows<T, O, false><<<grid, 256, 0, st>>>(R);
+  if (R.chunks > 1)
+    k_embed_join<O><<<dim3(static_cast<unsigned>(lm_div_up(R.chunks, kJoinWarps)),
+                           static_cast<unsigned>(lm_div_up(R.dim, kJoinCols))),
+                      kJoinWarps * 32, 0, st>>>(R);
   return cudaGetLastError();
 }
 
@@ -438,7 +539,7 @@ cudaError_t launch_embedding_grad(const EmbedGradArgs& A, int dy_dtype, int out_
   R.base = A.base, R.ldbase = A.ldbase, R.out = A.out, R.ldo = A.ldo;
   R.present = reinterpret_cast<const uint8_t*>(ws + g.present);
   R.part = reinterpret_cast<float*>(ws + g.part);
-  R.chunks = g.chunks;
+  R.chunks = g.chunks, R.run = run_of(A.tokens);
   R.slices = static_cast<int32_t>(lm_div_up(A.dim, kSlice));
   if (A.tokens > 0) {
     SortArgs S = {};
@@ -462,7 +563,9 @@ cudaError_t launch_embedding_grad(const EmbedGradArgs& A, int dy_dtype, int out_
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    const int nct = A.tokens <= 4096 ? 1 : A.tokens <= 8192 ? 2 : A.tokens <= 16384 ? 4 : 8;
+    // two steps of 32 a warp, up to 8 CTAs
+    int nct = 1;
+    while (nct < kMaxSortCtas && A.tokens > int64_t(nct) * kSortThreads * 2) nct *= 2;
     cfg.gridDim = dim3(nct);
     cfg.blockDim = dim3(kSortThreads);
     cfg.dynamicSmemBytes = kSortSmem;

@@ -25,34 +25,6 @@ namespace {
 
 constexpr int kChunk = 256;  // columns of one warp chunk: 32 lanes x 8
 
-// 8 elements of one lane in their own type.
-template <class T>
-struct Pack;
-template <>
-struct Pack<float> {
-  float v[8];
-  __device__ __forceinline__ void unpack(float (&o)[8]) const {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = v[j];
-  }
-  __device__ __forceinline__ void pack(const float (&o)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = o[j];
-  }
-  __device__ __forceinline__ void load(const float* p) { load8(p, v); }
-  __device__ __forceinline__ void store(float* p) const { store8(p, v); }
-};
-template <>
-struct Pack<__nv_bfloat16> {
-  uint4 u;
-  __device__ __forceinline__ void unpack(float (&o)[8]) const { unpack8(u, o); }
-  __device__ __forceinline__ void pack(const float (&o)[8]) {
-    u = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
-  }
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
-};
-
 // Column of element j of warp chunk c for this lane: 8 consecutive columns a
 // lane for 16-byte accesses, or 32 consecutive columns an access otherwise.
 template <bool VEC>
@@ -364,12 +336,19 @@ __global__ void __launch_bounds__(512) k_rms_norm_grad_ring(const NormGradArgs A
   if (A.part) {
     float* p = A.part + static_cast<int64_t>(blockIdx.x) * A.dim;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      Pack<float> o;
+      o.pack(dw[i]);
+      if (A.dim % 4 == 0) {
+        store_chunk<true>(p, warp + i * nw, lane, A.dim, o);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int col = col_of<true>(warp + i * nw, lane, j);
-        if (col < A.dim) p[col] = dw[i][j];
+        for (int j = 0; j < 8; ++j) {
+          const int col = col_of<true>(warp + i * nw, lane, j);
+          if (col < A.dim) p[col] = dw[i][j];
+        }
       }
+    }
   }
 }
 
