@@ -13,9 +13,7 @@
 //                    buffers, overwriting it;
 //   warp 2           copies each step's scales into a ring of their own, with
 //                    4-byte asynchronous copies that take any layout;
-//   warps 4-11       scale and add: a thread owns one output row and BN / 2
-//                    columns, so a row's scale is one register and a square
-//                    block's scale one multiplication per 128-deep step.
+//   warps 4-11       scale and add (add_square, add_rows), then store.
 // The two TMEM buffers let the additions of one step overlap the MMAs of the
 // next.  The running sums of a 128 x 256 tile take half of the SM's
 // registers, so the first four warps hand theirs to the other eight.
@@ -115,6 +113,50 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
                : "memory");
 }
 
+// 16 TMEM lanes x 32 fp32 columns in the 16x256b shape: of each 8 columns i,
+// v[4 i + {0, 1}] are lane / 4's columns 2 (lane % 4) + {0, 1}, and
+// v[4 i + {2, 3}] those of the TMEM lane 8 further.
+__device__ __forceinline__ void tmem_ld16x256_start(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16x256_wait(uint32_t (&v)[16], uint32_t (&w)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]), "+r"(w[4]), "+r"(w[5]), "+r"(w[6]), "+r"(w[7]),
+                 "+r"(w[8]), "+r"(w[9]), "+r"(w[10]), "+r"(w[11]), "+r"(w[12]), "+r"(w[13]), "+r"(w[14]), "+r"(w[15])
+               :
+               : "memory");
+}
+
+// Two fp32 values in a 64-bit register, with one instruction for both.
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ void fma_pair(uint64_t& acc, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pick4(const uint32_t (&w)[4], int i) {
+  const uint32_t a = i & 1 ? w[1] : w[0], b = i & 1 ? w[3] : w[2];
+  return i & 2 ? b : a;
+}
+
 struct TileAt {
   int tm, tn;
 };
@@ -127,6 +169,273 @@ __device__ __forceinline__ TileAt tile_at(int t, int tiles_m, int tiles_n) {
   const int g = t / per, in = t - g * per;
   const int h = min(kGroup, tiles_m - g * kGroup);
   return {g * kGroup + in % h, in / h};
+}
+
+// What the adding warps share with the others.
+template <int BN>
+struct Adder {
+  uint32_t tmem;
+  const float* scales;  // ring of slots: the tile's rows' scales, then its columns' (or square blocks')
+  int slot_floats, slots;
+  uint64_t *acc_full, *acc_empty, *sempty;
+};
+
+// Per-step bookkeeping of an adding warp: waits for a TMEM buffer and hands it
+// and the scales back.
+template <int BN>
+struct Steps {
+  uint32_t it = 0, slot = 0;
+  bool ok = true, ready;
+  // the first look at a step's barrier is taken before the last additions of
+  // the step before, so that its latency passes under them
+  __device__ __forceinline__ explicit Steps(const Adder<BN>& R) { ready = mbar_try_wait(&R.acc_full[0], 0); }
+  __device__ __forceinline__ uint32_t buf() const { return it & 1u; }
+  __device__ __forceinline__ const float* begin(const Adder<BN>& R, uint32_t* status) {
+    if (!ready) ok = ok && mbar_wait(&R.acc_full[buf()], (it >> 1) & 1u, status);
+    __syncwarp();
+    tc_fence_after();
+    return R.scales + slot * R.slot_floats;
+  }
+  __device__ __forceinline__ void loaded(const Adder<BN>& R, int lane) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&R.acc_empty[buf()]);
+    ready = mbar_try_wait(&R.acc_full[buf() ^ 1u], ((it + 1) >> 1) & 1u);
+  }
+  __device__ __forceinline__ void end(const Adder<BN>& R, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&R.sempty[slot]);
+    if (static_cast<int>(++slot) == R.slots) slot = 0;
+    ++it;
+  }
+};
+
+// 16 bf16 or 8 fp32 results of one row, 32 bytes a store: whole memory
+// sectors, although neighbouring lanes write different rows.
+__device__ __forceinline__ void store_bf16x16(const Fp8GemmArgs& A, __nv_bfloat16* p, int left, bool vec, float (&v)[16]) {
+  if (vec && left >= 16) {
+    if (A.accumulate) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float old[8];
+        load8(p + 8 * h, old);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * h + j] += old[j];
+      }
+    }
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+    store32(p, w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < left) p[j] = __float2bfloat16_rn(A.accumulate ? v[j] + __bfloat162float(p[j]) : v[j]);
+  }
+}
+__device__ __forceinline__ void store_f32x8(const Fp8GemmArgs& A, float* p, int left, bool vec, float (&v)[8]) {
+  if (vec && left >= 8) {
+    if (A.accumulate) {
+      float old[8];
+      load8(p, old);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += old[j];
+    }
+    store8(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) p[j] = A.accumulate ? v[j] + p[j] : v[j];
+  }
+}
+
+// B in square blocks: a thread owns one output row and BN / 2 columns, which
+// one block's scale covers, so a step's scales are one number a thread and an
+// addition is one fused multiply-add.
+template <int BN>
+__device__ __forceinline__ void add_square(const Fp8GemmArgs& A, const Adder<BN>& R, int tiles_m, int tiles_n, int nkb) {
+  constexpr int kCols = BN / 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = warp & 3;  // TMEM lane quarter of this warp
+  const int half = (warp - 4) >> 2;
+  const uint32_t tbase = R.tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kCols;
+  const int tiles = tiles_m * tiles_n;
+  Steps<BN> S(R);
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const TileAt at = tile_at(t, tiles_m, tiles_n);
+    const int row = at.tm * kTM + q * 32 + lane;
+    const int col0 = at.tn * BN + half * kCols;
+    float acc[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
+    for (int kb = 0; kb < nkb; ++kb) {
+      const float* sc = S.begin(R, A.status);
+      const uint32_t d = tbase + S.buf() * BN;
+      // 32 columns are loaded while the 32 before them are added
+      uint32_t v[2][32];
+      tmem_ld32_start(d, v[0]);
+      const float s = sc[q * 32 + lane] * sc[kTM + (half * kCols) / kFp8Group];
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) {
+        uint32_t(&x)[32] = v[(c / 32) & 1];
+        tmem_ld_wait(x);
+        if (c + 32 < kCols)
+          tmem_ld32_start(d + c + 32, v[(c / 32 + 1) & 1]);
+        else
+          S.loaded(R, lane);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(x[j]), s, acc[c + j]);
+      }
+      S.end(R, lane);
+    }
+    if (row >= A.m) continue;
+    const int eb = A.out_dtype == kDtBf16 ? 2 : 4;
+    char* o = static_cast<char*>(A.out) + (static_cast<int64_t>(row) * A.ldo + col0) * eb;
+    const bool vec = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
+    if (A.out_dtype == kDtBf16) {
+#pragma unroll
+      for (int c = 0; c < kCols; c += 16) {
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = acc[c + j];
+        store_bf16x16(A, reinterpret_cast<__nv_bfloat16*>(o) + c, A.n - col0 - c, vec, v);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kCols; c += 8) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = acc[c + j];
+        store_f32x8(A, reinterpret_cast<float*>(o) + c, A.n - col0 - c, vec, v);
+      }
+    }
+  }
+}
+
+// B in row groups: every column has a scale of its own.  With a row a thread,
+// each thread would read all of them from shared memory every step (128
+// floats, four clocks of the read path per 16 bytes and warp: twice the MMAs'
+// time).  In the 16x256b shape a thread owns 4 rows and a quarter of the
+// columns, so it reads 32; a product and a fused multiply-add per value are
+// left.  Column c of a 32-column chunk: pair i of lane quad position p holds
+// columns 8 i + 2 p and + 1; rows: half h (16 TMEM lanes), r: lane / 4 + 8 r.
+template <int BN>
+__device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN>& R, int tiles_m, int tiles_n, int nkb) {
+  constexpr int kCols = BN / 2;
+  constexpr int kChunks = kCols / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = warp & 3, p = lane & 3;
+  const int half = (warp - 4) >> 2;
+  const uint32_t tbase = R.tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kCols;
+  const int tiles = tiles_m * tiles_n;
+  Steps<BN> S(R);
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const TileAt at = tile_at(t, tiles_m, tiles_n);
+    const int row0 = at.tm * kTM + q * 32 + (lane >> 2);
+    const int col0 = at.tn * BN + half * kCols;
+    uint64_t acc[kChunks][4][2][2];  // [chunk][i][h][r], two columns each
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[c][i][0][0] = acc[c][i][0][1] = acc[c][i][1][0] = acc[c][i][1][1] = 0;
+    for (int kb = 0; kb < nkb; ++kb) {
+      const float* sc = S.begin(R, A.status);
+      const uint32_t d = tbase + S.buf() * BN;
+      uint32_t v[2][2][16];  // [in turn][half][4 i + 2 r + column]
+      tmem_ld16x256_start(d, v[0][0]);
+      tmem_ld16x256_start(d + (16u << 16), v[0][1]);
+      uint64_t sa[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float x = sc[q * 32 + h * 16 + r * 8 + (lane >> 2)];
+          sa[h][r] = pair_of(__float_as_uint(x), __float_as_uint(x));
+        }
+      const uint64_t* sb = reinterpret_cast<const uint64_t*>(sc + kTM + half * kCols) + p;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        uint32_t(&x)[2][16] = v[c & 1];
+        tmem_ld16x256_wait(x[0], x[1]);
+        if (c + 1 < kChunks) {
+          tmem_ld16x256_start(d + (c + 1) * 32, v[(c + 1) & 1][0]);
+          tmem_ld16x256_start(d + (16u << 16) + (c + 1) * 32, v[(c + 1) & 1][1]);
+        } else {
+          S.loaded(R, lane);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t w = sb[c * 16 + i * 4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              fma_pair(acc[c][i][h][r], mul_pair(pair_of(x[h][4 * i + 2 * r], x[h][4 * i + 2 * r + 1]), w), sa[h][r]);
+        }
+      }
+      S.end(R, lane);
+    }
+    const int eb = A.out_dtype == kDtBf16 ? 2 : 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = row0 + h * 16 + r * 8;
+        char* o = static_cast<char*>(A.out) + (static_cast<int64_t>(row) * A.ldo + col0) * eb;
+        // one answer for the warp: lanes hold different rows, and the quads trade values
+        const bool in = row < A.m, vec = __all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(o) & 15) == 0);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const int left = A.n - col0 - c * 32;  // columns of this chunk that exist
+          float v[4][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) unpair(acc[c][i][h][r], v[i][0], v[i][1]);
+          if (A.out_dtype == kDtBf16) {
+            __nv_bfloat16* b = reinterpret_cast<__nv_bfloat16*>(o) + c * 32;
+            if (vec && left >= 32 && !A.accumulate) {
+              // the quad's 4 x 4 pairs are transposed, so that each lane has 8
+              // consecutive columns and the quad 64 bytes
+              uint32_t w[4], u[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[i][0], v[i][1]);
+              u[0] = pick4(w, p);
+#pragma unroll
+              for (int e = 1; e < 4; ++e) u[e] = __shfl_xor_sync(0xffffffffu, pick4(w, p ^ e), e);
+              // u[e] came from quad position p ^ e
+              const uint4 z = make_uint4(pick4(u, p), pick4(u, p ^ 1), pick4(u, p ^ 2), pick4(u, p ^ 3));
+              if (in) *reinterpret_cast<uint4*>(b + 8 * p) = z;
+            } else if (in) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const int col = 8 * i + 2 * p + j;
+                  if (col < left)
+                    b[col] = __float2bfloat16_rn(A.accumulate ? v[i][j] + __bfloat162float(b[col]) : v[i][j]);
+                }
+            }
+          } else if (in) {
+            float* f = reinterpret_cast<float*>(o) + c * 32;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int col = 8 * i + 2 * p;
+              if (vec && col + 2 <= left) {
+                float2 z = make_float2(v[i][0], v[i][1]);
+                if (A.accumulate) {
+                  const float2 old = *reinterpret_cast<const float2*>(f + col);
+                  z.x += old.x, z.y += old.y;
+                }
+                *reinterpret_cast<float2*>(f + col) = z;
+              } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  if (col + j < left) f[col + j] = A.accumulate ? v[i][j] + f[col + j] : v[i][j];
+              }
+            }
+          }
+        }
+      }
+  }
 }
 
 template <int BN>
@@ -282,124 +591,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
-    constexpr int kCols = BN / 2;             // columns of a thread
-    const int q = warp & 3;                   // TMEM lane quarter of this warp
-    const int half = (warp - 4) >> 2;
-    const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kCols;
-    uint32_t it = 0, slot = 0;
-    bool ok = true;
-    // the first look at a step's barrier is taken before the last additions
-    // of the step before, so that its latency passes under them
-    bool ready = mbar_try_wait(&acc_full[0], 0);
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const TileAt at = tile_at(t, tiles_m, tiles_n);
-      const int row = at.tm * kTM + q * 32 + lane;
-      const int col0 = at.tn * BN + half * kCols;
-      float acc[kCols];
-#pragma unroll
-      for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t buf = it & 1u;
-        const float* sc = reinterpret_cast<const float*>(scales + slot * C::kScaleBytes);
-        if (!ready) ok = ok && mbar_wait(&acc_full[buf], (it >> 1) & 1u, A.status);
-        __syncwarp();
-        tc_fence_after();
-        // 32 columns are loaded while the 32 before them are added
-        uint32_t v[2][32];
-        tmem_ld32_start(tbase + buf * BN, v[0]);
-        float s = sc[q * 32 + lane];
-        // kCols divides 128, so one square block covers the thread's columns
-        if (A.b_square) s *= sc[kTM + (half * kCols) / kFp8Group];
-        const float4* sbc = reinterpret_cast<const float4*>(sc + kTM + half * kCols);
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-          uint32_t(&x)[32] = v[(c / 32) & 1];
-          tmem_ld_wait(x);
-          if (c + 32 < kCols) {
-            tmem_ld32_start(tbase + buf * BN + c + 32, v[(c / 32 + 1) & 1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
-            ready = mbar_try_wait(&acc_full[buf ^ 1u], ((it + 1) >> 1) & 1u);
-          }
-          if (A.b_square) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(x[j]), s, acc[c + j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 w = sbc[c / 4 + j];
-              acc[c + 4 * j] = fmaf(__uint_as_float(x[4 * j]) * w.x, s, acc[c + 4 * j]);
-              acc[c + 4 * j + 1] = fmaf(__uint_as_float(x[4 * j + 1]) * w.y, s, acc[c + 4 * j + 1]);
-              acc[c + 4 * j + 2] = fmaf(__uint_as_float(x[4 * j + 2]) * w.z, s, acc[c + 4 * j + 2]);
-              acc[c + 4 * j + 3] = fmaf(__uint_as_float(x[4 * j + 3]) * w.w, s, acc[c + 4 * j + 3]);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sempty[slot]);
-        if (++slot == C::kSlots) slot = 0;
-      }
-      if (row >= A.m) continue;
-      const int eb = A.out_dtype == kDtBf16 ? 2 : 4;
-      char* o = static_cast<char*>(A.out) + (static_cast<int64_t>(row) * A.ldo + col0) * eb;
-      // 32 bytes a store: whole memory sectors, although neighbouring lanes
-      // write different rows
-      const bool vec = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
-      if (A.out_dtype == kDtBf16) {
-        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(o);
-#pragma unroll
-        for (int c = 0; c < kCols; c += 16) {
-          float v[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = acc[c + j];
-          if (vec && col0 + c + 16 <= A.n) {
-            if (A.accumulate) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float old[8];
-                load8(p + c + 8 * h, old);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[8 * h + j] += old[j];
-              }
-            }
-            uint32_t w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-            store32(p + c, w);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (col0 + c + j < A.n) p[c + j] = __float2bfloat16_rn(A.accumulate ? v[j] + __bfloat162float(p[c + j]) : v[j]);
-          }
-        }
-      } else {
-        float* p = reinterpret_cast<float*>(o);
-#pragma unroll
-        for (int c = 0; c < kCols; c += 8) {
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = acc[c + j];
-          if (vec && col0 + c + 8 <= A.n) {
-            if (A.accumulate) {
-              float old[8];
-              load8(p + c, old);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] += old[j];
-            }
-            uint32_t w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[j]);
-            store32(p + c, w);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (col0 + c + j < A.n) p[c + j] = A.accumulate ? v[j] + p[c + j] : v[j];
-          }
-        }
-      }
-    }
+    const Adder<BN> R = {tmem, reinterpret_cast<const float*>(scales), C::kScaleBytes / 4, C::kSlots,
+                         acc_full, acc_empty, sempty};
+    if (A.b_square)
+      add_square<BN>(A, R, tiles_m, tiles_n, nkb);
+    else
+      add_rows<BN>(A, R, tiles_m, tiles_n, nkb);
   }
 
   tc_fence_before();
