@@ -37,12 +37,22 @@ constexpr int kCtlRegs = 40, kAddRegs = 232;
 static_assert(128 * kCtlRegs + 256 * kAddRegs <= kThreads * 168, "more registers than the launch holds");
 constexpr int kABytes = kTM * kTK;
 
+// TMEM buffers of a BN-column step: a power of two, as many as the 512 columns
+// hold, at most 4.
+template <int BN>
+struct Buffers {
+  static constexpr int kLog = BN > 128 ? 1 : 2;
+  static constexpr int kCount = 1 << kLog;
+  __host__ __device__ static constexpr uint32_t at(uint32_t it) { return it & (kCount - 1); }
+  __host__ __device__ static constexpr uint32_t parity(uint32_t it) { return (it >> kLog) & 1u; }
+};
+
 template <int BN>
 struct Tile {
   static constexpr int kBBytes = BN * kTK;
   static constexpr int kBytes = kABytes + kBBytes;
   static constexpr int kRing = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-  static constexpr int kCols = 2 * BN;  // TMEM columns
+  static constexpr int kCols = BN == 64 ? 256 : 512;  // TMEM columns: the buffers', up to a power of two
   static constexpr int kSlots = 8;                             // scale ring
   static constexpr int kScaleBytes = (kTM + BN) * 4;           // of one step
   static constexpr int kSmem = kRing * kBytes + kSlots * kScaleBytes + 1024 + 256;
@@ -171,38 +181,68 @@ __device__ __forceinline__ TileAt tile_at(int t, int tiles_m, int tiles_n) {
   return {g * kGroup + in % h, in / h};
 }
 
-// What the adding warps share with the others.
-template <int BN>
+// An arrival on a barrier of either CTA of a pair.  What it hands over is TMEM
+// (ordered by the tcgen05 fences around it), not memory, so it needs no
+// release at cluster scope, which would wait for the thread's outstanding
+// memory accesses every step.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// What the adding warps share with the others, and the CTA's walk over the
+// tiles.  PAIR: the two CTAs of a cluster hold the halves of 256-row tiles.
+template <int BN, bool PAIR>
 struct Adder {
+  int first, stride;        // tiles first, first + stride, ...
+  int row_step, row0;       // rows of a tile, and this CTA's first of them
   uint32_t tmem;
   const float* scales;  // ring of slots: the tile's rows' scales, then its columns' (or square blocks')
   int slot_floats, slots;
   uint64_t *acc_full, *acc_empty, *sempty;
+  uint32_t acc_empty_lead;  // PAIR: acc_empty of the cluster's first CTA
 };
 
 // Per-step bookkeeping of an adding warp: waits for a TMEM buffer and hands it
 // and the scales back.
-template <int BN>
+template <int BN, bool PAIR>
 struct Steps {
   uint32_t it = 0, slot = 0;
   bool ok = true, ready;
-  // the first look at a step's barrier is taken before the last additions of
-  // the step before, so that its latency passes under them
-  __device__ __forceinline__ explicit Steps(const Adder<BN>& R) { ready = mbar_try_wait(&R.acc_full[0], 0); }
-  __device__ __forceinline__ uint32_t buf() const { return it & 1u; }
-  __device__ __forceinline__ const float* begin(const Adder<BN>& R, uint32_t* status) {
-    if (!ready) ok = ok && mbar_wait(&R.acc_full[buf()], (it >> 1) & 1u, status);
+  // The first look at a step's barrier is taken before the last additions of
+  // the step before, so that its latency passes under them (a test, not a
+  // try: a try holds the warp until the barrier turns or a time limit passes).
+  __device__ __forceinline__ explicit Steps(const Adder<BN, PAIR>& R) { ready = mbar_test(&R.acc_full[0], 0); }
+  __device__ __forceinline__ uint32_t buf() const { return Buffers<BN>::at(it); }
+  __device__ __forceinline__ const float* begin(const Adder<BN, PAIR>& R, uint32_t* status) {
+    if (!ready) ok = ok && mbar_wait(&R.acc_full[buf()], Buffers<BN>::parity(it), status);
     __syncwarp();
     tc_fence_after();
     return R.scales + slot * R.slot_floats;
   }
-  __device__ __forceinline__ void loaded(const Adder<BN>& R, int lane) {
+  __device__ __forceinline__ void loaded(const Adder<BN, PAIR>& R, int lane) {
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&R.acc_empty[buf()]);
-    ready = mbar_try_wait(&R.acc_full[buf() ^ 1u], ((it + 1) >> 1) & 1u);
+    if (lane == 0) {
+      if (PAIR)
+        mbar_arrive_pair(R.acc_empty_lead + buf() * 8);
+      else
+        mbar_arrive(&R.acc_empty[buf()]);
+    }
+    ready = mbar_test(&R.acc_full[Buffers<BN>::at(it + 1)], Buffers<BN>::parity(it + 1));
   }
-  __device__ __forceinline__ void end(const Adder<BN>& R, int lane) {
+  __device__ __forceinline__ void end(const Adder<BN, PAIR>& R, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&R.sempty[slot]);
     if (static_cast<int>(++slot) == R.slots) slot = 0;
@@ -249,21 +289,21 @@ __device__ __forceinline__ void store_f32x8(const Fp8GemmArgs& A, float* p, int 
   }
 }
 
-// B in square blocks: a thread owns one output row and BN / 2 columns, which
-// one block's scale covers, so a step's scales are one number a thread and an
-// addition is one fused multiply-add.
-template <int BN>
-__device__ __forceinline__ void add_square(const Fp8GemmArgs& A, const Adder<BN>& R, int tiles_m, int tiles_n, int nkb) {
+// B in square blocks: a thread owns one output row and BN / 2 columns; one
+// block's scale covers 32 or more of them, so an addition is one fused
+// multiply-add.
+template <int BN, bool PAIR>
+__device__ __forceinline__ void add_square(const Fp8GemmArgs& A, const Adder<BN, PAIR>& R, int tiles_m, int tiles_n, int nkb) {
   constexpr int kCols = BN / 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = warp & 3;  // TMEM lane quarter of this warp
   const int half = (warp - 4) >> 2;
   const uint32_t tbase = R.tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kCols;
   const int tiles = tiles_m * tiles_n;
-  Steps<BN> S(R);
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+  Steps<BN, PAIR> S(R);
+  for (int t = R.first; t < tiles; t += R.stride) {
     const TileAt at = tile_at(t, tiles_m, tiles_n);
-    const int row = at.tm * kTM + q * 32 + lane;
+    const int row = at.tm * R.row_step + R.row0 + q * 32 + lane;
     const int col0 = at.tn * BN + half * kCols;
     float acc[kCols];
 #pragma unroll
@@ -271,20 +311,37 @@ __device__ __forceinline__ void add_square(const Fp8GemmArgs& A, const Adder<BN>
     for (int kb = 0; kb < nkb; ++kb) {
       const float* sc = S.begin(R, A.status);
       const uint32_t d = tbase + S.buf() * BN;
-      // 32 columns are loaded while the 32 before them are added
-      uint32_t v[2][32];
-      tmem_ld32_start(d, v[0]);
-      const float s = sc[q * 32 + lane] * sc[kTM + (half * kCols) / kFp8Group];
+      const float s = sc[q * 32 + lane];
+      const float* sb = sc + kTM - (at.tn * BN) / kFp8Group;
+      if constexpr (kCols <= 96) {
+        // the whole step at once: the buffer is free before the additions
+        uint32_t v[kCols / 32][32];
 #pragma unroll
-      for (int c = 0; c < kCols; c += 32) {
-        uint32_t(&x)[32] = v[(c / 32) & 1];
-        tmem_ld_wait(x);
-        if (c + 32 < kCols)
-          tmem_ld32_start(d + c + 32, v[(c / 32 + 1) & 1]);
-        else
-          S.loaded(R, lane);
+        for (int c = 0; c < kCols; c += 32) tmem_ld32_start(d + c, v[c / 32]);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(x[j]), s, acc[c + j]);
+        for (int c = 0; c < kCols; c += 32) tmem_ld_wait(v[c / 32]);
+        S.loaded(R, lane);
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          const float x = s * sb[(col0 + c) / kFp8Group];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(v[c / 32][j]), x, acc[c + j]);
+        }
+      } else {
+        // 32 columns are loaded while the 32 before them are added
+        uint32_t v[2][32];
+        tmem_ld32_start(d, v[0]);
+        const float x = s * sb[col0 / kFp8Group];  // 128 columns of one block
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          tmem_ld_wait(v[(c / 32) & 1]);
+          if (c + 32 < kCols)
+            tmem_ld32_start(d + c + 32, v[(c / 32 + 1) & 1]);
+          else
+            S.loaded(R, lane);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(v[(c / 32) & 1][j]), x, acc[c + j]);
+        }
       }
       S.end(R, lane);
     }
@@ -319,8 +376,8 @@ __device__ __forceinline__ void add_square(const Fp8GemmArgs& A, const Adder<BN>
 // columns, so it reads 32; a product and a fused multiply-add per value are
 // left.  Column c of a 32-column chunk: pair i of lane quad position p holds
 // columns 8 i + 2 p and + 1; rows: half h (16 TMEM lanes), r: lane / 4 + 8 r.
-template <int BN>
-__device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN>& R, int tiles_m, int tiles_n, int nkb) {
+template <int BN, bool PAIR>
+__device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN, PAIR>& R, int tiles_m, int tiles_n, int nkb) {
   constexpr int kCols = BN / 2;
   constexpr int kChunks = kCols / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -328,10 +385,10 @@ __device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN>& 
   const int half = (warp - 4) >> 2;
   const uint32_t tbase = R.tmem + (static_cast<uint32_t>(q * 32) << 16) + half * kCols;
   const int tiles = tiles_m * tiles_n;
-  Steps<BN> S(R);
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+  Steps<BN, PAIR> S(R);
+  for (int t = R.first; t < tiles; t += R.stride) {
     const TileAt at = tile_at(t, tiles_m, tiles_n);
-    const int row0 = at.tm * kTM + q * 32 + (lane >> 2);
+    const int row0 = at.tm * R.row_step + R.row0 + q * 32 + (lane >> 2);
     const int col0 = at.tn * BN + half * kCols;
     uint64_t acc[kChunks][4][2][2];  // [chunk][i][h][r], two columns each
 #pragma unroll
@@ -341,9 +398,16 @@ __device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN>& 
     for (int kb = 0; kb < nkb; ++kb) {
       const float* sc = S.begin(R, A.status);
       const uint32_t d = tbase + S.buf() * BN;
-      uint32_t v[2][2][16];  // [in turn][half][4 i + 2 r + column]
-      tmem_ld16x256_start(d, v[0][0]);
-      tmem_ld16x256_start(d + (16u << 16), v[0][1]);
+      // [chunk, or in turn][half][4 i + 2 r + column]: the whole step at once
+      // up to 96 columns (the buffer is then free before the additions), else
+      // a chunk ahead
+      constexpr int kHeld = kChunks <= 3 ? kChunks : 2;
+      uint32_t v[kHeld][2][16];
+#pragma unroll
+      for (int c = 0; c < (kChunks <= 3 ? kChunks : 1); ++c) {
+        tmem_ld16x256_start(d + c * 32, v[c][0]);
+        tmem_ld16x256_start(d + (16u << 16) + c * 32, v[c][1]);
+      }
       uint64_t sa[2][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -353,15 +417,22 @@ __device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN>& 
           sa[h][r] = pair_of(__float_as_uint(x), __float_as_uint(x));
         }
       const uint64_t* sb = reinterpret_cast<const uint64_t*>(sc + kTM + half * kCols) + p;
+      if (kChunks <= 3) {
+#pragma unroll
+        for (int c = 0; c < kHeld; ++c) tmem_ld16x256_wait(v[c][0], v[c][1]);
+        S.loaded(R, lane);
+      }
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
-        uint32_t(&x)[2][16] = v[c & 1];
-        tmem_ld16x256_wait(x[0], x[1]);
-        if (c + 1 < kChunks) {
-          tmem_ld16x256_start(d + (c + 1) * 32, v[(c + 1) & 1][0]);
-          tmem_ld16x256_start(d + (16u << 16) + (c + 1) * 32, v[(c + 1) & 1][1]);
-        } else {
-          S.loaded(R, lane);
+        uint32_t(&x)[2][16] = v[c % kHeld];
+        if (kChunks > 3) {
+          tmem_ld16x256_wait(x[0], x[1]);
+          if (c + 1 < kChunks) {
+            tmem_ld16x256_start(d + (c + 1) * 32, v[(c + 1) % kHeld][0]);
+            tmem_ld16x256_start(d + (16u << 16) + (c + 1) * 32, v[(c + 1) % kHeld][1]);
+          } else {
+            S.loaded(R, lane);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -438,6 +509,96 @@ __device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN>& 
   }
 }
 
+// 16 bytes, of which the first `bytes` come from global memory and the rest
+// are zeros.
+__device__ __forceinline__ void copy16(float* dst, const float* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+
+// Rows `row0 ..` of a matrix of scales, N of them, of one group: where they
+// lie group by group (as the quantiser writes them), four rows a copy.
+template <int N>
+struct ScaleRows {
+  const float* at;  // this lane's first row in group 0
+  int64_t step;     // to the next group
+  int64_t ld;
+  int left;         // rows from this lane's first to the end
+  bool fast;
+  __device__ __forceinline__ void set(const float* p, int64_t ld_row, int64_t ld_group, int row0, int rows, int lane) {
+    fast = ld_row == 1 && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld_group & 3) == 0;
+    const int r = row0 + lane * (fast ? 4 : 1);
+    at = p + static_cast<int64_t>(min(r, fast ? (rows - 1) & ~3 : rows - 1)) * ld_row;
+    step = ld_group;
+    ld = ld_row;
+    left = rows - r;
+  }
+  __device__ __forceinline__ void copy(float* dst, int lane) {
+    if (fast) {
+#pragma unroll
+      for (int i = 0; i < (N + 127) / 128; ++i) {
+        const int n = min(4, left - i * 128);
+        if (N % 128 == 0 || i * 128 + lane * 4 < N) copy16(dst + i * 128 + lane * 4, n > 0 ? at + i * 128 : at, n > 0 ? 4 * n : 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < (N + 31) / 32; ++i) {
+        const bool in = left > i * 32;
+        if (N % 32 == 0 || i * 32 + lane < N) copy4(dst + i * 32 + lane, in ? at + i * 32 * ld : at, in);
+      }
+    }
+    at += step;
+  }
+};
+
+// The scale warp: the tile's rows of A, then its rows of B, or the one or two
+// square blocks its columns meet, of every step; zeros outside.  It is one
+// warp with a step's time for a step, so it takes four rows a copy where they
+// lie next to each other (row groups, 11008 x 4096 x 8192 with 128 x 192 tiles:
+// 535 -> 448 us; no change for square blocks).
+template <int BN>
+__device__ __forceinline__ void copy_scales(const Fp8GemmArgs& A, float* ring, int slot_floats, int slots, uint64_t* sfull,
+                                            uint64_t* sempty, int first, int stride, int row_step, int row0, int tiles_m,
+                                            int tiles_n, int nkb) {
+  constexpr int kBlocks = (BN + kFp8Group - 1) / kFp8Group;
+  const int lane = threadIdx.x & 31, tiles = tiles_m * tiles_n;
+  int slot = 0;
+  uint32_t phase = 0;
+  for (int t = first; t < tiles; t += stride) {
+    const TileAt at = tile_at(t, tiles_m, tiles_n);
+    ScaleRows<kTM> a;
+    a.set(A.a_scale, A.lda_row, A.lda_group, at.tm * row_step + row0, A.m, lane);
+    ScaleRows<BN> b;
+    ScaleRows<kBlocks> sq;
+    if (A.b_square) {
+      sq.set(A.b_scale, A.ldb_row, A.ldb_group, at.tn * BN / kFp8Group, (A.n + kFp8Group - 1) / kFp8Group, lane);
+      if (sq.fast) {  // a block a lane: the tile's first need not be a multiple of four
+        sq.fast = false;
+        const int blocks = (A.n + kFp8Group - 1) / kFp8Group, r = at.tn * BN / kFp8Group + lane;
+        sq.at = A.b_scale + min(r, blocks - 1);
+        sq.left = blocks - r;
+      }
+    } else {
+      b.set(A.b_scale, A.ldb_row, A.ldb_group, at.tn * BN, A.n, lane);
+    }
+    for (int kb = 0; kb < nkb; ++kb) {
+      if (__any_sync(0xffffffffu, !mbar_wait(&sempty[slot], phase ^ 1u, A.status))) goto out;
+      float* sc = ring + slot * slot_floats;
+      a.copy(sc, lane);
+      if (A.b_square)
+        sq.copy(sc + kTM, lane);
+      else
+        b.copy(sc + kTM, lane);
+      copy_arrive(&sfull[slot]);
+      if (++slot == slots) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+  }
+out:
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 template <int BN>
 __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant__ Fp8GemmArgs A) {
   using C = Tile<BN>;
@@ -449,8 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
   uint64_t* sfull = empty + C::kRing;
   uint64_t* sempty = sfull + C::kSlots;
   uint64_t* acc_full = sempty + C::kSlots;
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* acc_empty = acc_full + Buffers<BN>::kCount;
+  uint64_t* drain = acc_empty + Buffers<BN>::kCount;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -463,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       mbar_init(&sfull[s], 32);
       mbar_init(&sempty[s], 8);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < Buffers<BN>::kCount; ++b) {
       mbar_init(&acc_full[b], 2);   // the MMAs, and the issuer, which has seen the step's scales
       mbar_init(&acc_empty[b], 8);
 
@@ -529,17 +690,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
         for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const uint32_t buf = it & 1u;
+          const uint32_t buf = Buffers<BN>::at(it);
           if (!mbar_wait(&full[stage], phase, A.status) || !mbar_wait(&sfull[slot], sphase, A.status) ||
-              !mbar_wait(&acc_empty[buf], ((it >> 1) & 1u) ^ 1u, A.status)) {
+              !mbar_wait(&acc_empty[buf], Buffers<BN>::parity(it) ^ 1u, A.status)) {
             ok = false;
             break;
           }
-          mbar_arrive(&acc_full[buf]);
           tc_fence_after();
           umma_f8_step(tmem + buf * BN, adesc0 + stage * kStep, bdesc0 + stage * kStep, idesc);
           umma_commit(&acc_full[buf]);
           umma_commit(&empty[stage]);
+          mbar_arrive(&acc_full[buf]);
           if (++stage == C::kRing) {
             stage = 0;
             phase ^= 1u;
@@ -555,54 +716,233 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
     }
     __syncwarp();
   } else if (warp == 2) {
-    // scales of one step: the tile's rows of A, then its rows of B, or the
-    // one or two square blocks its columns meet; zeros outside
-    const int nb = A.b_square ? (BN + kFp8Group - 1) / kFp8Group : BN;
-    const int b_rows = A.b_square ? (A.n + kFp8Group - 1) / kFp8Group : A.n;
-    uint32_t slot = 0, phase = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const TileAt at = tile_at(t, tiles_m, tiles_n);
-      const int a0 = at.tm * kTM, b0 = A.b_square ? at.tn * BN / kFp8Group : at.tn * BN;
-      for (int kb = 0; kb < nkb; ++kb) {
-        ok = mbar_wait(&sempty[slot], phase ^ 1u, A.status);
-        if (__any_sync(0xffffffffu, !ok)) {
-          ok = false;
-          break;
-        }
-        float* sc = reinterpret_cast<float*>(scales + slot * C::kScaleBytes);
-        const float* sa = A.a_scale + kb * A.lda_group;
-        const float* sb = A.b_scale + kb * A.ldb_group;
-#pragma unroll
-        for (int i = 0; i < kTM / 32; ++i) {
-          const int r = i * 32 + lane;
-          copy4(sc + r, sa + static_cast<int64_t>(min(a0 + r, A.m - 1)) * A.lda_row, a0 + r < A.m);
-        }
-        for (int r = lane; r < nb; r += 32)
-          copy4(sc + kTM + r, sb + static_cast<int64_t>(min(b0 + r, b_rows - 1)) * A.ldb_row, b0 + r < b_rows);
-        copy_arrive(&sfull[slot]);
-        if (++slot == C::kSlots) {
-          slot = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    copy_scales<BN>(A, reinterpret_cast<float*>(scales), C::kScaleBytes / 4, C::kSlots, sfull, sempty, blockIdx.x,
+                    gridDim.x, kTM, 0, tiles_m, tiles_n, nkb);
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
-    const Adder<BN> R = {tmem, reinterpret_cast<const float*>(scales), C::kScaleBytes / 4, C::kSlots,
-                         acc_full, acc_empty, sempty};
+    const Adder<BN, false> R = {static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), kTM, 0, tmem,
+                                reinterpret_cast<const float*>(scales), C::kScaleBytes / 4, C::kSlots,
+                                acc_full, acc_empty, sempty, 0};
     if (A.b_square)
-      add_square<BN>(A, R, tiles_m, tiles_n, nkb);
+      add_square<BN, false>(A, R, tiles_m, tiles_n, nkb);
     else
-      add_rows<BN>(A, R, tiles_m, tiles_n, nkb);
+      add_rows<BN, false>(A, R, tiles_m, tiles_n, nkb);
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, C::kCols);
+}
+
+// ------------------------------------------------------------- CTA pairs
+// The same over clusters of two CTAs on two SMs: one tcgen05.mma.cta_group::2
+// multiplies 256 rows of A (128 from each CTA's shared memory) with 256 rows
+// of B (128 from each), so a CTA loads and the tensor cores read 32 KB a step
+// instead of 48 (operands written and read at 128 bytes a clock take 1.5 times
+// the MMAs of a 128 x 256 tile).  Each CTA adds the 128 rows in its own TMEM.
+//
+// What bounds it: the way of a TMEM buffer, MMAs (512 clocks), commit, loads
+// by the adding warps (about 370), hand-over, and back; with two buffers a
+// step takes about 1000 clocks.  8192 x 11008 x 4096 with square blocks: 330 us,
+// 2.24 PFLOP/s (one CTA a tile 353 us); 8192 x 4096 x 11008: 302 us, 2.45.
+// Narrower tiles with more buffers cost more operand traffic than they save:
+// 256 x 192 388 us, 256 x 128 with four buffers 488 us.  Differences to the kernel above: the first CTA issues
+// the MMAs for both; its `full` barriers count both CTAs' copies; commits
+// arrive on both CTAs' `empty` and `acc_full`; both CTAs' adding warps hand
+// buffers back on the first one's `acc_empty`.  Two issuers take every other
+// step each: one waits for its barriers while the other's MMAs run.
+constexpr int kPN = 256;
+constexpr int kPairStage = kABytes + kPN / 2 * kTK;
+constexpr int kPairRing = 6, kPairSlots = 8, kPairScaleBytes = (kTM + kPN) * 4;
+constexpr int kPairSmem = kPairRing * kPairStage + kPairSlots * kPairScaleBytes + 1024 + 512;
+
+__device__ __forceinline__ uint32_t steps_of(int first, int stride, int tiles, int nkb) {
+  return first < tiles ? static_cast<uint32_t>((tiles - 1 - first) / stride + 1) * static_cast<uint32_t>(nkb) : 0u;
+}
+
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int32_t c0,
+                                                 int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar_cluster), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+__device__ __forceinline__ void umma_f8_step_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %3, %3;\n\t"
+      "setp.eq.b32 q, %3, %3;\n\t"
+      "add.s64 a1, %1, 2;\n\t"
+      "add.s64 b1, %2, 2;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 a2, %1, 4;\n\t"
+      "add.s64 b2, %2, 4;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a1, b1, %3, q;\n\t"
+      "add.s64 a3, %1, 6;\n\t"
+      "add.s64 b3, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a2, b2, %3, q;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc)
+      : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_fp8_gemm_pair(const __grid_constant__ Fp8GemmArgs A) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* scales = smem + kPairRing * kPairStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + kPairSlots * kPairScaleBytes);
+  uint64_t* empty = full + kPairRing;
+  uint64_t* sfull = empty + kPairRing;
+  uint64_t* sempty = sfull + kPairSlots;
+  uint64_t* acc_full = sempty + kPairSlots;
+  uint64_t* acc_empty = acc_full + Buffers<kPN>::kCount;
+  uint64_t* drain = acc_empty + Buffers<kPN>::kCount;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairRing; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kPairSlots; ++s) {
+      mbar_init(&sfull[s], 32);
+      mbar_init(&sempty[s], 8);
+    }
+    for (int b = 0; b < Buffers<kPN>::kCount; ++b) {
+      mbar_init(&acc_full[b], 2);    // the MMAs, and a thread that has seen the step's scales
+      mbar_init(&acc_empty[b], 16);  // the adding warps of both CTAs
+    }
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int tiles_m = (A.m + 2 * kTM - 1) / (2 * kTM), tiles_n = (A.n + kPN - 1) / kPN;
+  const int tiles = tiles_m * tiles_n;
+  const int nkb = (A.k + kTK - 1) / kTK;
+  const int first = blockIdx.x / 2, stride = gridDim.x / 2;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
+    if (warp == 0) {
+      if (lane == 0) {
+        prefetch_tmap(&A.amap);
+        prefetch_tmap(&A.bmap);
+        uint32_t stage = 0, phase = 0;
+        int64_t issued = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += stride) {
+          const TileAt at = tile_at(t, tiles_m, tiles_n);
+          for (int kb = 0; kb < nkb; ++kb) {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, A.status)) {
+              ok = false;
+              break;
+            }
+            uint8_t* sa = smem + stage * kPairStage;
+            if (rank == 0) mbar_expect_tx(&full[stage], 2 * kPairStage);
+            const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+            tma_load_2d_pair(sa, &A.amap, bar, kb * kTK, at.tm * 2 * kTM + rank * kTM);
+            tma_load_2d_pair(sa + kABytes, &A.bmap, bar, kb * kTK, at.tn * kPN + rank * (kPN / 2));
+            ++issued;
+            if (++stage == kPairRing) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        // no copy of either CTA may still be landing at exit (the first CTA
+        // sees them all; the other leaves after the cluster's last barrier)
+        if (rank == 0) {
+          const int64_t back = issued < kPairRing ? issued : kPairRing;
+          for (int64_t q = 1; q <= back; ++q) {
+            const int64_t idx = issued - q;
+            if (!mbar_wait_own_cluster(&full[idx % kPairRing], static_cast<uint32_t>((idx / kPairRing) & 1), A.status)) break;
+          }
+        }
+      }
+      __syncwarp();
+    } else if ((warp == 1 || warp == 3) && rank == 0) {
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_f16_f32(2 * kTM, kPN);  // format code 0 is e4m3 here
+        const uint32_t s0 = smem_u32(smem);
+        const uint64_t adesc0 = sw128_desc(s0), bdesc0 = sw128_desc(s0 + kABytes);
+        constexpr uint64_t kStep = kPairStage >> 4;
+        const uint32_t mine = warp >> 1;  // steps mine, mine + 2, ...
+        const uint32_t total = steps_of(first, stride, tiles, nkb);
+        for (uint32_t it = mine; it < total; it += 2) {
+          const uint32_t buf = Buffers<kPN>::at(it), stage = it % kPairRing, slot = it % kPairSlots;
+          if (!mbar_wait(&full[stage], (it / kPairRing) & 1u, A.status) ||
+              !mbar_wait(&sfull[slot], (it / kPairSlots) & 1u, A.status) ||
+              !mbar_wait(&acc_empty[buf], Buffers<kPN>::parity(it) ^ 1u, A.status))
+            break;
+          mbar_arrive(&acc_full[buf]);
+          tc_fence_after();
+          umma_f8_step_pair(tmem + buf * kPN, adesc0 + stage * kStep, bdesc0 + stage * kStep, idesc);
+          umma_commit_pair(&acc_full[buf], 3);
+          umma_commit_pair(&empty[stage], 3);
+        }
+        umma_commit_pair(&drain[mine], 1);
+        mbar_wait_own_cluster(&drain[mine], 0, A.status);
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      copy_scales<kPN>(A, reinterpret_cast<float*>(scales), kPairScaleBytes / 4, kPairSlots, sfull, sempty, first, stride,
+                       2 * kTM, rank * kTM, tiles_m, tiles_n, nkb);
+    } else if (warp == 1) {
+      if (lane == 0) {
+        // one arrival a step and buffer, after the buffer's step before is over
+        uint32_t slot = 0, sphase = 0, it = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += stride) {
+          for (int kb = 0; kb < nkb; ++kb, ++it) {
+            constexpr uint32_t kBufs = Buffers<kPN>::kCount;
+            const uint32_t buf = Buffers<kPN>::at(it);
+            if ((it >= kBufs && !mbar_wait(&acc_full[buf], Buffers<kPN>::parity(it - kBufs), A.status)) ||
+                !mbar_wait(&sfull[slot], sphase, A.status)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive(&acc_full[buf]);
+            if (++slot == kPairSlots) {
+              slot = 0;
+              sphase ^= 1u;
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
+    const Adder<kPN, true> R = {first, stride, 2 * kTM, rank * kTM, tmem,
+                                reinterpret_cast<const float*>(scales), kPairScaleBytes / 4, kPairSlots,
+                                acc_full, acc_empty, sempty, mapa_shared(smem_u32(acc_empty), 0)};
+    if (A.b_square)
+      add_square<kPN, true>(A, R, tiles_m, tiles_n, nkb);
+    else
+      add_rows<kPN, true>(A, R, tiles_m, tiles_n, nkb);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
 // ------------------------------------------------------------ a few tokens
@@ -739,6 +1079,18 @@ cudaError_t run_gemm(const Fp8GemmArgs& A, int num_sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+cudaError_t run_gemm_pair(const Fp8GemmArgs& A, int num_sms, cudaStream_t st) {
+  static PerDevice pd;
+  const cudaError_t e = once_per_device(pd, [](int) {
+    return cudaFuncSetAttribute(k_fp8_gemm_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = lm_div_up(A.m, 2 * kTM) * lm_div_up(A.n, kPN);
+  const int clusters = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
+  k_fp8_gemm_pair<<<2 * clusters, kThreads, kPairSmem, st>>>(A);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k, int num_sms) {
@@ -746,7 +1098,10 @@ Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k, int num_sms) {
   Fp8Plan P = {};
   P.skinny = m <= kSkinnyMax;
   P.box_a = kTM;
-  P.box_b = 256;
+  // 256 x 256 tiles of CTA pairs when there is one for every pair
+  P.pair = lm_div_up(m, 2 * kTM) * lm_div_up(n, kPN) >= num_sms / 2;
+  P.box_b = P.pair ? kPN / 2 : 256;
+  if (P.pair) return P;
   while (P.box_b > 64 && lm_div_up(m, kTM) * lm_div_up(n, P.box_b) < num_sms) P.box_b /= 2;
   return P;
 }
@@ -768,6 +1123,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& A, const Fp8Plan& P, void* worksp
       k_fp8_skinny<4><<<grid, threads, 0, st>>>(A);
     return cudaGetLastError();
   }
+  if (P.pair) return run_gemm_pair(A, num_sms, st);
   if (P.box_b == 256) return run_gemm<256>(A, num_sms, st);
   if (P.box_b == 128) return run_gemm<128>(A, num_sms, st);
   return run_gemm<64>(A, num_sms, st);

@@ -129,7 +129,8 @@ struct Fp8GemmArgs {
 };
 // What a product of this size runs as.
 struct Fp8Plan {
-  bool skinny;  // CUDA-core path for a few tokens
+  bool skinny;  // a few tokens
+  bool pair;    // CTA pairs
   int box_a, box_b;
 };
 Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k, int num_sms);

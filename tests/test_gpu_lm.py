@@ -335,7 +335,8 @@ def _check_product(a, b, got, out_dtype, old=None, extra=0.0):
 
 SIZES = [(1, 1, 1), (1, 5504, 2048), (2, 17, 130), (8, 64, 128), (9, 130, 1000), (16, 2048, 512), (31, 33, 257),
          (32, 100, 64), (33, 100, 64), (64, 64, 128), (100, 300, 200), (128, 256, 128), (129, 257, 129),
-         (200, 1000, 1111), (515, 2048, 2047), (1024, 1023, 640), (2048, 5504, 256), (37, 11008, 384)]
+         (200, 1000, 1111), (515, 2048, 2047), (1024, 1023, 640), (2048, 5504, 256), (37, 11008, 384), (2000, 2600, 300), (5003, 1290, 130),
+         (4096, 2304, 1152), (300, 19500, 128)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
