@@ -1,7 +1,8 @@
-"""In-tree build of libokls.so (sm_103a) with nvcc.
+"""In-tree build of libokls.so (sm_103a) with nvcc, and of the torch binding of
+its language-model operators (_lm_native.so) with the host compiler.
 
-Each translation unit is compiled in parallel, then linked into one shared
-library next to this file.  Used by ``__graft_entry__.build()`` and by the
+Each translation unit is compiled in parallel, then linked into shared
+libraries next to this file.  Used by ``__graft_entry__.build()`` and by the
 Python binding when the library is missing and a build is requested.
 """
 
@@ -23,6 +24,8 @@ SOURCES = ["okls_api.cu", "okls_gemm.cu", "okls_elementwise.cu", "okls_ns_small.
            "okls_soap_large.cu", "okls_eig.cu", "okls_bjacobi.cu", "okls_tc3.cu",
            "okls_lm_api.cu", "okls_lm_norm.cu", "okls_lm_embed.cu", "okls_lm_score.cu",
            "okls_fp8_quant.cu", "okls_fp8_gemm.cu"]
+BINDING = "lm_torch.cpp"
+BINDING_LIB = os.path.join(PKG, "_lm_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -49,6 +52,21 @@ def _run(cmd: list[str]) -> None:
         sys.stderr.write(r.stdout)
 
 
+def _torch_flags() -> tuple[list[str], list[str]]:
+    """Compile and link flags of the binding: torch's headers and libraries."""
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = ["-I" + p for p in (os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+                              os.path.join(cuda, "include"), sysconfig.get_paths()["include"])]
+    link = ["-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-Wl,-rpath," + os.path.join(t, "lib")]
+    return ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wno-sign-compare", "-DTORCH_API_INCLUDE_EXTENSION_H",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + inc, link
+
+
 def build_library(verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile every source for sm_103a and link libokls.so; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
@@ -63,11 +81,19 @@ def build_library(verbose: bool = False, ptxas_info: bool = False) -> str:
         _run(cmd)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    flags, link = _torch_flags()
+    binding = os.path.join(BUILD, BINDING + ".o")
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        host = ex.submit(_run, [cxx, "-c", os.path.join(CSRC, BINDING), "-o", binding] + flags)
         objs = list(ex.map(one, SOURCES))
+        host.result()
     tmp = LIB + ".tmp"
     _run([cc, "-shared", "-o", tmp] + objs + ARCH + ["--cudart", "static", "-Xcompiler", "-fPIC"])
     os.replace(tmp, LIB)
+    tmp = BINDING_LIB + ".tmp"
+    _run([cxx, "-shared", "-o", tmp, binding, "-L" + PKG, "-lokls", "-Wl,-rpath,$ORIGIN"] + link)
+    os.replace(tmp, BINDING_LIB)
     return LIB
 
 

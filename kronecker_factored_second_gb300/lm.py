@@ -25,7 +25,6 @@ apart from `query_status`.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -34,157 +33,46 @@ import torch
 from . import _lib as L
 
 FP8_GROUP = 128
-_FLOATS = {torch.float32: L.OKLS_F32, torch.bfloat16: L.OKLS_BF16}
-_BLOCKS = {"row": L.FP8_ROW, "square": L.FP8_SQUARE}
-_STATUS: dict[int, torch.Tensor] = {}
+_BLOCKS = ("row", "square")
+_NATIVE = None
 
 
-# ------------------------------------------------------------------ helpers
 def _fail(msg: str):
     raise ValueError("okls.lm: " + msg)
 
 
-def _dtype(t: torch.Tensor, name: str) -> int:
-    code = _FLOATS.get(t.dtype)
-    if code is None:
-        _fail(f"{name} must be fp32 or bf16, not {t.dtype}")
-    return code
-
-
-def _out_dtype(dtype: torch.dtype) -> int:
-    code = _FLOATS.get(dtype)
-    if code is None:
-        _fail(f"the output type must be fp32 or bf16, not {dtype}")
-    return code
-
-
-def _matrix(t: torch.Tensor, name: str) -> torch.Tensor:
-    """`t` as rows x columns without a copy."""
-    if t.dim() == 2:
-        if t.stride(1) == 1 or t.shape[1] <= 1 or t.numel() == 0:
-            return t
-        _fail(f"the last dimension of {name} must be contiguous")
-    if t.dim() == 0:
-        _fail(f"{name} needs at least one dimension")
-    try:
-        t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(t.shape[:-1].numel(), t.shape[-1])
-    except RuntimeError:
-        _fail(f"the leading dimensions of {name} do not fold into rows without a copy")
-    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
-        _fail(f"the last dimension of {name} must be contiguous")
-    return t
-
-
-def _vector(t: torch.Tensor, name: str, dtype=None, count: int | None = None) -> torch.Tensor:
-    if not t.is_contiguous():
-        _fail(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
-        _fail(f"{name} must be {dtype}, not {t.dtype}")
-    if count is not None and t.numel() != count:
-        _fail(f"{name} must hold {count} values, not {t.numel()}")
-    return t
-
-
-def _ids(t: torch.Tensor, count: int) -> int:
-    if t.dtype not in (torch.int32, torch.int64):
-        _fail(f"ids must be int32 or int64, not {t.dtype}")
-    _vector(t, "ids", count=count)
-    return int(t.dtype == torch.int64)
-
-
-def _ld(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _same(t: torch.Tensor, like: torch.Tensor, name: str):
-    if t.shape != like.shape:
-        _fail(f"{name} has shape {tuple(t.shape)}, not {tuple(like.shape)}")
-    if t.dtype != like.dtype:
-        _fail(f"{name} is {t.dtype}, not {like.dtype}")
-
-
-@contextlib.contextmanager
-def _other(device, stream):
-    with torch.cuda.device(device):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream):
-                yield
-
-
-_HERE = contextlib.nullcontext()
-
-
-def _on(stream, *tensors):
-    """The device and stream that a call runs on; its allocations belong to them."""
-    device = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            _fail("tensors must be on a CUDA device")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            _fail(f"tensors on {device} and {t.device}")
-    if stream is None and device.index == torch.cuda.current_device():
-        return _HERE
-    return _other(device, stream)
-
-
-def _stream(t: torch.Tensor) -> int:
-    """Handle of the current stream of t's device (the current device)."""
-    # the same handle as torch.cuda.current_stream().cuda_stream, without building a Stream object, which
-    # costs more than a launch
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
-
-
-def _ptr(t: torch.Tensor | None) -> int:
-    return 0 if t is None else t.data_ptr()
-
-
-def _status_word(device: torch.device) -> torch.Tensor:
-    w = _STATUS.get(device.index)
-    if w is None:
-        # zeroed and waited for, so that any stream may use it from now on
-        w = torch.zeros(64, dtype=torch.int32, device=device)
-        torch.cuda.current_stream().synchronize()
-        _STATUS[device.index] = w
-    return w
+def _n():
+    """The compiled torch binding (checks, allocation, the call of the C entry)."""
+    global _NATIVE
+    if _NATIVE is None:
+        L.lib()  # says how to build when the library is missing
+        from . import _lm_native
+        _NATIVE = _lm_native
+    return _NATIVE
 
 
 def query_status(device=None, stream=None) -> int:
     """Synchronise the stream and return (and clear) the device's status word;
     raises OklsError for a token id past the vocabulary or an expired wait."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    if dev.index is None:
-        dev = torch.device("cuda", torch.cuda.current_device())
-    with _other(dev, stream):
-        w = _status_word(dev)
+    index = torch.device("cuda" if device is None else device).index
+    if index is None:
+        index = torch.cuda.current_device()
+    with torch.cuda.device(index):
+        word = _n().status_word(index)
+        s = torch.cuda.current_stream() if stream is None else stream
         v = ctypes.c_uint32(0)
-        L.check(L.lib().okls_status_word_read(w.data_ptr(), _stream(w), ctypes.byref(v)))
+        L.check(L.lib().okls_status_word_read(word.data_ptr(), s.cuda_stream, ctypes.byref(v)))
     return v.value
-
-
-def _workspace(need: int, device) -> torch.Tensor | None:
-    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
 
 # ---------------------------------------------------------------- embedding
 def embedding(weight: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, out_dtype: torch.dtype | None = None,
               stream=None) -> torch.Tensor:
     """scale * weight[ids], of shape ids.shape + (dim,); zeros for padding."""
-    if weight.dim() != 2:
-        _fail("weight must be vocab x dim")
-    w = _matrix(weight, "weight")
-    dt, i64 = _dtype(w, "weight"), _ids(ids, ids.numel())
-    od = dt if out_dtype is None else _out_dtype(out_dtype)
-    with _on(stream, weight, ids):
-        out = torch.empty(*ids.shape, w.shape[1], dtype=out_dtype or w.dtype, device=w.device)
-        L.check(L.lib().okls_embedding(_ptr(w), dt, _ld(w), w.shape[0], w.shape[1], _ptr(ids), i64, ids.numel(),
-                                       scale, _ptr(out), od, w.shape[1], _ptr(_status_word(w.device)), _stream(w)))
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return embedding(weight, ids, scale=scale, out_dtype=out_dtype)
+    return _n().embedding(weight, ids, scale, out_dtype)
 
 
 def embedding_grad(dy: torch.Tensor, ids: torch.Tensor, vocab: int, *, scale: float = 1.0,
@@ -194,26 +82,11 @@ def embedding_grad(dy: torch.Tensor, ids: torch.Tensor, vocab: int, *, scale: fl
 
     `base` None stands for zeros.  With `out` the result goes there; out=base
     adds in place and touches only the rows of tokens that occur."""
-    d = _matrix(dy, "dy")
-    dt, i64 = _dtype(d, "dy"), _ids(ids, d.shape[0])
-    shape = (vocab, d.shape[1])
-    for t, name in ((base, "base"), (out, "out")):
-        if t is not None and (tuple(t.shape) != shape or _matrix(t, name) is not t):
-            _fail(f"{name} must be a matrix of shape {shape}")
-    if base is not None and out is not None and base.dtype != out.dtype:
-        _fail("base and out must have one type")
-    with _on(stream, dy, ids, base, out):
-        if out is None:
-            out = torch.empty(shape, dtype=dtype if base is None else base.dtype, device=d.device)
-        od = _out_dtype(out.dtype)
-        need = ctypes.c_size_t()
-        lib = L.lib()
-        L.check(lib.okls_embedding_grad_workspace_bytes(d.shape[0], vocab, d.shape[1], ctypes.byref(need)))
-        ws = _workspace(need.value, d.device)
-        L.check(lib.okls_embedding_grad(_ptr(d), dt, _ld(d), _ptr(ids), i64, d.shape[0], vocab, d.shape[1], scale,
-                                        _ptr(base), 0 if base is None else _ld(base), _ptr(out), od, _ld(out),
-                                        _ptr(ws), need.value, _ptr(_status_word(d.device)), _stream(d)))
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return embedding_grad(dy, ids, vocab, scale=scale, base=base, out=out, dtype=dtype)
+    got = _n().embedding_grad(dy, ids, vocab, scale, base, out, dtype)
+    return got if out is None else out
 
 
 # --------------------------------------------------------------------- norm
@@ -232,37 +105,13 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | 
     `out_dtype` may be fp32, bf16 (default: x's type) or float8_e4m3fn; an
     8-bit y is an Fp8Tensor with row groups.  `inplace` writes s over
     `residual`.  Without a residual, s is x itself."""
-    m = _matrix(x, "x")
-    dt = _dtype(m, "x")
-    wd = _dtype(_vector(weight, "weight", count=m.shape[1]), "weight")
-    out_dtype = out_dtype or m.dtype
-    fp8 = out_dtype == torch.float8_e4m3fn
-    od = L.OKLS_E4M3 if fp8 else _out_dtype(out_dtype)
-    r = None
-    if residual is not None:
-        r = _matrix(residual, "residual")
-        _same(residual, x, "residual")
-    rows, dim = m.shape
-    with _on(stream, x, weight, residual):
-        dev = m.device
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        r_ptr = ldr = s_ptr = lds = sc_ptr = sc_row = sc_group = 0
-        total = x
-        if r is not None:
-            r_ptr, ldr = r.data_ptr(), _ld(r)
-            total = residual if inplace else torch.empty(x.shape, dtype=x.dtype, device=dev)
-            s_ptr, lds = (r_ptr, ldr) if inplace else (total.data_ptr(), dim)
-        if fp8:
-            y = _fp8_empty(rows, dim, "row", dev)
-            y_ptr, ldy, sc_ptr = y.data.data_ptr(), y.data.stride(0), y.scale.data_ptr()
-            sc_row, sc_group = y.scale.stride()
-        else:
-            y = torch.empty(x.shape, dtype=out_dtype, device=dev)
-            y_ptr, ldy = y.data_ptr(), dim
-        L.check(L.lib().okls_rms_norm(m.data_ptr(), dt, _ld(m), r_ptr, ldr, weight.data_ptr(), wd, rows, dim, eps,
-                                      y_ptr, od, ldy, sc_ptr, sc_row, sc_group, s_ptr, lds, rstd.data_ptr(),
-                                      _stream(m)))
-    return NormOutput(y, total, rstd)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rms_norm(x, weight, residual=residual, eps=eps, out_dtype=out_dtype, inplace=inplace)
+    y, scale, total, rstd = _n().rms_norm(x, weight, residual, eps, out_dtype, inplace)
+    if scale is not None:
+        y = _fp8(y, scale, "row")
+    return NormOutput(y, x if residual is None else residual if inplace else total, rstd)
 
 
 def rms_norm_grad(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, *,
@@ -270,29 +119,10 @@ def rms_norm_grad(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd:
     """(ds, dweight): the gradient of x and residual alike, of s's type, and of
     the weight in fp32 (None unless `need_dweight`).  `s` and `rstd` are what
     rms_norm returned; `dresidual` is the gradient that reaches s from elsewhere."""
-    g, m = _matrix(dy, "dy"), _matrix(s, "s")
-    if g.shape != m.shape:
-        _fail(f"dy has shape {tuple(dy.shape)}, not {tuple(s.shape)}")
-    gd, sd = _dtype(g, "dy"), _dtype(m, "s")
-    rows, dim = m.shape
-    wd = _dtype(_vector(weight, "weight", count=dim), "weight")
-    _vector(rstd, "rstd", torch.float32, rows)
-    e = None
-    if dresidual is not None:
-        e = _matrix(dresidual, "dresidual")
-        _same(dresidual, s, "dresidual")
-    with _on(stream, dy, s, weight, rstd, dresidual):
-        ds = torch.empty(s.shape, dtype=m.dtype, device=m.device)
-        dw = torch.empty(dim, dtype=torch.float32, device=m.device) if need_dweight else None
-        need = ctypes.c_size_t()
-        lib = L.lib()
-        if need_dweight:
-            L.check(lib.okls_rms_norm_grad_workspace_bytes(rows, dim, ctypes.byref(need)))
-        ws = _workspace(need.value, m.device)
-        L.check(lib.okls_rms_norm_grad(_ptr(g), gd, _ld(g), _ptr(m), sd, _ld(m), _ptr(weight), wd, _ptr(rstd), _ptr(e),
-                                       0 if e is None else _ld(e), rows, dim, _ptr(ds), dim, _ptr(dw), _ptr(ws),
-                                       need.value, _stream(m)))
-    return ds, dw
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rms_norm_grad(dy, s, weight, rstd, dresidual=dresidual, need_dweight=need_dweight)
+    return _n().rms_norm_grad(dy, s, weight, rstd, dresidual, need_dweight)
 
 
 # -------------------------------------------------------------------- 8 bits
@@ -307,7 +137,7 @@ class Fp8Tensor:
 
     def __post_init__(self):
         if self.block not in _BLOCKS:
-            _fail(f"block must be one of {sorted(_BLOCKS)}")
+            _fail(f"block must be one of {_BLOCKS}")
         if self.data.dim() != 2 or self.data.dtype != torch.float8_e4m3fn:
             _fail("data must be a matrix of float8_e4m3fn")
         rows, cols = self.data.shape
@@ -329,14 +159,9 @@ class Fp8Tensor:
         return self.data.float() * s.repeat_interleave(FP8_GROUP, 1)[:, : self.data.shape[1]]
 
 
-def _fp8_empty(rows: int, cols: int, block: str, device) -> Fp8Tensor:
-    """Rows start at multiples of 128 bytes (the product's copies need 16); the
-    scales lie group by group, so that neighbouring rows' scales are neighbours."""
-    groups = -(-cols // FP8_GROUP)
-    data = torch.empty_strided((rows, cols), (max(groups, 1) * FP8_GROUP, 1), dtype=torch.float8_e4m3fn, device=device)
-    lines = rows if block == "row" else -(-rows // FP8_GROUP)
-    scale = torch.empty_strided((lines, groups), (1, max(-(-lines // 4) * 4, 1)), dtype=torch.float32, device=device)
-    q = object.__new__(Fp8Tensor)  # right by construction: __post_init__ has nothing to check
+def _fp8(data: torch.Tensor, scale: torch.Tensor, block: str) -> Fp8Tensor:
+    """An Fp8Tensor that is right by construction."""
+    q = object.__new__(Fp8Tensor)
     q.data, q.scale, q.block = data, scale, block
     return q
 
@@ -345,19 +170,14 @@ def fp8_quantize(x: torch.Tensor, *, block: str = "row", transpose: bool = False
     """An Fp8Tensor of x (rows x columns), of its transpose, or the pair of
     them from one read.  The groups of the transpose lie along its own rows."""
     if block not in _BLOCKS:
-        _fail(f"block must be one of {sorted(_BLOCKS)}")
-    m = _matrix(x, "x")
-    dt = _dtype(m, "x")
-    rows, cols = m.shape
-    with _on(stream, x):
-        q = _fp8_empty(rows, cols, block, m.device) if both or not transpose else None
-        t = _fp8_empty(cols, rows, block, m.device) if both or transpose else None
-        args = []
-        for f in (q, t):
-            args += (0, 0, 0, 0, 0) if f is None else (f.data.data_ptr(), f.data.stride(0), f.scale.data_ptr(),
-                                                       *f.scale.stride())
-        L.check(L.lib().okls_fp8_quantize(m.data_ptr(), dt, _ld(m), rows, cols, _BLOCKS[block], *args, _stream(m)))
-    return (q, t) if both else t if transpose else q
+        _fail(f"block must be one of {_BLOCKS}")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_quantize(x, block=block, transpose=transpose, both=both)
+    q, s, qt, st = _n().fp8_quantize(x, block == "square", both or not transpose, both or transpose)
+    if both:
+        return _fp8(q, s, block), _fp8(qt, st, block)
+    return _fp8(qt, st, block) if transpose else _fp8(q, s, block)
 
 
 def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, *, out_dtype: torch.dtype = torch.bfloat16,
@@ -366,29 +186,11 @@ def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, *, out_dtype: torch.dtype = torch.bfl
     blocks): m x n in bf16 or fp32.  With `accumulate` it is added to `out`."""
     if a.block != "row":
         _fail("the first factor needs row groups")
-    (m, k), (n, k2) = a.shape, b.shape
-    if k != k2:
-        _fail(f"sums of length {k} and {k2}")
-    if out is None and accumulate:
-        _fail("accumulate needs out")
-    if out is not None:
-        if tuple(out.shape) != (m, n) or _matrix(out, "out") is not out:
-            _fail(f"out must be a matrix of shape {(m, n)}")
-        out_dtype = out.dtype
-    od = _out_dtype(out_dtype)
-    with _on(stream, a.data, a.scale, b.data, b.scale, out):
-        dev = a.data.device
-        if out is None:
-            out = torch.empty((m, n), dtype=out_dtype, device=dev)
-        lib = L.lib()
-        need = ctypes.c_size_t()
-        L.check(lib.okls_fp8_matmul_workspace_bytes(m, n, k, ctypes.byref(need)))
-        ws = _workspace(need.value, dev)
-        L.check(lib.okls_fp8_matmul(a.data.data_ptr(), a.data.stride(0), a.scale.data_ptr(), *a.scale.stride(),
-                                    b.data.data_ptr(), b.data.stride(0), b.scale.data_ptr(), *b.scale.stride(),
-                                    _BLOCKS[b.block], m, n, k, out.data_ptr(), od, _ld(out), int(accumulate), _ptr(ws),
-                                    need.value, _status_word(dev).data_ptr(), _stream(out)))
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_matmul(a, b, out_dtype=out_dtype, out=out, accumulate=accumulate)
+    got = _n().fp8_matmul(a.data, a.scale, b.data, b.scale, b.block == "square", out, out_dtype, accumulate)
+    return got if out is None else out
 
 
 # --------------------------------------------------------- log probabilities
@@ -405,25 +207,12 @@ class TokenLogprobs:
 
 def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, *, top_k: int = 0, scale: float = 1.0,
                    stream=None) -> TokenLogprobs:
-    """Log probabilities of `ids` under softmax(scale * logits), shaped like
-    ids; `top_k` <= 32 best alternatives, equal logits in the order of their ids."""
-    z = _matrix(logits, "logits")
-    rows, vocab = z.shape
-    dt, i64 = _dtype(z, "logits"), _ids(ids, rows)
-    lead = logits.shape[:-1]
-    with _on(stream, logits, ids):
-        dev = z.device
-        logp = torch.empty(lead, dtype=torch.float32, device=dev)
-        entropy = torch.empty(lead, dtype=torch.float32, device=dev)
-        lse = torch.empty(lead, dtype=torch.float32, device=dev)
-        top_ids = top_logp = None
-        if top_k > 0:
-            top_ids = torch.empty((*lead, top_k), dtype=torch.int32, device=dev)
-            top_logp = torch.empty((*lead, top_k), dtype=torch.float32, device=dev)
-        L.check(L.lib().okls_token_logprobs(z.data_ptr(), dt, _ld(z), ids.data_ptr(), i64, rows, vocab, scale, top_k,
-                                            logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _ptr(top_ids),
-                                            _ptr(top_logp), _status_word(dev).data_ptr(), _stream(z)))
-    return TokenLogprobs(logp, entropy, lse, top_ids, top_logp)
+    """Log probabilities of `ids` under softmax(scale * logits), shaped like the
+    logits' rows; `top_k` <= 32 best alternatives, equal logits in the order of their ids."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return token_logprobs(logits, ids, top_k=top_k, scale=scale)
+    return TokenLogprobs(*_n().token_logprobs(logits, ids, top_k, scale))
 
 
 def token_logprobs_grad(logits: torch.Tensor, ids: torch.Tensor, result: TokenLogprobs, dlogp: torch.Tensor, *,
@@ -431,20 +220,10 @@ def token_logprobs_grad(logits: torch.Tensor, ids: torch.Tensor, result: TokenLo
                         stream=None) -> torch.Tensor:
     """Gradient of sum(dlogp * logp) + sum(dentropy * entropy) with respect to
     the logits, of their type; `inplace` writes it over the logits."""
-    z = _matrix(logits, "logits")
-    rows, vocab = z.shape
-    dt, i64 = _dtype(z, "logits"), _ids(ids, rows)
-    _vector(dlogp, "dlogp", torch.float32, rows)
-    _vector(result.lse, "lse", torch.float32, rows)
-    if dentropy is not None:
-        _vector(dentropy, "dentropy", torch.float32, rows)
-        _vector(result.entropy, "entropy", torch.float32, rows)
-    with _on(stream, logits, ids, result.lse, dlogp, dentropy):
-        d = z if inplace else torch.empty(logits.shape, dtype=z.dtype, device=z.device)
-        L.check(L.lib().okls_token_logprobs_grad(_ptr(z), dt, _ld(z), _ptr(ids), i64, rows, vocab, scale,
-                                                 _ptr(result.lse), _ptr(result.entropy if dentropy is not None else None),
-                                                 _ptr(dlogp), _ptr(dentropy), _ptr(d),
-                                                 _ld(d) if inplace else vocab, _stream(z)))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return token_logprobs_grad(logits, ids, result, dlogp, dentropy=dentropy, scale=scale, inplace=inplace)
+    d = _n().token_logprobs_grad(logits, ids, result.lse, result.entropy, dlogp, dentropy, scale, inplace)
     return logits if inplace else d
 
 
@@ -486,9 +265,8 @@ class _Norm(torch.autograd.Function):
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, out_dtype):
-        m = _matrix(x, "x")
         need_x, need_w = ctx.needs_input_grad[:2]
-        xq, xt = fp8_quantize(m, both=True) if need_w else (fp8_quantize(m), None)
+        xq, xt = fp8_quantize(x, both=True) if need_w else (fp8_quantize(x), None)
         wq, wt = fp8_quantize(weight, block="square", both=True) if need_x else (
             fp8_quantize(weight, block="square"), None)
         ctx.save_for_backward(*[t for f in (xt, wt) if f is not None for t in (f.data, f.scale)])
@@ -501,7 +279,7 @@ class _Linear(torch.autograd.Function):
         saved = list(ctx.saved_tensors)
         xt = Fp8Tensor(saved.pop(0), saved.pop(0), "row") if has_xt else None
         wt = Fp8Tensor(saved.pop(0), saved.pop(0), "square") if has_wt else None
-        g = _matrix(dy.contiguous(), "dy")
+        g = dy.contiguous()
         dx = dw = None
         if has_xt and has_wt:
             gq, gt = fp8_quantize(g, both=True)
