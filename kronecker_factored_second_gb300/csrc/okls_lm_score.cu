@@ -101,12 +101,14 @@ __device__ __forceinline__ V list_merge(V a, V b, int lane) {
   return v;
 }
 
-constexpr int kScoreThreads = 256;
+// 128 threads: a row's fixed costs are a CTA's, so small CTAs hide them under
+// other rows' loads (8192 x 32000 bf16: 512 threads 144 us, 256 110, 128 96).
+constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kVecs = 4;  // vectors of 8 values a thread loads at a time
 // A row goes to one warp when it is short, or when there are rows for 16
-// warps on every SM (8192 x 8000 bf16: 47 us with a CTA a row, 28 with a warp;
-// 8192 x 16000: 68 and 49); longer rows leave the SMs unevenly filled.
+// warps on every SM (bf16, a CTA a row against a warp: 8192 x 4000 22 and 13 us,
+// 8192 x 16000 56 and 48); longer rows leave the SMs unevenly filled.
 constexpr int kWarpRow = 16384, kWarpRowFew = 4096;
 
 __device__ __forceinline__ float ex2(float v) {
@@ -485,13 +487,14 @@ __global__ void __launch_bounds__(kScoreThreads) k_token_logprobs_warp(const Sco
 }
 
 // Longer rows: a cluster of CTAs each.
-constexpr int kCtaBlocks = 16;  // maxima a thread keeps: 131072 columns a CTA
+constexpr int kCtaBlocks = 32;  // maxima a thread keeps: 131072 columns a CTA
+constexpr int kCtaList = 256;   // keys
 constexpr int kHits = 512;
 template <class T, bool TOP, bool SCALED>
 __global__ void __launch_bounds__(kScoreThreads) k_token_logprobs(const ScoreArgs A, int keep_maxima) {
   __shared__ Stat stats[kScoreWarps];
   __shared__ Stat cta_stat;
-  __shared__ Key lists[TOP ? kScoreWarps : 1][32];  // kScoreThreads keys, or the warps' lists
+  __shared__ Key list[TOP ? kCtaList : 1];  // candidates, or the warps' lists
   __shared__ Key sorted[32];                        // the CTA's best
   __shared__ uint16_t hits[TOP ? kHits : 1];        // (thread, block) whose maximum reaches the bound
   __shared__ uint32_t tops[kScoreWarps];
@@ -540,7 +543,6 @@ __global__ void __launch_bounds__(kScoreThreads) k_token_logprobs(const ScoreArg
 #pragma unroll
     for (int w = 0; w < kScoreWarps; ++w) bound = min(bound, tops[w]);
     const float least = least_value(bound);
-    Key* list = &lists[0][0];
     if (keep_maxima) {
       const int blocks = static_cast<int>((Y.nvec - first + step * kVecs - 1) / (step * kVecs));
       for (int b = 0; b < blocks; ++b)
@@ -549,8 +551,8 @@ __global__ void __launch_bounds__(kScoreThreads) k_token_logprobs(const ScoreArg
           if (at < kHits) hits[at] = static_cast<uint16_t>(b * kScoreThreads + tid);
         }
       if (first == 0 && lane < Y.edge && edge_v >= least)
-        push_key(edge_v, static_cast<uint32_t>(lane < Y.head ? lane : Y.tail0 + (lane - Y.head)), list, kScoreThreads, &count);
-      if (rank == 0 && bound <= kOrdNegInf) collect_impossible(z, A.vocab, tid, k, list, kScoreThreads, &count);
+        push_key(edge_v, static_cast<uint32_t>(lane < Y.head ? lane : Y.tail0 + (lane - Y.head)), list, kCtaList, &count);
+      if (rank == 0 && bound <= kOrdNegInf) collect_impossible(z, A.vocab, tid, k, list, kCtaList, &count);
       __syncthreads();
       // a warp reads the 32 values of a hit, one a lane
       const int nh = nhits <= kHits ? nhits : 0;
@@ -560,17 +562,17 @@ __global__ void __launch_bounds__(kScoreThreads) k_token_logprobs(const ScoreArg
                           ((hits[h] / kScoreThreads) * kVecs + lane / 8) * step;
         const int64_t col = Y.head + i * 8 + lane % 8;
         const float v = i < Y.nvec ? to_f32(z[col]) : -CUDART_INF_F;
-        if (v >= least) push_key(v, static_cast<uint32_t>(col), list, kScoreThreads, &count);
+        if (v >= least) push_key(v, static_cast<uint32_t>(col), list, kCtaList, &count);
       }
-      if (tid == 0 && nhits > kHits) count = kScoreThreads + 1;
+      if (tid == 0 && nhits > kHits) count = kCtaList + 1;
     } else if (tid == 0) {
-      count = kScoreThreads + 1;
+      count = kCtaList + 1;
     }
     __syncthreads();
     const int n = count;
-    if (n <= kScoreThreads) {
-      if (tid < n) {
-        const Key mine = list[tid];
+    if (n <= kCtaList) {
+      for (int i = tid; i < n; i += kScoreThreads) {
+        const Key mine = list[i];
         const int at = rank_of(mine, list, n);
         if (at < 32) sorted[at] = mine;
       }
@@ -578,11 +580,11 @@ __global__ void __launch_bounds__(kScoreThreads) k_token_logprobs(const ScoreArg
     } else {
       const Key mine = insert_row(z, Y, first, step, lane, k, &cta_bound);
       __syncthreads();
-      lists[warp][lane] = mine;
+      list[warp * 32 + lane] = mine;
       __syncthreads();
       if (warp == 0) {
         Key best = mine;
-        for (int w = 1; w < kScoreWarps; ++w) best = list_merge(best, lists[w][lane], lane);
+        for (int w = 1; w < kScoreWarps; ++w) best = list_merge(best, list[w * 32 + lane], lane);
         sorted[lane] = best;
       }
     }
