@@ -13,6 +13,10 @@
 // for 8 rows), column maxima through shared memory.  The quotients are formed
 // once per group, one a thread, and read back; the transposed codes leave
 // through a shared-memory tile in runs of 8 bytes.
+//
+// Measured, 8192 x 11008 bf16: rows 47 us (85% of the copy rate), both
+// orientations 73 (73%), square blocks in both 67 (79%); with fp32 patches and a
+// quotient per thread and group 138, 190 and 156.
 #include "okls_internal.h"
 #include "okls_lm.cuh"
 

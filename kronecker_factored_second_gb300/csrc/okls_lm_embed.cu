@@ -11,6 +11,11 @@
 // order.  So a frequent token is spread over many CTAs, no sum depends on
 // the order in which CTAs run, and no row needs an atomic.  The rest of the
 // launch that sums writes the rows without a token.
+//
+// Measured, bf16 in: rows of 16363 tokens x 2048 21 us (95% of the copy rate);
+// gradient of them into 32000 x 2048 fp32 77 us against 48 of its bytes (sort
+// 15, sums and zero rows 53, join 9); 32768 tokens into 131072 x 2048 203 us
+// against 178.
 #include <cooperative_groups.h>
 
 #include "okls_internal.h"

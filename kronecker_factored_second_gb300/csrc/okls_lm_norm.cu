@@ -14,6 +14,11 @@
 // and loads rows ahead through a ring in shared memory: each thread copies
 // and later reads its own elements, so the ring needs no barrier.
 //
+// Measured, 16384 x 5504 bf16 with a residual: bf16 output 108 us (98% of the
+// copy rate), 8-bit output 113 (82%), gradient 114 (93%; 7 us of it the weight's
+// partial sums and their launch).  Eight chunks a warp were slower (128 and
+// 172 us: fewer rows in flight), rows ahead in registers too (gradient 239).
+//
 // A group of 128 columns with one 8-bit scale lies inside a warp chunk: its
 // largest magnitude is two warp reductions, each lane divides for one group
 // of the warp's, and the codes leave from the registers that hold y.

