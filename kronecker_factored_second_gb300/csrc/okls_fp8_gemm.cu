@@ -167,6 +167,18 @@ __device__ __forceinline__ uint32_t pick4(const uint32_t (&w)[4], int i) {
   return i & 2 ? b : a;
 }
 
+// The 4 x 4 words of a quad transposed: each lane then has 8 consecutive
+// columns (w[i]: columns 8 i + 2 p and + 1 of quad position p) and the quad 64
+// bytes.
+__device__ __forceinline__ uint4 quad_transpose(const uint32_t (&w)[4], int p) {
+  uint32_t u[4];
+  u[0] = pick4(w, p);
+#pragma unroll
+  for (int e = 1; e < 4; ++e) u[e] = __shfl_xor_sync(0xffffffffu, pick4(w, p ^ e), e);
+  // u[e] came from quad position p ^ e
+  return make_uint4(pick4(u, p), pick4(u, p ^ 1), pick4(u, p ^ 2), pick4(u, p ^ 3));
+}
+
 struct TileAt {
   int tm, tn;
 };
@@ -201,6 +213,36 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Results of a warp's 32 rows x 128 columns in bf16 on their way out: two boxes
+// of 64 columns (128 bytes a row, 128-byte swizzle) in shared memory, which the
+// copy engine stores while the warp goes on with the next tile.
+constexpr int kOutBox = 32 * 128;
+constexpr int kOutWarp = 2 * kOutBox;
+__device__ __forceinline__ void out_chunk(uint8_t* mine, int row, int chunk, uint4 v) {
+  // chunk: 8 columns; the 16-byte positions of a row are permuted by the row
+  *reinterpret_cast<uint4*>(mine + (chunk >> 3) * kOutBox + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = v;
+}
+// The warp's earlier stores have read their boxes.
+__device__ __forceinline__ void out_free(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+// Stores the boxes, rows row .. row + 31 and columns col .. col + 127 of the
+// output; what lies outside it is left out.
+__device__ __forceinline__ void out_store(const Fp8GemmArgs& A, const uint8_t* mine, int row, int col, int lane) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0 && row < A.m) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      if (col + b * 64 < A.n)
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(&A.omap),
+                     "r"(smem_u32(mine + b * kOutBox)), "r"(col + b * 64), "r"(row)
+                     : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
 // What the adding warps share with the others, and the CTA's walk over the
 // tiles.  PAIR: the two CTAs of a cluster hold the halves of 256-row tiles.
 template <int BN, bool PAIR>
@@ -212,6 +254,7 @@ struct Adder {
   int slot_floats, slots;
   uint64_t *acc_full, *acc_empty, *sempty;
   uint32_t acc_empty_lead;  // PAIR: acc_empty of the cluster's first CTA
+  uint8_t* out;             // PAIR: the warps' output boxes
 };
 
 // Per-step bookkeeping of an adding warp: waits for a TMEM buffer and hands it
@@ -345,6 +388,17 @@ __device__ __forceinline__ void add_square(const Fp8GemmArgs& A, const Adder<BN,
       }
       S.end(R, lane);
     }
+    if (PAIR && A.tma_out) {
+      uint8_t* mine = R.out + (warp - 4) * kOutWarp;
+      out_free(lane);
+#pragma unroll
+      for (int c = 0; c < kCols; c += 8)
+        out_chunk(mine, lane, c / 8,
+                  make_uint4(pack_bf16(acc[c], acc[c + 1]), pack_bf16(acc[c + 2], acc[c + 3]),
+                             pack_bf16(acc[c + 4], acc[c + 5]), pack_bf16(acc[c + 6], acc[c + 7])));
+      out_store(A, mine, row - lane, col0, lane);
+      continue;
+    }
     if (row >= A.m) continue;
     const int eb = A.out_dtype == kDtBf16 ? 2 : 4;
     char* o = static_cast<char*>(A.out) + (static_cast<int64_t>(row) * A.ldo + col0) * eb;
@@ -446,6 +500,27 @@ __device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN, P
       }
       S.end(R, lane);
     }
+    if (PAIR && A.tma_out) {
+      uint8_t* mine = R.out + (warp - 4) * kOutWarp;
+      out_free(lane);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float lo, hi;
+              unpair(acc[c][i][h][r], lo, hi);
+              w[i] = pack_bf16(lo, hi);
+            }
+            out_chunk(mine, h * 16 + r * 8 + (lane >> 2), c * 4 + p, quad_transpose(w, p));
+          }
+      out_store(A, mine, row0 - (lane >> 2), col0, lane);
+      continue;
+    }
     const int eb = A.out_dtype == kDtBf16 ? 2 : 4;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -464,16 +539,10 @@ __device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN, P
           if (A.out_dtype == kDtBf16) {
             __nv_bfloat16* b = reinterpret_cast<__nv_bfloat16*>(o) + c * 32;
             if (vec && left >= 32 && !A.accumulate) {
-              // the quad's 4 x 4 pairs are transposed, so that each lane has 8
-              // consecutive columns and the quad 64 bytes
-              uint32_t w[4], u[4];
+              uint32_t w[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[i][0], v[i][1]);
-              u[0] = pick4(w, p);
-#pragma unroll
-              for (int e = 1; e < 4; ++e) u[e] = __shfl_xor_sync(0xffffffffu, pick4(w, p ^ e), e);
-              // u[e] came from quad position p ^ e
-              const uint4 z = make_uint4(pick4(u, p), pick4(u, p ^ 1), pick4(u, p ^ 2), pick4(u, p ^ 3));
+              const uint4 z = quad_transpose(w, p);
               if (in) *reinterpret_cast<uint4*>(b + 8 * p) = z;
             } else if (in) {
 #pragma unroll
@@ -723,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
     const Adder<BN, false> R = {static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), kTM, 0, tmem,
                                 reinterpret_cast<const float*>(scales), C::kScaleBytes / 4, C::kSlots,
-                                acc_full, acc_empty, sempty, 0};
+                                acc_full, acc_empty, sempty, 0, nullptr};
     if (A.b_square)
       add_square<BN, false>(A, R, tiles_m, tiles_n, nkb);
     else
@@ -745,18 +814,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
 //
 // What bounds it: the way of a TMEM buffer, MMAs (512 clocks), commit, loads
 // by the adding warps (about 370), hand-over, and back; with two buffers a
-// step takes about 1000 clocks.  8192 x 11008 x 4096 with square blocks: 330 us,
-// 2.24 PFLOP/s (one CTA a tile 353 us); 8192 x 4096 x 11008: 302 us, 2.45.
-// Narrower tiles with more buffers cost more operand traffic than they save:
-// 256 x 192 388 us, 256 x 128 with four buffers 488 us.  Differences to the kernel above: the first CTA issues
+// step takes about 1000 clocks.  bf16 results leave through the copy engine
+// from shared memory, a tile's 64 KB under the next tile's first steps (threads
+// storing their rows took 2.7 us a tile).  8192 x 11008 x 4096 with square
+// blocks: 302 us, 2.44 PFLOP/s (threads storing 330, one CTA a tile 353);
+// 8192 x 4096 x 11008: 291 us, 2.54; 8192 x 5504 x 2048: 92 us, 2.01; with row
+// groups, 11008 x 4096 x 8192: 445 us, 1.66.  Narrower tiles with more buffers
+// cost more operand traffic than they save (before the change of stores): 256
+// x 192 388 us, 256 x 128 with four buffers 488 us.  Differences to the kernel above: the first CTA issues
 // the MMAs for both; its `full` barriers count both CTAs' copies; commits
 // arrive on both CTAs' `empty` and `acc_full`; both CTAs' adding warps hand
 // buffers back on the first one's `acc_empty`.  Two issuers take every other
 // step each: one waits for its barriers while the other's MMAs run.
 constexpr int kPN = 256;
 constexpr int kPairStage = kABytes + kPN / 2 * kTK;
-constexpr int kPairRing = 6, kPairSlots = 8, kPairScaleBytes = (kTM + kPN) * 4;
-constexpr int kPairSmem = kPairRing * kPairStage + kPairSlots * kPairScaleBytes + 1024 + 512;
+constexpr int kPairRing = 4, kPairSlots = 8, kPairScaleBytes = (kTM + kPN) * 4;
+constexpr int kPairSmem = kPairRing * kPairStage + 8 * kOutWarp + kPairSlots * kPairScaleBytes + 1024 + 512;
 
 __device__ __forceinline__ uint32_t steps_of(int first, int stride, int tiles, int nkb) {
   return first < tiles ? static_cast<uint32_t>((tiles - 1 - first) / stride + 1) * static_cast<uint32_t>(nkb) : 0u;
@@ -794,7 +867,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_fp8_gemm_pair(const __grid_constant__ Fp8GemmArgs A) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* scales = smem + kPairRing * kPairStage;
+  uint8_t* out = smem + kPairRing * kPairStage;
+  uint8_t* scales = out + 8 * kOutWarp;
   uint64_t* full = reinterpret_cast<uint64_t*>(scales + kPairSlots * kPairScaleBytes);
   uint64_t* empty = full + kPairRing;
   uint64_t* sfull = empty + kPairRing;
@@ -931,11 +1005,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
     const Adder<kPN, true> R = {first, stride, 2 * kTM, rank * kTM, tmem,
                                 reinterpret_cast<const float*>(scales), kPairScaleBytes / 4, kPairSlots,
-                                acc_full, acc_empty, sempty, mapa_shared(smem_u32(acc_empty), 0)};
+                                acc_full, acc_empty, sempty, mapa_shared(smem_u32(acc_empty), 0), out};
     if (A.b_square)
       add_square<kPN, true>(A, R, tiles_m, tiles_n, nkb);
     else
       add_rows<kPN, true>(A, R, tiles_m, tiles_n, nkb);
+    // shared memory is read until the stores are done
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
 
   __syncwarp();

@@ -111,7 +111,8 @@ cudaError_t launch_fp8_quantize(const QuantArgs& A, int dtype, int square, cudaS
 
 // --------------------------------------------------------------- product
 struct Fp8GemmArgs {
-  CUtensorMap amap, bmap;
+  CUtensorMap amap, bmap;  // codes: boxes of 128 columns
+  CUtensorMap omap;        // a bf16 output: boxes of 64 columns x 32 rows (tma_out)
   const uint8_t* a;
   const uint8_t* b;
   int64_t lda, ldb;
@@ -125,6 +126,7 @@ struct Fp8GemmArgs {
   int32_t out_dtype;
   int64_t ldo;
   int32_t accumulate;
+  int32_t tma_out;
   uint32_t* status;
 };
 // What a product of this size runs as.

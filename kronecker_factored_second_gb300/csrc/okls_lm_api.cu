@@ -312,6 +312,17 @@ okls_status okls_fp8_matmul(const void* a, int64_t lda, const float* a_scale, in
     LM_TRY(fp8_map(op, &A.amap, a, m, k, lda, P.box_a));
     LM_TRY(fp8_map(op, &A.bmap, b, n, k, ldb, P.box_b));
   }
+  // whole boxes of a bf16 output leave through the copy engine
+  if (P.pair && out_dtype == OKLS_BF16 && !accumulate && reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo % 8 == 0) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = host_encode_fn();
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(m)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldo) * 2};
+    cuuint32_t box[2] = {64, 32}, step[2] = {1, 1};
+    // (an output the map cannot describe is stored by the threads)
+    A.tma_out = fn(&A.omap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, box, step,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
   A.a = static_cast<const uint8_t*>(a), A.b = static_cast<const uint8_t*>(b);
   A.lda = lda, A.ldb = ldb;
   A.a_scale = a_scale, A.lda_row = lda_row, A.lda_group = lda_group;
