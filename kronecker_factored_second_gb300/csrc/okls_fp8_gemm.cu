@@ -7,16 +7,17 @@
 // e4m3, fp32 accumulators in TMEM); the scales change with every 128 of the
 // sum, so each partial product is taken out of TMEM, scaled and added to a
 // running sum in fp32 registers.  A persistent CTA per SM:
-//   warp 0 / lane 0  TMA producer: 128 x 128 A and BN x 128 B boxes (one
-//                    128-byte swizzle row per matrix row) into a ring;
-//   warp 1 / lane 0  MMA issuer: four K32 MMAs per stage into one of two TMEM
-//                    buffers, overwriting it;
+//   warp 0 / lane 0  TMA producer: 128 x 128 A and BN x 128 B boxes (BN 64 or
+//                    128 columns of the output; one 128-byte swizzle row per
+//                    matrix row) into a ring;
+//   warp 1 / lane 0  MMA issuer: four K32 MMAs per stage into one of the TMEM
+//                    buffers in turn, overwriting it;
 //   warp 2           copies each step's scales into a ring of their own, with
-//                    4-byte asynchronous copies that take any layout;
+//                    asynchronous copies that take any layout;
 //   warps 4-11       scale and add (add_square, add_rows), then store.
-// The two TMEM buffers let the additions of one step overlap the MMAs of the
-// next.  The running sums of a 128 x 256 tile take half of the SM's
-// registers, so the first four warps hand theirs to the other eight.
+// The TMEM buffers let the additions of one step overlap the MMAs of the
+// next.  The running sums of 128 x 256 results (CTA pairs, below) take half of
+// the SM's registers, so the first four warps hand theirs to the other eight.
 //
 // Every wait is bounded; when one expires the kernel raises kStTimeout and
 // runs to its end without further waits, apart from the bounded ones for its
@@ -51,7 +52,7 @@ template <int BN>
 struct Tile {
   static constexpr int kBBytes = BN * kTK;
   static constexpr int kBytes = kABytes + kBBytes;
-  static constexpr int kRing = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  static constexpr int kRing = BN == 128 ? 6 : 8;
   static constexpr int kCols = BN == 64 ? 256 : 512;  // TMEM columns: the buffers', up to a power of two
   static constexpr int kSlots = 8;                             // scale ring
   static constexpr int kScaleBytes = (kTM + BN) * 4;           // of one step
@@ -293,8 +294,9 @@ struct Steps {
   }
 };
 
-// 16 bf16 or 8 fp32 results of one row, 32 bytes a store: whole memory
-// sectors, although neighbouring lanes write different rows.
+// 16 bf16 or 8 fp32 results of one row (left: how many of them exist), 32 bytes
+// a store where the address allows: whole memory sectors, although neighbouring
+// lanes write different rows.  vec: the address is 16-byte aligned.
 __device__ __forceinline__ void store_bf16x16(const Fp8GemmArgs& A, __nv_bfloat16* p, int left, bool vec, float (&v)[16]) {
   if (vec && left >= 16) {
     if (A.accumulate) {
@@ -309,7 +311,12 @@ __device__ __forceinline__ void store_bf16x16(const Fp8GemmArgs& A, __nv_bfloat1
     uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-    store32(p, w);
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+      store32(p, w);
+    } else {
+      reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 16; ++j)
@@ -402,7 +409,7 @@ __device__ __forceinline__ void add_square(const Fp8GemmArgs& A, const Adder<BN,
     if (row >= A.m) continue;
     const int eb = A.out_dtype == kDtBf16 ? 2 : 4;
     char* o = static_cast<char*>(A.out) + (static_cast<int64_t>(row) * A.ldo + col0) * eb;
-    const bool vec = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
+    const bool vec = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
     if (A.out_dtype == kDtBf16) {
 #pragma unroll
       for (int c = 0; c < kCols; c += 16) {
@@ -1172,16 +1179,25 @@ cudaError_t run_gemm_pair(const Fp8GemmArgs& A, int num_sms, cudaStream_t st) {
 
 }  // namespace
 
-Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k, int num_sms) {
-  (void)k;
+// A step of a tile takes about the same time whatever its width, and a launch
+// as many tiles' times as its busiest SM (or pair) has tiles.  Measured at K =
+// 2048, us a step of one round, square blocks / row groups: CTA pairs 0.54 /
+// 0.77, 128 columns 0.47 / 0.52, 64 columns 0.40 / 0.42 (one CTA with 256
+// columns was never the best: 0.62 / 0.9).  512 x 5504 x 2048: pairs 13.6 us, 128
+// columns 18.8, 64 columns 22.8; 128 x 5504 x 2048: 13.3, 11.0, 10.0.
+Fp8Plan fp8_plan(int64_t m, int64_t n, bool b_square, int num_sms) {
   Fp8Plan P = {};
   P.skinny = m <= kSkinnyMax;
   P.box_a = kTM;
-  // 256 x 256 tiles of CTA pairs when there is one for every pair
-  P.pair = lm_div_up(m, 2 * kTM) * lm_div_up(n, kPN) >= num_sms / 2;
-  P.box_b = P.pair ? kPN / 2 : 256;
-  if (P.pair) return P;
-  while (P.box_b > 64 && lm_div_up(m, kTM) * lm_div_up(n, P.box_b) < num_sms) P.box_b /= 2;
+  auto cost = [&](int64_t tiles, int units, double square, double rows) {
+    return static_cast<double>(lm_div_up(tiles, units)) * (b_square ? square : rows);
+  };
+  const int64_t tm = lm_div_up(m, kTM);
+  const double pair = cost(lm_div_up(m, 2 * kTM) * lm_div_up(n, kPN), num_sms / 2, 0.54, 0.77);
+  const double wide = cost(tm * lm_div_up(n, 128), num_sms, 0.47, 0.52);
+  const double narrow = cost(tm * lm_div_up(n, 64), num_sms, 0.40, 0.42);
+  P.pair = pair <= wide && pair <= narrow;
+  P.box_b = P.pair ? kPN / 2 : wide <= narrow ? 128 : 64;
   return P;
 }
 
@@ -1203,7 +1219,6 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& A, const Fp8Plan& P, void* worksp
     return cudaGetLastError();
   }
   if (P.pair) return run_gemm_pair(A, num_sms, st);
-  if (P.box_b == 256) return run_gemm<256>(A, num_sms, st);
   if (P.box_b == 128) return run_gemm<128>(A, num_sms, st);
   return run_gemm<64>(A, num_sms, st);
 }

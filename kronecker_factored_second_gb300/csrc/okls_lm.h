@@ -135,7 +135,7 @@ struct Fp8Plan {
   bool pair;    // CTA pairs
   int box_a, box_b;
 };
-Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k, int num_sms);
+Fp8Plan fp8_plan(int64_t m, int64_t n, bool b_square, int num_sms);
 size_t fp8_workspace(int64_t m, int64_t n, int64_t k, int num_sms);
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& A, const Fp8Plan& P, void* workspace, int num_sms, cudaStream_t st);
 

@@ -302,7 +302,7 @@ okls_status okls_fp8_matmul(const void* a, int64_t lda, const float* a_scale, in
                                           static_cast<size_t>(n) * elem_size(out_dtype), static_cast<size_t>(m),
                                           static_cast<cudaStream_t>(stream)));
   }
-  const Fp8Plan P = fp8_plan(m, n, k, sms);
+  const Fp8Plan P = fp8_plan(m, n, b_block == OKLS_FP8_SQUARE, sms);
   Fp8GemmArgs A;
   memset(&A, 0, sizeof(A));
   // a single row's pitch is not used, but the map wants a multiple of 16

@@ -579,6 +579,27 @@ def test_linear_autograd_is_the_product_of_the_codes():
     _check_product(lm.fp8_quantize(G, transpose=True), lm.fp8_quantize(X, transpose=True), w.grad, BF16)
 
 
+def test_leading_dimensions_fold():
+    """Leading dimensions that step over one another are rows; others are refused, never copied."""
+    g = gen(15)
+    x = randn(g, 6, 5, 64, dtype=BF16)
+    w = randn(g, 64, dtype=BF16)
+    wide = torch.zeros(6, 5, 80, dtype=BF16, device="cuda")
+    wide[..., :64] = x
+    want = lm.rms_norm(x.view(30, 64), w)
+    for v in (x, wide[..., :64]):
+        out = lm.rms_norm(v, w)
+        assert out.y.shape == v.shape and torch.equal(out.y.reshape(30, 64), want.y)
+    assert torch.equal(lm.rms_norm(x[2], w).y, want.y[10:15])
+    assert torch.equal(lm.rms_norm(x[:, 3:4], w).y.reshape(6, 64), want.y[3::5])
+    ids = torch.randint(0, 64, (6, 5), generator=g, device="cuda")
+    assert torch.equal(lm.token_logprobs(wide[..., :64], ids).logp, lm.token_logprobs(x.view(30, 64), ids.view(30)).logp.view(6, 5))
+    for v in (x.transpose(0, 1), x[:, :4], torch.zeros((), device="cuda")):
+        with pytest.raises(ValueError):
+            lm.rms_norm(v, w)
+            pytest.fail("a layout that does not fold was taken")
+
+
 # ---------------------------------------------------------------- refusals
 def test_refusals():
     f = torch.float16
