@@ -526,6 +526,42 @@ def test_other_stream_gives_the_same_bits():
         assert torch.equal(a, b)
 
 
+def test_calls_can_be_captured():
+    """A captured chain of all operators, replayed on new inputs, gives what the calls give."""
+    g = gen(16)
+    x, dy = randn(g, 400, 256, dtype=BF16), randn(g, 400, 256, dtype=BF16)
+    w, nw = randn(g, 600, 256, dtype=BF16, std=0.05), randn(g, 256, dtype=BF16)
+    ids = torch.randint(-1, 600, (400,), generator=g, device="cuda")
+    gl = randn(g, 400)
+
+    def chain():
+        h = lm.embedding(w, ids, scale=2.0)
+        n = lm.rms_norm(x, nw, residual=h)
+        q, qt = lm.fp8_quantize(n.y, both=True)
+        z = lm.fp8_matmul(q, lm.fp8_quantize(w, block="square"))
+        r = lm.token_logprobs(z, ids, top_k=5)
+        dz = lm.token_logprobs_grad(z, ids, r, gl, dentropy=gl)
+        dw = lm.fp8_matmul(lm.fp8_quantize(dz, transpose=True), qt)
+        ds, dn = lm.rms_norm_grad(dy, n.residual, nw, n.rstd, dresidual=x)
+        return z, r.logp, r.top_ids, dz, dw, ds, dn, lm.embedding_grad(ds, ids, 600)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        chain()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = chain()
+    for seed in (1, 2):
+        h = gen(seed)
+        x.copy_(randn(h, 400, 256, dtype=BF16))
+        ids.copy_(torch.randint(-1, 600, (400,), generator=h, device="cuda"))
+        graph.replay()
+        for a, b in zip(captured, chain()):
+            assert torch.equal(a, b)
+
+
 def test_autograd_against_differences():
     """Directional differences of the loss through embed, norm and logprobs in fp32."""
     g = gen(13)
