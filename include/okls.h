@@ -599,15 +599,12 @@ okls_status okls_fp8_quantize(const void *x, int32_t dtype, int64_t ldx,
  * Row pitches lda and ldb are multiples of 16 bytes and the bases 16-byte
  * aligned (OKLS_ERR_UNSUPPORTED otherwise); m, n, k are any size.
  */
-okls_status okls_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k,
-                                            size_t *workspace_bytes);
 okls_status okls_fp8_matmul(const void *a, int64_t lda, const float *a_scale,
                             int64_t lda_row, int64_t lda_group, const void *b,
                             int64_t ldb, const float *b_scale, int64_t ldb_row,
                             int64_t ldb_group, int32_t b_block, int64_t m,
                             int64_t n, int64_t k, void *out,
                             int32_t out_dtype, int64_t ldo, int32_t accumulate,
-                            void *workspace, size_t workspace_bytes,
                             uint32_t *status_dev, void *stream);
 
 /*

@@ -139,9 +139,8 @@ _SIGS = {
                                   _P, _P, _SZ, _P]),
     "okls_fp8_quantize": (_I32, [_P, _I32, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64,
                                  _I64, _P]),
-    "okls_fp8_matmul_workspace_bytes": (_I32, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
     "okls_fp8_matmul": (_I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _I32, _I64, _I64, _I64, _P,
-                               _I32, _I64, _I32, _P, _SZ, _P, _P]),
+                               _I32, _I64, _I32, _P, _P]),
     "okls_token_logprobs": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _I64, _F, _I32, _P, _P, _P, _P, _P, _P, _P]),
     "okls_token_logprobs_grad": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _I64, _F, _P, _P, _P, _P, _P, _I64, _P]),
 }

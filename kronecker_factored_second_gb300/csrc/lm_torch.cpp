@@ -218,12 +218,9 @@ Tensor fp8_matmul(const Tensor& a, const Tensor& as, const Tensor& b, const Tens
     o = {out->data_ptr(), m, n, n};
   }
   const int od = float_code(out->scalar_type(), "the output type");
-  size_t need = 0;
-  check(okls_fp8_matmul_workspace_bytes(m, n, k, &need));
-  Tensor ws = c.workspace(need);
   check(okls_fp8_matmul(a.data_ptr(), a.stride(0), as.data_ptr<float>(), as.stride(0), as.stride(1), b.data_ptr(), b.stride(0),
                         bs.data_ptr<float>(), bs.stride(0), bs.stride(1), b_square ? OKLS_FP8_SQUARE : OKLS_FP8_ROW, m, n, k,
-                        o.p, od, o.ld, accumulate, ptr_of(ws), need, status_of(a), c.stream()));
+                        o.p, od, o.ld, accumulate, status_of(a), c.stream()));
   return *out;
 }
 

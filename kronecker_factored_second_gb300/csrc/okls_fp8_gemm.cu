@@ -1201,13 +1201,7 @@ Fp8Plan fp8_plan(int64_t m, int64_t n, bool b_square, int num_sms) {
   return P;
 }
 
-size_t fp8_workspace(int64_t m, int64_t n, int64_t k, int num_sms) {
-  (void)m, (void)n, (void)k, (void)num_sms;
-  return 0;
-}
-
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& A, const Fp8Plan& P, void* workspace, int num_sms, cudaStream_t st) {
-  (void)workspace;
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& A, const Fp8Plan& P, int num_sms, cudaStream_t st) {
   if (P.skinny) {
     const int grid = static_cast<int>(lm_div_up(A.n, 16)), threads = kSkinnyWarps * 32;
     if (A.m <= 8)

@@ -48,7 +48,7 @@ struct EmbedGradArgs {
   uint32_t* status;
 };
 size_t embedding_grad_workspace(int64_t tokens, int64_t vocab, int64_t dim);
-cudaError_t launch_embedding_grad(const EmbedGradArgs& A, int dy_dtype, int out_dtype, void* workspace, int num_sms,
+cudaError_t launch_embedding_grad(const EmbedGradArgs& A, int dy_dtype, int out_dtype, void* workspace,
                                   cudaStream_t st);
 
 // ------------------------------------------------------------------ norm
@@ -136,8 +136,7 @@ struct Fp8Plan {
   int box_a, box_b;
 };
 Fp8Plan fp8_plan(int64_t m, int64_t n, bool b_square, int num_sms);
-size_t fp8_workspace(int64_t m, int64_t n, int64_t k, int num_sms);
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& A, const Fp8Plan& P, void* workspace, int num_sms, cudaStream_t st);
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& A, const Fp8Plan& P, int num_sms, cudaStream_t st);
 
 // ----------------------------------------------------- log probabilities
 struct ScoreArgs {
@@ -171,6 +170,6 @@ struct ScoreGradArgs {
   void* dlogits;
   int64_t ldd;
 };
-cudaError_t launch_token_logprobs_grad(const ScoreGradArgs& A, int dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_token_logprobs_grad(const ScoreGradArgs& A, int dtype, cudaStream_t st);
 
 }  // namespace okls

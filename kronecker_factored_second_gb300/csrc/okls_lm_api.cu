@@ -136,7 +136,7 @@ okls_status okls_embedding_grad(const void* dy, int32_t dy_dtype, int64_t lddy, 
   int sms = 0;
   LM_TRY(host_device_sms(&sms));
   EmbedGradArgs A = {dy, lddy, ids, ids_i64, tokens, vocab, dim, scale, base, ldbase, out, ldo, status_dev};
-  return launched(op, launch_embedding_grad(A, dy_dtype, out_dtype, workspace, sms, static_cast<cudaStream_t>(stream)));
+  return launched(op, launch_embedding_grad(A, dy_dtype, out_dtype, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------------------------ norm
@@ -242,16 +242,6 @@ static okls_status check_product(const char* op, int64_t m, int64_t n, int64_t k
   return OKLS_OK;
 }
 
-okls_status okls_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, size_t* workspace_bytes) {
-  const char* op = "okls_fp8_matmul_workspace_bytes";
-  if (!workspace_bytes) return bad(op, "workspace_bytes is NULL");
-  LM_TRY(check_product(op, m, n, k));
-  int sms = 0;
-  LM_TRY(host_device_sms(&sms));
-  *workspace_bytes = fp8_workspace(m, n, k, sms);
-  return OKLS_OK;
-}
-
 // 2-D map of an e4m3 matrix: boxes of 128 columns x box_rows rows in 128-byte
 // swizzled rows; what lies outside the matrix arrives as zeros.
 static okls_status fp8_map(const char* op, CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld,
@@ -273,8 +263,7 @@ static okls_status fp8_map(const char* op, CUtensorMap* map, const void* p, int6
 okls_status okls_fp8_matmul(const void* a, int64_t lda, const float* a_scale, int64_t lda_row, int64_t lda_group,
                             const void* b, int64_t ldb, const float* b_scale, int64_t ldb_row, int64_t ldb_group,
                             int32_t b_block, int64_t m, int64_t n, int64_t k, void* out, int32_t out_dtype,
-                            int64_t ldo, int32_t accumulate, void* workspace, size_t workspace_bytes,
-                            uint32_t* status_dev, void* stream) {
+                            int64_t ldo, int32_t accumulate, uint32_t* status_dev, void* stream) {
   const char* op = "okls_fp8_matmul";
   if (!float_dtype(out_dtype)) return bad(op, "out_dtype must be fp32 or bf16");
   if (b_block != OKLS_FP8_ROW && b_block != OKLS_FP8_SQUARE)
@@ -294,7 +283,6 @@ okls_status okls_fp8_matmul(const void* a, int64_t lda, const float* a_scale, in
                      static_cast<ll>(lda), static_cast<ll>(ldb));
   int sms = 0;
   LM_TRY(host_device_sms(&sms));
-  LM_TRY(check_workspace(op, workspace, workspace_bytes, fp8_workspace(m, n, k, sms)));
   if (k == 0) {
     // an empty sum: zeros, or nothing to add
     if (accumulate) return OKLS_OK;
@@ -331,7 +319,7 @@ okls_status okls_fp8_matmul(const void* a, int64_t lda, const float* a_scale, in
   A.m = static_cast<int32_t>(m), A.n = static_cast<int32_t>(n), A.k = static_cast<int32_t>(k);
   A.out = out, A.out_dtype = out_dtype, A.ldo = ldo, A.accumulate = accumulate;
   A.status = status_dev;
-  return launched(op, launch_fp8_gemm(A, P, workspace, sms, static_cast<cudaStream_t>(stream)));
+  return launched(op, launch_fp8_gemm(A, P, sms, static_cast<cudaStream_t>(stream)));
 }
 
 // ----------------------------------------------------- log probabilities
@@ -373,7 +361,7 @@ okls_status okls_token_logprobs_grad(const void* logits, int32_t dtype, int64_t 
   int sms = 0;
   LM_TRY(host_device_sms(&sms));
   ScoreGradArgs A = {logits, ldl, ids, ids_i64, rows, vocab, scale, lse, entropy, dlogp, dentropy, dlogits, ldd};
-  return launched(op, launch_token_logprobs_grad(A, dtype, sms, static_cast<cudaStream_t>(stream)));
+  return launched(op, launch_token_logprobs_grad(A, dtype, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -533,9 +533,8 @@ size_t embedding_grad_workspace(int64_t tokens, int64_t vocab, int64_t dim) {
   return plan_grad(tokens, vocab, dim).total;
 }
 
-cudaError_t launch_embedding_grad(const EmbedGradArgs& A, int dy_dtype, int out_dtype, void* workspace, int num_sms,
+cudaError_t launch_embedding_grad(const EmbedGradArgs& A, int dy_dtype, int out_dtype, void* workspace,
                                   cudaStream_t st) {
-  (void)num_sms;
   const GradPlan g = plan_grad(A.tokens, A.vocab, A.dim);
   char* ws = static_cast<char*>(workspace);
   ReduceArgs R = {};

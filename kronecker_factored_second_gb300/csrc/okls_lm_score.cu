@@ -741,8 +741,7 @@ cudaError_t launch_token_logprobs(const ScoreArgs& A, int dtype, int num_sms, cu
   return dtype == kDtBf16 ? score_of<__nv_bfloat16>(A, num_sms, st) : score_of<float>(A, num_sms, st);
 }
 
-cudaError_t launch_token_logprobs_grad(const ScoreGradArgs& A, int dtype, int num_sms, cudaStream_t st) {
-  (void)num_sms;
+cudaError_t launch_token_logprobs_grad(const ScoreGradArgs& A, int dtype, cudaStream_t st) {
   if (A.rows <= 0) return cudaSuccess;
   return dtype == kDtBf16 ? grad_of_rows<__nv_bfloat16>(A, st) : grad_of_rows<float>(A, st);
 }

@@ -69,10 +69,10 @@ def test_fp8_arguments(lib):
     refused(ok, [({0: None}, BAD), ({1: 2}, BAD), ({2: 1}, BAD), ({3: -1}, BAD), ({5: 2}, BAD), ({6: None, 8: None}, BAD),
                  ({8: None}, BAD), ({6: None}, BAD), ({7: 32}, BAD), ({11: P, 12: 2, 13: P}, BAD), ({11: P}, BAD),
                  ({9: -1}, BAD), ({3: 1 << 25}, UNSUP)], lib.okls_fp8_quantize)
-    ok = [P, 128, P, 1, 12, P, 128, P, 1, 12, 1, 10, 20, 64, P, 1, 20, 0, None, 0, P, None]
+    ok = [P, 128, P, 1, 12, P, 128, P, 1, 12, 1, 10, 20, 64, P, 1, 20, 0, P, None]
     refused(ok, [({0: None}, BAD), ({1: 32}, BAD), ({1: 136}, UNSUP), ({0: P + 8}, UNSUP), ({5: P + 8}, UNSUP),
                  ({2: None}, BAD), ({7: None}, BAD), ({3: -1}, BAD), ({10: 2}, BAD), ({11: -1}, BAD), ({14: None}, BAD),
-                 ({14: P + 1}, BAD), ({15: 2}, BAD), ({16: 10}, BAD), ({17: 2}, BAD), ({20: None}, BAD)],
+                 ({14: P + 1}, BAD), ({15: 2}, BAD), ({16: 10}, BAD), ({17: 2}, BAD), ({18: None}, BAD)],
             lib.okls_fp8_matmul)
     # nothing to compute: taken without a device
     assert lib.okls_fp8_matmul(*[0 if i in (11,) else v for i, v in enumerate(ok)]) == L.OKLS_OK
