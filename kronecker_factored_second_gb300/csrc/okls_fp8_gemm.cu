@@ -24,6 +24,7 @@
 // own copies and MMAs.
 #include <cuda_fp16.h>
 
+#include "okls_fp8_layout.h"
 #include "okls_internal.h"
 #include "okls_lm.cuh"
 #include "okls_ptx.cuh"
@@ -31,33 +32,9 @@
 namespace okls {
 namespace {
 
-constexpr int kTM = 128;         // output rows of a tile
-constexpr int kTK = 128;         // depth of a stage: one scale group
-constexpr int kThreads = 384;    // 4 control warps, 8 that scale and add
-constexpr int kCtlRegs = 40, kAddRegs = 232;
-static_assert(128 * kCtlRegs + 256 * kAddRegs <= kThreads * 168, "more registers than the launch holds");
-constexpr int kABytes = kTM * kTK;
-
-// TMEM buffers of a BN-column step: a power of two, as many as the 512 columns
-// hold, at most 4.
-template <int BN>
-struct Buffers {
-  static constexpr int kLog = BN > 128 ? 1 : 2;
-  static constexpr int kCount = 1 << kLog;
-  __host__ __device__ static constexpr uint32_t at(uint32_t it) { return it & (kCount - 1); }
-  __host__ __device__ static constexpr uint32_t parity(uint32_t it) { return (it >> kLog) & 1u; }
-};
-
-template <int BN>
-struct Tile {
-  static constexpr int kBBytes = BN * kTK;
-  static constexpr int kBytes = kABytes + kBBytes;
-  static constexpr int kRing = BN == 128 ? 6 : 8;
-  static constexpr int kCols = BN == 64 ? 256 : 512;  // TMEM columns: the buffers', up to a power of two
-  static constexpr int kSlots = 8;                             // scale ring
-  static constexpr int kScaleBytes = (kTM + BN) * 4;           // of one step
-  static constexpr int kSmem = kRing * kBytes + kSlots * kScaleBytes + 1024 + 256;
-};
+__device__ __forceinline__ uint8_t* smem_base(uint8_t* raw) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + kSmemAlign - 1) & ~uintptr_t(kSmemAlign - 1));
+}
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1) {
   asm volatile(
@@ -217,8 +194,6 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 // Results of a warp's 32 rows x 128 columns in bf16 on their way out: two boxes
 // of 64 columns (128 bytes a row, 128-byte swizzle) in shared memory, which the
 // copy engine stores while the warp goes on with the next tile.
-constexpr int kOutBox = 32 * 128;
-constexpr int kOutWarp = 2 * kOutBox;
 __device__ __forceinline__ void out_chunk(uint8_t* mine, int row, int chunk, uint4 v) {
   // chunk: 8 columns; the 16-byte positions of a row are permuted by the row
   *reinterpret_cast<uint4*>(mine + (chunk >> 3) * kOutBox + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = v;
@@ -679,7 +654,7 @@ template <int BN>
 __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant__ Fp8GemmArgs A) {
   using C = Tile<BN>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_base(smem_raw);
   uint8_t* scales = smem + C::kRing * C::kBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(scales + C::kSlots * C::kScaleBytes);
   uint64_t* empty = full + C::kRing;
@@ -833,10 +808,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
 // arrive on both CTAs' `empty` and `acc_full`; both CTAs' adding warps hand
 // buffers back on the first one's `acc_empty`.  Two issuers take every other
 // step each: one waits for its barriers while the other's MMAs run.
-constexpr int kPN = 256;
-constexpr int kPairStage = kABytes + kPN / 2 * kTK;
-constexpr int kPairRing = 4, kPairSlots = 8, kPairScaleBytes = (kTM + kPN) * 4;
-constexpr int kPairSmem = kPairRing * kPairStage + 8 * kOutWarp + kPairSlots * kPairScaleBytes + 1024 + 512;
 
 __device__ __forceinline__ uint32_t steps_of(int first, int stride, int tiles, int nkb) {
   return first < tiles ? static_cast<uint32_t>((tiles - 1 - first) / stride + 1) * static_cast<uint32_t>(nkb) : 0u;
@@ -873,7 +844,7 @@ __device__ __forceinline__ void umma_f8_step_pair(uint32_t d, uint64_t adesc, ui
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_fp8_gemm_pair(const __grid_constant__ Fp8GemmArgs A) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_base(smem_raw);
   uint8_t* out = smem + kPairRing * kPairStage;
   uint8_t* scales = out + 8 * kOutWarp;
   uint64_t* full = reinterpret_cast<uint64_t*>(scales + kPairSlots * kPairScaleBytes);
