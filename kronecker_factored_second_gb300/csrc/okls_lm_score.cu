@@ -178,7 +178,11 @@ __device__ __forceinline__ V sort_lanes(V v, int lane) {
 template <class T, int N, int W>
 __device__ __forceinline__ void offer(Best& B, const float (&z)[N], float vm, int count, const T* row, uint32_t col,
                                       uint32_t stride, int lane, int k, Key* cta_bound) {
-  const Key shared = *reinterpret_cast<volatile Key*>(cta_bound);
+  // one lane reads it for the warp: other warps raise it at any time, and the
+  // steps below need every lane to hold the same bound
+  Key shared = 0;
+  if (lane == 0) shared = *reinterpret_cast<volatile Key*>(cta_bound);
+  shared = __shfl_sync(0xffffffffu, shared, 0);
   if (shared > B.bound) {
     B.bound = shared;
     B.bound_v = ord_value(static_cast<uint32_t>(shared >> 32));

@@ -1,0 +1,49 @@
+"""What the language-model operators promise beyond their formulas, on the GPU: equal results whatever warps run first,
+arguments that outlive a call, gradients that refuse what they cannot give, in-place writes that autograd sees."""
+
+import pytest
+import torch
+
+from kronecker_factored_second_gb300 import _lib as L
+from kronecker_factored_second_gb300 import lm
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    L.lib()
+    torch.cuda.set_device(0)
+    lm.query_status()
+    yield
+    assert lm.query_status() == 0
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape, dtype=F32, std=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,vocab", [(3, 131072), (600, 20000), (40, 300000)])
+def test_alternatives_among_many_equal_logits(dtype, rows, vocab):
+    """Rows in which thousands of columns share the best values, so that every warp inserts into its list and raises the
+    bound that the CTA's warps share: the alternatives are the same, call after call."""
+    g = gen(vocab)
+    z = torch.randint(0, 3, (rows, vocab), generator=g, device="cuda").to(dtype)
+    z[1::3] = torch.arange(vocab, device="cuda").to(dtype) % 128  # a new best value with every column up to 127
+    ids = torch.zeros(rows, dtype=torch.long, device="cuda")
+    for k in (1, 9, 32):
+        want = torch.sort(z.float(), dim=-1, descending=True, stable=True)[1][:, :k].int()
+        for _ in range(5):
+            assert torch.equal(lm.token_logprobs(z, ids, top_k=k).top_ids, want)
