@@ -35,6 +35,12 @@ okls_status check_mat(const char* op, const char* name, const void* p, int64_t r
   return OKLS_OK;
 }
 
+// A vector of 4-byte elements that may be absent.
+okls_status check_vec(const char* op, const char* name, const void* p) {
+  if (reinterpret_cast<uintptr_t>(p) % 4 == 0) return OKLS_OK;
+  return host_fail(OKLS_ERR_INVALID_ARG, "%s: %s is not aligned to its 4-byte elements", op, name);
+}
+
 #define LM_TRY(call)                   \
   do {                                 \
     const okls_status s_ = (call);     \
@@ -49,6 +55,11 @@ okls_status launched(const char* op, cudaError_t e) {
 okls_status check_ids(const char* op, const void* ids, int32_t ids_i64, int64_t count) {
   if (ids_i64 != 0 && ids_i64 != 1) return bad(op, "ids_i64 must be 0 or 1");
   return check_mat(op, "ids", ids, 1, count, count, ids_i64 ? 8 : 4);
+}
+
+okls_status check_status(const char* op, const uint32_t* status_dev) {
+  if (!status_dev) return bad(op, "status_dev is NULL");
+  return check_vec(op, "status_dev", status_dev);
 }
 
 okls_status check_workspace(const char* op, const void* ws, size_t have, size_t need) {
@@ -67,7 +78,7 @@ constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 extern "C" {
 
 okls_status okls_status_word_read(uint32_t* status_dev, void* stream, uint32_t* dev_status) {
-  if (!status_dev) return bad("okls_status_word_read", "status_dev is NULL");
+  LM_TRY(check_status("okls_status_word_read", status_dev));
   uint32_t v = 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemcpyAsync(&v, status_dev, sizeof(v), cudaMemcpyDeviceToHost, st);
@@ -88,7 +99,7 @@ okls_status okls_embedding(const void* weight, int32_t weight_dtype, int64_t ldw
   if (!float_dtype(weight_dtype) || !float_dtype(out_dtype)) return bad(op, "dtypes must be fp32 or bf16");
   if (vocab < 1 || dim < 1 || tokens < 0) return bad(op, "vocab and dim must be positive, tokens non-negative");
   if (vocab > kMaxSide || dim > kMaxSide || tokens > kMaxSide) return bad(op, "sizes must be below 2^31");
-  if (!status_dev) return bad(op, "status_dev is NULL");
+  LM_TRY(check_status(op, status_dev));
   LM_TRY(check_mat(op, "weight", weight, vocab, dim, ldw, elem_size(weight_dtype)));
   LM_TRY(check_ids(op, ids, ids_i64, tokens));
   LM_TRY(check_mat(op, "out", out, tokens, dim, ldo, elem_size(out_dtype)));
@@ -126,7 +137,7 @@ okls_status okls_embedding_grad(const void* dy, int32_t dy_dtype, int64_t lddy, 
   const char* op = "okls_embedding_grad";
   if (!float_dtype(dy_dtype) || !float_dtype(out_dtype)) return bad(op, "dtypes must be fp32 or bf16");
   LM_TRY(check_grad_sizes(op, tokens, vocab, dim));
-  if (!status_dev) return bad(op, "status_dev is NULL");
+  LM_TRY(check_status(op, status_dev));
   LM_TRY(check_mat(op, "dy", dy, tokens, dim, lddy, elem_size(dy_dtype)));
   LM_TRY(check_ids(op, ids, ids_i64, tokens));
   LM_TRY(check_mat(op, "out", out, vocab, dim, ldo, elem_size(out_dtype)));
@@ -163,6 +174,8 @@ okls_status okls_rms_norm(const void* x, int32_t dtype, int64_t ldx, const void*
   if ((out_dtype == OKLS_E4M3) != (out_scale != nullptr) && rows > 0)
     return bad(op, "out_scale belongs to an e4m3 output, and to no other");
   if (out_scale && (lds_row < 0 || lds_group < 0)) return bad(op, "negative scale pitch");
+  LM_TRY(check_vec(op, "out_scale", out_scale));
+  LM_TRY(check_vec(op, "rstd", rstd));
   int sms = 0;
   LM_TRY(host_device_sms(&sms));
   NormArgs A = {x,   ldx,       residual, ldr,       weight,  weight_dtype, rows,    static_cast<int32_t>(dim), eps,
@@ -224,6 +237,8 @@ okls_status okls_fp8_quantize(const void* x, int32_t dtype, int64_t ldx, int64_t
   if (q) LM_TRY(check_mat(op, "q", q, rows, cols, ldq, 1));
   if (qt) LM_TRY(check_mat(op, "qt", qt, cols, rows, ldqt, 1));
   if (lds_row < 0 || lds_group < 0 || ldst_row < 0 || ldst_group < 0) return bad(op, "negative scale pitch");
+  LM_TRY(check_vec(op, "scale", scale));
+  LM_TRY(check_vec(op, "scale_t", scale_t));
   if (lm_div_up(rows, kFp8Group) > 65535)
     return host_fail(OKLS_ERR_UNSUPPORTED, "%s: more than 65535 blocks of 128 rows", op);
   int sms = 0;
@@ -270,12 +285,14 @@ okls_status okls_fp8_matmul(const void* a, int64_t lda, const float* a_scale, in
     return bad(op, "b_block must be OKLS_FP8_ROW or OKLS_FP8_SQUARE");
   if (accumulate != 0 && accumulate != 1) return bad(op, "accumulate must be 0 or 1");
   LM_TRY(check_product(op, m, n, k));
-  if (!status_dev) return bad(op, "status_dev is NULL");
+  LM_TRY(check_status(op, status_dev));
   LM_TRY(check_mat(op, "a", a, m, k, lda, 1));
   LM_TRY(check_mat(op, "b", b, n, k, ldb, 1));
   LM_TRY(check_mat(op, "out", out, m, n, ldo, elem_size(out_dtype)));
   if (m == 0 || n == 0) return OKLS_OK;
   if (k > 0 && (!a_scale || !b_scale)) return bad(op, "a scale is NULL");
+  LM_TRY(check_vec(op, "a_scale", a_scale));
+  LM_TRY(check_vec(op, "b_scale", b_scale));
   if (lda_row < 0 || lda_group < 0 || ldb_row < 0 || ldb_group < 0) return bad(op, "negative scale pitch");
   if (k > 0 && (reinterpret_cast<uintptr_t>(a) % 16 || reinterpret_cast<uintptr_t>(b) % 16 ||
                 (m > 1 && lda % 16) || (n > 1 && ldb % 16)))
@@ -332,10 +349,15 @@ okls_status okls_token_logprobs(const void* logits, int32_t dtype, int64_t ldl, 
   if (rows > kMaxGrid / 8) return bad(op, "rows must be below 2^28");
   if (!(scale > 0.0f) || std::isinf(scale)) return bad(op, "scale must be positive and finite");
   if (top_k < 0 || top_k > 32 || top_k > vocab) return bad(op, "top_k must be in [0, min(vocab, 32)]");
-  if (!status_dev) return bad(op, "status_dev is NULL");
+  LM_TRY(check_status(op, status_dev));
   LM_TRY(check_mat(op, "logits", logits, rows, vocab, ldl, elem_size(dtype)));
   if (logp) LM_TRY(check_ids(op, ids, ids_i64, rows));
   if (top_k > 0 && rows > 0 && (!top_ids || !top_logp)) return bad(op, "top_ids and top_logp are needed for top_k > 0");
+  LM_TRY(check_vec(op, "logp", logp));
+  LM_TRY(check_vec(op, "entropy", entropy));
+  LM_TRY(check_vec(op, "lse", lse));
+  LM_TRY(check_vec(op, "top_ids", top_ids));
+  LM_TRY(check_vec(op, "top_logp", top_logp));
   int sms = 0;
   LM_TRY(host_device_sms(&sms));
   ScoreArgs A = {logits, ldl, ids, ids_i64, rows, vocab, scale, top_k, logp, entropy, lse, top_ids, top_logp, status_dev};
@@ -356,6 +378,8 @@ okls_status okls_token_logprobs_grad(const void* logits, int32_t dtype, int64_t 
   LM_TRY(check_mat(op, "lse", lse, 1, rows, rows, 4));
   LM_TRY(check_mat(op, "dlogp", dlogp, 1, rows, rows, 4));
   if (dentropy && !entropy) return bad(op, "dentropy needs entropy");
+  LM_TRY(check_vec(op, "entropy", entropy));
+  LM_TRY(check_vec(op, "dentropy", dentropy));
   if (lm_div_up(vocab, 8192) > kMaxGrid / (rows > 0 ? rows : 1))
     return host_fail(OKLS_ERR_UNSUPPORTED, "%s: rows x vocab is too large for one launch", op);
   int sms = 0;
