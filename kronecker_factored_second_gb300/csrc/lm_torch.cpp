@@ -200,15 +200,26 @@ std::tuple<Tensor, Tensor, Tensor, Tensor> fp8_quantize(const Tensor& x, bool sq
   return {q, s, qt, st};
 }
 
+// The kernels read one scale for each 128 x 1 or 128 x 128 of the codes, so
+// the fields of an Fp8Tensor, which a caller can assign, are checked here again.
+void check_fp8(const Tensor& q, const Tensor& s, bool square, const char* name) {
+  REFUSE(!q.is_cuda(), "tensors must be on a CUDA device");
+  REFUSE(q.dim() != 2 || q.scalar_type() != at::kFloat8_e4m3fn, name, " must be a matrix of float8_e4m3fn");
+  REFUSE(q.numel() != 0 && q.size(1) > 1 && q.stride(1) != 1, "the last dimension of ", name, " must be contiguous");
+  const int64_t lines = square ? (q.size(0) + kGroup - 1) / kGroup : q.size(0), groups = (q.size(1) + kGroup - 1) / kGroup;
+  REFUSE(s.dim() != 2 || s.scalar_type() != at::kFloat || s.size(0) != lines || s.size(1) != groups, "the scale of ", name,
+         " must be fp32 of shape (", lines, ", ", groups, ")");
+  same_device(q, s);
+}
+
 Tensor fp8_matmul(const Tensor& a, const Tensor& as, const Tensor& b, const Tensor& bs, bool b_square, Maybe out,
                   at::ScalarType out_dtype, bool accumulate) {
+  check_fp8(a, as, false, "the first factor");
+  check_fp8(b, bs, b_square, "the second factor");
   const int64_t m = a.size(0), k = a.size(1), n = b.size(0);
   REFUSE(b.size(1) != k, "sums of length ", k, " and ", b.size(1));
   REFUSE(accumulate && !out, "accumulate needs out");
-  REFUSE(!a.is_cuda(), "tensors must be on a CUDA device");
-  same_device(a, as);
   same_device(a, b);
-  same_device(a, bs);
   same_device(a, out);
   Mat o = {};
   if (out) o = plain_matrix(*out, "out", m, n);

@@ -47,3 +47,26 @@ def test_alternatives_among_many_equal_logits(dtype, rows, vocab):
         want = torch.sort(z.float(), dim=-1, descending=True, stable=True)[1][:, :k].int()
         for _ in range(5):
             assert torch.equal(lm.token_logprobs(z, ids, top_k=k).top_ids, want)
+
+
+def test_reassigned_fields_of_8_bit_tensors_are_checked():
+    """An Fp8Tensor's fields can be assigned; scales that do not cover the codes are refused, not read past their end."""
+    x = randn(gen(1), 300, 520)
+    good = lm.fp8_quantize(x)
+    want = lm.fp8_matmul(good, lm.fp8_quantize(x, block="square"))
+    changes = [dict(scale=good.scale[:299]), dict(scale=good.scale[:, :4]), dict(scale=good.scale.double()),
+               dict(scale=good.scale.cpu()), dict(scale=good.scale[0]), dict(data=x), dict(data=good.data.t()),
+               dict(data=torch.cat([good.data.view(torch.uint8)] * 2).view(E4M3)), dict(data=good.data.cpu())]
+    for i, change in enumerate(changes):
+        for first in (True, False):
+            f = lm.fp8_quantize(x)
+            for name, v in change.items():
+                setattr(f, name, v)
+            with pytest.raises(ValueError):
+                lm.fp8_matmul(*((f, good) if first else (good, f)))
+                pytest.fail(f"change {i} was taken")
+    f = lm.fp8_quantize(x)
+    f.block = "square"
+    with pytest.raises(ValueError):
+        lm.fp8_matmul(good, f)
+    assert torch.equal(lm.fp8_matmul(good, lm.fp8_quantize(x, block="square")), want)
