@@ -339,6 +339,7 @@ Tensor token_logprobs_grad(const Tensor& logits, const Tensor& ids, const Tensor
   same_device(logits, lse);
   same_device(logits, dlogp);
   same_device(logits, dentropy);
+  if (dentropy) same_device(logits, entropy);
   Call c(logits);
   Tensor d = inplace ? logits : c.empty(logits.sizes(), logits.scalar_type());
   check(okls_token_logprobs_grad(z.p, dt, z.ld, ids.data_ptr(), i64, z.rows, z.cols, static_cast<float>(scale), l, e, g, h,
