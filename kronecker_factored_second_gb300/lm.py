@@ -19,8 +19,12 @@ the vocabulary is treated as padding and recorded in the device's status
 word, which `query_status` reads.
 
 Every function runs on the current stream, or on `stream`.  Outputs and
-scratch come from torch's allocator on that stream.  No call synchronises,
-apart from `query_status`.
+scratch come from torch's allocator on that stream.  A call on another
+`stream` does not wait for the work that makes its inputs, nor does the
+current stream wait for its outputs: order the two streams as for any torch
+call.  The inputs' memory stays theirs until `stream` has passed the call;
+outputs used on another stream are the caller's to record there.  No call
+synchronises, apart from `query_status`.
 """
 
 from __future__ import annotations
@@ -51,6 +55,15 @@ def _n():
     return _NATIVE
 
 
+def _on(stream, *tensors):
+    """The context of a call on `stream`.  The allocator is told that the inputs are used there, so that a caller who
+    lets go of one does not have its memory handed out while the call still reads it."""
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            t.record_stream(stream)
+    return torch.cuda.stream(stream)
+
+
 def query_status(device=None, stream=None) -> int:
     """Synchronise the stream and return (and clear) the device's status word;
     raises OklsError for a token id past the vocabulary or an expired wait."""
@@ -70,7 +83,7 @@ def embedding(weight: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, ou
               stream=None) -> torch.Tensor:
     """scale * weight[ids], of shape ids.shape + (dim,); zeros for padding."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, weight, ids):
             return embedding(weight, ids, scale=scale, out_dtype=out_dtype)
     return _n().embedding(weight, ids, scale, out_dtype)
 
@@ -83,7 +96,7 @@ def embedding_grad(dy: torch.Tensor, ids: torch.Tensor, vocab: int, *, scale: fl
     `base` None stands for zeros.  With `out` the result goes there; out=base
     adds in place and touches only the rows of tokens that occur."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, dy, ids, base, out):
             return embedding_grad(dy, ids, vocab, scale=scale, base=base, out=out, dtype=dtype)
     got = _n().embedding_grad(dy, ids, vocab, scale, base, out, dtype)
     return got if out is None else out
@@ -106,7 +119,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | 
     8-bit y is an Fp8Tensor with row groups.  `inplace` writes s over
     `residual`.  Without a residual, s is x itself."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x, weight, residual):
             return rms_norm(x, weight, residual=residual, eps=eps, out_dtype=out_dtype, inplace=inplace)
     y, scale, total, rstd = _n().rms_norm(x, weight, residual, eps, out_dtype, inplace)
     if scale is not None:
@@ -120,7 +133,7 @@ def rms_norm_grad(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd:
     the weight in fp32 (None unless `need_dweight`).  `s` and `rstd` are what
     rms_norm returned; `dresidual` is the gradient that reaches s from elsewhere."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, dy, s, weight, rstd, dresidual):
             return rms_norm_grad(dy, s, weight, rstd, dresidual=dresidual, need_dweight=need_dweight)
     return _n().rms_norm_grad(dy, s, weight, rstd, dresidual, need_dweight)
 
@@ -172,7 +185,7 @@ def fp8_quantize(x: torch.Tensor, *, block: str = "row", transpose: bool = False
     if block not in _BLOCKS:
         _fail(f"block must be one of {_BLOCKS}")
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return fp8_quantize(x, block=block, transpose=transpose, both=both)
     q, s, qt, st = _n().fp8_quantize(x, block == "square", both or not transpose, both or transpose)
     if both:
@@ -187,7 +200,7 @@ def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, *, out_dtype: torch.dtype = torch.bfl
     if a.block != "row":
         _fail("the first factor needs row groups")
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, a.data, a.scale, b.data, b.scale, out):
             return fp8_matmul(a, b, out_dtype=out_dtype, out=out, accumulate=accumulate)
     got = _n().fp8_matmul(a.data, a.scale, b.data, b.scale, b.block == "square", out, out_dtype, accumulate)
     return got if out is None else out
@@ -210,7 +223,7 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, *, top_k: int = 0, s
     """Log probabilities of `ids` under softmax(scale * logits), shaped like the
     logits' rows; `top_k` <= 32 best alternatives, equal logits in the order of their ids."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, logits, ids):
             return token_logprobs(logits, ids, top_k=top_k, scale=scale)
     return TokenLogprobs(*_n().token_logprobs(logits, ids, top_k, scale))
 
@@ -221,7 +234,7 @@ def token_logprobs_grad(logits: torch.Tensor, ids: torch.Tensor, result: TokenLo
     """Gradient of sum(dlogp * logp) + sum(dentropy * entropy) with respect to
     the logits, of their type; `inplace` writes it over the logits."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, logits, ids, result.lse, result.entropy, dlogp, dentropy):
             return token_logprobs_grad(logits, ids, result, dlogp, dentropy=dentropy, scale=scale, inplace=inplace)
     d = _n().token_logprobs_grad(logits, ids, result.lse, result.entropy, dlogp, dentropy, scale, inplace)
     return logits if inplace else d

@@ -70,3 +70,24 @@ def test_reassigned_fields_of_8_bit_tensors_are_checked():
     with pytest.raises(ValueError):
         lm.fp8_matmul(good, f)
     assert torch.equal(lm.fp8_matmul(good, lm.fp8_quantize(x, block="square")), want)
+
+
+def test_inputs_outlive_a_call_on_another_stream():
+    """Temporaries handed to a call on a busy stream are not overwritten by what the current stream allocates next."""
+    g = gen(2)
+    keep = randn(g, 2048, 1024)
+    w = randn(g, 1024)
+    side = torch.cuda.Stream()
+    for call, value in ((lambda x, s: lm.rms_norm(x, w, stream=s).y, lambda y: y),
+                        (lambda x, s: lm.fp8_quantize(x, stream=s), lambda q: q.float())):
+        want = value(call(keep, None))
+        x = keep.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)  # some 25 ms
+        got = call(x, side)
+        del x
+        later = [torch.full_like(keep, float("nan")) for _ in range(3)]  # takes x's memory if it is free
+        torch.cuda.synchronize()
+        assert torch.equal(value(got), want)
+        del later

@@ -40,3 +40,51 @@ def test_misaligned_vectors_are_refused(lib):
             a[i] = P + 2
             assert fn(*a) == BAD, (fn.__name__, i, L.last_error())
             assert "aligned" in L.last_error(), (fn.__name__, i, L.last_error())
+
+
+class _Lent:
+    """Stands for a CUDA tensor: remembers the streams that were told of it."""
+    is_cuda = True
+
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, s):
+        self.streams.append(s)
+
+
+def test_inputs_of_a_call_on_another_stream_are_recorded(monkeypatch):
+    """The allocator learns that `stream` uses the inputs, so their memory is not handed out again too early."""
+    import contextlib
+    import dataclasses
+    import types
+
+    import torch
+
+    from kronecker_factored_second_gb300 import lm
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(lm, "_n", lambda: types.SimpleNamespace(
+        embedding=lambda *a: None, embedding_grad=lambda *a: None, rms_norm=lambda *a: (None,) * 4,
+        rms_norm_grad=lambda *a: None, fp8_quantize=lambda *a: (None,) * 4, fp8_matmul=lambda *a: None,
+        token_logprobs=lambda *a: (None,) * len(dataclasses.fields(lm.TokenLogprobs)), token_logprobs_grad=lambda *a: None))
+    t = [_Lent() for _ in range(6)]
+    f = [lm._fp8(t[0], t[1], "row"), lm._fp8(t[2], t[3], "square")]
+    r = lm.TokenLogprobs(None, t[2], t[3])
+    calls = [
+        (lambda s: lm.embedding(t[0], t[1], stream=s), 2),
+        (lambda s: lm.embedding_grad(t[0], t[1], 9, base=t[2], out=t[3], stream=s), 4),
+        (lambda s: lm.rms_norm(t[0], t[1], residual=t[2], stream=s), 3),
+        (lambda s: lm.rms_norm(t[0], t[1], stream=s), 2),
+        (lambda s: lm.rms_norm_grad(t[0], t[1], t[2], t[3], dresidual=t[4], stream=s), 5),
+        (lambda s: lm.fp8_quantize(t[0], stream=s), 1),
+        (lambda s: lm.fp8_matmul(*f, out=t[4], stream=s), 5),
+        (lambda s: lm.token_logprobs(t[0], t[1], stream=s), 2),
+        (lambda s: lm.token_logprobs_grad(t[0], t[1], r, t[4], dentropy=t[5], stream=s), 6),
+    ]
+    for i, (call, count) in enumerate(calls):
+        for stream in (None, f"stream {i}"):
+            for x in t:
+                x.streams.clear()
+            call(stream)
+            told = [] if stream is None else [stream]
+            assert [x.streams for x in t] == [told] * count + [[]] * (6 - count), (i, stream)
