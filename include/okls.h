@@ -629,6 +629,22 @@ okls_status okls_token_logprobs(const void *logits, int32_t dtype, int64_t ldl,
                                 uint32_t *status_dev, void *stream);
 
 /*
+ * The same with the remainder of lse's rounding: lse[r] + lse_rest[r] is
+ * m + log sum_j exp(z_rj - m), m the row's maximum (0 for a row without a
+ * possible token).  logp, top_logp and entropy do not depend on lse.
+ *   lse_rest  rows fp32, may be NULL.
+ */
+okls_status okls_token_logprobs_rest(const void *logits, int32_t dtype,
+                                     int64_t ldl, const void *ids,
+                                     int32_t ids_i64, int64_t rows,
+                                     int64_t vocab, float scale,
+                                     int32_t top_k, float *logp,
+                                     float *entropy, float *lse,
+                                     float *lse_rest, int32_t *top_ids,
+                                     float *top_logp, uint32_t *status_dev,
+                                     void *stream);
+
+/*
  * Gradient with respect to the logits of sum_r dlogp[r] logp[r] +
  * dentropy[r] entropy[r], with p = exp(z - lse):
  *   dlogits_rj = scale * (dlogp[r] ([j = ids[r]] - p_rj)
@@ -637,6 +653,10 @@ okls_status okls_token_logprobs(const void *logits, int32_t dtype, int64_t ldl,
  *   lse, entropy  as okls_token_logprobs wrote them (entropy may be NULL when
  *                 dentropy is NULL).
  *   dlogits       rows x vocab of logits' type; may be logits (in place).
+ * lse carries its own rounding, so a row's probabilities are off by a common
+ * factor of up to |lse| 2^-24 here: rows whose logits share a large offset
+ * (rows masked to nothing but the type's lowest value above all) need the
+ * form below.
  */
 okls_status okls_token_logprobs_grad(const void *logits, int32_t dtype,
                                      int64_t ldl, const void *ids,
@@ -645,6 +665,15 @@ okls_status okls_token_logprobs_grad(const void *logits, int32_t dtype,
                                      const float *lse, const float *entropy,
                                      const float *dlogp, const float *dentropy,
                                      void *dlogits, int64_t ldd, void *stream);
+
+/* The same from lse and its remainder (NULL: none), with
+ * p = exp((z - lse) - lse_rest): no error that grows with a common offset. */
+okls_status okls_token_logprobs_grad_rest(
+    const void *logits, int32_t dtype, int64_t ldl, const void *ids,
+    int32_t ids_i64, int64_t rows, int64_t vocab, float scale,
+    const float *lse, const float *lse_rest, const float *entropy,
+    const float *dlogp, const float *dentropy, void *dlogits, int64_t ldd,
+    void *stream);
 
 #ifdef __cplusplus
 }

@@ -142,6 +142,9 @@ _SIGS = {
     "okls_fp8_matmul": (_I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _I32, _I64, _I64, _I64, _P,
                                _I32, _I64, _I32, _P, _P]),
     "okls_token_logprobs": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _I64, _F, _I32, _P, _P, _P, _P, _P, _P, _P]),
+    "okls_token_logprobs_rest": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _I64, _F, _I32, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "okls_token_logprobs_grad_rest": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _I64, _F, _P, _P, _P, _P, _P, _P, _I64,
+                                             _P]),
     "okls_token_logprobs_grad": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _I64, _F, _P, _P, _P, _P, _P, _I64, _P]),
 }
 

@@ -301,14 +301,15 @@ std::tuple<Tensor, Maybe> rms_norm_grad(const Tensor& dy, const Tensor& s, const
 }
 
 // --------------------------------------------------------- log probabilities
-std::tuple<Tensor, Tensor, Tensor, Maybe, Maybe> token_logprobs(const Tensor& logits, const Tensor& ids, int64_t top_k,
-                                                                double scale) {
+std::tuple<Tensor, Tensor, Tensor, Maybe, Maybe, Tensor> token_logprobs(const Tensor& logits, const Tensor& ids,
+                                                                        int64_t top_k, double scale) {
   const Mat z = matrix(logits, "logits");
   const int dt = float_code(logits.scalar_type(), "logits"), i64 = ids_code(ids, z.rows);
   same_device(logits, ids);
   Call c(logits);
   const at::IntArrayRef lead = logits.sizes().slice(0, logits.dim() - 1);
   Tensor logp = c.empty(lead, at::kFloat), entropy = c.empty(lead, at::kFloat), lse = c.empty(lead, at::kFloat);
+  Tensor rest = c.empty(lead, at::kFloat);
   Maybe top_ids, top_logp;
   if (top_k > 0) {
     std::vector<int64_t> shape = lead.vec();
@@ -316,19 +317,21 @@ std::tuple<Tensor, Tensor, Tensor, Maybe, Maybe> token_logprobs(const Tensor& lo
     top_ids = c.empty(shape, at::kInt);
     top_logp = c.empty(shape, at::kFloat);
   }
-  check(okls_token_logprobs(z.p, dt, z.ld, ids.data_ptr(), i64, z.rows, z.cols, static_cast<float>(scale),
-                            static_cast<int32_t>(std::max<int64_t>(-1, std::min<int64_t>(top_k, 64))), logp.data_ptr<float>(),
-                            entropy.data_ptr<float>(), lse.data_ptr<float>(), top_ids ? top_ids->data_ptr<int32_t>() : nullptr,
-                            top_logp ? top_logp->data_ptr<float>() : nullptr, status_of(logits), c.stream()));
-  return {logp, entropy, lse, top_ids, top_logp};
+  check(okls_token_logprobs_rest(z.p, dt, z.ld, ids.data_ptr(), i64, z.rows, z.cols, static_cast<float>(scale),
+                                 static_cast<int32_t>(std::max<int64_t>(-1, std::min<int64_t>(top_k, 64))),
+                                 logp.data_ptr<float>(), entropy.data_ptr<float>(), lse.data_ptr<float>(),
+                                 rest.data_ptr<float>(), top_ids ? top_ids->data_ptr<int32_t>() : nullptr,
+                                 top_logp ? top_logp->data_ptr<float>() : nullptr, status_of(logits), c.stream()));
+  return {logp, entropy, lse, top_ids, top_logp, rest};
 }
 
-Tensor token_logprobs_grad(const Tensor& logits, const Tensor& ids, const Tensor& lse, const Maybe& entropy,
-                           const Tensor& dlogp, const Maybe& dentropy, double scale, bool inplace) {
+Tensor token_logprobs_grad(const Tensor& logits, const Tensor& ids, const Tensor& lse, const Maybe& rest,
+                           const Maybe& entropy, const Tensor& dlogp, const Maybe& dentropy, double scale, bool inplace) {
   const Mat z = matrix(logits, "logits");
   const int dt = float_code(logits.scalar_type(), "logits"), i64 = ids_code(ids, z.rows);
   const float* l = floats(lse, "lse", z.rows);
   const float* g = floats(dlogp, "dlogp", z.rows);
+  const float* lr = rest ? floats(*rest, "lse_rest", z.rows) : nullptr;
   const float *h = nullptr, *e = nullptr;
   if (dentropy) {
     REFUSE(!entropy, "dentropy needs the entropy");
@@ -337,13 +340,14 @@ Tensor token_logprobs_grad(const Tensor& logits, const Tensor& ids, const Tensor
   }
   same_device(logits, ids);
   same_device(logits, lse);
+  same_device(logits, rest);
   same_device(logits, dlogp);
   same_device(logits, dentropy);
   if (dentropy) same_device(logits, entropy);
   Call c(logits);
   Tensor d = inplace ? logits : c.empty(logits.sizes(), logits.scalar_type());
-  check(okls_token_logprobs_grad(z.p, dt, z.ld, ids.data_ptr(), i64, z.rows, z.cols, static_cast<float>(scale), l, e, g, h,
-                                 d.data_ptr(), inplace ? z.ld : z.cols, c.stream()));
+  check(okls_token_logprobs_grad_rest(z.p, dt, z.ld, ids.data_ptr(), i64, z.rows, z.cols, static_cast<float>(scale), l, lr,
+                                      e, g, h, d.data_ptr(), inplace ? z.ld : z.cols, c.stream()));
   return d;
 }
 

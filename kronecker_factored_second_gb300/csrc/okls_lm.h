@@ -150,6 +150,7 @@ struct ScoreArgs {
   float* logp;
   float* entropy;
   float* lse;
+  float* lse_rest;
   int32_t* top_ids;
   float* top_logp;
   uint32_t* status;
@@ -164,6 +165,7 @@ struct ScoreGradArgs {
   int64_t rows, vocab;
   float scale;
   const float* lse;
+  const float* lse_rest;
   const float* entropy;
   const float* dlogp;
   const float* dentropy;

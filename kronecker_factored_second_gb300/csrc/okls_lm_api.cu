@@ -340,9 +340,10 @@ okls_status okls_fp8_matmul(const void* a, int64_t lda, const float* a_scale, in
 }
 
 // ----------------------------------------------------- log probabilities
-okls_status okls_token_logprobs(const void* logits, int32_t dtype, int64_t ldl, const void* ids, int32_t ids_i64,
-                                int64_t rows, int64_t vocab, float scale, int32_t top_k, float* logp, float* entropy,
-                                float* lse, int32_t* top_ids, float* top_logp, uint32_t* status_dev, void* stream) {
+okls_status okls_token_logprobs_rest(const void* logits, int32_t dtype, int64_t ldl, const void* ids, int32_t ids_i64,
+                                     int64_t rows, int64_t vocab, float scale, int32_t top_k, float* logp,
+                                     float* entropy, float* lse, float* lse_rest, int32_t* top_ids, float* top_logp,
+                                     uint32_t* status_dev, void* stream) {
   const char* op = "okls_token_logprobs";
   if (!float_dtype(dtype)) return bad(op, "dtype must be fp32 or bf16");
   if (rows < 0 || vocab < 1 || vocab > kMaxSide) return bad(op, "rows must be non-negative, vocab in [1, 2^31)");
@@ -356,18 +357,26 @@ okls_status okls_token_logprobs(const void* logits, int32_t dtype, int64_t ldl, 
   LM_TRY(check_vec(op, "logp", logp));
   LM_TRY(check_vec(op, "entropy", entropy));
   LM_TRY(check_vec(op, "lse", lse));
+  LM_TRY(check_vec(op, "lse_rest", lse_rest));
   LM_TRY(check_vec(op, "top_ids", top_ids));
   LM_TRY(check_vec(op, "top_logp", top_logp));
   int sms = 0;
   LM_TRY(host_device_sms(&sms));
-  ScoreArgs A = {logits, ldl, ids, ids_i64, rows, vocab, scale, top_k, logp, entropy, lse, top_ids, top_logp, status_dev};
+  ScoreArgs A = {logits, ldl, ids, ids_i64, rows, vocab, scale, top_k, logp, entropy, lse, lse_rest, top_ids, top_logp, status_dev};
   return launched(op, launch_token_logprobs(A, dtype, sms, static_cast<cudaStream_t>(stream)));
 }
 
-okls_status okls_token_logprobs_grad(const void* logits, int32_t dtype, int64_t ldl, const void* ids, int32_t ids_i64,
-                                     int64_t rows, int64_t vocab, float scale, const float* lse, const float* entropy,
-                                     const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd,
-                                     void* stream) {
+okls_status okls_token_logprobs(const void* logits, int32_t dtype, int64_t ldl, const void* ids, int32_t ids_i64,
+                                int64_t rows, int64_t vocab, float scale, int32_t top_k, float* logp, float* entropy,
+                                float* lse, int32_t* top_ids, float* top_logp, uint32_t* status_dev, void* stream) {
+  return okls_token_logprobs_rest(logits, dtype, ldl, ids, ids_i64, rows, vocab, scale, top_k, logp, entropy, lse, nullptr,
+                                  top_ids, top_logp, status_dev, stream);
+}
+
+okls_status okls_token_logprobs_grad_rest(const void* logits, int32_t dtype, int64_t ldl, const void* ids,
+                                          int32_t ids_i64, int64_t rows, int64_t vocab, float scale, const float* lse,
+                                          const float* lse_rest, const float* entropy, const float* dlogp,
+                                          const float* dentropy, void* dlogits, int64_t ldd, void* stream) {
   const char* op = "okls_token_logprobs_grad";
   if (!float_dtype(dtype)) return bad(op, "dtype must be fp32 or bf16");
   if (rows < 0 || vocab < 1 || vocab > kMaxSide) return bad(op, "rows must be non-negative, vocab in [1, 2^31)");
@@ -378,14 +387,23 @@ okls_status okls_token_logprobs_grad(const void* logits, int32_t dtype, int64_t 
   LM_TRY(check_mat(op, "lse", lse, 1, rows, rows, 4));
   LM_TRY(check_mat(op, "dlogp", dlogp, 1, rows, rows, 4));
   if (dentropy && !entropy) return bad(op, "dentropy needs entropy");
+  LM_TRY(check_vec(op, "lse_rest", lse_rest));
   LM_TRY(check_vec(op, "entropy", entropy));
   LM_TRY(check_vec(op, "dentropy", dentropy));
   if (lm_div_up(vocab, 8192) > kMaxGrid / (rows > 0 ? rows : 1))
     return host_fail(OKLS_ERR_UNSUPPORTED, "%s: rows x vocab is too large for one launch", op);
   int sms = 0;
   LM_TRY(host_device_sms(&sms));
-  ScoreGradArgs A = {logits, ldl, ids, ids_i64, rows, vocab, scale, lse, entropy, dlogp, dentropy, dlogits, ldd};
+  ScoreGradArgs A = {logits, ldl, ids, ids_i64, rows, vocab, scale, lse, lse_rest, entropy, dlogp, dentropy, dlogits, ldd};
   return launched(op, launch_token_logprobs_grad(A, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+okls_status okls_token_logprobs_grad(const void* logits, int32_t dtype, int64_t ldl, const void* ids, int32_t ids_i64,
+                                     int64_t rows, int64_t vocab, float scale, const float* lse, const float* entropy,
+                                     const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd,
+                                     void* stream) {
+  return okls_token_logprobs_grad_rest(logits, dtype, ldl, ids, ids_i64, rows, vocab, scale, lse, nullptr, entropy, dlogp,
+                                       dentropy, dlogits, ldd, stream);
 }
 
 }  // extern "C"

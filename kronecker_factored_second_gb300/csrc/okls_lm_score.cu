@@ -2,12 +2,15 @@
 // their gradient (sm_103a).
 //
 // With z = scale * logits, m = max z, S = sum e^(z - m), Q = sum e^(z - m)(z - m):
-//   lse = m + log S,   logp = z_id - lse,   entropy = log S - Q / S.
+//   lse = m + log S,   logp = (z_id - m) - log S,   entropy = log S - Q / S.
 // One pass over the logits: every thread keeps a running (m, S, Q); when the
 // maximum grows by t = m_old - m_new <= 0, S <- S e^t and Q <- e^t (Q + t S).
-// Pairs of partial results are joined by the same rule.  The entropy is taken
+// Pairs of partial results are joined by the same rule.  Everything is taken
 // from differences to the maximum, so an offset common to the row does not
-// cancel digits.
+// cancel digits; lse, which holds the offset, comes with the remainder of its
+// rounding, so that the gradient can form p = e^((z - lse) - rest) without it
+// (a row of nothing but the type's lowest value has lse = that value: without
+// the remainder every p would be 1).
 //
 // A row is read by a cluster of 1 to 8 CTAs (few long rows need many SMs);
 // partial results are joined through shared memory and then distributed
@@ -287,23 +290,30 @@ __device__ __forceinline__ void write_row(const ScoreArgs& A, int64_t row, const
   // a sum that is NaN (a NaN logit) makes everything NaN, and so does an
   // infinite maximum, whose sum is 0
   const float logs = logf(L.s);
-  const float lse = none ? -CUDART_INF_F : (L.s != L.s ? L.s : L.m + logs);
+  const float lse = none ? -CUDART_INF_F : (L.s != L.s ? L.s : __fadd_rn(L.m, logs));
+  // a log probability is -inf where no token is possible
+  auto logp_of = [&](float v) { return none ? -CUDART_INF_F : __fsub_rn(__fsub_rn(__fmul_rn(v, A.scale), L.m), logs); };
   if (lane == 0) {
     if (A.lse) A.lse[row] = lse;
+    if (A.lse_rest) {
+      // m + log S - lse exactly: the error of a rounded sum of two, whichever is larger
+      const float t = __fsub_rn(lse, L.m);
+      const float rest = __fadd_rn(__fsub_rn(L.m, __fsub_rn(lse, t)), __fsub_rn(logs, t));
+      A.lse_rest[row] = none ? 0.0f : rest;
+    }
     if (A.entropy) A.entropy[row] = none ? 0.0f : logs - L.q / L.s;
     if (A.logp) {
       const int64_t id = token_at(A.ids, A.ids_i64, row);
       if (id >= A.vocab) atomicOr(A.status, kStBadToken);
       float lp = 0.0f;
-      if (id >= 0 && id < A.vocab) lp = none ? -CUDART_INF_F : __fsub_rn(__fmul_rn(to_f32(z[id]), A.scale), lse);
+      if (id >= 0 && id < A.vocab) lp = logp_of(to_f32(z[id]));
       A.logp[row] = lp;
     }
   }
   if (TOP && lane < k) {
     const uint32_t col = ~static_cast<uint32_t>(best);
     A.top_ids[row * k + lane] = static_cast<int32_t>(col);
-    A.top_logp[row * k + lane] =
-        none ? -CUDART_INF_F : __fsub_rn(__fmul_rn(ord_value(static_cast<uint32_t>(best >> 32)), A.scale), lse);
+    A.top_logp[row * k + lane] = logp_of(ord_value(static_cast<uint32_t>(best >> 32)));
   }
 }
 
@@ -621,15 +631,17 @@ constexpr int kGradVecs = 4;
 constexpr int kGradCols = kGradThreads * 8 * kGradVecs;
 
 struct RowGrad {
-  float scale, lse, h, c;  // c = -g - h entropy
+  float scale, lse, h;
+  float rest2;  // -rest log2(e)
+  float c;      // -g - h (entropy - rest)
 };
 
 template <bool ENT>
 __device__ __forceinline__ float grad_of(const RowGrad& R, float z) {
-  // log p = z - lse; -inf logits have p = 0 and no gradient
-  const float lp = __fsub_rn(__fmul_rn(z, R.scale), R.lse);
-  const float p = ex2(lp * kLog2e) * R.scale;
-  return p * (ENT ? fmaf(-R.h, fmaxf(lp, kFar), R.c) : R.c);
+  // log p = (z - lse) - rest; -inf logits have p = 0 and no gradient
+  const float d = __fsub_rn(__fmul_rn(z, R.scale), R.lse);
+  const float p = ex2(fmaf(d, kLog2e, R.rest2)) * R.scale;
+  return p * (ENT ? fmaf(-R.h, fmaxf(d, kFar), R.c) : R.c);
 }
 
 template <class T, bool ENT>
@@ -646,11 +658,13 @@ __global__ void __launch_bounds__(kGradThreads) k_token_logprobs_grad(const Scor
   if (id < 0 || id >= A.vocab) id = -1;
   const float g = id >= 0 ? A.dlogp[row] : 0.0f;
   R.h = ENT ? A.dentropy[row] : 0.0f;
-  R.c = ENT ? -g - R.h * A.entropy[row] : -g;
+  const float rest = A.lse_rest ? A.lse_rest[row] : 0.0f;
+  R.rest2 = -rest * kLog2e;
+  R.c = ENT ? -g - R.h * (A.entropy[row] - rest) : -g;
   float own = g * A.scale;  // the given token's own term
   if (R.lse == -CUDART_INF_F) {
     // no possible token: z - lse would be NaN
-    R.lse = R.h = R.c = own = 0.0f;
+    R.lse = R.rest2 = R.h = R.c = own = 0.0f;
   }
   auto one = [&](int64_t c) {
     const float d = grad_of<ENT>(R, to_f32(z[c]));

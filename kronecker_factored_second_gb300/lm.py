@@ -210,12 +210,15 @@ def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, *, out_dtype: torch.dtype = torch.bfl
 @dataclass
 class TokenLogprobs:
     """Per row: log probability of the given token, entropy, log of the sum of
-    exponentials; with top_k, the best tokens and their log probabilities."""
+    exponentials; with top_k, the best tokens and their log probabilities.
+    lse + lse_rest is the logarithm before its rounding: the gradient needs the
+    remainder where a row's logits share a large offset."""
     logp: torch.Tensor
     entropy: torch.Tensor
     lse: torch.Tensor
     top_ids: torch.Tensor | None = None
     top_logp: torch.Tensor | None = None
+    lse_rest: torch.Tensor | None = None
 
 
 def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, *, top_k: int = 0, scale: float = 1.0,
@@ -234,9 +237,9 @@ def token_logprobs_grad(logits: torch.Tensor, ids: torch.Tensor, result: TokenLo
     """Gradient of sum(dlogp * logp) + sum(dentropy * entropy) with respect to
     the logits, of their type; `inplace` writes it over the logits."""
     if stream is not None:
-        with _on(stream, logits, ids, result.lse, result.entropy, dlogp, dentropy):
+        with _on(stream, logits, ids, result.lse, result.lse_rest, result.entropy, dlogp, dentropy):
             return token_logprobs_grad(logits, ids, result, dlogp, dentropy=dentropy, scale=scale, inplace=inplace)
-    d = _n().token_logprobs_grad(logits, ids, result.lse, result.entropy, dlogp, dentropy, scale, inplace)
+    d = _n().token_logprobs_grad(logits, ids, result.lse, result.lse_rest, result.entropy, dlogp, dentropy, scale, inplace)
     return logits if inplace else d
 
 
@@ -309,14 +312,14 @@ class _Logprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, ids, scale):
         r = token_logprobs(logits, ids, scale=scale)
-        ctx.save_for_backward(logits, ids, r.entropy, r.lse)
+        ctx.save_for_backward(logits, ids, r.entropy, r.lse, r.lse_rest)
         ctx.scale = scale
         return r.logp, r.entropy
 
     @staticmethod
     def backward(ctx, dlogp, dentropy):
-        logits, ids, entropy, lse = ctx.saved_tensors
-        r = TokenLogprobs(None, entropy, lse)
+        logits, ids, entropy, lse, rest = ctx.saved_tensors
+        r = TokenLogprobs(None, entropy, lse, lse_rest=rest)
         return token_logprobs_grad(logits, ids, r, dlogp.contiguous(), dentropy=dentropy.contiguous(),
                                    scale=ctx.scale), None, None
 

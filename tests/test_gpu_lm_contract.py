@@ -91,3 +91,84 @@ def test_inputs_outlive_a_call_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(value(got), want)
         del later
+
+
+def _probabilities(z, ids, r, k):
+    """logp, entropy, alternatives and gradients of rows whose logits share an offset, against 64 bits.  Differences to the
+    row's maximum are exact, so the bounds hold the spread of the possible logits and not their size: an exponent is off by
+    a few u of the spread, a sum of V terms on 128 threads and more by V / 256 + 64 u of itself, the logarithm by the same."""
+    rows, vocab = z.shape
+    s = z.double()
+    m = s.amax(-1, keepdim=True)
+    d = torch.where(s == -float("inf"), s, s - m)
+    logs = torch.logsumexp(d, -1, keepdim=True)
+    lp = d - logs
+    p = lp.exp()
+    plp = torch.xlogy(p, p)
+    ent = -plp.sum(-1)
+    spread = torch.where(p > 1e-40, d.abs(), 0.0).amax(-1)
+    e = (64 + 16 * spread + vocab / 256) * U
+    keep = ids >= 0
+    at = ids.clamp_min(0)[:, None]
+    want = torch.where(keep, lp.gather(1, at)[:, 0], 0.0)
+    fin = torch.isfinite(want)
+    assert torch.equal(torch.isfinite(r.logp), fin)
+    assert ((r.logp - want).abs() - e - 4 * U * want.abs())[fin].max().item() <= 0
+    # the entropy's terms p log p are off by e (|log p| + 1) relative to p
+    assert ((r.entropy - ent).abs() - e * (2 + 4 * spread + 2 * logs[:, 0])).max().item() <= 0
+    if k:
+        v, i = torch.sort(z.float(), dim=-1, descending=True, stable=True)
+        assert torch.equal(r.top_ids, i[:, :k].int())
+        tl = torch.gather(lp, 1, i[:, :k])
+        fin = torch.isfinite(tl.float())  # lowest - largest is below every fp32 value: -inf
+        assert torch.equal(torch.isfinite(r.top_logp), fin)
+        assert ((r.top_logp - tl).abs() - e[:, None] - 4 * U * tl.abs())[fin].max().item() <= 0
+    g, h = randn(gen(1), rows).abs() + 0.5, randn(gen(2), rows)
+    gl = torch.where(keep, g.double(), 0.0)[:, None]
+    own = torch.zeros_like(p).scatter_(1, at, 1.0) * gl
+    hd = h.double()[:, None]
+    out = 2.0 ** -8 if z.dtype == BF16 else U
+    for dent in (None, h):
+        d = lm.token_logprobs_grad(z, ids, r, g, dentropy=dent)
+        want, mag = own - p * gl, own + p * gl
+        if dent is not None:
+            want = want - hd * (plp + p * ent[:, None])
+            mag = mag + hd.abs() * (plp.abs() + p * (ent[:, None] + 1 + logs.abs()))
+        bound = 4 * e[:, None] * mag + out * want.abs() + 2.0 ** -140
+        assert ((d.double() - want).abs() - bound).max().item() <= 0
+
+
+@pytest.mark.parametrize("dtype,offsets", [(F32, (0.0, 4096.0, -65536.0, 2.0 ** 20)), (BF16, (0.0, 64.0, -64.0))])
+@pytest.mark.parametrize("rows,vocab,k", [(3, 5000, 0), (40, 777, 5), (1, 40000, 20), (5, 131072, 3)])
+def test_a_common_offset_costs_no_digits(dtype, offsets, rows, vocab, k):
+    g = gen(vocab)
+    # whole steps that are exact at every offset
+    z = torch.randint(-16, 17, (rows, vocab), generator=g, device="cuda").float() * (0.125 if dtype == F32 else 0.5)
+    ids = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    ids[rows // 2] = -1 if rows > 1 else ids[0]
+    first = None
+    for o in offsets:
+        zz = (z + o).to(dtype)
+        assert torch.equal(zz.float(), z + o)
+        r = lm.token_logprobs(zz, ids, top_k=k)
+        _probabilities(zz, ids, r, k)
+        if first is None:
+            first = r
+        # the same differences to the maximum: the same bits
+        assert torch.equal(r.logp, first.logp) and torch.equal(r.entropy, first.entropy)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("vocab", [7, 1000, 4097, 50000])
+def test_rows_of_the_lowest_value(dtype, vocab):
+    """A mask of the type's lowest value that leaves nothing, or one token, and the same where the rest is -inf."""
+    low = torch.finfo(dtype).min
+    z = torch.full((5, vocab), low, device="cuda", dtype=dtype)
+    z[1, 3] = 1.5
+    z[2, 2:] = -float("inf")
+    z[3, 5:] = torch.finfo(dtype).max
+    ids = torch.tensor([3, 3, 1, vocab - 1, -1], device="cuda")
+    r = lm.token_logprobs(z, ids, top_k=3)
+    _probabilities(z, ids, r, 3)
+    d = lm.token_logprobs_grad(z, ids, r, torch.ones(5, device="cuda"))
+    assert d[4].abs().max().item() == 0
