@@ -12,6 +12,9 @@ and the same as differentiable functions of torch.autograd:
 
 `embed`, `norm`, `linear`, `logprobs`
 
+Their gradients are not differentiable: a second derivative through one of
+them raises RuntimeError.
+
 Tensors are CUDA tensors on one device whose last dimension is contiguous;
 rows may have any pitch.  fp32 and bf16 are taken, ids are int32 or int64.
 Negative ids are padding: zeros out, no loss, no gradient.  An id at or past
@@ -244,6 +247,29 @@ def token_logprobs_grad(logits: torch.Tensor, ids: torch.Tensor, result: TokenLo
 
 
 # ------------------------------------------------------------------ autograd
+class _FirstOrder(torch.autograd.Function):
+    """Gradients that depend on `sources`, as they are, but not to be differentiated."""
+
+    @staticmethod
+    def forward(ctx, name, count, *tensors):
+        ctx.name = name
+        return tuple(t.view_as(t) for t in tensors[:count])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"okls.lm: the gradient of {ctx.name} cannot be differentiated")
+
+
+def _first_order(name, grads, *sources):
+    """The gradients a backward returns.  The kernels leave no graph: where one is asked for (create_graph), a gradient
+    is tied to the tensors that it is made of, so that a second derivative through it raises instead of being dropped."""
+    if not torch.is_grad_enabled():
+        return grads
+    some = [g for g in grads if g is not None]
+    tied = iter(_FirstOrder.apply(name, len(some), *some, *(s for s in sources if s is not None)))
+    return tuple(None if g is None else next(tied) for g in grads)
+
+
 class _Embed(torch.autograd.Function):
     @staticmethod
     def forward(ctx, weight, ids, scale, out_dtype):
@@ -255,7 +281,8 @@ class _Embed(torch.autograd.Function):
     def backward(ctx, dy):
         (ids,) = ctx.saved_tensors
         vocab, scale, dtype = ctx.meta
-        return embedding_grad(dy.contiguous(), ids, vocab, scale=scale, dtype=dtype), None, None, None
+        dw = embedding_grad(dy.contiguous(), ids, vocab, scale=scale, dtype=dtype)
+        return *_first_order("embed", (dw,), dy), None, None, None
 
 
 class _Norm(torch.autograd.Function):
@@ -274,8 +301,8 @@ class _Norm(torch.autograd.Function):
         dx, dw = rms_norm_grad(dy.contiguous(), s, weight, rstd,
                                dresidual=None if ds is None else ds.contiguous(),
                                need_dweight=ctx.needs_input_grad[1])
-        return (dx, None if dw is None else dw.to(weight.dtype).view(weight.shape), dx if ctx.has_residual else None,
-                None, None)
+        grads = (dx, None if dw is None else dw.to(weight.dtype).view(weight.shape), dx if ctx.has_residual else None)
+        return *_first_order("norm", grads, dy, ds, s, weight), None, None
 
 
 class _Linear(torch.autograd.Function):
@@ -285,14 +312,16 @@ class _Linear(torch.autograd.Function):
         xq, xt = fp8_quantize(x, both=True) if need_w else (fp8_quantize(x), None)
         wq, wt = fp8_quantize(weight, block="square", both=True) if need_x else (
             fp8_quantize(weight, block="square"), None)
-        ctx.save_for_backward(*[t for f in (xt, wt) if f is not None for t in (f.data, f.scale)])
+        # an empty output of this node: stands in the backward for x and weight, which are not kept
+        tie = x.new_empty(0)
+        ctx.save_for_backward(*[t for f in (xt, wt) if f is not None for t in (f.data, f.scale)], tie)
         ctx.meta = (xt is not None, wt is not None, x.shape, x.dtype, weight.dtype)
-        return fp8_matmul(xq, wq, out_dtype=out_dtype or x.dtype).view(*x.shape[:-1], weight.shape[0])
+        return fp8_matmul(xq, wq, out_dtype=out_dtype or x.dtype).view(*x.shape[:-1], weight.shape[0]), tie
 
     @staticmethod
-    def backward(ctx, dy):
+    def backward(ctx, dy, _):
         has_xt, has_wt, shape, xd, wd = ctx.meta
-        saved = list(ctx.saved_tensors)
+        *saved, tie = ctx.saved_tensors
         xt = Fp8Tensor(saved.pop(0), saved.pop(0), "row") if has_xt else None
         wt = Fp8Tensor(saved.pop(0), saved.pop(0), "square") if has_wt else None
         g = dy.contiguous()
@@ -305,7 +334,7 @@ class _Linear(torch.autograd.Function):
             dx = fp8_matmul(gq, wt, out_dtype=xd).view(shape)
         if has_xt:
             dw = fp8_matmul(gt, xt, out_dtype=wd)
-        return dx, dw, None
+        return *_first_order("linear", (dx, dw), dy, tie), None
 
 
 class _Logprobs(torch.autograd.Function):
@@ -320,8 +349,8 @@ class _Logprobs(torch.autograd.Function):
     def backward(ctx, dlogp, dentropy):
         logits, ids, entropy, lse, rest = ctx.saved_tensors
         r = TokenLogprobs(None, entropy, lse, lse_rest=rest)
-        return token_logprobs_grad(logits, ids, r, dlogp.contiguous(), dentropy=dentropy.contiguous(),
-                                   scale=ctx.scale), None, None
+        dz = token_logprobs_grad(logits, ids, r, dlogp.contiguous(), dentropy=dentropy.contiguous(), scale=ctx.scale)
+        return *_first_order("logprobs", (dz,), dlogp, dentropy, logits), None, None
 
 
 def embed(weight: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, out_dtype=None) -> torch.Tensor:
@@ -339,7 +368,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, *, out_dtype=None) -> torch.Te
     """x weight^T with every product in 8 bits: the activations and the output's
     gradient in groups of 128 along each product's sum, the weight in 128 x 128
     blocks.  Gradients have the types of x and weight."""
-    return _Linear.apply(x, weight, out_dtype)
+    return _Linear.apply(x, weight, out_dtype)[0]
 
 
 def logprobs(logits: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0):

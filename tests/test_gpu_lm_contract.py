@@ -172,3 +172,52 @@ def test_rows_of_the_lowest_value(dtype, vocab):
     _probabilities(z, ids, r, 3)
     d = lm.token_logprobs_grad(z, ids, r, torch.ones(5, device="cuda"))
     assert d[4].abs().max().item() == 0
+
+
+def test_second_derivatives_are_refused():
+    """With the kernels: gradients in a graph of gradients are the same, and differentiating them raises."""
+    g = gen(3)
+    ids = torch.tensor([1, 3, 3, 0], device="cuda")
+    x, w, r = (randn(g, *s).requires_grad_() for s in ((4, 256), (256,), (4, 256)))
+    a, b, z, t = (randn(g, *s).requires_grad_() for s in ((4, 256), (200, 256), (4, 99), (5, 64)))
+    cases = [("norm", x, lambda: lm.norm(x, w)[:, :5].sum()), ("norm", w, lambda: lm.norm(x, w, r)[0].pow(2).sum()),
+             ("norm", r, lambda: sum(y.pow(2).sum() for y in lm.norm(x, w, r))),
+             ("linear", a, lambda: lm.linear(a, b).sum()), ("linear", b, lambda: lm.linear(a, b).sum()),
+             ("logprobs", z, lambda: lm.logprobs(z, ids)[0].sum()), ("logprobs", z, lambda: lm.logprobs(z, ids)[1].sum()),
+             ("embed", t, lambda: lm.embed(t, ids).pow(2).sum())]
+    for name, v, fn in cases:
+        plain, = torch.autograd.grad(fn(), v)
+        loss = fn() + v.pow(3).sum()
+        first, = torch.autograd.grad(loss, v, create_graph=True)
+        assert torch.equal(first, plain + 3 * v.detach() ** 2)
+        for second in (lambda: torch.autograd.grad(first.sum(), v, retain_graph=True),
+                       lambda: (loss + first.pow(2).sum()).backward()):
+            with pytest.raises(RuntimeError, match=name):
+                second()
+                pytest.fail(f"a second derivative through {name} was lost")
+
+
+def test_backward_with_an_output_that_nobody_uses():
+    """A loss that uses one of two outputs has the gradient of that output alone."""
+    g = gen(4)
+    x, w, r = (randn(g, *s).requires_grad_() for s in ((40, 300), (300,), (40, 300)))
+    s = (x + r).detach()
+    rstd = lm.rms_norm(s, w.detach()).rstd
+    y, _ = lm.norm(x, w, r)
+    c = randn(g, 40, 300)
+    want = lm.rms_norm_grad(c, s, w.detach(), rstd)
+    for got, v in zip(torch.autograd.grad(y, (x, r, w), c), (want[0], want[0], want[1])):
+        assert torch.equal(got, v)
+    _, t = lm.norm(x, w, r)
+    dx, dr, dw = torch.autograd.grad(t, (x, r, w), c)
+    assert torch.equal(dx, c) and torch.equal(dr, c) and dw.abs().max().item() == 0
+    z = randn(g, 30, 500).requires_grad_()
+    ids = torch.randint(-1, 500, (30,), generator=g, device="cuda")
+    c = randn(g, 30)
+    q = lm.token_logprobs(z.detach(), ids)
+    zero = torch.zeros_like(c)
+    got, = torch.autograd.grad(lm.logprobs(z, ids)[0], z, c)
+    want = lm.token_logprobs_grad(z.detach(), ids, q, c)
+    assert (got - want).abs().max().item() <= 4 * U * want.abs().max().item()
+    got, = torch.autograd.grad(lm.logprobs(z, ids)[1], z, c)
+    assert torch.equal(got, lm.token_logprobs_grad(z.detach(), ids, q, zero, dentropy=c))

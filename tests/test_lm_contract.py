@@ -88,3 +88,110 @@ def test_inputs_of_a_call_on_another_stream_are_recorded(monkeypatch):
             call(stream)
             told = [] if stream is None else [stream]
             assert [x.streams for x in t] == [told] * count + [[]] * (6 - count), (i, stream)
+
+
+@pytest.fixture
+def on_cpu(monkeypatch):
+    """The calls under the differentiable functions, computed on the CPU by torch."""
+    import torch
+
+    from kronecker_factored_second_gb300 import lm
+
+    def embedding(weight, ids, *, scale=1.0, out_dtype=None):
+        return weight.detach()[ids] * scale
+
+    def embedding_grad(dy, ids, vocab, *, scale=1.0, dtype=torch.float32):
+        return torch.zeros(vocab, dy.shape[-1]).index_add_(0, ids, dy.detach() * scale)
+
+    def rms_norm(x, weight, *, residual=None, eps=1e-6, out_dtype=None):
+        s = x.detach() if residual is None else x.detach() + residual.detach()
+        rstd = torch.rsqrt((s * s).mean(-1) + eps)
+        return lm.NormOutput(s * rstd[:, None] * weight.detach(), x if residual is None else s, rstd)
+
+    def rms_norm_grad(dy, s, weight, rstd, *, dresidual=None, need_dweight=True):
+        dy, s, weight = dy.detach(), s.detach(), weight.detach()
+        xh, g = s * rstd[:, None], dy * weight
+        ds = rstd[:, None] * (g - xh * (g * xh).mean(-1, keepdim=True))
+        return ds if dresidual is None else ds + dresidual.detach(), (dy * xh).sum(0)
+
+    def fp8_quantize(x, *, block="row", transpose=False, both=False):
+        def q(m):
+            lines = m.shape[0] if block == "row" else -(-m.shape[0] // 128)
+            return lm._fp8(m.to(torch.float8_e4m3fn), torch.ones(lines, -(-m.shape[1] // 128)), block)
+        x = x.detach()
+        return (q(x), q(x.t().contiguous())) if both else q(x.t().contiguous() if transpose else x)
+
+    def fp8_matmul(a, b, *, out_dtype=torch.bfloat16):
+        return (a.data.float() @ b.data.float().t()).to(out_dtype)
+
+    def token_logprobs(logits, ids, *, scale=1.0):
+        lp = torch.log_softmax(logits.detach() * scale, -1)
+        ent = -(lp.exp() * lp).sum(-1)
+        lse = torch.logsumexp(logits.detach() * scale, -1)
+        return lm.TokenLogprobs(lp.gather(1, ids[:, None])[:, 0], ent, lse, lse_rest=torch.zeros_like(lse))
+
+    def token_logprobs_grad(logits, ids, result, dlogp, *, dentropy=None, scale=1.0):
+        lp = logits.detach() * scale - result.lse[:, None]
+        p, g = lp.exp(), dlogp.detach()[:, None]
+        d = torch.zeros_like(p).scatter_(1, ids[:, None], 1.0) * g - p * g
+        return scale * (d - dentropy.detach()[:, None] * p * (lp + result.entropy[:, None]))
+
+    for f in (embedding, embedding_grad, rms_norm, rms_norm_grad, fp8_quantize, fp8_matmul, token_logprobs,
+              token_logprobs_grad):
+        monkeypatch.setattr(lm, f.__name__, f)
+    return lm
+
+
+def _second_order_cases(lm):
+    import torch
+    g = torch.Generator().manual_seed(0)
+    ids = torch.tensor([1, 3, 3, 0])
+
+    def leaf(*shape):
+        return torch.randn(*shape, generator=g).requires_grad_()
+    # each output is summed, so that the gradient that comes back is a constant, and squared, so that it is not
+    x, w, r = leaf(4, 8), leaf(8), leaf(4, 8)
+    yield "norm", x, lambda: lm.norm(x, w)[:, :5].sum()
+    yield "norm", w, lambda: lm.norm(x, w)[:, :5].sum()
+    yield "norm", r, lambda: lm.norm(x, w, r)[0][:, :5].sum()
+    yield "norm", x, lambda: lm.norm(x.detach().requires_grad_(), w, r)[1].sum() + lm.norm(x * 1.0, w, r)[0].pow(2).sum()
+    a, b = leaf(4, 8), leaf(6, 8)
+    yield "linear", a, lambda: lm.linear(a, b).sum()
+    yield "linear", b, lambda: lm.linear(a, b).sum()
+    yield "linear", b, lambda: lm.linear(a.detach(), b).pow(2).sum()
+    z = leaf(4, 9)
+    yield "logprobs", z, lambda: lm.logprobs(z, ids)[0].sum()
+    yield "logprobs", z, lambda: lm.logprobs(z, ids)[1].sum()
+    t = leaf(5, 6)
+    yield "embed", t, lambda: lm.embed(t, ids).pow(2).sum()
+
+
+def test_second_derivatives_are_refused(on_cpu):
+    """A gradient of a gradient through these functions is not computed: it has to raise, also where another path to the
+    same input is differentiable twice, and only where it is asked for."""
+    import torch
+    for i, (name, x, fn) in enumerate(_second_order_cases(on_cpu)):
+        plain, = torch.autograd.grad(fn(), x)
+        loss = fn() + x.pow(3).sum()
+        first, = torch.autograd.grad(loss, x, create_graph=True)
+        assert torch.allclose(first, plain + 3 * x.detach() ** 2), (i, name)
+        for second in (lambda: torch.autograd.grad(first.sum(), x, retain_graph=True),
+                       lambda: (loss + first.pow(2).sum()).backward()):
+            with pytest.raises(RuntimeError, match=name):
+                second()
+                pytest.fail(f"case {i} lost a second derivative")
+
+
+def test_first_derivatives_in_a_graph_of_gradients(on_cpu):
+    """What does not go through the refused part is differentiable twice: the embedding is linear in its table."""
+    import torch
+    t = torch.randn(5, 6).requires_grad_()
+    ids = torch.tensor([1, 3, 3, 0])
+    loss = on_cpu.embed(t, ids).sum() + t.pow(3).sum()
+    first, = torch.autograd.grad(loss, t, create_graph=True)
+    second, = torch.autograd.grad(first.sum(), t)
+    assert torch.allclose(second, 6 * t.detach())
+    # and gradients in a graph that nobody differentiates are plain gradients
+    x, w = torch.randn(4, 8).requires_grad_(), torch.randn(8).requires_grad_()
+    on_cpu.norm(x, w).sum().backward(create_graph=True)
+    assert x.grad is not None and w.grad is not None
