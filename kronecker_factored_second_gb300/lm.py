@@ -361,6 +361,8 @@ def embed(weight: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, out_dt
 def norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, *, eps: float = 1e-6,
          out_dtype=None):
     """Differentiable `rms_norm` in 16 or 32 bits: y, or (y, x + residual)."""
+    if out_dtype not in (None, torch.float32, torch.bfloat16):
+        _fail(f"norm gives fp32 or bf16, not {out_dtype} (rms_norm has the 8-bit output)")
     return _Norm.apply(x, weight, residual, eps, out_dtype)
 
 

@@ -195,3 +195,16 @@ def test_first_derivatives_in_a_graph_of_gradients(on_cpu):
     x, w = torch.randn(4, 8).requires_grad_(), torch.randn(8).requires_grad_()
     on_cpu.norm(x, w).sum().backward(create_graph=True)
     assert x.grad is not None and w.grad is not None
+
+
+def test_norm_refuses_outputs_without_a_gradient(on_cpu):
+    """An 8-bit output is not a tensor of autograd: the differentiable norm does not offer it."""
+    import torch
+    x, w = torch.randn(4, 8).requires_grad_(), torch.randn(8).requires_grad_()
+    for dtype in (torch.float8_e4m3fn, torch.float16, torch.int8):
+        for res in (None, torch.randn(4, 8)):
+            with pytest.raises(ValueError, match="norm"):
+                on_cpu.norm(x, w, res, out_dtype=dtype)
+                pytest.fail(f"{dtype} was taken")
+    for dtype in (None, torch.float32, torch.bfloat16):
+        assert on_cpu.norm(x, w, out_dtype=dtype).requires_grad
