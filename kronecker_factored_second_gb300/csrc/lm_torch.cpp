@@ -5,6 +5,8 @@
 //
 // Wrong tensors raise ValueError; what the C entry refuses raises OklsError.
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
+#include <c10/core/InferenceMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -102,6 +104,18 @@ void same_device(const Tensor& a, const Maybe& b) {
   if (b) same_device(a, *b);
 }
 
+// A tensor of the caller that a call writes over.  Autograd learns of the write
+// from the tensor's version, by which a backward that saved the tensor finds
+// out; it cannot learn of a new value of a tensor that requires a gradient.
+void writable(const Tensor& t, const char* name) {
+  REFUSE(at::GradMode::is_enabled() && t.requires_grad(), name,
+         " requires a gradient, which a write in place would not have: detach it, or call under no_grad");
+  REFUSE(t.is_inference() && !c10::InferenceMode::is_enabled(), name, " is an inference tensor, written outside inference mode");
+}
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // Current device and stream of a call; scratch and outputs come from it.
 struct Call {
   c10::cuda::CUDAGuard guard;
@@ -156,7 +170,8 @@ Tensor embedding_grad(const Tensor& dy, const Tensor& ids, int64_t vocab, double
   const int dt = float_code(dy.scalar_type(), "dy"), i64 = ids_code(ids, d.rows);
   Mat b = {}, o = {};
   if (base) b = plain_matrix(*base, "base", vocab, d.cols);
-  if (out) o = plain_matrix(*out, "out", vocab, d.cols);
+  const bool given = out.has_value();
+  if (given) o = plain_matrix(*out, "out", vocab, d.cols), writable(*out, "out");
   REFUSE(base && out && base->scalar_type() != out->scalar_type(), "base and out must have one type");
   same_device(dy, ids);
   same_device(dy, base);
@@ -172,6 +187,7 @@ Tensor embedding_grad(const Tensor& dy, const Tensor& ids, int64_t vocab, double
   Tensor ws = c.workspace(need);
   check(okls_embedding_grad(d.p, dt, d.ld, ids.data_ptr(), i64, d.rows, vocab, d.cols, static_cast<float>(scale), b.p, b.ld,
                             o.p, od, o.ld, ptr_of(ws), need, status_of(dy), c.stream()));
+  if (given) written(*out);
   return *out;
 }
 
@@ -222,7 +238,8 @@ Tensor fp8_matmul(const Tensor& a, const Tensor& as, const Tensor& b, const Tens
   same_device(a, b);
   same_device(a, out);
   Mat o = {};
-  if (out) o = plain_matrix(*out, "out", m, n);
+  const bool given = out.has_value();
+  if (given) o = plain_matrix(*out, "out", m, n), writable(*out, "out");
   Call c(a);
   if (!out) {
     out = c.empty({m, n}, out_dtype);
@@ -232,6 +249,7 @@ Tensor fp8_matmul(const Tensor& a, const Tensor& as, const Tensor& b, const Tens
   check(okls_fp8_matmul(a.data_ptr(), a.stride(0), as.data_ptr<float>(), as.stride(0), as.stride(1), b.data_ptr(), b.stride(0),
                         bs.data_ptr<float>(), bs.stride(0), bs.stride(1), b_square ? OKLS_FP8_SQUARE : OKLS_FP8_ROW, m, n, k,
                         o.p, od, o.ld, accumulate, status_of(a), c.stream()));
+  if (given) written(*out);
   return *out;
 }
 
@@ -251,6 +269,7 @@ std::tuple<Tensor, Maybe, Tensor, Tensor> rms_norm(const Tensor& x, const Tensor
     REFUSE(residual->sizes() != x.sizes(), "residual has shape ", residual->sizes(), ", not ", x.sizes());
     REFUSE(residual->scalar_type() != x.scalar_type(), "residual is ", residual->scalar_type(), ", not ", x.scalar_type());
     r = matrix(*residual, "residual");
+    if (inplace) writable(*residual, "residual");
   }
   Call c(x);
   Tensor total = x, rstd = c.empty({m.rows}, at::kFloat), y, ys;
@@ -266,6 +285,7 @@ std::tuple<Tensor, Maybe, Tensor, Tensor> rms_norm(const Tensor& x, const Tensor
   check(okls_rms_norm(m.p, dt, m.ld, r.p, r.ld, w, wd, m.rows, m.cols, static_cast<float>(eps), y.data_ptr(), od,
                       fp8 ? y.stride(0) : m.cols, fp8 ? ys.data_ptr<float>() : nullptr, fp8 ? ys.stride(0) : 0,
                       fp8 ? ys.stride(1) : 0, s.p, s.ld, rstd.data_ptr<float>(), c.stream()));
+  if (residual && inplace) written(total);
   return {y, fp8 ? Maybe(ys) : std::nullopt, total, rstd};
 }
 
@@ -344,10 +364,12 @@ Tensor token_logprobs_grad(const Tensor& logits, const Tensor& ids, const Tensor
   same_device(logits, dlogp);
   same_device(logits, dentropy);
   if (dentropy) same_device(logits, entropy);
+  if (inplace) writable(logits, "logits");
   Call c(logits);
   Tensor d = inplace ? logits : c.empty(logits.sizes(), logits.scalar_type());
   check(okls_token_logprobs_grad_rest(z.p, dt, z.ld, ids.data_ptr(), i64, z.rows, z.cols, static_cast<float>(scale), l, lr,
                                       e, g, h, d.data_ptr(), inplace ? z.ld : z.cols, c.stream()));
+  if (inplace) written(logits);
   return d;
 }
 

@@ -15,6 +15,10 @@ and the same as differentiable functions of torch.autograd:
 Their gradients are not differentiable: a second derivative through one of
 them raises RuntimeError.
 
+Calls that write over a tensor of the caller (`out`, `inplace`) raise its
+version, so that a backward which saved it says so, and refuse a tensor that
+requires a gradient.
+
 Tensors are CUDA tensors on one device whose last dimension is contiguous;
 rows may have any pitch.  fp32 and bf16 are taken, ids are int32 or int64.
 Negative ids are padding: zeros out, no loss, no gradient.  An id at or past

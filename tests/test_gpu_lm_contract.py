@@ -221,3 +221,63 @@ def test_backward_with_an_output_that_nobody_uses():
     assert (got - want).abs().max().item() <= 4 * U * want.abs().max().item()
     got, = torch.autograd.grad(lm.logprobs(z, ids)[1], z, c)
     assert torch.equal(got, lm.token_logprobs_grad(z.detach(), ids, q, zero, dentropy=c))
+
+
+def _writes(g):
+    """(tensor that is written, call that writes it) of every call that writes over a tensor of the caller."""
+    x, w, ids = randn(g, 6, 256), randn(g, 256), torch.tensor([1, 2, 0, 3, 3, -1], device="cuda")
+    q, wq = lm.fp8_quantize(x), lm.fp8_quantize(randn(g, 40, 256), block="square")
+    r, z, t, o = randn(g, 6, 256), randn(g, 6, 50), randn(g, 9, 256), randn(g, 6, 40)
+    s = lm.token_logprobs(z, ids)
+    one = torch.ones(6, device="cuda")
+    return [(r, lambda v: lm.rms_norm(x, w, residual=v, inplace=True)),
+            (z, lambda v: lm.token_logprobs_grad(v, ids, s, one, inplace=True)),
+            (t, lambda v: lm.embedding_grad(x, ids, 9, out=v)), (t, lambda v: lm.embedding_grad(x, ids, 9, base=v, out=v)),
+            (o, lambda v: lm.fp8_matmul(q, wq, out=v)), (o, lambda v: lm.fp8_matmul(q, wq, out=v, accumulate=True))]
+
+
+def test_in_place_writes_are_known_to_autograd():
+    for i, (v, call) in enumerate(_writes(gen(5))):
+        leaf = torch.ones_like(v).requires_grad_()
+        saved = leaf * v  # keeps v for its backward
+        before, old = v._version, v.clone()
+        call(v)
+        assert v._version > before and not torch.equal(v, old), i
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            saved.sum().backward()
+            pytest.fail(f"write {i} went unnoticed")
+        # a tensor that requires a gradient: a leaf, and the result of a step that autograd knows
+        for grad in (v.clone().requires_grad_(), v.clone().requires_grad_() * 1.0):
+            with pytest.raises(ValueError, match="requires a gradient"):
+                call(grad)
+                pytest.fail(f"write {i} took a tensor that requires a gradient")
+            with torch.no_grad():
+                before = grad._version
+                call(grad)
+                assert grad._version > before, i
+    with torch.inference_mode():
+        inside = _writes(gen(5))
+        for v, call in inside:
+            call(v)
+    for i, (v, call) in enumerate(inside):
+        with pytest.raises(ValueError, match="inference"):
+            call(v)
+            pytest.fail(f"write {i} took an inference tensor")
+
+
+def test_saved_stream_and_logits_are_guarded():
+    """The norm's backward keeps the stream and the loss' keeps the logits: later writes in place are found out."""
+    g = gen(6)
+    x, w, r = (randn(g, *s).requires_grad_() for s in ((6, 256), (256,), (6, 256)))
+    y, s = lm.norm(x, w, r)
+    with torch.no_grad():
+        lm.rms_norm(x, w, residual=s, inplace=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    z = randn(g, 6, 50).requires_grad_() * 1.0
+    ids = torch.tensor([1, 2, 0, 3, 3, -1], device="cuda")
+    logp, _ = lm.logprobs(z, ids)
+    with torch.no_grad():
+        lm.token_logprobs_grad(z, ids, lm.token_logprobs(z, ids), torch.ones(6, device="cuda"), inplace=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        logp.sum().backward()
