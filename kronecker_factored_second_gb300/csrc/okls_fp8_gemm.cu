@@ -19,9 +19,11 @@
 // next.  The running sums of 128 x 256 results (CTA pairs, below) take half of
 // the SM's registers, so the first four warps hand theirs to the other eight.
 //
-// Every wait is bounded; when one expires the kernel raises kStTimeout and
-// runs to its end without further waits, apart from the bounded ones for its
-// own copies and MMAs.
+// Every wait is bounded; when one expires the CTA raises kStTimeout and runs to
+// its end without further waits, apart from the bounded ones for its own copies
+// and MMAs.  The CTA's waits look at a word in its shared memory, which joins
+// the caller's status word at the end: a timeout that an earlier product left
+// there must not make this one give up.
 #include <cuda_fp16.h>
 
 #include "okls_fp8_layout.h"
@@ -231,6 +233,7 @@ struct Adder {
   uint64_t *acc_full, *acc_empty, *sempty;
   uint32_t acc_empty_lead;  // PAIR: acc_empty of the cluster's first CTA
   uint8_t* out;             // PAIR: the warps' output boxes
+  uint32_t* stop;           // the CTA's status word
 };
 
 // Per-step bookkeeping of an adding warp: waits for a TMEM buffer and hands it
@@ -244,8 +247,8 @@ struct Steps {
   // try: a try holds the warp until the barrier turns or a time limit passes).
   __device__ __forceinline__ explicit Steps(const Adder<BN, PAIR>& R) { ready = mbar_test(&R.acc_full[0], 0); }
   __device__ __forceinline__ uint32_t buf() const { return Buffers<BN>::at(it); }
-  __device__ __forceinline__ const float* begin(const Adder<BN, PAIR>& R, uint32_t* status) {
-    if (!ready) ok = ok && mbar_wait(&R.acc_full[buf()], Buffers<BN>::parity(it), status);
+  __device__ __forceinline__ const float* begin(const Adder<BN, PAIR>& R) {
+    if (!ready) ok = ok && mbar_wait(&R.acc_full[buf()], Buffers<BN>::parity(it), R.stop);
     __syncwarp();
     tc_fence_after();
     return R.scales + slot * R.slot_floats;
@@ -334,7 +337,7 @@ __device__ __forceinline__ void add_square(const Fp8GemmArgs& A, const Adder<BN,
 #pragma unroll
     for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
     for (int kb = 0; kb < nkb; ++kb) {
-      const float* sc = S.begin(R, A.status);
+      const float* sc = S.begin(R);
       const uint32_t d = tbase + S.buf() * BN;
       const float s = sc[q * 32 + lane];
       const float* sb = sc + kTM - (at.tn * BN) / kFp8Group;
@@ -432,7 +435,7 @@ __device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN, P
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[c][i][0][0] = acc[c][i][0][1] = acc[c][i][1][0] = acc[c][i][1][1] = 0;
     for (int kb = 0; kb < nkb; ++kb) {
-      const float* sc = S.begin(R, A.status);
+      const float* sc = S.begin(R);
       const uint32_t d = tbase + S.buf() * BN;
       // [chunk, or in turn][half][4 i + 2 r + column]: the whole step at once
       // up to 96 columns (the buffer is then free before the additions), else
@@ -609,7 +612,7 @@ struct ScaleRows {
 template <int BN>
 __device__ __forceinline__ void copy_scales(const Fp8GemmArgs& A, float* ring, int slot_floats, int slots, uint64_t* sfull,
                                             uint64_t* sempty, int first, int stride, int row_step, int row0, int tiles_m,
-                                            int tiles_n, int nkb) {
+                                            int tiles_n, int nkb, uint32_t* stop) {
   constexpr int kBlocks = (BN + kFp8Group - 1) / kFp8Group;
   const int lane = threadIdx.x & 31, tiles = tiles_m * tiles_n;
   int slot = 0;
@@ -632,7 +635,7 @@ __device__ __forceinline__ void copy_scales(const Fp8GemmArgs& A, float* ring, i
       b.set(A.b_scale, A.ldb_row, A.ldb_group, at.tn * BN, A.n, lane);
     }
     for (int kb = 0; kb < nkb; ++kb) {
-      if (__any_sync(0xffffffffu, !mbar_wait(&sempty[slot], phase ^ 1u, A.status))) goto out;
+      if (__any_sync(0xffffffffu, !mbar_wait(&sempty[slot], phase ^ 1u, stop))) goto out;
       float* sc = ring + slot * slot_floats;
       a.copy(sc, lane);
       if (A.b_square)
@@ -654,6 +657,7 @@ template <int BN>
 __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant__ Fp8GemmArgs A) {
   using C = Tile<BN>;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t stop;  // the CTA's status word
   uint8_t* smem = smem_base(smem_raw);
   uint8_t* scales = smem + C::kRing * C::kBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(scales + C::kSlots * C::kScaleBytes);
@@ -678,9 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
     for (int b = 0; b < Buffers<BN>::kCount; ++b) {
       mbar_init(&acc_full[b], 2);   // the MMAs, and the issuer, which has seen the step's scales
       mbar_init(&acc_empty[b], 8);
-
     }
     mbar_init(drain, 1);
+    stop = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -708,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
         const TileAt at = tile_at(t, tiles_m, tiles_n);
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, A.status)) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, &stop)) {
             ok = false;
             break;
           }
@@ -727,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       const int64_t back = issued < C::kRing ? issued : C::kRing;
       for (int64_t q = 1; q <= back; ++q) {
         const int64_t idx = issued - q;
-        if (!mbar_wait_own(&full[idx % C::kRing], static_cast<uint32_t>((idx / C::kRing) & 1), A.status)) break;
+        if (!mbar_wait_own(&full[idx % C::kRing], static_cast<uint32_t>((idx / C::kRing) & 1), &stop)) break;
       }
     }
     __syncwarp();
@@ -742,8 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const uint32_t buf = Buffers<BN>::at(it);
-          if (!mbar_wait(&full[stage], phase, A.status) || !mbar_wait(&sfull[slot], sphase, A.status) ||
-              !mbar_wait(&acc_empty[buf], Buffers<BN>::parity(it) ^ 1u, A.status)) {
+          if (!mbar_wait(&full[stage], phase, &stop) || !mbar_wait(&sfull[slot], sphase, &stop) ||
+              !mbar_wait(&acc_empty[buf], Buffers<BN>::parity(it) ^ 1u, &stop)) {
             ok = false;
             break;
           }
@@ -763,18 +767,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
         }
       }
       umma_commit(drain);
-      mbar_wait_own(drain, 0, A.status);
+      mbar_wait_own(drain, 0, &stop);
     }
     __syncwarp();
   } else if (warp == 2) {
     copy_scales<BN>(A, reinterpret_cast<float*>(scales), C::kScaleBytes / 4, C::kSlots, sfull, sempty, blockIdx.x,
-                    gridDim.x, kTM, 0, tiles_m, tiles_n, nkb);
+                    gridDim.x, kTM, 0, tiles_m, tiles_n, nkb, &stop);
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
     const Adder<BN, false> R = {static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), kTM, 0, tmem,
                                 reinterpret_cast<const float*>(scales), C::kScaleBytes / 4, C::kSlots,
-                                acc_full, acc_empty, sempty, 0, nullptr};
+                                acc_full, acc_empty, sempty, 0, nullptr, &stop};
     if (A.b_square)
       add_square<BN, false>(A, R, tiles_m, tiles_n, nkb);
     else
@@ -785,6 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, C::kCols);
+  if (threadIdx.x == 0 && stop) atomicOr(A.status, stop);
 }
 
 // ------------------------------------------------------------- CTA pairs
@@ -844,6 +849,7 @@ __device__ __forceinline__ void umma_f8_step_pair(uint32_t d, uint64_t adesc, ui
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_fp8_gemm_pair(const __grid_constant__ Fp8GemmArgs A) {
   extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t stop;  // the CTA's status word
   uint8_t* smem = smem_base(smem_raw);
   uint8_t* out = smem + kPairRing * kPairStage;
   uint8_t* scales = out + 8 * kOutWarp;
@@ -873,6 +879,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
+    stop = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -901,7 +908,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int t = first; t < tiles && ok; t += stride) {
           const TileAt at = tile_at(t, tiles_m, tiles_n);
           for (int kb = 0; kb < nkb; ++kb) {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, A.status)) {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, &stop)) {
               ok = false;
               break;
             }
@@ -923,7 +930,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int64_t back = issued < kPairRing ? issued : kPairRing;
           for (int64_t q = 1; q <= back; ++q) {
             const int64_t idx = issued - q;
-            if (!mbar_wait_own_cluster(&full[idx % kPairRing], static_cast<uint32_t>((idx / kPairRing) & 1), A.status)) break;
+            if (!mbar_wait_own_cluster(&full[idx % kPairRing], static_cast<uint32_t>((idx / kPairRing) & 1), &stop)) break;
           }
         }
       }
@@ -938,9 +945,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t total = steps_of(first, stride, tiles, nkb);
         for (uint32_t it = mine; it < total; it += 2) {
           const uint32_t buf = Buffers<kPN>::at(it), stage = it % kPairRing, slot = it % kPairSlots;
-          if (!mbar_wait(&full[stage], (it / kPairRing) & 1u, A.status) ||
-              !mbar_wait(&sfull[slot], (it / kPairSlots) & 1u, A.status) ||
-              !mbar_wait(&acc_empty[buf], Buffers<kPN>::parity(it) ^ 1u, A.status))
+          if (!mbar_wait(&full[stage], (it / kPairRing) & 1u, &stop) ||
+              !mbar_wait(&sfull[slot], (it / kPairSlots) & 1u, &stop) ||
+              !mbar_wait(&acc_empty[buf], Buffers<kPN>::parity(it) ^ 1u, &stop))
             break;
           mbar_arrive(&acc_full[buf]);
           tc_fence_after();
@@ -949,12 +956,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           umma_commit_pair(&empty[stage], 3);
         }
         umma_commit_pair(&drain[mine], 1);
-        mbar_wait_own_cluster(&drain[mine], 0, A.status);
+        mbar_wait_own_cluster(&drain[mine], 0, &stop);
       }
       __syncwarp();
     } else if (warp == 2) {
       copy_scales<kPN>(A, reinterpret_cast<float*>(scales), kPairScaleBytes / 4, kPairSlots, sfull, sempty, first, stride,
-                       2 * kTM, rank * kTM, tiles_m, tiles_n, nkb);
+                       2 * kTM, rank * kTM, tiles_m, tiles_n, nkb, &stop);
     } else if (warp == 1) {
       if (lane == 0) {
         // one arrival a step and buffer, after the buffer's step before is over
@@ -964,8 +971,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int kb = 0; kb < nkb; ++kb, ++it) {
             constexpr uint32_t kBufs = Buffers<kPN>::kCount;
             const uint32_t buf = Buffers<kPN>::at(it);
-            if ((it >= kBufs && !mbar_wait(&acc_full[buf], Buffers<kPN>::parity(it - kBufs), A.status)) ||
-                !mbar_wait(&sfull[slot], sphase, A.status)) {
+            if ((it >= kBufs && !mbar_wait(&acc_full[buf], Buffers<kPN>::parity(it - kBufs), &stop)) ||
+                !mbar_wait(&sfull[slot], sphase, &stop)) {
               ok = false;
               break;
             }
@@ -983,7 +990,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
     const Adder<kPN, true> R = {first, stride, 2 * kTM, rank * kTM, tmem,
                                 reinterpret_cast<const float*>(scales), kPairScaleBytes / 4, kPairSlots,
-                                acc_full, acc_empty, sempty, mapa_shared(smem_u32(acc_empty), 0), out};
+                                acc_full, acc_empty, sempty, mapa_shared(smem_u32(acc_empty), 0), out, &stop};
     if (A.b_square)
       add_square<kPN, true>(A, R, tiles_m, tiles_n, nkb);
     else
@@ -998,6 +1005,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (threadIdx.x == 0 && stop) atomicOr(A.status, stop);
 }
 
 // ------------------------------------------------------------ a few tokens

@@ -16,8 +16,8 @@ static_assert(128 * kCtlRegs + 256 * kAddRegs <= kThreads * 168, "more registers
 constexpr int kABytes = kTM * kTK;
 
 // The swizzled boxes start at a multiple of 1024 bytes; dynamic shared memory
-// is only known to start at a multiple of 16, so a launch asks for what the
-// rounding up may take.
+// is only known to start at a multiple of 16 (the kernels' static variables
+// come before it), so a launch asks for what the rounding up may take.
 constexpr int kSmemAlign = 1024;
 
 // 8-byte barriers, and the word that takes the TMEM address.

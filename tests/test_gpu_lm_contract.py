@@ -281,3 +281,23 @@ def test_saved_stream_and_logits_are_guarded():
         lm.token_logprobs_grad(z, ids, lm.token_logprobs(z, ids), torch.ones(6, device="cuda"), inplace=True)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         logp.sum().backward()
+
+
+@pytest.mark.parametrize("m,n,k", [(300, 19500, 128), (2048, 5504, 1024), (200, 1000, 4096)])
+def test_an_old_timeout_does_not_stop_a_product(m, n, k):
+    """A timeout that another call left in the status word stays to be read, and changes no later product."""
+    g = gen(m)
+    a, b = lm.fp8_quantize(randn(g, m, k)), lm.fp8_quantize(randn(g, n, k), block="square")
+    want = lm.fp8_matmul(a, b)
+    out = torch.empty_like(want)
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    word[0] = L.DEV_TIMEOUT | L.DEV_BAD_TOKEN
+    stream = torch.cuda.current_stream().cuda_stream
+    for _ in range(3):
+        out.fill_(float("nan"))
+        assert L.lib().okls_fp8_matmul(
+            a.data.data_ptr(), a.data.stride(0), a.scale.data_ptr(), a.scale.stride(0), a.scale.stride(1),
+            b.data.data_ptr(), b.data.stride(0), b.scale.data_ptr(), b.scale.stride(0), b.scale.stride(1), L.FP8_SQUARE,
+            m, n, k, out.data_ptr(), L.OKLS_BF16, n, 0, word.data_ptr(), stream) == L.OKLS_OK
+        assert torch.equal(out, want)
+    assert word.item() == L.DEV_TIMEOUT | L.DEV_BAD_TOKEN
