@@ -481,8 +481,10 @@ okls_status okls_inv_root_noalloc(const float *S_dev, float *P_dev, int64_t d,
  *     OKLS_DEV_BAD_TOKEN.
  * ====================================================================== */
 
-/* Synchronise `stream`, read the status word into *dev_status (may be NULL)
- * and clear it.  Returns OKLS_ERR_TIMEOUT / OKLS_ERR_INVALID_ARG when
+/* Read the status word into *dev_status (may be NULL) and clear it, in one
+ * step and in `stream`'s order, and synchronise `stream`.  Covers the work
+ * ordered before it; what runs on other streams may raise bits before or
+ * after, and none is lost.  Returns OKLS_ERR_TIMEOUT / OKLS_ERR_INVALID_ARG when
  * OKLS_DEV_TIMEOUT / OKLS_DEV_BAD_TOKEN was set, OKLS_OK otherwise. */
 okls_status okls_status_word_read(uint32_t *status_dev, void *stream,
                                   uint32_t *dev_status);

@@ -2,6 +2,7 @@
 // include/okls.h for the contract).
 #include <string.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "okls_host.h"
@@ -70,6 +71,15 @@ okls_status check_workspace(const char* op, const void* ws, size_t have, size_t 
   return OKLS_OK;
 }
 
+// Words that status reads take their bits through: calls at the same time use
+// words of their own.
+constexpr uint32_t kTaken = 256;
+__device__ uint32_t g_taken[kTaken];
+
+// Reads and clears in one step: bits that a launch on another stream raises
+// meanwhile are read now or stay for the next read.
+__global__ void k_status_take(uint32_t* status, uint32_t* taken) { *taken = atomicExch(status, 0u); }
+
 constexpr int64_t kMaxSide = (int64_t(1) << 31) - 2;
 constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 
@@ -79,11 +89,18 @@ extern "C" {
 
 okls_status okls_status_word_read(uint32_t* status_dev, void* stream, uint32_t* dev_status) {
   LM_TRY(check_status("okls_status_word_read", status_dev));
+  static std::atomic<uint32_t> next{0};
   uint32_t v = 0;
+  void* words = nullptr;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemcpyAsync(&v, status_dev, sizeof(v), cudaMemcpyDeviceToHost, st);
-  if (e == cudaSuccess) e = cudaMemsetAsync(status_dev, 0, sizeof(v), st);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  cudaError_t e = cudaGetSymbolAddress(&words, g_taken);
+  if (e == cudaSuccess) {
+    uint32_t* taken = static_cast<uint32_t*>(words) + next.fetch_add(1) % kTaken;
+    k_status_take<<<1, 1, 0, st>>>(status_dev, taken);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&v, taken, sizeof(v), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  }
   if (e != cudaSuccess) return launched("okls_status_word_read", e);
   if (dev_status) *dev_status = v;
   if (v & OKLS_DEV_TIMEOUT) return host_fail(OKLS_ERR_TIMEOUT, "a bounded device wait expired");

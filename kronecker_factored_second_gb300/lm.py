@@ -73,7 +73,11 @@ def _on(stream, *tensors):
 
 def query_status(device=None, stream=None) -> int:
     """Synchronise the stream and return (and clear) the device's status word;
-    raises OklsError for a token id past the vocabulary or an expired wait."""
+    raises OklsError for a token id past the vocabulary or an expired wait.
+
+    One word serves all streams of the device.  The read covers the work
+    ordered before it on the given stream; other streams' work may report to
+    this read or to the next."""
     index = torch.device("cuda" if device is None else device).index
     if index is None:
         index = torch.cuda.current_device()

@@ -301,3 +301,28 @@ def test_an_old_timeout_does_not_stop_a_product(m, n, k):
             m, n, k, out.data_ptr(), L.OKLS_BF16, n, 0, word.data_ptr(), stream) == L.OKLS_OK
         assert torch.equal(out, want)
     assert word.item() == L.DEV_TIMEOUT | L.DEV_BAD_TOKEN
+
+
+def test_status_bits_of_other_streams_are_not_lost():
+    """Bad tokens on one stream while another reads and clears the word: each is reported once they are both done."""
+    w = randn(gen(7), 10, 16)
+    bad, good = torch.tensor([11], device="cuda"), torch.tensor([1], device="cuda")
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def read(stream=None):
+        try:
+            return lm.query_status(stream=stream)
+        except L.OklsError as e:
+            assert e.code == L.OKLS_ERR_INVALID_ARG
+            return L.DEV_BAD_TOKEN
+
+    for i in range(300):
+        with torch.cuda.stream(one):
+            for _ in range(i % 7):
+                lm.embedding(w, good)
+            lm.embedding(w, bad)
+        seen = read(two)
+        one.synchronize()
+        assert seen | read(two) == L.DEV_BAD_TOKEN, i
+        assert read(one) == 0
