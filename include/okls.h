@@ -481,6 +481,10 @@ okls_status okls_inv_root_noalloc(const float *S_dev, float *P_dev, int64_t d,
  *     OKLS_DEV_BAD_TOKEN.
  * ====================================================================== */
 
+/* The library's own status word on the current device, zero since the library
+ * was loaded: for callers that keep none of their own.  Synchronises nothing. */
+okls_status okls_status_word(uint32_t **status_dev);
+
 /* Read the status word into *dev_status (may be NULL) and clear it, in one
  * step and in `stream`'s order, and synchronise `stream`.  Covers the work
  * ordered before it; what runs on other streams may raise bits before or

@@ -127,6 +127,7 @@ _SIGS = {
     "okls_inv_root": (_I32, [_P, _P, _P, _P, _I64, _I64, _I32, _I32, _F, _F, _P, _SZ, _P]),
     "okls_inv_root_noalloc_capacity": (_SZ, []),
     "okls_inv_root_noalloc": (_I32, [_P, _P, _I64, _I64, _I32, _I32, _F, _F, _P]),
+    "okls_status_word": (_I32, [ctypes.POINTER(_P)]),
     "okls_status_word_read": (_I32, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
     "okls_embedding": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _I32, _I64, _F, _P, _I32, _I64, _P, _P]),
     "okls_embedding_grad_workspace_bytes": (_I32, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),

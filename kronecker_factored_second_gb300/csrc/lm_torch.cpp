@@ -11,7 +11,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
-#include <mutex>
+#include <atomic>
 #include <optional>
 #include <tuple>
 
@@ -130,22 +130,19 @@ struct Call {
 
 void* ptr_of(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
-// One status word a device, zeroed and waited for before its first use, so
-// that any stream may use it.  Kept to the end of the process.
-Tensor status_word(int64_t device) {
-  static std::mutex mu;
-  static Tensor* words[64] = {};
+// The library's status word of a device, by its address.
+uint32_t* status_word(int64_t device) {
+  static std::atomic<uint32_t*> words[64] = {};
   REFUSE(device < 0 || device >= 64, "device index ", device);
-  std::lock_guard<std::mutex> lock(mu);
-  if (!words[device]) {
+  uint32_t* w = words[device].load();
+  if (!w) {
     c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
-    Tensor w = at::zeros({64}, at::TensorOptions().dtype(at::kInt).device(at::kCUDA, static_cast<c10::DeviceIndex>(device)));
-    c10::cuda::getCurrentCUDAStream().synchronize();
-    words[device] = new Tensor(w);
+    check(okls_status_word(&w));
+    words[device].store(w);
   }
-  return *words[device];
+  return w;
 }
-uint32_t* status_of(const Tensor& t) { return static_cast<uint32_t*>(status_word(t.device().index()).data_ptr()); }
+uint32_t* status_of(const Tensor& t) { return status_word(t.device().index()); }
 
 // ---------------------------------------------------------------- embedding
 Tensor embedding(const Tensor& weight, const Tensor& ids, double scale, std::optional<at::ScalarType> out_dtype) {
@@ -378,7 +375,7 @@ Tensor token_logprobs_grad(const Tensor& logits, const Tensor& ids, const Tensor
 PYBIND11_MODULE(_lm_native, m) {
   py::object error = py::module_::import("kronecker_factored_second_gb300._lib").attr("OklsError");
   g_okls_error = error.release().ptr();
-  m.def("status_word", &status_word);
+  m.def("status_word", [](int64_t device) { return reinterpret_cast<uintptr_t>(status_word(device)); });
   m.def("embedding", &embedding);
   m.def("embedding_grad", &embedding_grad);
   m.def("rms_norm", &rms_norm);

@@ -71,6 +71,9 @@ okls_status check_workspace(const char* op, const void* ws, size_t have, size_t 
   return OKLS_OK;
 }
 
+// The library's own status word (okls_status_word).
+__device__ uint32_t g_status;
+
 // Words that status reads take their bits through: calls at the same time use
 // words of their own.
 constexpr uint32_t kTaken = 256;
@@ -86,6 +89,16 @@ constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 }  // namespace
 
 extern "C" {
+
+okls_status okls_status_word(uint32_t** status_dev) {
+  if (!status_dev) return bad("okls_status_word", "status_dev is NULL");
+  int sms = 0;
+  LM_TRY(host_device_sms(&sms));
+  void* p = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&p, g_status);
+  if (e == cudaSuccess) *status_dev = static_cast<uint32_t*>(p);
+  return launched("okls_status_word", e);
+}
 
 okls_status okls_status_word_read(uint32_t* status_dev, void* stream, uint32_t* dev_status) {
   LM_TRY(check_status("okls_status_word_read", status_dev));

@@ -85,7 +85,7 @@ def query_status(device=None, stream=None) -> int:
         word = _n().status_word(index)
         s = torch.cuda.current_stream() if stream is None else stream
         v = ctypes.c_uint32(0)
-        L.check(L.lib().okls_status_word_read(word.data_ptr(), s.cuda_stream, ctypes.byref(v)))
+        L.check(L.lib().okls_status_word_read(word, s.cuda_stream, ctypes.byref(v)))
     return v.value
 
 

@@ -326,3 +326,39 @@ def test_status_bits_of_other_streams_are_not_lost():
         one.synchronize()
         assert seen | read(two) == L.DEV_BAD_TOKEN, i
         assert read(one) == 0
+
+
+FIRST = """
+import torch
+from kronecker_factored_second_gb300 import lm
+g = torch.Generator(device="cuda"); g.manual_seed(0)
+W = torch.randn(300, 256, generator=g, device="cuda"); nw = torch.ones(256, device="cuda")
+ids = torch.randint(-1, 300, (200,), generator=g, device="cuda"); gl = torch.ones(200, device="cuda")
+def chain():
+    x = lm.embedding(W, ids)
+    n = lm.rms_norm(x, nw, residual=x)
+    z = lm.fp8_matmul(lm.fp8_quantize(n.y), lm.fp8_quantize(W, block="square"), out_dtype=torch.float32)
+    r = lm.token_logprobs(z, ids, top_k=3)
+    dz = lm.token_logprobs_grad(z, ids, r, gl, dentropy=gl)
+    ds, dw = lm.rms_norm_grad(x, n.residual, nw, n.rstd)
+    return z, r.logp, r.top_ids, dz, ds, dw, lm.embedding_grad(ds, ids, 300)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    first = chain()
+graph.replay()
+for a, b in zip(first, chain()):
+    assert torch.equal(a, b)
+assert lm.query_status() == 0
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    """No call synchronises or sets anything up that a capture forbids, the first of a process included."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
