@@ -67,8 +67,19 @@ def _torch_flags() -> tuple[list[str], list[str]]:
             "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + inc, link
 
 
+def _compile_binding() -> tuple[str, str, list[str]]:
+    """Compile the torch binding; returns the compiler, the object and the link flags."""
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    flags, link = _torch_flags()
+    obj = os.path.join(BUILD, BINDING + ".o")
+    _run([cxx, "-c", os.path.join(CSRC, BINDING), "-o", obj] + flags)
+    return cxx, obj, link
+
+
 def build_library(verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every source for sm_103a and link libokls.so; returns its path."""
+    """Compile every source for sm_103a and link libokls.so, then the torch binding; returns libokls.so's path.
+
+    The C library needs nvcc alone: it is in place before anything of the binding (torch, the host compiler) can fail."""
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
@@ -81,19 +92,19 @@ def build_library(verbose: bool = False, ptxas_info: bool = False) -> str:
         _run(cmd)
         return obj
 
-    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
-    flags, link = _torch_flags()
-    binding = os.path.join(BUILD, BINDING + ".o")
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        host = ex.submit(_run, [cxx, "-c", os.path.join(CSRC, BINDING), "-o", binding] + flags)
+        host = ex.submit(_compile_binding)
         objs = list(ex.map(one, SOURCES))
-        host.result()
-    tmp = LIB + ".tmp"
-    _run([cc, "-shared", "-o", tmp] + objs + ARCH + ["--cudart", "static", "-Xcompiler", "-fPIC"])
-    os.replace(tmp, LIB)
-    tmp = BINDING_LIB + ".tmp"
-    _run([cxx, "-shared", "-o", tmp, binding, "-L" + PKG, "-lokls", "-Wl,-rpath,$ORIGIN"] + link)
-    os.replace(tmp, BINDING_LIB)
+        tmp = LIB + ".tmp"
+        _run([cc, "-shared", "-o", tmp] + objs + ARCH + ["--cudart", "static", "-Xcompiler", "-fPIC"])
+        os.replace(tmp, LIB)
+        try:
+            cxx, obj, link = host.result()
+            tmp = BINDING_LIB + ".tmp"
+            _run([cxx, "-shared", "-o", tmp, obj, "-L" + PKG, "-lokls", "-Wl,-rpath,$ORIGIN"] + link)
+            os.replace(tmp, BINDING_LIB)
+        except Exception as e:
+            raise RuntimeError(f"libokls.so is built, its torch binding (lm.py) is not: {e}") from e
     return LIB
 
 

@@ -208,3 +208,42 @@ def test_norm_refuses_outputs_without_a_gradient(on_cpu):
                 pytest.fail(f"{dtype} was taken")
     for dtype in (None, torch.float32, torch.bfloat16):
         assert on_cpu.norm(x, w, out_dtype=dtype).requires_grad
+
+
+def test_library_status_word_needs_a_place(lib):
+    assert lib.okls_status_word(None) == BAD
+
+
+def test_c_library_is_built_without_the_torch_binding(monkeypatch, tmp_path):
+    """A C client needs nvcc alone: whatever fails in the torch binding, the C library is in place and the error says so."""
+    from kronecker_factored_second_gb300 import build
+    for name in ("BUILD", "LIB", "BINDING_LIB"):
+        monkeypatch.setattr(build, name, str(tmp_path / name))
+
+    def run_without(broken):
+        def run(cmd):
+            if broken in " ".join(cmd):
+                raise RuntimeError("command failed")
+            if "-o" in cmd:
+                open(cmd[cmd.index("-o") + 1], "w").close()
+        return run
+
+    def no_torch():
+        raise ImportError("no torch here")
+
+    import os
+    for broken in ("torch", build.BINDING, "-lokls"):
+        for f in ("LIB", "BINDING_LIB"):
+            if os.path.exists(tmp_path / f):
+                os.remove(tmp_path / f)
+        with monkeypatch.context() as m:
+            m.setattr(build, "_run", run_without(broken if broken != "torch" else "nothing"))
+            m.setattr(build, "_torch_flags", no_torch if broken == "torch" else lambda: ([], []))
+            with pytest.raises((RuntimeError, ImportError), match="libokls.so is built"):
+                build.build_library()
+        assert os.path.exists(tmp_path / "LIB") and not os.path.exists(tmp_path / "BINDING_LIB"), broken
+    with monkeypatch.context() as m:
+        m.setattr(build, "_run", run_without("nothing"))
+        m.setattr(build, "_torch_flags", lambda: ([], []))
+        assert build.build_library() == str(tmp_path / "LIB")
+    assert os.path.exists(tmp_path / "BINDING_LIB")
