@@ -362,3 +362,59 @@ def test_first_calls_of_a_process_can_be_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dim", [1, 153, 257, 1001, 1028, 2044, 2049, 3001, 4102])
+@pytest.mark.parametrize("dtype,out_dtype", [(BF16, F32), (F32, F32), (F32, BF16)])
+def test_embedding_gradient_of_rows_that_are_not_aligned(dtype, out_dtype, dim):
+    """Rows that start off 16-byte boundaries in any of dy, base and out: new, added, in place, and with few tokens."""
+    g = gen(dim)
+    vocab = 700
+    for tokens, pd, pb, po in ((5, 0, 0, 0), (900, 0, 0, 0), (900, 3, 1, 8), (900, 1, 8, 5), (2500, 8, 0, 1)):
+        def rows(n, pitch, dt):
+            return randn(g, n, dim + pitch, dtype=dt)[:, :dim]
+        dy, base, out = rows(tokens, pd, dtype), rows(vocab, pb, out_dtype), rows(vocab, po, out_dtype)
+        ids = torch.randint(-20, vocab, (tokens,), generator=g, device="cuda").clamp_min(-1)
+        ids[tokens // 3:tokens // 2] = 17  # a token of many chunks
+        keep = ids >= 0
+        zero = torch.zeros(vocab, dim, dtype=torch.float64, device="cuda")
+        total = zero.index_add(0, ids[keep], dy[keep].double())
+        mag = zero.index_add(0, ids[keep], dy[keep].double().abs())
+        n = torch.bincount(ids[keep], minlength=vocab).double()[:, None]
+        for b in (None, base):
+            want = total * 0.5 + (0 if b is None else b.double())
+            # n additions, the scaling and the base: one rounding each, then the output's
+            bound = (n + 2) * U * (mag * 0.5 + (0 if b is None else b.double().abs()))
+            bound = bound + (2.0 ** -8 if out_dtype == BF16 else U) * want.abs()
+            fresh = lm.embedding_grad(dy, ids, vocab, scale=0.5, base=b, dtype=out_dtype)
+            assert ((fresh.double() - want).abs() - bound).max().item() <= 0
+            lm.embedding_grad(dy, ids, vocab, scale=0.5, base=b, out=out)
+            assert torch.equal(out, fresh)
+        lm.embedding_grad(dy, ids, vocab, scale=0.5, base=base, out=base)
+        assert torch.equal(base, fresh)
+
+
+@pytest.mark.parametrize("tokens,vocab,dim", [(79, 37178, 3435), (9, 55846, 1662), (2112, 33216, 5217), (100, 65536, 1001)])
+def test_embedding_gradient_is_no_slower_than_a_plain_one(tokens, vocab, dim):
+    """Rows off 16-byte boundaries: the new and the added gradient against torch's fill or copy and index_add_."""
+    g = gen(tokens)
+    dy, base = randn(g, tokens, dim), randn(g, vocab, dim)
+    ids = torch.randint(0, vocab, (tokens,), generator=g, device="cuda")
+
+    def us(f):
+        times = []
+        for i in range(13):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            f()
+            b.record()
+            b.synchronize()
+            if i >= 3:
+                times.append(a.elapsed_time(b) * 1e3)
+        return sorted(times)[len(times) // 2]
+
+    for own, plain in ((lambda: lm.embedding_grad(dy, ids, vocab),
+                        lambda: torch.zeros(vocab, dim, device="cuda").index_add_(0, ids, dy)),
+                       (lambda: lm.embedding_grad(dy, ids, vocab, base=base), lambda: base.clone().index_add_(0, ids, dy))):
+        a, b = us(own), us(plain)
+        assert a <= 1.5 * b, f"{a:.0f} us, plain {b:.0f}"
