@@ -418,3 +418,132 @@ def test_embedding_gradient_is_no_slower_than_a_plain_one(tokens, vocab, dim):
                        (lambda: lm.embedding_grad(dy, ids, vocab, base=base), lambda: base.clone().index_add_(0, ids, dy))):
         a, b = us(own), us(plain)
         assert a <= 1.5 * b, f"{a:.0f} us, plain {b:.0f}"
+
+
+@pytest.mark.parametrize("m,n,k", [(7, 300, 520), (300, 19500, 130), (2048, 5504, 256), (515, 700, 2047)])
+def test_scales_laid_out_by_the_caller(m, n, k):
+    """Scale matrices with contiguous rows, and cut out of wider ones: the products of the quantiser's own layout."""
+    g = gen(m + n)
+    x, w = randn(g, m, k) * torch.exp(randn(g, m, 1)), randn(g, n, k)
+    a = lm.fp8_quantize(x)
+
+    def laid_out(f):
+        wide = torch.full((f.scale.shape[0], f.scale.shape[1] + 3), float("nan"), device="cuda")
+        wide[:, 1:1 + f.scale.shape[1]] = f.scale
+        tall = torch.full((f.scale.shape[1], f.scale.shape[0] + 5), float("nan"), device="cuda")
+        tall[:, 2:2 + f.scale.shape[0]] = f.scale.t()
+        return [lm.Fp8Tensor(f.data, s, f.block) for s in
+                (f.scale.contiguous(), wide[:, 1:1 + f.scale.shape[1]], tall[:, 2:2 + f.scale.shape[0]].t())]
+
+    for block in ("row", "square"):
+        b = lm.fp8_quantize(w, block=block)
+        for out_dtype in (BF16, F32):
+            want = lm.fp8_matmul(a, b, out_dtype=out_dtype)
+            for f, h in zip(laid_out(a), laid_out(b)):
+                assert torch.equal(lm.fp8_matmul(f, h, out_dtype=out_dtype), want)
+                assert torch.equal(lm.fp8_matmul(a, h, out_dtype=out_dtype), want)
+
+
+def test_two_streams_at_once():
+    """Two chains of all operators that run at the same time give what they give one after the other."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    data = []
+    for seed in (1, 2):
+        g = gen(seed)
+        rows = 1500 + 700 * seed
+        data.append((randn(g, rows, 1024, dtype=BF16), randn(g, 2304, 1024, dtype=BF16, std=0.03), randn(g, 1024, dtype=BF16),
+                     torch.randint(-1, 2304, (rows,), generator=g, device="cuda")))
+
+    def chain(x, w, nw, ids):
+        h = lm.embedding(w, ids, scale=2.0)
+        n = lm.rms_norm(x, nw, residual=h)
+        q, qt = lm.fp8_quantize(n.y, both=True)
+        z = lm.fp8_matmul(q, lm.fp8_quantize(w, block="square"))
+        r = lm.token_logprobs(z, ids, top_k=9)
+        one = torch.ones(x.shape[0], device="cuda")
+        dz = lm.token_logprobs_grad(z, ids, r, one, dentropy=one)
+        dw = lm.fp8_matmul(lm.fp8_quantize(dz, transpose=True), qt)
+        ds, dn = lm.rms_norm_grad(x, n.residual, nw, n.rstd)
+        return z, r.logp, r.top_ids, dz, dw, ds, dn, lm.embedding_grad(ds, ids, 2304)
+
+    want = [chain(*d) for d in data]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [[], []]
+        for _ in range(3):
+            for i, (s, d) in enumerate(zip(streams, data)):
+                with torch.cuda.stream(s):
+                    got[i].append(chain(*d))
+        torch.cuda.synchronize()
+        for i in range(2):
+            for each in got[i]:
+                for a, b in zip(each, want[i]):
+                    assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: the last rows are those of the same rows alone."""
+    g = gen(8)
+    rows, cols, tail = 66000, 32768, 200
+    x = torch.empty(rows, cols, device="cuda", dtype=BF16)
+    x[:-tail] = 0.25
+    x[-tail:] = randn(g, tail, cols, dtype=BF16)
+    assert x.numel() > 1 << 31
+    end = x[-tail:].clone()
+    ids = torch.randint(0, cols, (rows,), generator=g, device="cuda")
+    # norm and its gradient, and the 8-bit output
+    w = randn(g, cols, dtype=BF16)
+    n, m = lm.rms_norm(x, w), lm.rms_norm(end, w)
+    assert torch.equal(n.y[-tail:], m.y) and torch.equal(n.rstd[-tail:], m.rstd)
+    del n
+    n = lm.rms_norm(x, w, out_dtype=E4M3)
+    e8 = lm.rms_norm(end, w, out_dtype=E4M3).y
+    assert torch.equal(n.y.data[-tail:].view(torch.uint8), e8.data.view(torch.uint8))
+    assert torch.equal(n.y.scale[-tail:], e8.scale)
+    del n
+    ds, _ = lm.rms_norm_grad(x, x, w, torch.ones(rows, device="cuda"), need_dweight=False)
+    assert torch.equal(ds[-tail:], lm.rms_norm_grad(end, end, w, torch.ones(tail, device="cuda"), need_dweight=False)[0])
+    del ds
+    # log probabilities and their gradient in place, over the same memory
+    r, s = lm.token_logprobs(x, ids, top_k=4), lm.token_logprobs(end, ids[-tail:], top_k=4)
+    assert torch.equal(r.top_ids[-tail:], s.top_ids)
+    # few rows are split between CTAs, so the sums have another order: each is off by (64 + 16 spread + vocab / 256) u
+    for a, b in ((r.logp, s.logp), (r.entropy, s.entropy), (r.lse, s.lse)):
+        assert ((a[-tail:] - b).abs() - 2 * (64 + 16 * 12 + cols / 256) * U - 4 * U * b.abs()).max().item() <= 0
+    s = lm.TokenLogprobs(None, r.entropy[-tail:], r.lse[-tail:], lse_rest=r.lse_rest[-tail:])
+    one = torch.ones(rows, device="cuda")
+    d = lm.token_logprobs_grad(x, ids, r, one)
+    assert torch.equal(d[-tail:], lm.token_logprobs_grad(end, ids[-tail:], s, one[-tail:]))
+    del d
+    # codes of both orientations, and a product whose output passes 2^31
+    q, qt = lm.fp8_quantize(x, both=True)
+    e = lm.fp8_quantize(end)
+    assert torch.equal(q.data[-tail:].view(torch.uint8), e.data.view(torch.uint8)) and torch.equal(q.scale[-tail:], e.scale)
+    assert torch.equal(lm.fp8_quantize(x[rows // 128 * 128:], transpose=True).data.view(torch.uint8),
+                       qt.data[:, rows // 128 * 128:].view(torch.uint8))
+    del q, qt
+    # the table, its rows and its gradient
+    at = torch.cat([torch.arange(rows - tail, rows, device="cuda"), torch.tensor([-1], device="cuda")])
+    y = lm.embedding(x, at)
+    assert torch.equal(y[:-1], end) and y[-1].abs().max().item() == 0
+    dw = lm.embedding_grad(y, at, rows, dtype=BF16)
+    assert torch.equal(dw[-tail:], end) and dw[:-tail].abs().max().item() == 0
+    del dw, y, x
+    a, b = lm.fp8_quantize(randn(g, rows, 128)), lm.fp8_quantize(randn(g, cols, 128), block="square")
+    c = lm.fp8_matmul(a, b)
+    last = lm.Fp8Tensor(a.data[-512:], a.scale[-512:], "row")
+    want = last.float() @ b.float().t()
+    # bf16's rounding, and the order of 128 additions
+    assert ((c[-512:].float() - want).abs() - 2.0 ** -8 * want.abs() - 1e-3).max().item() <= 0
+
+
+def test_alternatives_of_a_very_long_row():
+    """Rows longer than the maxima that a cluster keeps (131072 columns a CTA, 8 CTAs)."""
+    g = gen(9)
+    z = randn(g, 2, 1_100_003, dtype=BF16)
+    ids = torch.tensor([1_100_002, 5], device="cuda")
+    r = lm.token_logprobs(z, ids, top_k=7)
+    i = torch.sort(z.float(), dim=-1, descending=True, stable=True)[1][:, :7]
+    assert torch.equal(r.top_ids, i.int())
+    lp = torch.log_softmax(z.double(), -1)
+    assert (r.logp - lp.gather(1, ids[:, None])[:, 0]).abs().max().item() < 1e-4
