@@ -651,6 +651,18 @@ __global__ void __launch_bounds__(kGradThreads) k_token_logprobs_grad(const Scor
   const int64_t c1 = min(A.vocab, c0 + kGradCols);
   const T* z = static_cast<const T*>(A.logits) + row * A.ldl;
   T* o = static_cast<T*>(A.dlogits) + row * A.ldd;
+  const int64_t mz = (reinterpret_cast<uintptr_t>(z + c0) & 15) / sizeof(T);
+  const int64_t mo = (reinterpret_cast<uintptr_t>(o + c0) & 15) / sizeof(T);
+  const int64_t head = min(c1 - c0, mz ? static_cast<int64_t>(16 / sizeof(T)) - mz : int64_t(0));
+  const int64_t b0 = c0 + head;
+  const int nvec = mz == mo ? static_cast<int>((c1 - b0) / 8) : 0;
+  // the logits are on their way before the row's statistics are looked up
+  Pack<T> v[kGradVecs];
+#pragma unroll
+  for (int u = 0; u < kGradVecs; ++u) {
+    const int i = threadIdx.x + u * kGradThreads;
+    if (i < nvec) v[u].load(z + b0 + i * 8);
+  }
   RowGrad R;
   R.scale = A.scale;
   R.lse = A.lse[row];
@@ -670,39 +682,30 @@ __global__ void __launch_bounds__(kGradThreads) k_token_logprobs_grad(const Scor
     const float d = grad_of<ENT>(R, to_f32(z[c]));
     o[c] = from_f32<T>(c == id ? d + own : d);
   };
-  const int64_t mz = (reinterpret_cast<uintptr_t>(z + c0) & 15) / sizeof(T);
-  const int64_t mo = (reinterpret_cast<uintptr_t>(o + c0) & 15) / sizeof(T);
   if (mz != mo) {
     // the two rows are aligned differently: element by element
 #pragma unroll 4
     for (int64_t c = c0 + threadIdx.x; c < c1; c += kGradThreads) one(c);
     return;
   }
-  const int64_t head = min(c1 - c0, mz ? static_cast<int64_t>(16 / sizeof(T)) - mz : int64_t(0));
-  const int64_t b0 = c0 + head;
-  const int nvec = static_cast<int>((c1 - b0) / 8);
   const int64_t t0 = b0 + nvec * 8;
   if (threadIdx.x < head) one(c0 + threadIdx.x);
   if (threadIdx.x < c1 - t0) one(t0 + threadIdx.x);
-  float v[kGradVecs][8];
-#pragma unroll
-  for (int u = 0; u < kGradVecs; ++u) {
-    const int i = threadIdx.x + u * kGradThreads;
-    if (i < nvec) load8(z + b0 + i * 8, v[u]);
-  }
 #pragma unroll
   for (int u = 0; u < kGradVecs; ++u) {
     const int i = threadIdx.x + u * kGradThreads;
     if (i >= nvec) break;
     const int64_t c = b0 + i * 8;
+    float d[8];
+    v[u].unpack(d);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[u][j] = grad_of<ENT>(R, v[u][j]);
+    for (int j = 0; j < 8; ++j) d[j] = grad_of<ENT>(R, d[j]);
     if (id >= c && id < c + 8) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (c + j == id) v[u][j] += own;
+        if (c + j == id) d[j] += own;
     }
-    store8(o + c, v[u]);
+    store8(o + c, d);
   }
 }
 
