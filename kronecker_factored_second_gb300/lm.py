@@ -322,6 +322,7 @@ class _Linear(torch.autograd.Function):
             fp8_quantize(weight, block="square"), None)
         # an empty output of this node: stands in the backward for x and weight, which are not kept
         tie = x.new_empty(0)
+        ctx.set_materialize_grads(False)  # nothing flows back into it
         ctx.save_for_backward(*[t for f in (xt, wt) if f is not None for t in (f.data, f.scale)], tie)
         ctx.meta = (xt is not None, wt is not None, x.shape, x.dtype, weight.dtype)
         return fp8_matmul(xq, wq, out_dtype=out_dtype or x.dtype).view(*x.shape[:-1], weight.shape[0]), tie
