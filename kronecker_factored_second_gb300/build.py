@@ -61,7 +61,7 @@ def _torch_flags() -> tuple[list[str], list[str]]:
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     inc = ["-I" + p for p in (os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
                               os.path.join(cuda, "include"), sysconfig.get_paths()["include"])]
-    link = ["-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+    link = ["-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
             "-Wl,-rpath," + os.path.join(t, "lib")]
     return ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wno-sign-compare", "-DTORCH_API_INCLUDE_EXTENSION_H",
             "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + inc, link

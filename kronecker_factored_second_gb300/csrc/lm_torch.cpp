@@ -5,6 +5,7 @@
 //
 // Wrong tensors raise ValueError; what the C entry refuses raises OklsError.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/GradMode.h>
 #include <c10/core/InferenceMode.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -122,7 +123,10 @@ struct Call {
   at::TensorOptions opt;
   explicit Call(const Tensor& t) : guard(t.device()), opt(t.options().requires_grad(false)) {}
   void* stream() const { return c10::cuda::getCurrentCUDAStream().stream(); }
-  Tensor empty(at::IntArrayRef shape, at::ScalarType type) const { return at::empty(shape, opt.dtype(type)); }
+  // (straight to the allocator: through the dispatcher a call of five outputs takes 2 us longer)
+  Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
+    return at::detail::empty_cuda(shape, type, opt.device(), std::nullopt);
+  }
   Tensor workspace(size_t bytes) const {
     return bytes ? at::empty({static_cast<int64_t>(bytes)}, opt.dtype(at::kByte)) : Tensor();
   }
