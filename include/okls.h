@@ -469,14 +469,17 @@ okls_status okls_inv_root_noalloc(const float *S_dev, float *P_dev, int64_t d,
  *     scratch comes from the caller (the *_workspace_bytes functions), may be
  *     uninitialised and is free again when the call's work has run.  Calls
  *     that run at the same time need workspaces of their own.
- *   - Sums are taken in fp32 in an order fixed by the sizes and the device,
- *     without floating-point atomics: the same inputs give the same bits.
+ *   - Sums are taken in fp32 in an order fixed by the sizes, the device and
+ *     the layout (row pitch and alignment of the tensors, which decide how a
+ *     row is split), without floating-point atomics: the same call on the same
+ *     memory gives the same bits.
  *   - A size of zero rows or tokens is valid and writes nothing that has no
  *     elements.
  *   - `status_dev` is a device word of the caller, zeroed before its first
  *     use, into which a launch ORs OKLS_DEV_* bits (okls_status_word_read).
  *   - Token ids are int32 (ids_i64 = 0) or int64 (ids_i64 = 1).  A negative
- *     id is padding: it has no embedding, no loss and no gradient.  An id
+ *     id is padding: it has no embedding, no log probability and no gradient
+ *     of either; a row's entropy, and its gradient, do not ask for the id.  An id
  *     at or past the vocabulary is treated the same and raises
  *     OKLS_DEV_BAD_TOKEN.
  * ====================================================================== */
@@ -576,7 +579,7 @@ okls_status okls_rms_norm_grad(const void *dy, int32_t dy_dtype, int64_t lddy,
  *   that holds an infinity or a NaN stands for NaN.
  *   block  OKLS_FP8_ROW: groups of 128 consecutive columns of one row;
  *          OKLS_FP8_SQUARE: blocks of 128 rows x 128 columns.
- *   x      rows x cols, fp32 or bf16.
+ *   x      rows x cols, fp32 or bf16; rows <= 128 * 65535.
  *   q      rows x cols e4m3, row pitch ldq, or NULL; scale of element (i, j):
  *          scale[(row block or row i) * lds_row + (j / 128) * lds_group].
  *   qt     the same of the transposed matrix (cols x rows, groups along its

@@ -341,8 +341,9 @@ __device__ __forceinline__ void add_square(const Fp8GemmArgs& A, const Adder<BN,
       const uint32_t d = tbase + S.buf() * BN;
       const float s = sc[q * 32 + lane];
       const float* sb = sc + kTM - (at.tn * BN) / kFp8Group;
-      if constexpr (kCols <= 96) {
-        // the whole step at once: the buffer is free before the additions
+      if constexpr (kCols <= 64) {
+        // one CTA's 32 or 64 columns, the whole step at once: the buffer is free
+        // before the additions
         uint32_t v[kCols / 32][32];
 #pragma unroll
         for (int c = 0; c < kCols; c += 32) tmem_ld32_start(d + c, v[c / 32]);
@@ -437,13 +438,13 @@ __device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN, P
     for (int kb = 0; kb < nkb; ++kb) {
       const float* sc = S.begin(R);
       const uint32_t d = tbase + S.buf() * BN;
-      // [chunk, or in turn][half][4 i + 2 r + column]: the whole step at once
-      // up to 96 columns (the buffer is then free before the additions), else
-      // a chunk ahead
-      constexpr int kHeld = kChunks <= 3 ? kChunks : 2;
+      // [chunk, or in turn][half][4 i + 2 r + column]: one CTA's 32 or 64 columns
+      // at once (the buffer is then free before the additions), a pair's 128 a
+      // chunk ahead
+      constexpr int kHeld = kChunks <= 2 ? kChunks : 2;
       uint32_t v[kHeld][2][16];
 #pragma unroll
-      for (int c = 0; c < (kChunks <= 3 ? kChunks : 1); ++c) {
+      for (int c = 0; c < (kChunks <= 2 ? kChunks : 1); ++c) {
         tmem_ld16x256_start(d + c * 32, v[c][0]);
         tmem_ld16x256_start(d + (16u << 16) + c * 32, v[c][1]);
       }
@@ -456,7 +457,7 @@ __device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN, P
           sa[h][r] = pair_of(__float_as_uint(x), __float_as_uint(x));
         }
       const uint64_t* sb = reinterpret_cast<const uint64_t*>(sc + kTM + half * kCols) + p;
-      if (kChunks <= 3) {
+      if (kChunks <= 2) {
 #pragma unroll
         for (int c = 0; c < kHeld; ++c) tmem_ld16x256_wait(v[c][0], v[c][1]);
         S.loaded(R, lane);
@@ -464,7 +465,7 @@ __device__ __forceinline__ void add_rows(const Fp8GemmArgs& A, const Adder<BN, P
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         uint32_t(&x)[2][16] = v[c % kHeld];
-        if (kChunks > 3) {
+        if (kChunks > 2) {
           tmem_ld16x256_wait(x[0], x[1]);
           if (c + 1 < kChunks) {
             tmem_ld16x256_start(d + (c + 1) * 32, v[(c + 1) % kHeld][0]);
@@ -607,8 +608,8 @@ struct ScaleRows {
 // The scale warp: the tile's rows of A, then its rows of B, or the one or two
 // square blocks its columns meet, of every step; zeros outside.  It is one
 // warp with a step's time for a step, so it takes four rows a copy where they
-// lie next to each other (row groups, 11008 x 4096 x 8192 with 128 x 192 tiles:
-// 535 -> 448 us; no change for square blocks).
+// lie next to each other (row groups, 11008 x 4096 x 8192: 441 us, with scales
+// that lie row by row 855; square blocks, 8192 x 11008 x 4096: 305 and 320).
 template <int BN>
 __device__ __forceinline__ void copy_scales(const Fp8GemmArgs& A, float* ring, int slot_floats, int slots, uint64_t* sfull,
                                             uint64_t* sempty, int first, int stride, int row_step, int row0, int tiles_m,
@@ -804,12 +805,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8_gemm(const __grid_constant_
 // step takes about 1000 clocks.  bf16 results leave through the copy engine
 // from shared memory, a tile's 64 KB under the next tile's first steps (threads
 // storing their rows took 2.7 us a tile).  8192 x 11008 x 4096 with square
-// blocks: 302 us, 2.44 PFLOP/s (threads storing 330, one CTA a tile 353);
-// 8192 x 4096 x 11008: 291 us, 2.54; 8192 x 5504 x 2048: 92 us, 2.01; with row
-// groups, 11008 x 4096 x 8192: 445 us, 1.66.  Narrower tiles with more buffers
+// blocks: 305 us, 2.42 PFLOP/s (threads storing 330, one CTA a tile 353);
+// 8192 x 4096 x 11008: 295 us, 2.50; 8192 x 5504 x 2048: 93 us, 1.99; with row
+// groups, 11008 x 4096 x 8192: 441 us, 1.68.  Narrower tiles with more buffers
 // cost more operand traffic than they save (before the change of stores): 256
-// x 192 388 us, 256 x 128 with four buffers 488 us.  Differences to the kernel above: the first CTA issues
-// the MMAs for both; its `full` barriers count both CTAs' copies; commits
+// x 192 388 us, 256 x 128 with four buffers 488 us.  With row groups a step takes
+// about 1400 clocks: its additions are 512 of them on the fp32 units, and wait,
+// TMEM loads and hand-over are not hidden under another step's.
+//
+// Differences to the kernel above: the first CTA issues the MMAs for both; its `full` barriers count both CTAs' copies; commits
 // arrive on both CTAs' `empty` and `acc_full`; both CTAs' adding warps hand
 // buffers back on the first one's `acc_empty`.  Two issuers take every other
 // step each: one waits for its barriers while the other's MMAs run.

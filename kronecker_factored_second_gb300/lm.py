@@ -21,9 +21,10 @@ requires a gradient.
 
 Tensors are CUDA tensors on one device whose last dimension is contiguous;
 rows may have any pitch.  fp32 and bf16 are taken, ids are int32 or int64.
-Negative ids are padding: zeros out, no loss, no gradient.  An id at or past
-the vocabulary is treated as padding and recorded in the device's status
-word, which `query_status` reads.
+Negative ids are padding: zeros out, log probability 0, and no gradient of
+either (a row's entropy does not depend on its id, and keeps its gradient).  An
+id at or past the vocabulary is treated as padding and recorded in the device's
+status word, which only `query_status` reads.
 
 Every function runs on the current stream, or on `stream`.  Outputs and
 scratch come from torch's allocator on that stream.  A call on another
@@ -105,7 +106,8 @@ def embedding_grad(dy: torch.Tensor, ids: torch.Tensor, vocab: int, *, scale: fl
     """base + scale * (sum of dy's rows by token), vocab x dim.
 
     `base` None stands for zeros.  With `out` the result goes there; out=base
-    adds in place and touches only the rows of tokens that occur."""
+    adds in place and touches only the rows of tokens that occur.  A new result
+    has the type of `base`, or `dtype` without one."""
     if stream is not None:
         with _on(stream, dy, ids, base, out):
             return embedding_grad(dy, ids, vocab, scale=scale, base=base, out=out, dtype=dtype)
