@@ -684,6 +684,146 @@ okls_status okls_token_logprobs_grad_rest(
     const float *dlogp, const float *dentropy, void *dlogits, int64_t ldd,
     void *stream);
 
+/* ======================================================================
+ * What a model needs beside the matrix steps: AdamW for the parameters that
+ * are no matrices, products with 4-bit weights and the sampling of tokens for
+ * generation.  The conventions of the section above hold.
+ * ====================================================================== */
+
+/*
+ * AdamW over many tensors.  With t the step's number, counted from 1,
+ *   m <- beta1 m + (1 - beta1) g,   v <- beta2 v + (1 - beta2) g^2
+ *   p <- p - lr weight_decay p
+ *          - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps).
+ *   param   count elements, fp32 or bf16, rounded to nearest; grad likewise.
+ *   exp_avg, exp_avg_sq  m and v: fp32, or (state_dtype OKLS_E4M3) e4m3 codes
+ *           of m and of sqrt(v) with avg_scale and sq_scale, ceil(count / 128)
+ *           fp32 values each (NULL for fp32): code * scale stands for the
+ *           value, scale = max(largest magnitude of the 128, 2^-100) / 448.
+ *           Codes and scales of zeros are a valid start.  A group that holds
+ *           a NaN or an infinity stands for NaN.
+ *   id      the tensor's number among those of the step.
+ * The update uses the moments before their rounding to 8 bits.  That rounding
+ * is by chance, with the mean kept: a value between two codes, at the fraction
+ * f of their distance (a fixed distance of 2^-9 below 2^-6), takes the upper
+ * one when f + (d + 1/2) / 65536 >= 1.  d is a 16-bit half (lower for m, upper
+ * for sqrt(v)) of the word of element i in Philox-2x32 with five rounds:
+ * counter (i / 2, id + low word of s), key the high word of s = seed + t *
+ * 0x9E3779B97F4A7C15 (mod 2^64), first word of the result for even i, second
+ * for odd.  A sqrt(v) that is not zero keeps at least the smallest code.
+ * Tensors of one call have one set of types; they do not overlap.  A gradient
+ * that is not finite reaches p, m and v.
+ */
+typedef struct okls_adamw_tensor {
+  void *param;
+  const void *grad;
+  void *exp_avg;
+  void *exp_avg_sq;
+  float *avg_scale;
+  float *sq_scale;
+  int64_t count;  /* at most 2^33 */
+  int32_t id;
+  int32_t reserved;
+} okls_adamw_tensor;
+typedef struct okls_adamw_config {
+  double lr, beta1, beta2, eps, weight_decay;
+  uint64_t seed;
+} okls_adamw_config;
+
+/* `tensors` and `config` are host memory and free again when the call
+ * returns.  scalars_dev: NULL, and the step's number is `step`; or what
+ * okls_adamw_clock wrote in this step (`step` and the config's values are not
+ * used then). */
+okls_status okls_adamw_step(const okls_adamw_tensor *tensors, int64_t num,
+                            int32_t param_dtype, int32_t grad_dtype,
+                            int32_t state_dtype,
+                            const okls_adamw_config *config, int64_t step,
+                            const void *scalars_dev, void *stream);
+
+/* For steps that are captured and replayed: *step_dev, the number of steps
+ * done, is raised by one on the device, and what okls_adamw_step uses of that
+ * number and the config (lr from *lr_dev if that is not NULL) is written to
+ * scalars_dev, OKLS_ADAMW_SCALARS_BYTES on a 16-byte boundary. */
+#define OKLS_ADAMW_SCALARS_BYTES 64
+okls_status okls_adamw_clock(const okls_adamw_config *config,
+                             const float *lr_dev, int64_t *step_dev,
+                             void *scalars_dev, void *stream);
+
+/*
+ * 4-bit weights: codes c in 0..15, two in a byte (the even column in the low
+ * half), with a bf16 scale, and a bf16 zero point or 8, for each `group`
+ * consecutive columns of a row: (c - zero) * scale stands for the value.
+ *   group  32, 64 or a multiple of 128.
+ *   codes  rows x ceil(cols / 2) bytes, pitch ldq; scale of column j of row i:
+ *          scale[i * lds_row + (j / group) * lds_group], zero likewise.
+ * Quantisation without zero points (zero NULL): scale = bf16(amax / 7),
+ * c = round(x / scale) + 8 in 1..15.  With them, lo <= 0 <= hi the range of
+ * the group and 0: scale = bf16((hi - lo) / 15), zero = bf16(-lo / scale),
+ * c = round(x / scale + zero) in 0..15.  scale is at least 2^-100.  A group that
+ * holds an infinity or a NaN has scale NaN.
+ */
+okls_status okls_int4_quantize(const void *x, int32_t dtype, int64_t ldx,
+                               int64_t rows, int64_t cols, int64_t group,
+                               void *codes, int64_t ldq, void *scale,
+                               int64_t lds_row, int64_t lds_group, void *zero,
+                               int64_t ldz_row, int64_t ldz_group,
+                               void *stream);
+
+/*
+ * out = x W^T (+ out when accumulate = 1) for a few rows of x and n x k 4-bit
+ * weights W as above.
+ *   x     rows x k, fp32 or bf16; out  rows x n, fp32 or bf16.
+ * Products are exact; each group's sum and the sum of the scaled groups are
+ * fp32.  Any number of rows is taken, but the way through the kernel is made
+ * for tokens that are generated, up to some 64 (rows <= 524280).  Rows of codes start
+ * on 16-byte boundaries (OKLS_ERR_UNSUPPORTED otherwise).  An infinity in x
+ * gives NaN or an infinity, a NaN gives NaN, in that row of out.
+ */
+okls_status okls_int4_matmul(const void *x, int32_t x_dtype, int64_t ldx,
+                             const void *codes, int64_t ldq,
+                             const void *scale, int64_t lds_row,
+                             int64_t lds_group, const void *zero,
+                             int64_t ldz_row, int64_t ldz_group, int64_t group,
+                             int64_t rows, int64_t n, int64_t k, void *out,
+                             int32_t out_dtype, int64_t ldo,
+                             int32_t accumulate, void *stream);
+
+/*
+ * Sampling of one token from each row of logits z, from the given random
+ * number u of the row.  With w_j = exp((z_j - max z) / temperature) and the
+ * tokens in falling order of z, equal ones in the order of their ids:
+ *   1. top_k > 0 keeps the first top_k of them;
+ *   2. 0 < top_p < 1 keeps the shortest prefix of those whose sum of w is at
+ *      least top_p times the sum over all of those (top_p <= 0: the first);
+ *   3. min_p > 0 keeps those of z >= max z + temperature * ln(min(min_p, 1)).
+ * The drawn token is the first in the order of ids at which the running sum
+ * of the kept w is above u times their sum; logp is ln(w / sum).  A
+ * temperature below 2^-20, or NaN, takes the first token of the order.  Other
+ * NaN settings leave their filter off; u outside [0, 1) is moved to the nearest value
+ * inside, NaN to 0.
+ *   logits  rows x vocab, fp32 or bf16, pitch ldl; vocab <= 2^20.
+ *   u, ids, logp  one for each row.
+ * Logits of -inf or NaN are impossible tokens; a row of nothing else gets id
+ * -1 and logp -inf.  Where a logit is +inf, tokens of +inf are equally
+ * possible and no others are.
+ * Settings are one value for all rows, or (not NULL) a device vector with a
+ * value for each row.
+ */
+typedef struct okls_sample_settings {
+  const float *temperature_dev;
+  const int32_t *top_k_dev;
+  const float *top_p_dev;
+  const float *min_p_dev;
+  float temperature;
+  int32_t top_k;
+  float top_p;
+  float min_p;
+} okls_sample_settings;
+okls_status okls_sample(const void *logits, int32_t dtype, int64_t ldl,
+                        int64_t rows, int64_t vocab, const float *u,
+                        const okls_sample_settings *settings, int32_t *ids,
+                        float *logp, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

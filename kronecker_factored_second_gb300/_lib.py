@@ -89,6 +89,44 @@ class okls_profile(ctypes.Structure):
     ]
 
 
+class okls_adamw_tensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("exp_avg", ctypes.c_void_p),
+        ("exp_avg_sq", ctypes.c_void_p),
+        ("avg_scale", ctypes.c_void_p),
+        ("sq_scale", ctypes.c_void_p),
+        ("count", ctypes.c_int64),
+        ("id", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class okls_adamw_config(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("seed", ctypes.c_uint64),
+    ]
+
+
+class okls_sample_settings(ctypes.Structure):
+    _fields_ = [
+        ("temperature_dev", ctypes.c_void_p),
+        ("top_k_dev", ctypes.c_void_p),
+        ("top_p_dev", ctypes.c_void_p),
+        ("min_p_dev", ctypes.c_void_p),
+        ("temperature", ctypes.c_float),
+        ("top_k", ctypes.c_int32),
+        ("top_p", ctypes.c_float),
+        ("min_p", ctypes.c_float),
+    ]
+
+
 class OklsError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"okls error {code}: {msg}")
@@ -146,6 +184,13 @@ _SIGS = {
     "okls_token_logprobs_rest": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _I64, _F, _I32, _P, _P, _P, _P, _P, _P, _P, _P]),
     "okls_token_logprobs_grad_rest": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _I64, _F, _P, _P, _P, _P, _P, _P, _I64,
                                              _P]),
+    "okls_adamw_step": (_I32, [ctypes.POINTER(okls_adamw_tensor), _I64, _I32, _I32, _I32, ctypes.POINTER(okls_adamw_config),
+                               _I64, _P, _P]),
+    "okls_adamw_clock": (_I32, [ctypes.POINTER(okls_adamw_config), _P, _P, _P, _P]),
+    "okls_int4_quantize": (_I32, [_P, _I32, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P]),
+    "okls_int4_matmul": (_I32, [_P, _I32, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _I32,
+                                _I64, _I32, _P]),
+    "okls_sample": (_I32, [_P, _I32, _I64, _I64, _I64, _P, ctypes.POINTER(okls_sample_settings), _P, _P, _P]),
     "okls_token_logprobs_grad": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _I64, _F, _P, _P, _P, _P, _P, _I64, _P]),
 }
 

@@ -1,6 +1,6 @@
-// Torch binding of the language-model operators: checks of tensors, output
-// and scratch allocation on the current stream, and the call of the C entry
-// (include/okls.h).  It computes nothing.  A call costs a few microseconds of
+// Torch binding of the language-model operators and of the AdamW step: checks
+// of tensors, output and scratch allocation on the current stream, and the call
+// of the C entry (include/okls.h).  It computes nothing.  A call costs a few microseconds of
 // host time, where the same in Python cost 15 to 25 (one token's norm: 20).
 //
 // Wrong tensors raise ValueError; what the C entry refuses raises OklsError.
@@ -8,13 +8,19 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/GradMode.h>
 #include <c10/core/InferenceMode.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
+#include <limits>
 #include <optional>
 #include <tuple>
+#include <vector>
 
 #include "../../include/okls.h"
 
@@ -374,6 +380,252 @@ Tensor token_logprobs_grad(const Tensor& logits, const Tensor& ids, const Tensor
   return d;
 }
 
+// -------------------------------------------------------------------- AdamW
+// The tensors of a list or tuple.
+class TensorList {
+ public:
+  TensorList(const py::object& o, const char* name) : name_(name) {
+    PyObject* fast = PySequence_Fast(o.ptr(), name);
+    if (!fast) throw py::error_already_set();
+    seq_ = py::reinterpret_steal<py::object>(fast);
+  }
+  int64_t size() const { return PySequence_Fast_GET_SIZE(seq_.ptr()); }
+  const Tensor& operator[](int64_t i) const {
+    PyObject* o = PySequence_Fast_GET_ITEM(seq_.ptr(), i);
+    REFUSE(!THPVariable_Check(o), name_, " must hold tensors");
+    return THPVariable_Unpack(o);
+  }
+
+ private:
+  const char* name_;
+  py::object seq_;
+};
+
+// Memory that a step writes: [begin, end) of each tensor.
+typedef std::pair<uintptr_t, uintptr_t> Range;
+
+void refuse_overlaps(std::vector<Range>& r) {
+  if (!std::is_sorted(r.begin(), r.end())) std::sort(r.begin(), r.end());
+  for (size_t i = 1; i < r.size(); ++i)
+    REFUSE(r[i].first < r[i - 1].second, "a parameter or a state appears twice, or two of them overlap");
+}
+
+// A tensor of a step, as the kernels see it: `count` elements in a row.
+void* flat(const Tensor& t, const char* name, const Tensor& first, int64_t count, bool writes, std::vector<Range>& ranges) {
+  REFUSE(!t.is_cuda(), name, " must be on a CUDA device");
+  same_device(first, t);
+  REFUSE(!t.is_contiguous(), name, " must be contiguous");
+  REFUSE(t.numel() != count, name, " must hold ", count, " values, not ", t.numel());
+  void* p = t.data_ptr();
+  if (writes) {
+    writable(t, name);
+    if (count) ranges.emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + count * t.element_size());
+  }
+  return p;
+}
+
+void adamw_step(const py::object& params, const py::object& grads, const py::object& avgs, const py::object& sqs,
+                const py::object& avg_scales, const py::object& sq_scales, const py::object& step, const py::object& lr,
+                double beta1, double beta2, double eps, double weight_decay, uint64_t seed) {
+  const TensorList P(params, "params"), G(grads, "grads"), M(avgs, "exp_avgs"), V(sqs, "exp_avg_sqs");
+  const int64_t num = P.size();
+  REFUSE(G.size() != num || M.size() != num || V.size() != num, "params, grads, exp_avgs and exp_avg_sqs must be as many");
+  REFUSE(avg_scales.is_none() != sq_scales.is_none(), "avg_scales and sq_scales go together");
+  const bool bits8 = !avg_scales.is_none();
+  std::optional<TensorList> MS, VS;
+  if (bits8) {
+    MS.emplace(avg_scales, "avg_scales"), VS.emplace(sq_scales, "sq_scales");
+    REFUSE(MS->size() != num || VS->size() != num, "avg_scales and sq_scales must be as many as params");
+  }
+  okls_adamw_config cfg = {0.0, beta1, beta2, eps, weight_decay, seed};
+  const bool counted = THPVariable_Check(step.ptr()), lr_given = THPVariable_Check(lr.ptr());
+  const float* lr_dev = nullptr;
+  int64_t number = 0;
+  int64_t* step_dev = nullptr;
+  if (lr_given) {
+    const Tensor& t = THPVariable_Unpack(lr.ptr());
+    REFUSE(!counted, "a learning rate on the device needs the step's number there, too");
+    lr_dev = floats(t, "lr", 1);
+  } else {
+    cfg.lr = lr.cast<double>();
+  }
+  if (counted) {
+    const Tensor& t = THPVariable_Unpack(step.ptr());
+    REFUSE(t.scalar_type() != at::kLong, "step must be int64, not ", t.scalar_type());
+    step_dev = static_cast<int64_t*>(const_cast<void*>(vector(t, "step", 1)));
+    writable(t, "step");
+  } else {
+    number = step.cast<int64_t>();
+  }
+  if (num == 0 && !counted) return;
+  const Tensor& first = counted ? THPVariable_Unpack(step.ptr()) : P[0];
+  REFUSE(!first.is_cuda(), "tensors must be on a CUDA device");
+  if (lr_given) same_device(first, THPVariable_Unpack(lr.ptr()));
+
+  // one call of the C entry for each pair of types
+  std::vector<okls_adamw_tensor> lists[4];
+  std::vector<Range> ranges;
+  ranges.reserve(num * (bits8 ? 5 : 3));
+  for (auto& l : lists) l.reserve(lists == &l ? num : 0);
+  for (int64_t i = 0; i < num; ++i) {
+    const Tensor &p = P[i], &g = G[i], &m = M[i], &v = V[i];
+    const int64_t n = p.numel();
+    okls_adamw_tensor e = {};
+    const int pd = float_code(p.scalar_type(), "a parameter"), gd = float_code(g.scalar_type(), "a gradient");
+    const at::ScalarType sd = bits8 ? at::kFloat8_e4m3fn : at::kFloat;
+    REFUSE(m.scalar_type() != sd || v.scalar_type() != sd, "exp_avgs and exp_avg_sqs must be ", sd,
+           bits8 ? " where scales are given" : "");
+    e.param = flat(p, "a parameter", first, n, true, ranges);
+    e.grad = flat(g, "a gradient", first, n, false, ranges);
+    e.exp_avg = flat(m, "exp_avg", first, n, true, ranges);
+    e.exp_avg_sq = flat(v, "exp_avg_sq", first, n, true, ranges);
+    if (bits8) {
+      const Tensor &ms = (*MS)[i], &vs = (*VS)[i];
+      REFUSE(ms.scalar_type() != at::kFloat || vs.scalar_type() != at::kFloat, "scales must be fp32");
+      const int64_t groups = (n + kGroup - 1) / kGroup;
+      e.avg_scale = static_cast<float*>(flat(ms, "avg_scale", first, groups, true, ranges));
+      e.sq_scale = static_cast<float*>(flat(vs, "sq_scale", first, groups, true, ranges));
+    }
+    e.count = n, e.id = static_cast<int32_t>(i);
+    lists[2 * pd + gd].push_back(e);
+  }
+  refuse_overlaps(ranges);
+
+  Call c(first);
+  Tensor scalars;
+  if (counted) {
+    scalars = c.workspace(OKLS_ADAMW_SCALARS_BYTES);
+  } else {
+    REFUSE(c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None,
+           "a captured step needs its number on the device (step as a tensor), or every replay would be the same step");
+  }
+  // everything is checked before anything is written
+  for (int k = 0; k < 4; ++k) {
+    if (lists[k].empty() && k > 0) continue;
+    check(okls_adamw_step(nullptr, 0, k / 2, k % 2, bits8 ? OKLS_E4M3 : OKLS_F32, &cfg, counted ? 1 : number, ptr_of(scalars),
+                          c.stream()));
+  }
+  if (counted) {
+    check(okls_adamw_clock(&cfg, lr_dev, step_dev, scalars.data_ptr(), c.stream()));
+    written(first);
+  }
+  for (int k = 0; k < 4; ++k) {
+    if (lists[k].empty()) continue;
+    check(okls_adamw_step(lists[k].data(), static_cast<int64_t>(lists[k].size()), k / 2, k % 2, bits8 ? OKLS_E4M3 : OKLS_F32,
+                          &cfg, counted ? 1 : number, ptr_of(scalars), c.stream()));
+  }
+  for (int64_t i = 0; i < num; ++i) {
+    written(P[i]), written(M[i]), written(V[i]);
+    if (bits8) written((*MS)[i]), written((*VS)[i]);
+  }
+}
+
+// -------------------------------------------------------------------- 4 bits
+// bf16 values laid group by group, so that neighbouring rows' are neighbours.
+Tensor group_values(const Call& c, int64_t rows, int64_t groups) {
+  return at::empty_strided({rows, groups}, {1, std::max<int64_t>((rows + 7) / 8 * 8, 1)}, c.opt.dtype(at::kBFloat16));
+}
+
+void check_group(int64_t group) {
+  REFUSE(group != 32 && group != 64 && (group < 128 || group % 128 != 0), "group must be 32, 64 or a multiple of 128, not ", group);
+}
+
+std::tuple<Tensor, Tensor, Maybe> int4_quantize(const Tensor& x, int64_t group, bool symmetric) {
+  REFUSE(x.dim() != 2, "a weight is a matrix");
+  const Mat m = matrix(x, "x");
+  const int dt = float_code(x.scalar_type(), "x");
+  check_group(group);
+  Call c(x);
+  const int64_t groups = (m.cols + group - 1) / group, pitch = std::max<int64_t>((m.cols + 127) / 128, 1) * 64;
+  Tensor q = at::empty_strided({m.rows, (m.cols + 1) / 2}, {pitch, 1}, c.opt.dtype(at::kByte));
+  Tensor s = group_values(c, m.rows, groups), z;
+  if (!symmetric) z = group_values(c, m.rows, groups);
+  check(okls_int4_quantize(m.p, dt, m.ld, m.rows, m.cols, group, q.data_ptr(), pitch, s.data_ptr(), s.stride(0), s.stride(1),
+                           ptr_of(z), symmetric ? 0 : z.stride(0), symmetric ? 0 : z.stride(1), c.stream()));
+  return {q, s, symmetric ? std::nullopt : Maybe(z)};
+}
+
+Tensor int4_matmul(const Tensor& x, const Tensor& codes, const Tensor& scale, const Maybe& zero, int64_t cols, int64_t group,
+                   Maybe out, std::optional<at::ScalarType> out_dtype, bool accumulate) {
+  const Mat m = matrix(x, "x");
+  const int dt = float_code(x.scalar_type(), "x");
+  // (the fields of an Int4Tensor can be assigned)
+  check_group(group);
+  REFUSE(!codes.is_cuda(), "the weight must be on a CUDA device");
+  REFUSE(cols < 0 || codes.dim() != 2 || codes.scalar_type() != at::kByte || codes.size(1) != (cols + 1) / 2,
+         "codes must be a matrix of uint8 with ", (cols + 1) / 2, " columns");
+  REFUSE(codes.numel() != 0 && codes.size(1) > 1 && codes.stride(1) != 1, "the last dimension of codes must be contiguous");
+  const int64_t n = codes.size(0), groups = (cols + group - 1) / group;
+  const auto check_values = [&](const Tensor& t, const char* name) {
+    REFUSE(t.dim() != 2 || t.scalar_type() != at::kBFloat16 || t.size(0) != n || t.size(1) != groups, name,
+           " must be bf16 of shape (", n, ", ", groups, ")");
+    same_device(x, t);
+  };
+  check_values(scale, "scale");
+  if (zero) check_values(*zero, "zero");
+  REFUSE(m.cols != cols, "sums of length ", m.cols, " and ", cols);
+  REFUSE(accumulate && !out, "accumulate needs out");
+  same_device(x, codes);
+  same_device(x, out);
+  Mat o = {};
+  const bool given = out.has_value();
+  if (given) o = plain_matrix(*out, "out", m.rows, n), writable(*out, "out");
+  Call c(x);
+  if (!out) {
+    std::vector<int64_t> shape = x.sizes().vec();
+    shape.back() = n;
+    out = c.empty(shape, out_dtype.value_or(x.scalar_type()));
+    o = {out->data_ptr(), m.rows, n, n};
+  }
+  const int od = float_code(out->scalar_type(), "the output type");
+  check(okls_int4_matmul(m.p, dt, m.ld, codes.data_ptr(), codes.stride(0), scale.data_ptr(), scale.stride(0), scale.stride(1),
+                         zero ? zero->data_ptr() : nullptr, zero ? zero->stride(0) : 0, zero ? zero->stride(1) : 0, group,
+                         m.rows, n, cols, o.p, od, o.ld, accumulate, c.stream()));
+  if (given) written(*out);
+  return *out;
+}
+
+// ------------------------------------------------------------------ sampling
+// A setting of `sample`: None, a number for all rows, or a value for each row.
+template <class N>
+void setting(const py::object& o, const char* name, at::ScalarType type, const Tensor& logits, int64_t rows, N& all, const N*& dev) {
+  if (o.is_none()) return;
+  if (!THPVariable_Check(o.ptr())) {
+    all = static_cast<N>(o.cast<double>());
+    return;
+  }
+  const Tensor& t = THPVariable_Unpack(o.ptr());
+  REFUSE(t.scalar_type() != type, name, " must be ", type, ", not ", t.scalar_type());
+  dev = static_cast<const N*>(vector(t, name, rows));
+  same_device(logits, t);
+}
+
+std::tuple<Tensor, Tensor> sample(const Tensor& logits, const Tensor& u, const py::object& temperature, const py::object& top_k,
+                                  const py::object& top_p, const py::object& min_p) {
+  const Mat z = matrix(logits, "logits");
+  const int dt = float_code(logits.scalar_type(), "logits");
+  const float* r = floats(u, "u", z.rows);
+  same_device(logits, u);
+  okls_sample_settings s = {nullptr, nullptr, nullptr, nullptr, 1.0f, 0, 1.0f, 0.0f};
+  double k = 0.0;
+  const double* unused = nullptr;
+  setting(temperature, "temperature", at::kFloat, logits, z.rows, s.temperature, s.temperature_dev);
+  if (!top_k.is_none() && THPVariable_Check(top_k.ptr()))
+    setting(top_k, "top_k", at::kInt, logits, z.rows, s.top_k, s.top_k_dev);
+  else
+    setting(top_k, "top_k", at::kInt, logits, z.rows, k, unused);
+  setting(top_p, "top_p", at::kFloat, logits, z.rows, s.top_p, s.top_p_dev);
+  setting(min_p, "min_p", at::kFloat, logits, z.rows, s.min_p, s.min_p_dev);
+  REFUSE(!(s.temperature >= 0.0f), "temperature must not be negative");
+  REFUSE(std::isnan(s.top_p) || std::isnan(s.min_p) || std::isnan(k) || k != std::floor(k), "top_k must be a whole number, top_p and min_p numbers");
+  if (!s.top_k_dev) s.top_k = static_cast<int32_t>(std::max(-1.0, std::min(k, 2147483647.0)));
+  Call c(logits);
+  const at::IntArrayRef lead = logits.sizes().slice(0, logits.dim() - 1);
+  Tensor ids = c.empty(lead, at::kInt), logp = c.empty(lead, at::kFloat);
+  check(okls_sample(z.p, dt, z.ld, z.rows, z.cols, r, &s, ids.data_ptr<int32_t>(), logp.data_ptr<float>(), c.stream()));
+  return {ids, logp};
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_lm_native, m) {
@@ -388,4 +640,8 @@ PYBIND11_MODULE(_lm_native, m) {
   m.def("fp8_matmul", &fp8_matmul);
   m.def("token_logprobs", &token_logprobs);
   m.def("token_logprobs_grad", &token_logprobs_grad);
+  m.def("adamw_step", &adamw_step);
+  m.def("int4_quantize", &int4_quantize);
+  m.def("int4_matmul", &int4_matmul);
+  m.def("sample", &sample);
 }

@@ -1,10 +1,12 @@
 // Launch interface of the language-model operators (token embedding, RMS
-// norm, 8-bit quantisation and product, token log probabilities).  The entry
-// file validates; these functions pick the launch shape.
+// norm, 8-bit quantisation and product, token log probabilities, AdamW step,
+// 4-bit product, sampling).  The entry file validates; these functions pick
+// the launch shape.
 #pragma once
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 namespace okls {
@@ -173,5 +175,99 @@ struct ScoreGradArgs {
   int64_t ldd;
 };
 cudaError_t launch_token_logprobs_grad(const ScoreGradArgs& A, int dtype, cudaStream_t st);
+
+// ----------------------------------------------------------------- AdamW
+struct AdamwEntry {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* ms;  // scales of 8-bit moments
+  float* vs;
+  int64_t count;
+  int32_t id;  // the tensor's number, for its random numbers
+};
+constexpr int kAdamwTable = 400;  // tensors in one launch: 27 of the 32 KB that parameters may take
+
+struct AdamwHyper {
+  double lr, beta1, beta2, eps, weight_decay;
+  uint64_t seed;
+};
+// What the kernels use of the hyperparameters and the step's number.
+struct AdamwScalars {
+  float beta1, rest1, beta2, rest2;  // rest = 1 - beta
+  float rate;                        // lr / (1 - beta1^t)
+  float root;                        // 1 / sqrt(1 - beta2^t)
+  float eps, decay;                  // lr * weight_decay
+  uint32_t key, low;                 // words of seed + t * 0x9E3779B97F4A7C15
+};
+__host__ __device__ inline AdamwScalars adamw_scalars(const AdamwHyper& h, int64_t t) {
+  AdamwScalars s;
+  s.beta1 = static_cast<float>(h.beta1), s.rest1 = static_cast<float>(1.0 - h.beta1);
+  s.beta2 = static_cast<float>(h.beta2), s.rest2 = static_cast<float>(1.0 - h.beta2);
+  s.rate = static_cast<float>(h.lr / (1.0 - pow(h.beta1, static_cast<double>(t))));
+  s.root = static_cast<float>(1.0 / sqrt(1.0 - pow(h.beta2, static_cast<double>(t))));
+  s.eps = static_cast<float>(h.eps), s.decay = static_cast<float>(h.lr * h.weight_decay);
+  const uint64_t w = h.seed + static_cast<uint64_t>(t) * 0x9E3779B97F4A7C15ull;
+  s.key = static_cast<uint32_t>(w >> 32), s.low = static_cast<uint32_t>(w);
+  return s;
+}
+cudaError_t launch_adamw(const AdamwEntry* e, int num, int param_dtype, int grad_dtype, bool bits8,
+                         const AdamwScalars& s, const AdamwScalars* s_dev, cudaStream_t st);
+cudaError_t launch_adamw_clock(const AdamwHyper& h, const float* lr_dev, int64_t* step_dev, AdamwScalars* out,
+                               cudaStream_t st);
+
+// ---------------------------------------------------------------- 4 bits
+struct Int4Args {
+  const uint8_t* codes;  // n x ceil(k / 2), the even column in the low half
+  int64_t ldq;
+  const void* scale;  // bf16
+  int64_t lds_row, lds_group;
+  const void* zero;  // bf16, or null for 8
+  int64_t ldz_row, ldz_group;
+  int64_t group;
+  const void* x;
+  int64_t ldx;
+  int32_t x_vec;  // x's rows start on 16-byte boundaries
+  int64_t rows, n, k;
+  void* out;
+  int32_t out_dtype;
+  int64_t ldy;
+  int32_t accumulate;
+};
+cudaError_t launch_int4_matmul(const Int4Args& A, int x_dtype, cudaStream_t st);
+
+struct Int4QuantArgs {
+  const void* x;
+  int64_t ldx, rows, cols, group;
+  uint8_t* codes;
+  int64_t ldq;
+  void* scale;
+  int64_t lds_row, lds_group;
+  void* zero;
+  int64_t ldz_row, ldz_group;
+};
+cudaError_t launch_int4_quantize(const Int4QuantArgs& A, int dtype, cudaStream_t st);
+
+// -------------------------------------------------------------- sampling
+constexpr float kSampleColdest = 9.5367431640625e-07f;  // 2^-20: a lower temperature takes the best token
+constexpr int64_t kSampleMaxVocab = int64_t(1) << 20;
+struct SampleArgs {
+  const void* logits;
+  int64_t ldl, rows, vocab;
+  const float* u;
+  // settings: for each row, or one for all
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  float temperature_all;
+  int32_t top_k_all;
+  float top_p_all, min_p_all;
+  int32_t* ids;
+  float* logp;
+  int32_t shift;  // log2 of the vocabulary, rounded up, at least 1 (the launch fills it in)
+};
+cudaError_t launch_sample(const SampleArgs& A, int dtype, int num_sms, cudaStream_t st);
 
 }  // namespace okls

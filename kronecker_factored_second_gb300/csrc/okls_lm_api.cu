@@ -436,4 +436,159 @@ okls_status okls_token_logprobs_grad(const void* logits, int32_t dtype, int64_t 
                                        dentropy, dlogits, ldd, stream);
 }
 
+// ----------------------------------------------------------------- AdamW
+static_assert(sizeof(AdamwScalars) <= OKLS_ADAMW_SCALARS_BYTES, "okls.h holds the size");
+
+static okls_status check_adamw(const char* op, const okls_adamw_config* c) {
+  if (!c) return bad(op, "config is NULL");
+  if (!(c->lr >= 0.0) || std::isinf(c->lr)) return bad(op, "lr must be finite and non-negative");
+  if (!(c->beta1 >= 0.0 && c->beta1 < 1.0) || !(c->beta2 >= 0.0 && c->beta2 < 1.0)) return bad(op, "betas must be in [0, 1)");
+  if (!(c->eps >= 0.0) || std::isinf(c->eps)) return bad(op, "eps must be finite and non-negative");
+  if (!(c->weight_decay >= 0.0) || std::isinf(c->weight_decay)) return bad(op, "weight_decay must be finite and non-negative");
+  return OKLS_OK;
+}
+
+static AdamwHyper adamw_hyper(const okls_adamw_config* c) {
+  return {c->lr, c->beta1, c->beta2, c->eps, c->weight_decay, c->seed};
+}
+
+okls_status okls_adamw_clock(const okls_adamw_config* config, const float* lr_dev, int64_t* step_dev, void* scalars_dev,
+                             void* stream) {
+  const char* op = "okls_adamw_clock";
+  LM_TRY(check_adamw(op, config));
+  LM_TRY(check_vec(op, "lr_dev", lr_dev));
+  LM_TRY(check_mat(op, "step_dev", step_dev, 1, 1, 1, 8));
+  LM_TRY(check_mat(op, "scalars_dev", scalars_dev, 1, 1, 1, 16));
+  int sms = 0;
+  LM_TRY(host_device_sms(&sms));
+  return launched(op, launch_adamw_clock(adamw_hyper(config), lr_dev, step_dev, static_cast<AdamwScalars*>(scalars_dev),
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+okls_status okls_adamw_step(const okls_adamw_tensor* tensors, int64_t num, int32_t param_dtype, int32_t grad_dtype,
+                            int32_t state_dtype, const okls_adamw_config* config, int64_t step, const void* scalars_dev,
+                            void* stream) {
+  const char* op = "okls_adamw_step";
+  if (!float_dtype(param_dtype) || !float_dtype(grad_dtype)) return bad(op, "param and grad dtypes must be fp32 or bf16");
+  if (state_dtype != OKLS_F32 && state_dtype != OKLS_E4M3) return bad(op, "state_dtype must be fp32 or e4m3");
+  LM_TRY(check_adamw(op, config));
+  if (num < 0 || (num > 0 && !tensors)) return bad(op, "tensors is NULL or num negative");
+  if (!scalars_dev && step < 1) return bad(op, "step counts from 1");
+  LM_TRY(check_mat(op, "scalars_dev", scalars_dev ? scalars_dev : tensors, 1, scalars_dev ? 1 : 0, 1, 16));
+  const bool bits8 = state_dtype == OKLS_E4M3;
+  const int se = bits8 ? 1 : 4;
+  int sms = 0;
+  const AdamwScalars s = adamw_scalars(adamw_hyper(config), scalars_dev ? 1 : step);
+  AdamwEntry e[kAdamwTable];
+  for (int64_t i = 0; i < num;) {
+    int k = 0;
+    for (; i < num && k < kAdamwTable; ++i) {
+      const okls_adamw_tensor& t = tensors[i];
+      if (t.count < 0 || t.count > (int64_t(1) << 33)) return bad(op, "a tensor's count must be in [0, 2^33]");
+      if (t.count == 0) continue;
+      LM_TRY(check_mat(op, "param", t.param, 1, t.count, t.count, elem_size(param_dtype)));
+      LM_TRY(check_mat(op, "grad", t.grad, 1, t.count, t.count, elem_size(grad_dtype)));
+      LM_TRY(check_mat(op, "exp_avg", t.exp_avg, 1, t.count, t.count, se));
+      LM_TRY(check_mat(op, "exp_avg_sq", t.exp_avg_sq, 1, t.count, t.count, se));
+      if (bits8) {
+        LM_TRY(check_mat(op, "avg_scale", t.avg_scale, 1, 1, 1, 4));
+        LM_TRY(check_mat(op, "sq_scale", t.sq_scale, 1, 1, 1, 4));
+      }
+      e[k++] = {t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.avg_scale, t.sq_scale, t.count, t.id};
+    }
+    if (k == 0) break;
+    if (sms == 0) LM_TRY(host_device_sms(&sms));
+    LM_TRY(launched(op, launch_adamw(e, k, param_dtype, grad_dtype, bits8, s, static_cast<const AdamwScalars*>(scalars_dev),
+                                     static_cast<cudaStream_t>(stream))));
+  }
+  return OKLS_OK;
+}
+
+// ---------------------------------------------------------------- 4 bits
+// Sizes and the vectors of a group's bf16 scales and zero points.
+static okls_status check_int4(const char* op, int64_t rows, int64_t cols, int64_t group, const void* scale, int64_t lds_row,
+                              int64_t lds_group, const void* zero, int64_t ldz_row, int64_t ldz_group) {
+  if (rows < 0 || cols < 0 || rows > kMaxSide || cols > kMaxSide) return bad(op, "sizes must be in [0, 2^31)");
+  if (group != 32 && group != 64 && (group < 128 || group % 128 != 0 || group > kMaxSide))
+    return bad(op, "group must be 32, 64 or a multiple of 128");
+  LM_TRY(check_mat(op, "scale", scale, 1, rows > 0 && cols > 0, 1, 2));
+  if (zero) LM_TRY(check_mat(op, "zero", zero, 1, 1, 1, 2));
+  if (lds_row < 0 || lds_group < 0 || ldz_row < 0 || ldz_group < 0) return bad(op, "negative scale pitch");
+  return OKLS_OK;
+}
+
+okls_status okls_int4_quantize(const void* x, int32_t dtype, int64_t ldx, int64_t rows, int64_t cols, int64_t group,
+                               void* codes, int64_t ldq, void* scale, int64_t lds_row, int64_t lds_group, void* zero,
+                               int64_t ldz_row, int64_t ldz_group, void* stream) {
+  const char* op = "okls_int4_quantize";
+  if (!float_dtype(dtype)) return bad(op, "dtype must be fp32 or bf16");
+  LM_TRY(check_int4(op, rows, cols, group, scale, lds_row, lds_group, zero, ldz_row, ldz_group));
+  LM_TRY(check_mat(op, "x", x, rows, cols, ldx, elem_size(dtype)));
+  LM_TRY(check_mat(op, "codes", codes, rows, lm_div_up(cols, 2), ldq, 1));
+  if (rows == 0 || cols == 0) return OKLS_OK;
+  if (lm_div_up(cols, group) > kMaxGrid / rows) return host_fail(OKLS_ERR_UNSUPPORTED, "%s: too many groups for one launch", op);
+  int sms = 0;
+  LM_TRY(host_device_sms(&sms));
+  Int4QuantArgs A = {x,     ldx,       rows, cols,    group,    static_cast<uint8_t*>(codes), ldq, scale, lds_row,
+                     lds_group, zero, ldz_row, ldz_group};
+  return launched(op, launch_int4_quantize(A, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+okls_status okls_int4_matmul(const void* x, int32_t x_dtype, int64_t ldx, const void* codes, int64_t ldq, const void* scale,
+                             int64_t lds_row, int64_t lds_group, const void* zero, int64_t ldz_row, int64_t ldz_group,
+                             int64_t group, int64_t rows, int64_t n, int64_t k, void* out, int32_t out_dtype, int64_t ldo,
+                             int32_t accumulate, void* stream) {
+  const char* op = "okls_int4_matmul";
+  if (!float_dtype(x_dtype) || !float_dtype(out_dtype)) return bad(op, "dtypes must be fp32 or bf16");
+  if (accumulate != 0 && accumulate != 1) return bad(op, "accumulate must be 0 or 1");
+  if (rows < 0 || rows > kMaxSide) return bad(op, "sizes must be in [0, 2^31)");
+  LM_TRY(check_int4(op, n, k, group, scale, lds_row, lds_group, zero, ldz_row, ldz_group));
+  LM_TRY(check_mat(op, "x", x, rows, k, ldx, elem_size(x_dtype)));
+  LM_TRY(check_mat(op, "codes", codes, n, lm_div_up(k, 2), ldq, 1));
+  LM_TRY(check_mat(op, "out", out, rows, n, ldo, elem_size(out_dtype)));
+  if (rows == 0 || n == 0) return OKLS_OK;
+  if (k > 0 && (reinterpret_cast<uintptr_t>(codes) % 16 || (n > 1 && ldq % 16)))
+    return host_fail(OKLS_ERR_UNSUPPORTED, "%s: codes need 16-byte aligned rows (ldq %lld)", op, static_cast<ll>(ldq));
+  if (rows > 65535 * int64_t(8)) return host_fail(OKLS_ERR_UNSUPPORTED, "%s: more than 524280 rows", op);
+  int sms = 0;
+  LM_TRY(host_device_sms(&sms));
+  if (k == 0) {
+    // an empty sum: zeros, or nothing to add
+    if (accumulate) return OKLS_OK;
+    return launched(op, cudaMemset2DAsync(out, static_cast<size_t>(ldo) * elem_size(out_dtype), 0,
+                                          static_cast<size_t>(n) * elem_size(out_dtype), static_cast<size_t>(rows),
+                                          static_cast<cudaStream_t>(stream)));
+  }
+  Int4Args A = {static_cast<const uint8_t*>(codes), ldq, scale, lds_row, lds_group, zero, ldz_row, ldz_group, group, x, ldx,
+                reinterpret_cast<uintptr_t>(x) % 16 == 0 && (rows <= 1 || ldx * elem_size(x_dtype) % 16 == 0),
+                rows, n, k, out, out_dtype, ldo, accumulate};
+  return launched(op, launch_int4_matmul(A, x_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+// -------------------------------------------------------------- sampling
+okls_status okls_sample(const void* logits, int32_t dtype, int64_t ldl, int64_t rows, int64_t vocab, const float* u,
+                        const okls_sample_settings* settings, int32_t* ids, float* logp, void* stream) {
+  const char* op = "okls_sample";
+  if (!float_dtype(dtype)) return bad(op, "dtype must be fp32 or bf16");
+  if (rows < 0 || rows > kMaxSide || vocab < 1) return bad(op, "rows must be in [0, 2^31), vocab positive");
+  if (vocab > kSampleMaxVocab)
+    return host_fail(OKLS_ERR_UNSUPPORTED, "%s: vocab %lld is above %lld", op, static_cast<ll>(vocab), static_cast<ll>(kSampleMaxVocab));
+  if (!settings) return bad(op, "settings is NULL");
+  LM_TRY(check_mat(op, "logits", logits, rows, vocab, ldl, elem_size(dtype)));
+  LM_TRY(check_mat(op, "u", u, 1, rows, rows, 4));
+  LM_TRY(check_mat(op, "ids", ids, 1, rows, rows, 4));
+  LM_TRY(check_mat(op, "logp", logp, 1, rows, rows, 4));
+  const okls_sample_settings& s = *settings;
+  LM_TRY(check_vec(op, "temperature", s.temperature_dev));
+  LM_TRY(check_vec(op, "top_k", s.top_k_dev));
+  LM_TRY(check_vec(op, "top_p", s.top_p_dev));
+  LM_TRY(check_vec(op, "min_p", s.min_p_dev));
+  if (rows == 0) return OKLS_OK;
+  int sms = 0;
+  LM_TRY(host_device_sms(&sms));
+  SampleArgs A = {logits, ldl, rows, vocab, u, s.temperature_dev, s.top_k_dev, s.top_p_dev, s.min_p_dev, s.temperature,
+                  s.top_k, s.top_p, s.min_p, ids, logp, 0};
+  return launched(op, launch_sample(A, dtype, sms, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

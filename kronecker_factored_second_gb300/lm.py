@@ -7,6 +7,8 @@ as in okls.py):
 `rms_norm`, `rms_norm_grad`              norm with the residual's addition, output in 32, 16 or 8 bits
 `fp8_quantize`, `fp8_matmul`             e4m3 values with a scale for each 128, and their product
 `token_logprobs`, `token_logprobs_grad`  log probabilities of given tokens, entropy, best alternatives
+`int4_quantize`, `int4_matmul`           4-bit weights with a scale for each group, and their product with a few rows
+`sample`                                 tokens drawn with temperature, top-k, top-p and min-p from given random numbers
 
 and the same as differentiable functions of torch.autograd:
 
@@ -254,6 +256,94 @@ def token_logprobs_grad(logits: torch.Tensor, ids: torch.Tensor, result: TokenLo
             return token_logprobs_grad(logits, ids, result, dlogp, dentropy=dentropy, scale=scale, inplace=inplace)
     d = _n().token_logprobs_grad(logits, ids, result.lse, result.lse_rest, result.entropy, dlogp, dentropy, scale, inplace)
     return logits if inplace else d
+
+
+# -------------------------------------------------------------------- 4 bits
+@dataclass
+class Int4Tensor:
+    """A weight (rows x cols) in 4 bits: codes 0..15, two in a byte with the even column in the low half (`data`, uint8,
+    rows x ceil(cols / 2)), and a bf16 scale for each `group` consecutive columns of a row (32, 64 or a multiple of 128).
+    (code - zero) * scale stands for the value; `zero` is bf16 of scale's shape, or None for 8.
+
+    Codes from elsewhere are taken as they are; `int4_matmul` needs rows of data that start on 16-byte boundaries."""
+    data: torch.Tensor
+    scale: torch.Tensor
+    cols: int
+    group: int = 128
+    zero: torch.Tensor | None = None
+
+    def __post_init__(self):
+        if self.group not in (32, 64) and (self.group < 128 or self.group % 128):
+            _fail(f"group must be 32, 64 or a multiple of 128, not {self.group}")
+        if self.data.dim() != 2 or self.data.dtype != torch.uint8 or self.data.shape[1] != -(-self.cols // 2):
+            _fail(f"data must be a matrix of uint8 with {-(-self.cols // 2)} columns")
+        if self.data.numel() and self.data.shape[1] > 1 and self.data.stride(1) != 1:
+            _fail("the last dimension of data must be contiguous")
+        want = (self.data.shape[0], -(-self.cols // self.group))
+        for name, t in (("scale", self.scale), ("zero", self.zero)):
+            if t is not None and (tuple(t.shape) != want or t.dtype != torch.bfloat16):
+                _fail(f"{name} must be bf16 of shape {want}")
+
+    @property
+    def shape(self):
+        return torch.Size((self.data.shape[0], self.cols))
+
+    def float(self) -> torch.Tensor:
+        """The values in fp32."""
+        c = torch.stack((self.data & 15, self.data >> 4), 2).view(self.data.shape[0], -1)[:, : self.cols].float()
+
+        def spread(t):
+            return t.float().repeat_interleave(self.group, 1)[:, : self.cols]
+        return (c - (8.0 if self.zero is None else spread(self.zero))) * spread(self.scale)
+
+
+def int4_quantize(w: torch.Tensor, *, group: int = 128, symmetric: bool = True, stream=None) -> Int4Tensor:
+    """An Int4Tensor of w (rows x columns).  `symmetric` codes are 1..15 around
+    8; otherwise a group's range, 0 included, is spread over 0..15 with a zero point."""
+    if stream is not None:
+        with _on(stream, w):
+            return int4_quantize(w, group=group, symmetric=symmetric)
+    q, s, z = _n().int4_quantize(w, group, symmetric)
+    return Int4Tensor(q, s, w.shape[1], group, z)
+
+
+def int4_matmul(x: torch.Tensor, w: Int4Tensor, *, out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                accumulate: bool = False, stream=None) -> torch.Tensor:
+    """x w^T in fp32 or bf16 (default: x's type) for the tokens of a generation
+    step: x (..., columns of w) fp32 or bf16, up to some 64 rows of it.  More
+    rows are right but not fast; a prompt is `fp8_matmul`'s.  With `accumulate`
+    it is added to `out` (rows x rows of w).  No gradient flows through it."""
+    if stream is not None:
+        with _on(stream, x, w.data, w.scale, w.zero, out):
+            return int4_matmul(x, w, out_dtype=out_dtype, out=out, accumulate=accumulate)
+    got = _n().int4_matmul(x, w.data, w.scale, w.zero, w.cols, w.group, out, out_dtype, accumulate)
+    return got if out is None else out
+
+
+# ------------------------------------------------------------------ sampling
+@dataclass
+class TokenSample:
+    """Per row: the drawn token (int32), and its log probability among the tokens that were left to draw from."""
+    ids: torch.Tensor
+    logp: torch.Tensor
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=1.0, top_k=None, top_p=None, min_p=None,
+           stream=None) -> TokenSample:
+    """A token from each row of logits, drawn with the row's `u` in [0, 1) (fp32).
+
+    `temperature` divides the logits (0: the best token); `top_k` keeps the k
+    best tokens, equal logits in the order of their ids; `top_p` of those the
+    shortest prefix that has at least this share of their probability; `min_p`
+    those with at least this share of the best token's probability.  The token
+    is the first, in the order of ids, at which the running probability of what
+    is kept is above u.  A setting is a number, None (off), or a tensor with a
+    value for each row (fp32; top_k int32, 0 or less: off).  A row without a possible token
+    (all -inf) gets id -1 and log probability -inf."""
+    if stream is not None:
+        with _on(stream, logits, u, *(t for t in (temperature, top_k, top_p, min_p) if isinstance(t, torch.Tensor))):
+            return sample(logits, u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
+    return TokenSample(*_n().sample(logits, u, temperature, top_k, top_p, min_p))
 
 
 # ------------------------------------------------------------------ autograd

@@ -15,6 +15,9 @@
                    matrices up to 16384 x 16384 and rank + oversample <= 544
                    in this build); the sketch's Gaussian draws come from a
                    torch.Generator and are passed to the library as an input.
+`AdamW`            AdamW for the parameters that are no matrices (or for all),
+                   one launch for many tensors, states in 32 or in 8 bits;
+                   `adamw_step` is its step on given tensors.
 
 All arithmetic happens in libokls.so; nothing here computes on the CPU.
 """
@@ -408,3 +411,119 @@ class Clean(torch.optim.Optimizer):
                                         dtype=torch.float32)
                 ob.step(p.data, p.grad.contiguous(), g["lr"], noise=noise)
         return loss
+
+
+# -------------------------------------------------------------------- AdamW
+def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1: float = 0.9, beta2: float = 0.999,
+               eps: float = 1e-8, weight_decay: float = 0.01, avg_scales=None, sq_scales=None, seed: int = 0, stream=None):
+    """One AdamW step over lists of tensors, written over params, exp_avgs and
+    exp_avg_sqs (and the scales):
+
+        m <- beta1 m + (1 - beta1) g,   v <- beta2 v + (1 - beta2) g^2
+        p <- p - lr weight_decay p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+
+    Tensors are contiguous CUDA tensors on one device; params and grads are
+    fp32 or bf16, each on its own.  exp_avgs and exp_avg_sqs are fp32; or, with
+    `avg_scales` and `sq_scales` (lists of fp32 tensors, a value for each 128 elements
+    of a tensor), e4m3 codes of m and of the root of v, rounded by chance with the mean kept;
+    `seed` with the step's number, the tensor's place in the list and the
+    element decides the chances.  The update uses the moments before that rounding.
+
+    `step` is the step's number, from 1; or an int64 CUDA tensor with the number of steps done, which
+    the call raises by one (what a captured step needs), and then `lr` may be an fp32 CUDA tensor."""
+    from . import lm
+    if stream is not None:
+        def tensors():
+            for group in (params, grads, exp_avgs, exp_avg_sqs, avg_scales or (), sq_scales or (), (step, lr)):
+                yield from (t for t in group if isinstance(t, torch.Tensor))
+        with lm._on(stream, *tensors()):
+            return adamw_step(params, grads, exp_avgs, exp_avg_sqs, step=step, lr=lr, beta1=beta1, beta2=beta2, eps=eps,
+                              weight_decay=weight_decay, avg_scales=avg_scales, sq_scales=sq_scales, seed=seed)
+    with torch.no_grad():
+        lm._n().adamw_step(params, grads, exp_avgs, exp_avg_sqs, avg_scales, sq_scales, step, lr, beta1, beta2, eps,
+                           weight_decay, seed % (1 << 64))
+
+
+class AdamW(torch.optim.Optimizer):
+    """AdamW over contiguous fp32 and bf16 CUDA parameters of any shape: what a
+    model has besides the matrices of the optimizers above (token tables,
+    norms, biases), or all of it.
+
+    `state_bits` 8 keeps the moments as e4m3 codes with a scale for each 128
+    elements, rounded by chance (see `adamw_step`); `seed` decides the chances.
+    `capturable` keeps the steps' numbers on the device, for a step that is
+    captured into a CUDA graph (run one outside of it first, which makes the
+    states); lr may then be an fp32 CUDA tensor.  Every parameter of a
+    capturable group needs a gradient at each of its steps."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+                 state_bits: int = 32, seed: int = 0, capturable: bool = False):
+        if state_bits not in (8, 32):
+            raise ValueError("okls: state_bits must be 8 or 32")
+        if isinstance(lr, torch.Tensor) and not capturable:
+            raise ValueError("okls: a learning rate on the device needs capturable=True")
+        if not all(0.0 <= b < 1.0 for b in betas) or not eps >= 0.0 or not weight_decay >= 0.0:
+            raise ValueError("okls: betas must be in [0, 1), eps and weight_decay not negative")
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits,
+                                      seed=seed, capturable=capturable))
+
+    def _new_state(self, p, group):
+        dt = torch.float32 if group["state_bits"] == 32 else torch.float8_e4m3fn
+        st = dict(step=0, exp_avg=torch.zeros(p.shape, dtype=dt, device=p.device),
+                  exp_avg_sq=torch.zeros(p.shape, dtype=dt, device=p.device))
+        if group["state_bits"] == 8:
+            for name in ("avg_scale", "sq_scale"):
+                st[name] = torch.zeros(-(-p.numel() // 128), device=p.device)
+        return st
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for g in self.param_groups:
+            # parameters whose steps have one number go together
+            lists = {}
+            for p in g["params"]:
+                if p.grad is None:
+                    if g["capturable"] and self.state[p]:
+                        raise RuntimeError("okls: every parameter of a capturable group needs a gradient at each step")
+                    continue
+                st = self.state[p]
+                if not st:
+                    st.update(self._new_state(p, g))
+                    if g["capturable"]:
+                        st["step"] = lists.setdefault(("new", p.device), torch.zeros(1, dtype=torch.int64, device=p.device))
+                key = id(st["step"]) if g["capturable"] else (st["step"] + 1, p.device)
+                lists.setdefault(key, []).append((p, st))
+            for key, items in lists.items():
+                if not isinstance(items, list):
+                    continue
+                number = items[0][1]["step"] if g["capturable"] else key[0]
+                names = ("exp_avg", "exp_avg_sq") + (("avg_scale", "sq_scale") if g["state_bits"] == 8 else ())
+                m, v, *scales = ([st[n] for _, st in items] for n in names)
+                beta1, beta2 = g["betas"]
+                adamw_step([p for p, _ in items], [p.grad.contiguous() for p, _ in items], m, v, step=number, lr=g["lr"],
+                           beta1=beta1, beta2=beta2, eps=g["eps"], weight_decay=g["weight_decay"],
+                           avg_scales=scales[0] if scales else None, sq_scales=scales[1] if scales else None,
+                           seed=g["seed"])
+                if not g["capturable"]:
+                    for _, st in items:
+                        st["step"] = number
+        return loss
+
+    def load_state_dict(self, state_dict):
+        """As torch's, but the moments keep their own types (torch gives them the parameters')."""
+        super().load_state_dict(state_dict)
+        shared = {}  # parameters that counted their steps together do so again
+        for saved, group in zip(state_dict["param_groups"], self.param_groups):
+            for index, p in zip(saved["params"], group["params"]):
+                for name, x in state_dict["state"].get(index, {}).items():
+                    if isinstance(x, torch.Tensor):
+                        if name != "step":
+                            x = x.detach().to(p.device, copy=True)
+                        else:
+                            key = (x.data_ptr(), p.device)
+                            x = shared[key] if key in shared else shared.setdefault(key, x.detach().to(p.device, copy=True))
+                    self.state[p][name] = x
