@@ -136,19 +136,44 @@ __device__ __forceinline__ float round_exact(float x, float mul, float rest, uin
   const float y = t + low, under = low - (y - t);  // y + under, with under at most half of y's last bit
   uint32_t b = __float_as_uint(y) + (random << 4) + 8u;
   if ((b & 0xFFFFFu) == 0 && under < 0.0f) --b;
-  const float q = fminf(__uint_as_float(b & 0xFFF00000u) - off, kFp8Max);
+  const float q = __uint_as_float(b & 0xFFF00000u) - off;
   return root && x > 0.0f ? fmaxf(q, kCodeTiny) : q;
 }
 
-// The same from one word, which is off by two of its last bits at most.  `near`
-// keeps the least distance from a border, and `small` the least y that is not
-// 0: where a sum ends within 4 bits of a border, and below the normal values,
-// round_exact has to decide.
-__device__ __forceinline__ float round_code(float x, float mul, uint32_t random, uint32_t& near, uint32_t& small) {
-  const uint32_t y = __float_as_uint(x * mul), b = y + (random << 4) + 8u;
-  near = min(near, (b + 4u) & 0xFFFFFu);
-  small = min(small, y - 1u);
-  return fminf(__uint_as_float(b & 0xFFF00000u), kFp8Max);
+// The same from one word with its sign, which is off by two of its last bits
+// at most.  A sum that ends within 4 bits of a border (12 instead of 8 bits
+// are added, so that those are the last 8), and a y below the normal values
+// that is not 0, leave it to round_exact: `near` keeps the least distance, `small`
+// the least y.  A y past 448 by its own error stays below the next code.
+struct Doubt {
+  uint32_t near = ~0u, small = ~0u;
+  __device__ __forceinline__ bool any() const { return near < 8u || small < 2u * __float_as_uint(kCodeSmall) - 1u; }
+};
+// random20: the random number 4 bits up.
+__device__ __forceinline__ float round_code(float y, uint32_t random20, Doubt& d) {
+  const uint32_t u = __float_as_uint(y), b = u + random20 + 12u;
+  d.near = min(d.near, b & 0xFFFFFu);
+  d.small = min(d.small, u + u - 1u);
+  return __uint_as_float(b & 0xFFF00000u);
+}
+
+// fp32's root of v >= 2^-126, to its last bit but for one in some thousands; 0 for 0.
+__device__ __forceinline__ float root_of(float v) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(v, 1.1754944e-38f)));
+  const float r = v * y;
+  return fmaf(fmaf(-r, r, v), 0.5f * y, r);
+}
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// The larger magnitude, or NaN.
+__device__ __forceinline__ float max_mag(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
 }
 
 __device__ __forceinline__ void codes_to_f32(uint32_t w, float* v) {
@@ -230,8 +255,8 @@ __global__ void __launch_bounds__(kAdamThreads, 3) k_adamw8(const __grid_constan
       // (each product and sum rounded: what a code is must not hang on how a compiler joins them)
       const float rv = __fmul_rn(r[j], vs), gv = __fmul_rn(__fmul_rn(s.rest2, b[j]), b[j]);
       m[j] = __fadd_rn(__fmul_rn(s.beta1, __fmul_rn(m[j], ms)), __fmul_rn(s.rest1, b[j]));
-      r[j] = __fsqrt_rn(__fadd_rn(__fmul_rn(s.beta2, __fmul_rn(rv, rv)), gv));
-      a[j] = fmaf(-s.rate, __fdividef(m[j], fmaf(r[j], s.root, s.eps)), fmaf(-s.decay, a[j], a[j]));
+      r[j] = root_of(__fadd_rn(__fmul_rn(s.beta2, __fmul_rn(rv, rv)), gv));
+      a[j] = fmaf(-s.rate * m[j], reciprocal(fmaf(r[j], s.root, s.eps)), fmaf(-s.decay, a[j], a[j]));
     }
   }
   if (vec) {
@@ -248,9 +273,10 @@ __global__ void __launch_bounds__(kAdamThreads, 3) k_adamw8(const __grid_constan
   }
 
   // (elements past the end are zeros: they change no maximum)
-  uint32_t am = 0, av = 0;
+  float top_m = 0.0f, top_r = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kOwn8; ++j) am = max(am, mag_bits(m[j])), av = max(av, mag_bits(r[j]));
+  for (int j = 0; j < kOwn8; ++j) top_m = max_mag(top_m, m[j]), top_r = max_mag(top_r, r[j]);
+  uint32_t am = __float_as_uint(top_m), av = __float_as_uint(top_r);
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) {
     am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
@@ -260,22 +286,23 @@ __global__ void __launch_bounds__(kAdamThreads, 3) k_adamw8(const __grid_constan
   state_scales(am, &mmul, &mscale);
   state_scales(av, &vmul, &vscale);
   const uint32_t low = s.low + static_cast<uint32_t>(e.id);
-  uint32_t wm[4], wv[4], near = ~0u, small = ~0u;
+  uint32_t wm[4], wv[4];
+  Doubt doubt;
 #pragma unroll
   for (int j = 0; j < kOwn8; j += 4) {
     float qm[4], qv[4];
 #pragma unroll
     for (int h = 0; h < 4; h += 2) {
       const uint2 w = philox(static_cast<uint32_t>((i + j + h) >> 1), low, s.key);
-      qm[h] = copysignf(round_code(fabsf(m[j + h]), mmul, w.x & 0xFFFFu, near, small), m[j + h]);
-      qm[h + 1] = copysignf(round_code(fabsf(m[j + h + 1]), mmul, w.y & 0xFFFFu, near, small), m[j + h + 1]);
-      qv[h] = round_code(r[j + h], vmul, w.x >> 16, near, small);
-      qv[h + 1] = round_code(r[j + h + 1], vmul, w.y >> 16, near, small);
+      qm[h] = round_code(m[j + h] * mmul, (w.x << 4) & 0xFFFF0u, doubt);
+      qm[h + 1] = round_code(m[j + h + 1] * mmul, (w.y << 4) & 0xFFFF0u, doubt);
+      qv[h] = round_code(r[j + h] * vmul, (w.x >> 12) & 0xFFFF0u, doubt);
+      qv[h + 1] = round_code(r[j + h + 1] * vmul, (w.y >> 12) & 0xFFFF0u, doubt);
     }
     wm[j / 4] = e4m3x2(qm[0], qm[1]) | (e4m3x2(qm[2], qm[3]) << 16);
     wv[j / 4] = e4m3x2(qv[0], qv[1]) | (e4m3x2(qv[2], qv[3]) << 16);
   }
-  if (near < 8u || small < __float_as_uint(kCodeSmall) - 1u) {
+  if (doubt.any()) {
     const float mrest = mul_rest(am, mmul), vrest = mul_rest(av, vmul);
 #pragma unroll
     for (int j = 0; j < kOwn8; ++j) {

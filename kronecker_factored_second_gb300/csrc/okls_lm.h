@@ -235,7 +235,7 @@ struct Int4Args {
   int64_t ldy;
   int32_t accumulate;
 };
-cudaError_t launch_int4_matmul(const Int4Args& A, int x_dtype, cudaStream_t st);
+cudaError_t launch_int4_matmul(const Int4Args& A, int x_dtype, int num_sms, cudaStream_t st);
 
 struct Int4QuantArgs {
   const void* x;

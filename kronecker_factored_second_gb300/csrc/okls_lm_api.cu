@@ -562,7 +562,7 @@ okls_status okls_int4_matmul(const void* x, int32_t x_dtype, int64_t ldx, const 
   Int4Args A = {static_cast<const uint8_t*>(codes), ldq, scale, lds_row, lds_group, zero, ldz_row, ldz_group, group, x, ldx,
                 reinterpret_cast<uintptr_t>(x) % 16 == 0 && (rows <= 1 || ldx * elem_size(x_dtype) % 16 == 0),
                 rows, n, k, out, out_dtype, ldo, accumulate};
-  return launched(op, launch_int4_matmul(A, x_dtype, static_cast<cudaStream_t>(stream)));
+  return launched(op, launch_int4_matmul(A, x_dtype, sms, static_cast<cudaStream_t>(stream)));
 }
 
 // -------------------------------------------------------------- sampling

@@ -447,19 +447,15 @@ def _weight(g, n, k, group, zero, rowwise=False):
 
 
 def _check_int4(x, w, got, od, old=None):
-    """Products are exact; a group's sum is fp32 (its terms c - 8 and, with zero points, 8 - z apart: at most 15 + 8 of
-    |x| each), the groups' sums are joined in fp32.  Every addition of a sum of k terms, on the tensor core (which may cut
-    off instead of rounding: 2 u) or off it, is off by 2 u of at most the sum of magnitudes; of k terms, no chain is longer
-    than k / 4 + 16."""
-    v, x64 = w.float().double(), x.double()
-    if w.zero is not None:
-        k, gr = w.cols, w.group
-        s, z = (t.double().repeat_interleave(gr, 1)[:, :k] for t in (w.scale, w.zero))
-        c = torch.stack((w.data & 15, w.data >> 4), 2).view(w.data.shape[0], -1)[:, :k].double()
-        v = (c - z) * s
-        mag = x64.abs() @ (((c - 8).abs() + (8 - z).abs()) * s).t()
-    else:
-        mag = x64.abs() @ v.abs().t()
+    """Products are exact; a group's sum is fp32, of 16 + c and of -(16 + zero) times x apart; the groups' sums are joined in
+    fp32.  Every addition of a sum of k terms, on the tensor core (which may cut off instead of rounding: 2 u) or off it, is
+    off by 2 u of at most the sum of magnitudes; of k terms, no chain is longer than k / 4 + 16."""
+    x64, k, gr = x.double(), w.cols, w.group
+    s = w.scale.double().repeat_interleave(gr, 1)[:, :k]
+    z = torch.full_like(s, 8.0) if w.zero is None else w.zero.double().repeat_interleave(gr, 1)[:, :k]
+    c = torch.stack((w.data & 15, w.data >> 4), 2).view(w.data.shape[0], -1)[:, :k].double()
+    v = (c - z) * s
+    mag = x64.abs() @ ((32 + c + z) * s).t()
     want = x64 @ v.t()
     if old is not None:
         want, mag = want + old.double(), mag + old.double().abs()
