@@ -9,12 +9,13 @@
 // id (Cut).  The drawn token is the first, in the order of ids, at which the
 // running sum of the kept weights is above u times their sum.
 //
-// Sums are whole numbers.  A weight is rounded to a multiple of 2^-(62 -
-// log2 vocab), so a row's sum fits 63 bits and does not depend on the order in
-// which threads add; a running sum past u W is found by exact comparisons.  What
-// decides which token is drawn is then the weights' error alone: a hundred
-// thousand tokens have as many borders, and with weights to fp32's 2^-24 one row
-// in a thousand drew a neighbour.  So a weight is formed to about 2^-34:
+// Sums are whole numbers.  A weight is rounded to an odd multiple of 2^-(63 -
+// log2 vocab) of the largest (the middle of the interval that it lies in), so a
+// row's sum fits 63 bits and does not depend on the order in which threads add; a
+// running sum past u W is found by exact comparisons.  What decides which token
+// is drawn is then the weights' error alone: a hundred thousand tokens have as
+// many borders, and with weights to fp32's 2^-24 one row in a thousand drew a
+// neighbour.  So a weight is formed to about 2^-33:
 //   z log2(e) 2048 / T = k + r, with k whole and r in two roundings (the factor in
 //   two words, one fused product each);  k_m - k and r_m - r of the maximum are
 //   the exponent in 2048ths;  2^-(j / 2048) comes from a table of 62 bits,
@@ -22,11 +23,18 @@
 //   32 x 32 + 64 bit product joins them.
 //
 // A row belongs to a cluster of 1 to 8 CTAs (few rows need many SMs), and a
-// CTA to one row after the other.  The first pass over a row takes its maximum; what
-// follows reads it again from L2.  A cut by count or mass is found from 2048
-// bins of the order-preserving image of the values left in question; when the bin that holds the
-// border has at most 512 values they are sorted, otherwise that bin is cut into 2048
-// again (three times at most for 32 bits).
+// CTA to one row after the other.  The first pass over a row takes the maxima of
+// its segments; what follows reads it again from L2.
+//   The best token, and the first k for k up to some 256, come from the
+//   segments' maxima: the k-th largest of them is a bound that few values reach;
+//   these are listed, sorted, weighed and drawn from, and the row is not read again.
+//   A cut by mass takes two passes: one puts every weight to 14 bits into 2048
+//   bins, 64 to an octave, and shows in which bins the border lies; the second
+//   weighs every token exactly, sums what lies above those bins by segments (the
+//   sums that the drawing needs) and lists the rest, where the border is found.
+//   A cut by a larger count, and one by mass whose border's bins hold too many
+//   tokens (runs of equal logits), bins the order-preserving image of the values
+//   instead, and bins the border's bin again (three times at most for 32 bits).
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -44,7 +52,8 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kBinsThread = kBins / kThreads;
-constexpr int kList = kThreads;  // values of a border bin that are sorted
+constexpr int kList = 2 * kThreads;  // tokens that are sorted
+constexpr int kFewSegs = 320;        // segments whose maxima are ranked by counting
 constexpr int kSegs = 1024;      // segments of a CTA's part of a row
 constexpr int kSteps = 2048;     // table entries in an octave
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: added to |x| <= 2^22, leaves x rounded in the low bits
@@ -76,10 +85,26 @@ struct Heat {
   float base;    // taken from a value first: 0, or the maximum where that has many steps (then exact)
   float least;   // values below this have weight 0
   float ch, cl;  // 2048 log2(e) / T in two words
-  int kb;        // bits of the maximum's k + kMagic
+  int kb;        // bits of the maximum's k + kMagic, 62 bits to the row's unit in the octaves
   float r;       // the maximum's r
-  int shift;     // 62 bits to the row's unit, at least 1
+  float top, c;  // the maximum, log2(e) / T
+  int shift;     // 62 bits to the row's unit
 };
+
+// Two fp32 values in one instruction.
+typedef u64 Pair;
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(Pair p, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Pair both(float v) { return pair_of(v, v); }
 
 __device__ __forceinline__ void steps_of(const Heat& h, float z, int& kb, float& r) {
   const float d = fmaxf(z - h.base, h.least);
@@ -97,26 +122,52 @@ __device__ Heat make_heat(float m, float temperature, int shift) {
   // 70 octaves below the maximum there is nothing left of 62 bits
   h.least = static_cast<float>(fmax(static_cast<double>(far ? 0.0f : m) - 70.0 * 2048.0 / c, -3.4e38));
   h.shift = shift;
+  h.top = m, h.c = static_cast<float>(c / 2048.0);
   steps_of(h, m, h.kb, h.r);
+  h.kb += (shift - 1) * kSteps;
   return h;
 }
 
-__device__ __forceinline__ u64 weight(const Heat& h, const u64* powers, float z) {
-  constexpr float a = 3.3845077175778578e-4f;  // ln 2 / 2048
-  constexpr float s = 4294967296.0f;
-  int kb;
-  float r;
-  steps_of(h, z, kb, r);
-  const int k = h.kb - kb;
-  const float d = h.r - r;
-  // q 2^32 = (1 - 2^(-d / 2048)) 2^32, rounded
-  const float q = fmaf(d, fmaf(d, fmaf(d, s * (a * a * a / 6.0f), -s * (a * a / 2.0f)), s * a), kMagic);
+// q 2^32 = (1 - 2^(-d / 2048)) 2^32 for d steps, + kMagic
+constexpr float kA = 3.3845077175778578e-4f;  // ln 2 / 2048
+constexpr float kQ1 = 4294967296.0f * kA, kQ2 = -4294967296.0f * (kA * kA / 2.0f), kQ3 = 4294967296.0f * (kA * kA * kA / 6.0f);
+
+__device__ __forceinline__ u64 weight_of(const u64* powers, int k, float q) {
   const u64 p = powers[k & (kSteps - 1)];
   u64 w = p - static_cast<u64>(static_cast<long long>(static_cast<int>(p >> 32)) *
                                (__float_as_int(q) - __float_as_int(kMagic)));
-  // (rounded: a hundred thousand weights cut off are half as many units)
-  asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(w), "r"((k >> 11) + h.shift - 1));
-  return (w + 1) >> 1;
+  asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(w), "r"(k >> 11));
+  return w | 1u;
+}
+__device__ __forceinline__ u64 weight(const Heat& h, const u64* powers, float z) {
+  int kb;
+  float r;
+  steps_of(h, z, kb, r);
+  const float d = h.r - r;
+  return weight_of(powers, h.kb - kb, fmaf(d, fmaf(d, fmaf(d, kQ3, kQ2), kQ1), kMagic));
+}
+// The same of eight values: what fp32 does, two at a time.
+__device__ __forceinline__ void weights8(const Heat& h, const u64* powers, const float (&z)[8], u64 (&w)[8]) {
+  const Pair ch = both(h.ch), cl = both(h.cl), magic = both(kMagic), minus = both(-1.0f), hr = both(h.r);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const Pair d = pair_of(fmaxf(z[j] - h.base, h.least), fmaxf(z[j + 1] - h.base, h.least));
+    const Pair k = fma2(d, ch, magic);
+    const Pair r = fma2(d, cl, fma2(d, ch, fma2(k, minus, magic)));
+    const Pair s = fma2(r, minus, hr);
+    const Pair q = fma2(s, fma2(s, fma2(s, both(kQ3), both(kQ2)), both(kQ1)), magic);
+    float k0, k1, q0, q1;
+    unpair(k, k0, k1), unpair(q, q0, q1);
+    w[j] = weight_of(powers, h.kb - __float_as_int(k0), q0);
+    w[j + 1] = weight_of(powers, h.kb - __float_as_int(k1), q1);
+  }
+}
+
+// The bin of a value among 2048, 64 to an octave below the maximum: it does not
+// fall when the value does.
+__device__ __forceinline__ int mass_bin(const Heat& h, float z) {
+  const float t = fminf((h.top - z) * (h.c * 64.0f), 2047.0f);
+  return __float_as_int(t + 8388608.0f) & 0x7FFFFF;
 }
 
 // floor(f * w) or ceil for a fraction f in [0, 1).
@@ -172,13 +223,16 @@ struct Shared {
     } list;
   };
   u64 seg[kSegs];
+  float seg_max[kSegs];
   u64 warp_sum[kWarps + 1];
-  u64 total;
-  float warp_max[kWarps], max;
+  u64 total, rest;
+  float max;
+  float warp_max[kWarps];
   int listed, found;
   // the border bin
   u64 border_above;
   int border, border_count;
+  float bound;
   Cut cut;
 };
 
@@ -237,6 +291,11 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {
   }
   return v;
 }
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 __device__ __forceinline__ u64 warp_total(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -262,7 +321,7 @@ __device__ u64 cta_scan(Shared& S, u64 v) {
   return own + before;
 }
 
-// Sum of fn(value, id) over the row; segments' sums stay in S.seg and the CTA's in S.total.
+// Sum of fn(value, id) over the row; the segments' sums stay in S.seg and the CTA's in S.total.
 template <int NV, class T, class Fn>
 __device__ u64 sum_row(Shared& S, const Group& G, const Part<T>& R, Fn fn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -289,7 +348,36 @@ __device__ u64 sum_row(Shared& S, const Group& G, const Part<T>& R, Fn fn) {
   return all;
 }
 
-// The first id at which the running sum of the last sum_row is above
+// The same of the weights of all values from `least` on.
+template <int NV, class T>
+__device__ u64 sum_above(Shared& S, const Group& G, const Part<T>& R, const Heat& h, float least) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64 mine = 0;
+  for (int s = warp; s < R.segs; s += kWarps) {
+    u64 sum = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float z[8];
+      u64 w[8];
+      load_finite(R, R.from + (s * NV + v) * 256 + lane * 8, z);
+      weights8(h, S.powers, z, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (z[j] >= least) sum += w[j];
+    }
+    sum = warp_total(sum);
+    if (lane == 0) S.seg[s] = sum;
+    mine += sum;
+  }
+  cta_scan(S, lane == 0 ? mine : 0);
+  if (threadIdx.x == 0) S.total = S.warp_sum[kWarps];
+  G.sync();
+  u64 all = 0;
+  for (int r = 0; r < G.size; ++r) all += *G.of(&S.total, r);
+  return all;
+}
+
+// The first id at which the running sum of the last sums by segments is above
 // `target`; -1 in the CTAs that do not hold it (the same in all threads).
 template <int NV, class T, class Fn>
 __device__ int locate(Shared& S, const Group& G, const Part<T>& R, u64 target, Fn fn) {
@@ -348,6 +436,55 @@ __device__ int locate(Shared& S, const Group& G, const Part<T>& R, u64 target, F
   }
   __syncthreads();
   return S.found;
+}
+
+// ------------------------------------------------------------------- list
+__device__ __forceinline__ void list_begin(Shared& S) {
+  if (threadIdx.x == 0) S.listed = 0;
+  __syncthreads();
+}
+__device__ __forceinline__ void list_put(Shared& S, float z, int id) {
+  const int at = atomicAdd(&S.listed, 1);
+  if (at < kList) S.list.mine[at] = (static_cast<u64>(ord_bits(z)) << 32) | static_cast<uint32_t>(~id);
+}
+__device__ __forceinline__ float list_value(const Shared& S, int i) { return ord_value(static_cast<uint32_t>(S.list.all[i] >> 32)); }
+__device__ __forceinline__ int list_id(const Shared& S, int i) { return static_cast<int>(~static_cast<uint32_t>(S.list.all[i])); }
+
+// Joins the CTAs' lists in S.list.all and sorts them in falling order of (value,
+// -id): every CTA the same.  Returns the number of tokens, or -1 if they are too many.
+__device__ int list_sorted(Shared& S, const Group& G) {
+  G.sync();
+  int n = 0;
+  for (int r = 0; r < G.size; ++r) n += *G.of(&S.listed, r);
+  if (n > kList) return -1;
+  for (int r = 0, at = 0; r < G.size; ++r) {
+    const int c = *G.of(&S.listed, r);
+    const u64* src = G.of(S.list.mine, r);
+    for (int i = threadIdx.x; i < c; i += kThreads) S.list.all[at + i] = src[i];
+    at += c;
+  }
+  int padded = 2;
+  while (padded < n) padded <<= 1;
+  for (int i = n + threadIdx.x; i < padded; i += kThreads) S.list.all[i] = 0;
+  __syncthreads();
+  const bool small = padded <= 64;  // one warp's work
+  if (!small || threadIdx.x < 32) {
+    for (int size = 2; size <= padded; size <<= 1) {
+      for (int stride = size >> 1; stride > 0; stride >>= 1) {
+        const int t = threadIdx.x, i = 2 * t - (t & (stride - 1)), k = i + stride;
+        if (k < padded) {
+          const u64 a = S.list.all[i], b = S.list.all[k];
+          if ((a < b) == ((i & size) == 0)) S.list.all[i] = b, S.list.all[k] = a;
+        }
+        if (small)
+          __syncwarp();
+        else
+          __syncthreads();
+      }
+    }
+  }
+  __syncthreads();
+  return n;
 }
 
 // The first token, in falling order of (value, -id) among those that `in`
@@ -453,8 +590,7 @@ __device__ bool select(Shared& S, const Group& G, const Part<T>& R, const Heat& 
     if (count <= kList) break;
   }
   // sort what lies in the border bin
-  if (threadIdx.x == 0) S.listed = 0;
-  __syncthreads();
+  list_begin(S);
   for (int s = warp; s < R.segs; s += kWarps) {
 #pragma unroll 1
     for (int v = 0; v < NV; ++v) {
@@ -466,47 +602,223 @@ __device__ bool select(Shared& S, const Group& G, const Part<T>& R, const Heat& 
         const int id = q + j - R.shift;
         if (!kept(in, z[j], id)) continue;
         const uint32_t key = ord_bits(z[j]);
-        if (key > high || key < low) continue;
-        S.list.mine[atomicAdd(&S.listed, 1)] = (static_cast<u64>(key) << 32) | static_cast<uint32_t>(~id);
+        if (key <= high && key >= low) list_put(S, z[j], id);
       }
     }
   }
-  G.sync();
-  int n = 0;
-  for (int r = 0; r < G.size; ++r) {
-    const int c = *G.of(&S.listed, r);
-    const u64* src = G.of(S.list.mine, r);
-    for (int i = threadIdx.x; i < c; i += kThreads) S.list.all[n + i] = src[i];
-    n += c;
+  const int n = list_sorted(S, G);
+  u64 w[2], run[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = 2 * threadIdx.x + i;
+    w[i] = at >= n ? 0 : MASS ? weight(h, S.powers, list_value(S, at)) : 1;
   }
-  int padded = 2;
-  while (padded < n) padded <<= 1;
-  for (int i = n + threadIdx.x; i < padded; i += kThreads) S.list.all[i] = 0;
-  __syncthreads();
-  for (int size = 2; size <= padded; size <<= 1) {
-    for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      const int i = threadIdx.x, k = i ^ stride;
-      if (i < padded && k > i) {
-        const u64 a = S.list.all[i], b = S.list.all[k];
-        if ((a < b) == ((i & size) == 0)) S.list.all[i] = b, S.list.all[k] = a;
-      }
-      __syncthreads();
-    }
+  run[1] = cta_scan(S, w[0] + w[1]), run[0] = run[1] - w[1];
+  const u64 need = target - above;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = 2 * threadIdx.x + i;
+    if (at < n && run[i] >= need && run[i] - w[i] < need) S.cut = {list_value(S, at), list_id(S, at)};
   }
-  const u64 entry = threadIdx.x < n ? S.list.all[threadIdx.x] : 0;
-  const float value = ord_value(static_cast<uint32_t>(entry >> 32));
-  u64 a = 0;
-  if (threadIdx.x < n) a = MASS ? weight(h, S.powers, value) : 1;
-  const u64 run = cta_scan(S, a), need = target - above;
-  if (threadIdx.x < n && run >= need && run - a < need) S.cut = {value, static_cast<int>(~static_cast<uint32_t>(entry))};
   __syncthreads();
   *out = S.cut;
   G.sync();
   return true;
 }
 
+// The first k tokens, from the segments' maxima: sorted in S.list.all, their
+// number returned.  0 where that does not work out (too many segments or
+// tokens at the bound).
+template <int NV, class T>
+__device__ int list_best(Shared& S, const Group& G, const Part<T>& R, int k) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int all = 0;
+  for (int r = 0; r < G.size; ++r) all += *G.of(&S.border_count, r);
+  if (all > kFewSegs || 2 * k > all) return 0;
+  // every CTA ranks all maxima; equal ones by their place
+  float* maxima = reinterpret_cast<float*>(S.list.all);
+  for (int r = 0, at = 0; r < G.size; ++r) {
+    const int n = *G.of(&S.border_count, r);
+    for (int i = threadIdx.x; i < n; i += kThreads) maxima[at + i] = G.of(S.seg_max, r)[i];
+    at += n;
+  }
+  if (threadIdx.x == 0) S.listed = 0;
+  __syncthreads();
+  if (threadIdx.x < all) {
+    const float own = maxima[threadIdx.x];
+    int rank = 0;
+    for (int i = 0; i < all; ++i) rank += maxima[i] > own || (maxima[i] == own && i < static_cast<int>(threadIdx.x));
+    if (rank == k - 1) S.bound = own;
+  }
+  __syncthreads();
+  const float bound = R.infinite ? 0.0f : S.bound;
+  // (a bound of -inf: fewer than k segments have a possible token)
+  if (bound == -CUDART_INF_F) {
+    G.sync();
+    return 0;
+  }
+  for (int s = warp; s < R.segs; s += kWarps) {
+    if (S.seg_max[s] < S.bound) continue;
+#pragma unroll 1
+    for (int v = 0; v < NV; ++v) {
+      const int q = R.from + (s * NV + v) * 256 + lane * 8;
+      float z[8];
+      load_finite(R, q, z);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (z[j] >= bound) list_put(S, z[j], q + j - R.shift);
+    }
+  }
+  return list_sorted(S, G);
+}
+
+// Cut by mass: the shortest prefix of the tokens that `of` keeps whose mass is
+// at least p of theirs, and that `in` keeps (tighter than `of`).  Leaves in S.seg
+// and S.total the sums by segments of what is kept, and returns their sum; 0
+// where the border's bins hold too many tokens.
+template <int NV, class T>
+__device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const Heat& h, float p, const Cut& of, const Cut& in,
+                           Cut* out) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) S.bin.low[i] = 0;
+  __syncthreads();
+  for (int s = warp; s < R.segs; s += kWarps) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int q = R.from + (s * NV + v) * 256 + lane * 8;
+      float z[8];
+      load_finite(R, q, z);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!kept(of, z[j], q + j - R.shift)) continue;
+        const int b = mass_bin(h, z[j]);
+        // the weight in its bin's octave, to 14 bits
+        const float w = exp2f(static_cast<float>((b >> 6) + 14) - (h.top - z[j]) * h.c);
+        if (b < kBins - 1) atomicAdd(&S.bin.low[b], static_cast<uint32_t>(__float2int_rn(w)));
+      }
+    }
+  }
+  G.sync();
+  float mass[kBinsThread], sum = 0.0f;
+  const int b0 = threadIdx.x * kBinsThread;
+#pragma unroll
+  for (int i = 0; i < kBinsThread; ++i) {
+    uint64_t n = 0;
+    for (int r = 0; r < G.size; ++r) n += *G.of(&S.bin.low[b0 + i], r);
+    mass[i] = exp2f(-static_cast<float>(((b0 + i) >> 6) + 14)) * static_cast<float>(n);
+    sum += mass[i];
+  }
+  // (in whole numbers again: 2^-40 of the largest weight)
+  const u64 run = cta_scan(S, static_cast<u64>(static_cast<double>(sum) * 1099511627776.0));
+  const double goal = static_cast<double>(p) * static_cast<double>(S.warp_sum[kWarps]) * (1.0 / 1099511627776.0);
+  const double margin = static_cast<double>(S.warp_sum[kWarps]) * (1.0 / 1099511627776.0) * (1.0 / 4096.0);
+  if (threadIdx.x == 0) S.border = 0, S.border_count = kBins - 1;
+  __syncthreads();
+  double at = static_cast<double>(run) * (1.0 / 1099511627776.0) - static_cast<double>(sum);
+#pragma unroll
+  for (int i = 0; i < kBinsThread; ++i) {
+    const double next = at + static_cast<double>(mass[i]);
+    if (at < goal - margin && next >= goal - margin) S.border = b0 + i;
+    if (at < goal + margin && next >= goal + margin) S.border_count = b0 + i;
+    at = next;
+  }
+  __syncthreads();
+  const int first = S.border, last = S.border_count;
+  G.sync();
+
+  // exact masses: of all, of what lies above the border's bins by segments; the border's bins are listed
+  list_begin(S);
+  u64 above = 0, rest = 0;
+  for (int s = warp; s < R.segs; s += kWarps) {
+    u64 part = 0;
+#pragma unroll 1
+    for (int v = 0; v < NV; ++v) {
+      const int q = R.from + (s * NV + v) * 256 + lane * 8;
+      float z[8];
+      u64 w[8];
+      load_finite(R, q, z);
+      weights8(h, S.powers, z, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int id = q + j - R.shift;
+        if (!kept(of, z[j], id)) continue;
+        const int b = mass_bin(h, z[j]);
+        if (b > last || !kept(in, z[j], id))
+          rest += w[j];
+        else if (b < first)
+          part += w[j];
+        else
+          list_put(S, z[j], id);
+      }
+    }
+    part = warp_total(part);
+    if (lane == 0) S.seg[s] = part;
+    above += part;
+  }
+  rest = warp_total(rest);
+  cta_scan(S, lane == 0 ? above : 0);
+  if (threadIdx.x == 0) S.total = S.warp_sum[kWarps];
+  cta_scan(S, lane == 0 ? rest : 0);
+  if (threadIdx.x == 0) S.rest = S.warp_sum[kWarps];
+  const int n = list_sorted(S, G);
+  u64 mass_above = 0, mass_rest = 0;
+  for (int r = 0; r < G.size; ++r) mass_above += *G.of(&S.total, r), mass_rest += *G.of(&S.rest, r);
+  if (n < 0) {
+    G.sync();
+    return 0;
+  }
+  u64 w[2], at_run[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) w[i] = 2 * static_cast<int>(threadIdx.x) + i < n ? weight(h, S.powers, list_value(S, 2 * threadIdx.x + i)) : 0;
+  at_run[1] = cta_scan(S, w[0] + w[1]), at_run[0] = at_run[1] - w[1];
+  const u64 listed = S.warp_sum[kWarps], all = mass_above + listed + mass_rest;
+  u64 target = fraction_of(p, all, true);
+  if (target < 1) target = 1;
+  if (threadIdx.x == 0) S.cut = in, S.found = n;
+  __syncthreads();
+  // the border lies above the bins: they were chosen wrongly; or below: `in` ends before it, or wrongly
+  const bool wrong = mass_above >= target || (mass_above + listed < target && mass_bin(h, in.value) > last);
+  const u64 need = target - mass_above;
+  if (!wrong && listed >= need) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (at_run[i] >= need && at_run[i] - w[i] < need) {
+        const int e = 2 * threadIdx.x + i;
+        S.cut = {list_value(S, e), list_id(S, e)}, S.found = e + 1;
+      }
+    }
+  }
+  __syncthreads();
+  *out = S.cut;
+  const int some = S.found;
+  if (wrong) {
+    G.sync();
+    return 0;
+  }
+  // the listed tokens that stay join their segments
+  u64 more = 0, own = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = 2 * threadIdx.x + i;
+    if (e >= some) continue;
+    more += w[i];
+    const int s = list_id(S, e) + R.shift - R.from;
+    if (s >= 0 && s / (NV * 256) < R.segs) {
+      atomicAdd(&S.seg[s / (NV * 256)], w[i]);
+      own += w[i];
+    }
+  }
+  cta_scan(S, more);
+  const u64 kept_sum = mass_above + S.warp_sum[kWarps];
+  cta_scan(S, own);
+  G.sync();
+  if (threadIdx.x == 0) S.total += S.warp_sum[kWarps];
+  G.sync();
+  return kept_sum;
+}
+
 template <class T, int NV>
-__global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs A) {
+__global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs A) {
   extern __shared__ unsigned char raw[];
   Shared& S = *reinterpret_cast<Shared*>(raw);
   Group G = {cg::this_cluster(), 0, 1};
@@ -527,23 +839,30 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs A) {
     R.infinite = false;
 
     float top = -CUDART_INF_F;
-    for (int s = warp; s < R.segs; s += kWarps) {
+    constexpr int kTogether = 4 / NV;  // segments on their way together
+    for (int s0 = warp; s0 < R.segs; s0 += kWarps * kTogether) {
+      float z[4][8];
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float z[8];
-        load_block(R, R.from + (s * NV + v) * 256 + lane * 8, z);
+      for (int i = 0; i < 4; ++i) load_block(R, R.from + ((s0 + i / NV * kWarps) * NV + i % NV) * 256 + lane * 8, z[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, z[j]);
+      for (int i = 0; i < kTogether; ++i) {
+        float best = -CUDART_INF_F;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) best = fmaxf(best, z[i * NV + v][j]);
+        best = warp_max(best);
+        const int s = s0 + i * kWarps;
+        if (lane == 0 && s < R.segs) S.seg_max[s] = best;
+        // (a segment behind this CTA's is another's, or -inf)
+        if (s < R.segs) top = fmaxf(top, best);
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    __syncthreads();
     if (lane == 0) S.warp_max[warp] = top;
     __syncthreads();
     if (threadIdx.x == 0) {
       for (int w = 1; w < kWarps; ++w) top = fmaxf(top, S.warp_max[w]);
-      S.max = top;
+      S.max = top, S.border_count = R.segs;
     }
     G.sync();
     top = -CUDART_INF_F;
@@ -553,27 +872,100 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs A) {
       G.sync();
       continue;
     }
-    if (top == CUDART_INF_F) R.infinite = true, top = 0.0f;
 
     float temperature = A.temperature ? A.temperature[row] : A.temperature_all;
     int64_t k = A.top_k ? A.top_k[row] : A.top_k_all;
     const float p = A.top_p ? A.top_p[row] : A.top_p_all;
     float least = A.min_p ? A.min_p[row] : A.min_p_all;
     // (a NaN fails the comparison that would turn its filter on)
-    if (!(temperature >= kSampleColdest)) temperature = 1.0f, k = 1;
-    if (p <= 0.0f) k = 1;
-    const bool by_count = k > 0 && k < vocab, by_mass = p < 1.0f && p > 0.0f && k != 1;
+    if (!(temperature >= kSampleColdest) || p <= 0.0f) k = 1;
+    if (k == 1) {
+      // the first token of the largest value
+      if (threadIdx.x == 0) S.found = kAllIds;
+      __syncthreads();
+      for (int s = warp; s < R.segs; s += kWarps) {
+        if (S.seg_max[s] != top) continue;
+#pragma unroll 1
+        for (int v = 0; v < NV; ++v) {
+          const int q = R.from + (s * NV + v) * 256 + lane * 8;
+          float z[8];
+          load_block(R, q, z);
+          int id = kAllIds;
+#pragma unroll
+          for (int j = 7; j >= 0; --j)
+            if (z[j] == top) id = q + j - R.shift;
+          if (id != kAllIds) atomicMin(&S.found, id);
+        }
+      }
+      G.sync();
+      if (G.rank == 0 && threadIdx.x == 0) {
+        int id = kAllIds;
+        for (int r = 0; r < G.size; ++r) id = min(id, *G.of(&S.found, r));
+        A.ids[row] = id, A.logp[row] = 0.0f;
+      }
+      G.sync();
+      continue;
+    }
+    if (top == CUDART_INF_F) R.infinite = true, top = 0.0f;
+    const bool by_count = k > 0 && k < vocab, by_mass = p < 1.0f;
     const Heat h = make_heat(top, temperature, A.shift);
 
     const Cut all = {-3.402823466e38f, kAllIds};  // every possible token
-    Cut floor_cut = all;
+    // no token whose weight is below half a unit is drawn (a mask of the type's lowest value among them)
+    const double unit_at = static_cast<double>(top) - static_cast<double>(temperature) * (kLn2 * (63 - A.shift));
+    const float unit_cut = static_cast<float>(fmax(unit_at, -3.402823466e38));
+    Cut floor_cut = {unit_cut, kAllIds};
     if (least > 0.0f) {
       // the least value is rounded up to fp32, so that comparing values is exact
       const double t = static_cast<double>(top) + static_cast<double>(temperature) * log(static_cast<double>(fminf(least, 1.0f)));
       float f = static_cast<float>(fmax(t, -3.402823466e38));
       if (static_cast<double>(f) < t) f = nextafterf(f, CUDART_INF_F);
-      floor_cut.value = f;
+      floor_cut.value = fmaxf(floor_cut.value, f);
     }
+    float u = A.u[row];
+    u = u > 0.0f ? fminf(u, 0.99999994f) : 0.0f;
+    const auto answer = [&](int id, float z, u64 mass) {
+      A.ids[row] = id;
+      A.logp[row] = static_cast<float>((static_cast<double>(z) - static_cast<double>(top)) / static_cast<double>(temperature) -
+                                       log(static_cast<double>(mass) / static_cast<double>(weight(h, S.powers, top))));
+    };
+
+    const int listed = by_count && k <= kFewSegs / 2 ? list_best<NV>(S, G, R, static_cast<int>(k)) : 0;
+    if (listed > 0) {
+      // everything happens in the list (every CTA does the same)
+      const int n = min(static_cast<int>(k), listed);
+      u64 w[2], run[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) w[i] = 2 * static_cast<int>(threadIdx.x) + i < n ? weight(h, S.powers, list_value(S, 2 * threadIdx.x + i)) : 0;
+      run[1] = cta_scan(S, w[0] + w[1]), run[0] = run[1] - w[1];
+      const u64 target = by_mass ? fraction_of(p, S.warp_sum[kWarps], true) : S.warp_sum[kWarps];
+      u64 mine = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int e = 2 * threadIdx.x + i;
+        if (e < n && (run[i] - w[i] >= target || list_value(S, e) < floor_cut.value) && e > 0) w[i] = 0;
+        if (e < n) S.seg[e] = w[i];
+        mine += w[i];
+      }
+      cta_scan(S, mine);
+      const u64 mass = S.warp_sum[kWarps], past = fraction_of(u, mass, false);
+      if (threadIdx.x == 0) S.found = kAllIds;
+      __syncthreads();
+      for (int e = threadIdx.x; e < n; e += kThreads) {
+        if (S.seg[e] == 0) continue;
+        const int id = list_id(S, e);
+        u64 sum = 0;
+        for (int i = 0; i < n; ++i) sum += list_id(S, i) <= id ? S.seg[i] : 0;
+        if (sum > past) atomicMin(&S.found, id);
+      }
+      __syncthreads();
+      if (G.rank == 0)
+        for (int e = threadIdx.x; e < n; e += kThreads)
+          if (list_id(S, e) == S.found) answer(S.found, list_value(S, e), mass);
+      G.sync();
+      continue;
+    }
+
     const auto possible = [&](const Cut& c) {
       return [&](float z, int id) { return kept(c, z, id) ? weight(h, S.powers, z) : 0ull; };
     };
@@ -583,36 +975,25 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleArgs A) {
       const Cut in = by_mass ? all : floor_cut;
       if (!select<false, NV>(S, G, R, h, static_cast<u64>(k), in, top, &cut)) cut = in;
     }
+    u64 mass = 0;
     if (by_mass) {
-      const u64 total = sum_row<NV>(S, G, R, possible(cut));
-      const u64 target = fraction_of(p, total, true);
-      Cut in = tighter(cut, floor_cut), c;
-      G.sync();
-      // tokens lighter than an equal share of what may be missing hold less than that together
-      const u64 share = (total - target) / static_cast<u64>(vocab);
-      if (share > 1) {
-        const double t = static_cast<double>(top) + static_cast<double>(temperature) *
-                         (log(static_cast<double>(share)) - kLn2 * (62 - A.shift));
-        const float f = static_cast<float>(fmax(t - 1e-6 * fabs(t) - 1e-6 * temperature, -3.402823466e38));
-        if (f > in.value) in = {f, kAllIds};
+      const Cut in = tighter(cut, floor_cut);
+      Cut c;
+      const Cut of = tighter(cut, Cut{unit_cut, kAllIds});
+      mass = cut_by_mass<NV>(S, G, R, h, p, of, in, &c);
+      if (mass == 0) {
+        const u64 target = fraction_of(p, sum_row<NV>(S, G, R, possible(of)), true);
+        G.sync();
+        if (!select<true, NV>(S, G, R, h, target < 1 ? 1 : target, in, top, &c)) c = in;
       }
-      cut = tighter(cut, floor_cut);
-      if (select<true, NV>(S, G, R, h, target < 1 ? 1 : target, in, top, &c)) cut = tighter(cut, c);
-    } else {
-      cut = tighter(cut, floor_cut);
+      cut = c;
     }
-
-    float u = A.u[row];
-    u = u > 0.0f ? fminf(u, 0.99999994f) : 0.0f;
-    const u64 mass = sum_row<NV>(S, G, R, possible(cut));
+    cut = tighter(cut, floor_cut);
+    if (mass == 0) {
+      mass = cut.id == kAllIds ? sum_above<NV>(S, G, R, h, cut.value) : sum_row<NV>(S, G, R, possible(cut));
+    }
     const int id = locate<NV>(S, G, R, fraction_of(u, mass, false), possible(cut));
-    if (id >= 0 && threadIdx.x == 0) {
-      A.ids[row] = id;
-      const float z = R.infinite ? 0.0f : to_f32(z0[id]);
-      // (a greedy row has one token: log 1)
-      A.logp[row] = static_cast<float>((static_cast<double>(z) - static_cast<double>(top)) / static_cast<double>(temperature) -
-                                       log(ldexp(static_cast<double>(mass), A.shift - 62)));
-    }
+    if (id >= 0 && threadIdx.x == 0) answer(id, R.infinite ? 0.0f : to_f32(z0[id]), mass);
     G.sync();
   }
 }
@@ -651,7 +1032,8 @@ cudaError_t launch_sample(const SampleArgs& args, int dtype, int num_sms, cudaSt
   while (lm_div_up(A.vocab + 8, size) > (kSegs - 8) * 1024) size *= 2;
   const int64_t resident = static_cast<int64_t>(num_sms) * 2 / size;
   const int clusters = static_cast<int>(A.rows < resident ? A.rows : resident);
-  const bool wide = lm_div_up(A.vocab, size) > 16384;
+  // segments of 256 values, and of 1024 where that would be more than kFewSegs
+  const bool wide = lm_div_up(A.vocab, size) > 65536;
   if (dtype == kDtF32) return wide ? launch_nv<float, 4>(A, clusters, size, st) : launch_nv<float, 1>(A, clusters, size, st);
   return wide ? launch_nv<__nv_bfloat16, 4>(A, clusters, size, st) : launch_nv<__nv_bfloat16, 1>(A, clusters, size, st);
 }
