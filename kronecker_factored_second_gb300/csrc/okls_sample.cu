@@ -25,16 +25,17 @@
 // A row belongs to a cluster of 1 to 8 CTAs (few rows need many SMs), and a
 // CTA to one row after the other.  The first pass over a row takes the maxima of
 // its segments; what follows reads it again from L2.
-//   The best token, and the first k for k up to some 256, come from the
-//   segments' maxima: the k-th largest of them is a bound that few values reach;
-//   these are listed, sorted, weighed and drawn from, and the row is not read again.
-//   A cut by mass takes two passes: one puts every weight to 14 bits into 2048
-//   bins, 64 to an octave, and shows in which bins the border lies; the second
-//   weighs every token exactly, sums what lies above those bins by segments (the
-//   sums that the drawing needs) and lists the rest, where the border is found.
-//   A cut by a larger count, and one by mass whose border's bins hold too many
-//   tokens (runs of equal logits), bins the order-preserving image of the values
-//   instead, and bins the border's bin again (three times at most for 32 bits).
+//   The best token is looked up there.  The first k of few come from a bound that
+// few values reach, the k-th largest of the segments' maxima.
+//   Other cuts put the tokens into 2048 bins first, 64 to an octave of the weight:
+// their number, or their weights to 14 bits; so the bin with the border is known, or
+// the few bins among which it is.  A second pass lists what lies in them (or, for a count that
+// fits, everything from them on); for a mass it also weighs every token exactly and sums
+// what lies above those bins by segments, which is what the drawing needs.
+//   Lists are sorted, and the border, the mass and the segments' sums found from them.
+//   Where bins hold too many tokens (runs of equal logits), the order-preserving
+// image of the values is binned instead, and the border's bin again (three times at
+// most for 32 bits).
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -57,7 +58,6 @@ constexpr int kFewSegs = 320;        // segments whose maxima are ranked by coun
 constexpr int kSegs = 1024;      // segments of a CTA's part of a row
 constexpr int kSteps = 2048;     // table entries in an octave
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: added to |x| <= 2^22, leaves x rounded in the low bits
-constexpr double kLn2 = 0.6931471805599453094;
 
 // ------------------------------------------------------------------ weights
 // 2^62 * 2^(-j / 2048).
@@ -87,24 +87,9 @@ struct Heat {
   float ch, cl;  // 2048 log2(e) / T in two words
   int kb;        // bits of the maximum's k + kMagic, 62 bits to the row's unit in the octaves
   float r;       // the maximum's r
-  float top, c;  // the maximum, log2(e) / T
+  float top, c;  // the maximum, 64 log2(e) / T
   int shift;     // 62 bits to the row's unit
 };
-
-// Two fp32 values in one instruction.
-typedef u64 Pair;
-__device__ __forceinline__ Pair pair_of(float lo, float hi) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair(Pair p, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ Pair both(float v) { return pair_of(v, v); }
 
 __device__ __forceinline__ void steps_of(const Heat& h, float z, int& kb, float& r) {
   const float d = fmaxf(z - h.base, h.least);
@@ -114,60 +99,55 @@ __device__ __forceinline__ void steps_of(const Heat& h, float z, int& kb, float&
 }
 
 __device__ Heat make_heat(float m, float temperature, int shift) {
+  // 2048 log2(e) in two words, divided to two words (fp64 is slow here: a row's
+  // few quotients and logarithms in it took longer than reading 32000 logits)
+  constexpr float c_high = 2954.639404296875f, c_low = 3.9443722e-5f;
   Heat h;
-  const double c = 2048.0 / kLn2 / static_cast<double>(temperature);
-  h.ch = static_cast<float>(c), h.cl = static_cast<float>(c - static_cast<double>(h.ch));
-  const bool far = fabs(static_cast<double>(m) * c) > 1900.0 * 2048.0;
+  h.ch = __fdiv_rn(c_high, temperature);
+  const float rest = isinf(temperature) ? 0.0f : fmaf(-h.ch, temperature, c_high) + c_low;
+  h.cl = __fdiv_rn(rest, temperature);
+  const bool far = fabsf(m * h.ch) > 1900.0f * 2048.0f;
   h.base = far ? m : 0.0f;
   // 70 octaves below the maximum there is nothing left of 62 bits
-  h.least = static_cast<float>(fmax(static_cast<double>(far ? 0.0f : m) - 70.0 * 2048.0 / c, -3.4e38));
+  h.least = fmaxf((far ? 0.0f : m) - 70.0f * 2048.0f / h.ch, -3.4e38f);
   h.shift = shift;
-  h.top = m, h.c = static_cast<float>(c / 2048.0);
+  h.top = m, h.c = h.ch * (1.0f / 32.0f);
   steps_of(h, m, h.kb, h.r);
   h.kb += (shift - 1) * kSteps;
   return h;
 }
 
-// q 2^32 = (1 - 2^(-d / 2048)) 2^32 for d steps, + kMagic
+// -q 2^32 = (2^(-d / 2048) - 1) 2^32 for d steps, + kMagic
 constexpr float kA = 3.3845077175778578e-4f;  // ln 2 / 2048
-constexpr float kQ1 = 4294967296.0f * kA, kQ2 = -4294967296.0f * (kA * kA / 2.0f), kQ3 = 4294967296.0f * (kA * kA * kA / 6.0f);
+constexpr float kQ1 = -4294967296.0f * kA, kQ2 = 4294967296.0f * (kA * kA / 2.0f), kQ3 = -4294967296.0f * (kA * kA * kA / 6.0f);
 
-__device__ __forceinline__ u64 weight_of(const u64* powers, int k, float q) {
-  const u64 p = powers[k & (kSteps - 1)];
-  u64 w = p - static_cast<u64>(static_cast<long long>(static_cast<int>(p >> 32)) *
-                               (__float_as_int(q) - __float_as_int(kMagic)));
-  asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(w), "r"(k >> 11));
-  return w | 1u;
-}
 __device__ __forceinline__ u64 weight(const Heat& h, const u64* powers, float z) {
   int kb;
   float r;
   steps_of(h, z, kb, r);
+  const int k = h.kb - kb;
   const float d = h.r - r;
-  return weight_of(powers, h.kb - kb, fmaf(d, fmaf(d, fmaf(d, kQ3, kQ2), kQ1), kMagic));
-}
-// The same of eight values: what fp32 does, two at a time.
-__device__ __forceinline__ void weights8(const Heat& h, const u64* powers, const float (&z)[8], u64 (&w)[8]) {
-  const Pair ch = both(h.ch), cl = both(h.cl), magic = both(kMagic), minus = both(-1.0f), hr = both(h.r);
-#pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    const Pair d = pair_of(fmaxf(z[j] - h.base, h.least), fmaxf(z[j + 1] - h.base, h.least));
-    const Pair k = fma2(d, ch, magic);
-    const Pair r = fma2(d, cl, fma2(d, ch, fma2(k, minus, magic)));
-    const Pair s = fma2(r, minus, hr);
-    const Pair q = fma2(s, fma2(s, fma2(s, both(kQ3), both(kQ2)), both(kQ1)), magic);
-    float k0, k1, q0, q1;
-    unpair(k, k0, k1), unpair(q, q0, q1);
-    w[j] = weight_of(powers, h.kb - __float_as_int(k0), q0);
-    w[j + 1] = weight_of(powers, h.kb - __float_as_int(k1), q1);
-  }
+  const float q = fmaf(d, fmaf(d, fmaf(d, kQ3, kQ2), kQ1), kMagic);
+  const u64 p = powers[k & (kSteps - 1)];
+  u64 w = p + static_cast<u64>(static_cast<long long>(static_cast<int>(p >> 32)) *
+                               (__float_as_int(q) - __float_as_int(kMagic)));
+  asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(w), "r"(k >> 11));
+  return w | 1u;
 }
 
 // The bin of a value among 2048, 64 to an octave below the maximum: it does not
 // fall when the value does.
-__device__ __forceinline__ int mass_bin(const Heat& h, float z) {
-  const float t = fminf((h.top - z) * (h.c * 64.0f), 2047.0f);
-  return __float_as_int(t + 8388608.0f) & 0x7FFFFF;
+__device__ __forceinline__ int bin_of(const Heat& h, float z) {
+  return __float_as_int(fminf((h.top - z) * h.c, 2047.0f) + 8388608.0f) & (kBins - 1);
+}
+// And the weight in units of 2^-14 of its bin's octave, 2^-(bin / 64).
+__device__ __forceinline__ uint32_t bin_weight(const Heat& h, float z, int& bin) {
+  const float t = fminf((h.top - z) * h.c, 2047.0f), b = t + 8388608.0f;
+  bin = __float_as_int(b) & (kBins - 1);
+  const float octave = __int_as_float(__float_as_int(b) & ~63) - 8388608.0f;
+  float w;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(octave - t, 1.0f / 64.0f, 14.0f)));
+  return __float_as_int(w + 8388608.0f) & 0xFFFFu;
 }
 
 // floor(f * w) or ceil for a fraction f in [0, 1).
@@ -232,8 +212,9 @@ struct Shared {
   // the border bin
   u64 border_above;
   int border, border_count;
-  float bound;
+  float bound, high, low;
   Cut cut;
+  double floor_below;  // temperature * ln(min_p)
 };
 
 struct Group {  // a cluster, or a CTA alone
@@ -358,12 +339,12 @@ __device__ u64 sum_above(Shared& S, const Group& G, const Part<T>& R, const Heat
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float z[8];
-      u64 w[8];
       load_finite(R, R.from + (s * NV + v) * 256 + lane * 8, z);
-      weights8(h, S.powers, z, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (z[j] >= least) sum += w[j];
+      for (int j = 0; j < 8; ++j) {
+        const u64 w = weight(h, S.powers, z[j]);
+        if (z[j] >= least) sum += w;
+      }
     }
     sum = warp_total(sum);
     if (lane == 0) S.seg[s] = sum;
@@ -626,15 +607,36 @@ __device__ bool select(Shared& S, const Group& G, const Part<T>& R, const Heat& 
   return true;
 }
 
-// The first k tokens, from the segments' maxima: sorted in S.list.all, their
-// number returned.  0 where that does not work out (too many segments or
-// tokens at the bound).
-template <int NV, class T>
-__device__ int list_best(Shared& S, const Group& G, const Part<T>& R, int k) {
+// Lists the tokens from `low` to below `high` (of a finite row's values).
+template <int NV, class T, class Keep>
+__device__ void list_between(Shared& S, const Group& G, const Part<T>& R, float low, float high, Keep keep) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  list_begin(S);
+  const float least = R.infinite ? -CUDART_INF_F : low;
+  for (int s = warp; s < R.segs; s += kWarps) {
+    if (S.seg_max[s] < least) continue;
+#pragma unroll 1
+    for (int v = 0; v < NV; ++v) {
+      const int q = R.from + (s * NV + v) * 256 + lane * 8;
+      float z[8];
+      load_finite(R, q, z);
+      unsigned found = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) found |= z[j] >= low && z[j] < high ? 1u << j : 0u;
+      if (found == 0) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if ((found >> j & 1) && keep(z[j], q + j - R.shift)) list_put(S, z[j], q + j - R.shift);
+    }
+  }
+}
+
+// A bound that the first k tokens reach, from the segments' maxima; -inf where
+// that does not work out (too few or too many segments).
+__device__ float bound_of_best(Shared& S, const Group& G, int k) {
   int all = 0;
   for (int r = 0; r < G.size; ++r) all += *G.of(&S.border_count, r);
-  if (all > kFewSegs || 2 * k > all) return 0;
+  if (all > kFewSegs || 2 * k > all) return -CUDART_INF_F;
   // every CTA ranks all maxima; equal ones by their place
   float* maxima = reinterpret_cast<float*>(S.list.all);
   for (int r = 0, at = 0; r < G.size; ++r) {
@@ -642,43 +644,44 @@ __device__ int list_best(Shared& S, const Group& G, const Part<T>& R, int k) {
     for (int i = threadIdx.x; i < n; i += kThreads) maxima[at + i] = G.of(S.seg_max, r)[i];
     at += n;
   }
-  if (threadIdx.x == 0) S.listed = 0;
   __syncthreads();
   if (threadIdx.x < all) {
     const float own = maxima[threadIdx.x];
     int rank = 0;
+#pragma unroll 8
     for (int i = 0; i < all; ++i) rank += maxima[i] > own || (maxima[i] == own && i < static_cast<int>(threadIdx.x));
     if (rank == k - 1) S.bound = own;
   }
   __syncthreads();
-  const float bound = R.infinite ? 0.0f : S.bound;
-  // (a bound of -inf: fewer than k segments have a possible token)
-  if (bound == -CUDART_INF_F) {
-    G.sync();
-    return 0;
-  }
-  for (int s = warp; s < R.segs; s += kWarps) {
-    if (S.seg_max[s] < S.bound) continue;
-#pragma unroll 1
-    for (int v = 0; v < NV; ++v) {
-      const int q = R.from + (s * NV + v) * 256 + lane * 8;
-      float z[8];
-      load_finite(R, q, z);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (z[j] >= bound) list_put(S, z[j], q + j - R.shift);
-    }
-  }
-  return list_sorted(S, G);
+  return S.bound;
 }
 
-// Cut by mass: the shortest prefix of the tokens that `of` keeps whose mass is
-// at least p of theirs, and that `in` keeps (tighter than `of`).  Leaves in S.seg
-// and S.total the sums by segments of what is kept, and returns their sum; 0
-// where the border's bins hold too many tokens.
-template <int NV, class T>
-__device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const Heat& h, float p, const Cut& of, const Cut& in,
-                           Cut* out) {
+// The values at which bins begin: S.high, from which on bins are below `first`,
+// and S.low, from which on they are at most `last`.
+__device__ void bins_to_values(Shared& S, const Heat& h, int first, int last) {
+  if (threadIdx.x < 2) {
+    // the least key whose bin is at most `most`
+    const int most = threadIdx.x == 0 ? first - 1 : last;
+    uint32_t low = ord_bits(-3.402823466e38f), high = ord_bits(h.top) + 1;
+    while (low < high) {
+      const uint32_t mid = low + (high - low) / 2;
+      if (bin_of(h, ord_value(mid)) <= most)
+        high = mid;
+      else
+        low = mid + 1;
+    }
+    const float v = low > ord_bits(h.top) ? CUDART_INF_F : ord_value(low);
+    if (threadIdx.x == 0)
+      S.high = v;
+    else
+      S.low = v;
+  }
+  __syncthreads();
+}
+
+// Fills the bins with the tokens that `keep` keeps: their number, or their weights.
+template <bool MASS, int NV, class T, class Keep>
+__device__ void fill_bins(Shared& S, const Group& G, const Part<T>& R, const Heat& h, Keep keep) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < kBins; i += kThreads) S.bin.low[i] = 0;
   __syncthreads();
@@ -690,41 +693,156 @@ __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const He
       load_finite(R, q, z);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (!kept(of, z[j], q + j - R.shift)) continue;
-        const int b = mass_bin(h, z[j]);
-        // the weight in its bin's octave, to 14 bits
-        const float w = exp2f(static_cast<float>((b >> 6) + 14) - (h.top - z[j]) * h.c);
-        if (b < kBins - 1) atomicAdd(&S.bin.low[b], static_cast<uint32_t>(__float2int_rn(w)));
+        int b;
+        uint32_t n = 1;
+        if (MASS)
+          n = bin_weight(h, z[j], b);
+        else
+          b = bin_of(h, z[j]);
+        if (keep(z[j], q + j - R.shift)) atomicAdd(&S.bin.low[b], n);
       }
     }
   }
   G.sync();
-  float mass[kBinsThread], sum = 0.0f;
+}
+
+// The first k tokens where they are many: a list that holds them (its length
+// returned, sorted), or else the cut after the k-th (0 returned), or -1: bins that
+// hold too many.
+template <int NV, class T>
+__device__ int list_by_count(Shared& S, const Group& G, const Part<T>& R, const Heat& h, int k, float least, Cut* out) {
+  const auto every = [&](float z, int) { return z >= least; };
+  fill_bins<false, NV>(S, G, R, h, every);
+  u64 count[kBinsThread] = {}, sum = 0;
   const int b0 = threadIdx.x * kBinsThread;
 #pragma unroll
   for (int i = 0; i < kBinsThread; ++i) {
-    uint64_t n = 0;
-    for (int r = 0; r < G.size; ++r) n += *G.of(&S.bin.low[b0 + i], r);
-    mass[i] = exp2f(-static_cast<float>(((b0 + i) >> 6) + 14)) * static_cast<float>(n);
-    sum += mass[i];
+    for (int r = 0; r < G.size; ++r) count[i] += *G.of(&S.bin.low[b0 + i], r);
+    sum += count[i];
   }
-  // (in whole numbers again: 2^-40 of the largest weight)
-  const u64 run = cta_scan(S, static_cast<u64>(static_cast<double>(sum) * 1099511627776.0));
-  const double goal = static_cast<double>(p) * static_cast<double>(S.warp_sum[kWarps]) * (1.0 / 1099511627776.0);
-  const double margin = static_cast<double>(S.warp_sum[kWarps]) * (1.0 / 1099511627776.0) * (1.0 / 4096.0);
-  if (threadIdx.x == 0) S.border = 0, S.border_count = kBins - 1;
-  __syncthreads();
-  double at = static_cast<double>(run) * (1.0 / 1099511627776.0) - static_cast<double>(sum);
+  if (threadIdx.x == 0) S.border = kBins - 1, S.border_above = 0, S.border_count = kList + 1;
+  const u64 run = cta_scan(S, sum);
+  const u64 need = static_cast<u64>(k), all = S.warp_sum[kWarps];
+  u64 before = run - sum;
 #pragma unroll
   for (int i = 0; i < kBinsThread; ++i) {
-    const double next = at + static_cast<double>(mass[i]);
-    if (at < goal - margin && next >= goal - margin) S.border = b0 + i;
+    if (before < need && before + count[i] >= need) {
+      S.border = b0 + i, S.border_above = before;
+      S.border_count = static_cast<int>(min(count[i], static_cast<u64>(kList + 1)));
+    }
+    before += count[i];
+  }
+  __syncthreads();
+  if (all <= need) {  // there are no more than k
+    *out = {least, kAllIds};
+    G.sync();
+    if (all > kList) return 0;
+    list_between<NV>(S, G, R, least, CUDART_INF_F, every);
+    return list_sorted(S, G);
+  }
+  const int border = S.border, count_in = S.border_count;
+  const u64 above = S.border_above;
+  bins_to_values(S, h, border, border);
+  const float high = S.high, low = fmaxf(S.low, least);
+  G.sync();  // the bins are free
+  if (count_in > kList) return -1;
+  const bool whole = above + count_in <= kList;
+  list_between<NV>(S, G, R, low, whole ? CUDART_INF_F : high, every);
+  const int n = list_sorted(S, G);
+  if (whole) return n;
+  const int at = static_cast<int>(need - above) - 1;
+  *out = {list_value(S, at), list_id(S, at)};
+  G.sync();
+  return 0;
+}
+
+// The listed tokens e < some, with weights w of this thread's two, join their
+// segments' sums.  Returns their sum; S.total has grown by this CTA's.
+template <int NV, class T>
+__device__ u64 join_segments(Shared& S, const Group& G, const Part<T>& R, int some, const u64 (&w)[2]) {
+  u64 more = 0, own = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = 2 * threadIdx.x + i;
+    if (e >= some || w[i] == 0) continue;
+    more += w[i];
+    const int s = list_id(S, e) + R.shift - R.from;
+    if (s >= 0 && s / (NV * 256) < R.segs) {
+      atomicAdd(&S.seg[s / (NV * 256)], w[i]);
+      own += w[i];
+    }
+  }
+  cta_scan(S, more);
+  const u64 all = S.warp_sum[kWarps];
+  cta_scan(S, own);
+  G.sync();
+  if (threadIdx.x == 0) S.total += S.warp_sum[kWarps];
+  G.sync();
+  return all;
+}
+
+// Cuts a sorted list of n tokens, among them all that are kept: the first k, of
+// those the prefix of at least p of their mass (p < 1), of those the values from `least` on.
+template <int NV, class T>
+__device__ u64 cut_list(Shared& S, const Group& G, const Part<T>& R, const Heat& h, int n, int k, float p, float least, Cut* out) {
+  n = min(n, k);
+  u64 w[2], run[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) w[i] = 2 * static_cast<int>(threadIdx.x) + i < n ? weight(h, S.powers, list_value(S, 2 * threadIdx.x + i)) : 0;
+  run[1] = cta_scan(S, w[0] + w[1]), run[0] = run[1] - w[1];
+  const u64 target = p < 1.0f ? fraction_of(p, S.warp_sum[kWarps], true) : S.warp_sum[kWarps];
+  for (int i = threadIdx.x; i < R.segs; i += kThreads) S.seg[i] = 0;
+  if (threadIdx.x == 0) S.total = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = 2 * threadIdx.x + i;
+    if (e >= n) continue;
+    const bool stays = e == 0 || (run[i] - w[i] < target && list_value(S, e) >= least);
+    const bool next = e + 1 < n && run[i] < target && list_value(S, e + 1) >= least;
+    if (stays && !next) S.cut = {list_value(S, e), list_id(S, e)};
+    if (!stays) w[i] = 0;
+  }
+  const u64 mass = join_segments<NV>(S, G, R, n, w);
+  *out = S.cut;
+  return mass;
+}
+
+// Cut by mass: the shortest prefix of the tokens that `of` keeps whose mass is
+// at least p of theirs, and that `in` keeps (tighter than `of`).  Leaves in S.seg
+// and S.total the sums by segments of what is kept, and returns their sum; 0
+// where the border's bins hold too many tokens.
+template <bool TIES, int NV, class T>
+__device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const Heat& h, float p, const Cut& of, const Cut& in,
+                           Cut* out) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const auto of_these = [&](float z, int id) { return TIES ? kept(of, z, id) : z >= of.value; };
+  const auto in_these = [&](float z, int id) { return TIES ? kept(in, z, id) : z >= in.value; };
+  fill_bins<true, NV>(S, G, R, h, of_these);
+  // in units of 2^-40 of the largest weight
+  u64 mass[kBinsThread], sum = 0;
+  const int b0 = threadIdx.x * kBinsThread, octave = b0 >> 6;
+#pragma unroll
+  for (int i = 0; i < kBinsThread; ++i) {
+    u64 n = 0;
+    for (int r = 0; r < G.size; ++r) n += *G.of(&S.bin.low[b0 + i], r);
+    mass[i] = octave < 26 ? n << (26 - octave) : n >> (octave - 26);
+    sum += mass[i];
+  }
+  if (threadIdx.x == 0) S.border = 0, S.border_count = kBins - 1;
+  const u64 run = cta_scan(S, sum), goal = fraction_of(p, S.warp_sum[kWarps], true), margin = S.warp_sum[kWarps] >> 12;
+  u64 at = run - sum;
+#pragma unroll
+  for (int i = 0; i < kBinsThread; ++i) {
+    const u64 next = at + mass[i];
+    if (at + margin < goal && next + margin >= goal) S.border = b0 + i;
     if (at < goal + margin && next >= goal + margin) S.border_count = b0 + i;
     at = next;
   }
   __syncthreads();
-  const int first = S.border, last = S.border_count;
-  G.sync();
+  bins_to_values(S, h, S.border, S.border_count);
+  const float high = S.high, low = S.low;
+  G.sync();  // the bins are free
 
   // exact masses: of all, of what lies above the border's bins by segments; the border's bins are listed
   list_begin(S);
@@ -735,20 +853,22 @@ __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const He
     for (int v = 0; v < NV; ++v) {
       const int q = R.from + (s * NV + v) * 256 + lane * 8;
       float z[8];
-      u64 w[8];
       load_finite(R, q, z);
-      weights8(h, S.powers, z, w);
+      unsigned listed = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int id = q + j - R.shift;
-        if (!kept(of, z[j], id)) continue;
-        const int b = mass_bin(h, z[j]);
-        if (b > last || !kept(in, z[j], id))
-          rest += w[j];
-        else if (b < first)
-          part += w[j];
-        else
-          list_put(S, z[j], id);
+        const u64 w = weight(h, S.powers, z[j]);
+        const bool inside = in_these(z[j], id);
+        const bool upper = inside && z[j] >= high, lists = inside && z[j] >= low && !upper;
+        if (upper) part += w;
+        if (of_these(z[j], id) && !upper && !lists) rest += w;
+        listed |= lists ? 1u << j : 0u;
+      }
+      if (listed != 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (listed >> j & 1) list_put(S, z[j], q + j - R.shift);
       }
     }
     part = warp_total(part);
@@ -772,12 +892,11 @@ __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const He
   for (int i = 0; i < 2; ++i) w[i] = 2 * static_cast<int>(threadIdx.x) + i < n ? weight(h, S.powers, list_value(S, 2 * threadIdx.x + i)) : 0;
   at_run[1] = cta_scan(S, w[0] + w[1]), at_run[0] = at_run[1] - w[1];
   const u64 listed = S.warp_sum[kWarps], all = mass_above + listed + mass_rest;
-  u64 target = fraction_of(p, all, true);
-  if (target < 1) target = 1;
+  const u64 target = max(fraction_of(p, all, true), static_cast<u64>(1));
   if (threadIdx.x == 0) S.cut = in, S.found = n;
   __syncthreads();
   // the border lies above the bins: they were chosen wrongly; or below: `in` ends before it, or wrongly
-  const bool wrong = mass_above >= target || (mass_above + listed < target && mass_bin(h, in.value) > last);
+  const bool wrong = mass_above >= target || (mass_above + listed < target && in.value < low);
   const u64 need = target - mass_above;
   if (!wrong && listed >= need) {
 #pragma unroll
@@ -795,26 +914,7 @@ __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const He
     G.sync();
     return 0;
   }
-  // the listed tokens that stay join their segments
-  u64 more = 0, own = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * threadIdx.x + i;
-    if (e >= some) continue;
-    more += w[i];
-    const int s = list_id(S, e) + R.shift - R.from;
-    if (s >= 0 && s / (NV * 256) < R.segs) {
-      atomicAdd(&S.seg[s / (NV * 256)], w[i]);
-      own += w[i];
-    }
-  }
-  cta_scan(S, more);
-  const u64 kept_sum = mass_above + S.warp_sum[kWarps];
-  cta_scan(S, own);
-  G.sync();
-  if (threadIdx.x == 0) S.total += S.warp_sum[kWarps];
-  G.sync();
-  return kept_sum;
+  return mass_above + join_segments<NV>(S, G, R, some, w);
 }
 
 template <class T, int NV>
@@ -837,6 +937,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs A) {
     R.from = G.rank * per * unit;
     R.segs = min(per, max(0, (R.end - R.from + unit - 1) / unit));
     R.infinite = false;
+
+    float temperature = A.temperature ? A.temperature[row] : A.temperature_all;
+    int64_t k = A.top_k ? A.top_k[row] : A.top_k_all;
+    const float p = A.top_p ? A.top_p[row] : A.top_p_all;
+    const float least = A.min_p ? A.min_p[row] : A.min_p_all;
+    // (a NaN fails the comparison that would turn its filter on)
+    if (!(temperature >= kSampleColdest) || p <= 0.0f) k = 1;
+    if (least > 0.0f && threadIdx.x == kThreads - 1)
+      S.floor_below = static_cast<double>(temperature) * log(static_cast<double>(fminf(least, 1.0f)));
 
     float top = -CUDART_INF_F;
     constexpr int kTogether = 4 / NV;  // segments on their way together
@@ -873,12 +982,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs A) {
       continue;
     }
 
-    float temperature = A.temperature ? A.temperature[row] : A.temperature_all;
-    int64_t k = A.top_k ? A.top_k[row] : A.top_k_all;
-    const float p = A.top_p ? A.top_p[row] : A.top_p_all;
-    float least = A.min_p ? A.min_p[row] : A.min_p_all;
-    // (a NaN fails the comparison that would turn its filter on)
-    if (!(temperature >= kSampleColdest) || p <= 0.0f) k = 1;
     if (k == 1) {
       // the first token of the largest value
       if (threadIdx.x == 0) S.found = kAllIds;
@@ -910,90 +1013,75 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs A) {
     const bool by_count = k > 0 && k < vocab, by_mass = p < 1.0f;
     const Heat h = make_heat(top, temperature, A.shift);
 
-    const Cut all = {-3.402823466e38f, kAllIds};  // every possible token
     // no token whose weight is below half a unit is drawn (a mask of the type's lowest value among them)
-    const double unit_at = static_cast<double>(top) - static_cast<double>(temperature) * (kLn2 * (63 - A.shift));
-    const float unit_cut = static_cast<float>(fmax(unit_at, -3.402823466e38));
-    Cut floor_cut = {unit_cut, kAllIds};
+    const float unit_cut = fmaxf(top - temperature * (0.69314718f * static_cast<float>(63 - A.shift)), -3.402823466e38f);
+    float floor = unit_cut;
     if (least > 0.0f) {
       // the least value is rounded up to fp32, so that comparing values is exact
-      const double t = static_cast<double>(top) + static_cast<double>(temperature) * log(static_cast<double>(fminf(least, 1.0f)));
-      float f = static_cast<float>(fmax(t, -3.402823466e38));
-      if (static_cast<double>(f) < t) f = nextafterf(f, CUDART_INF_F);
-      floor_cut.value = fmaxf(floor_cut.value, f);
-    }
-    float u = A.u[row];
-    u = u > 0.0f ? fminf(u, 0.99999994f) : 0.0f;
-    const auto answer = [&](int id, float z, u64 mass) {
-      A.ids[row] = id;
-      A.logp[row] = static_cast<float>((static_cast<double>(z) - static_cast<double>(top)) / static_cast<double>(temperature) -
-                                       log(static_cast<double>(mass) / static_cast<double>(weight(h, S.powers, top))));
-    };
-
-    const int listed = by_count && k <= kFewSegs / 2 ? list_best<NV>(S, G, R, static_cast<int>(k)) : 0;
-    if (listed > 0) {
-      // everything happens in the list (every CTA does the same)
-      const int n = min(static_cast<int>(k), listed);
-      u64 w[2], run[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) w[i] = 2 * static_cast<int>(threadIdx.x) + i < n ? weight(h, S.powers, list_value(S, 2 * threadIdx.x + i)) : 0;
-      run[1] = cta_scan(S, w[0] + w[1]), run[0] = run[1] - w[1];
-      const u64 target = by_mass ? fraction_of(p, S.warp_sum[kWarps], true) : S.warp_sum[kWarps];
-      u64 mine = 0;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int e = 2 * threadIdx.x + i;
-        if (e < n && (run[i] - w[i] >= target || list_value(S, e) < floor_cut.value) && e > 0) w[i] = 0;
-        if (e < n) S.seg[e] = w[i];
-        mine += w[i];
-      }
-      cta_scan(S, mine);
-      const u64 mass = S.warp_sum[kWarps], past = fraction_of(u, mass, false);
-      if (threadIdx.x == 0) S.found = kAllIds;
-      __syncthreads();
-      for (int e = threadIdx.x; e < n; e += kThreads) {
-        if (S.seg[e] == 0) continue;
-        const int id = list_id(S, e);
-        u64 sum = 0;
-        for (int i = 0; i < n; ++i) sum += list_id(S, i) <= id ? S.seg[i] : 0;
-        if (sum > past) atomicMin(&S.found, id);
+      if (threadIdx.x == 0) {
+        const double t = static_cast<double>(top) + S.floor_below;
+        float f = static_cast<float>(fmax(t, -3.402823466e38));
+        if (static_cast<double>(f) < t) f = nextafterf(f, CUDART_INF_F);
+        S.bound = f;
       }
       __syncthreads();
-      if (G.rank == 0)
-        for (int e = threadIdx.x; e < n; e += kThreads)
-          if (list_id(S, e) == S.found) answer(S.found, list_value(S, e), mass);
-      G.sync();
-      continue;
+      floor = fmaxf(floor, S.bound);
+      __syncthreads();
     }
-
+    const Cut floor_cut = {floor, kAllIds};
     const auto possible = [&](const Cut& c) {
       return [&](float z, int id) { return kept(c, z, id) ? weight(h, S.powers, z) : 0ull; };
     };
-    Cut cut = all;
-    if (by_count) {
-      // (the mass of the first k is asked for where a cut by mass follows)
-      const Cut in = by_mass ? all : floor_cut;
-      if (!select<false, NV>(S, G, R, h, static_cast<u64>(k), in, top, &cut)) cut = in;
-    }
+
+    // (the mass of the first k, whatever their weights, is asked for where a cut by mass follows)
+    const float least_counted = by_mass ? -3.402823466e38f : floor;
+    Cut cut = {least_counted, kAllIds};
     u64 mass = 0;
-    if (by_mass) {
-      const Cut in = tighter(cut, floor_cut);
+    if (by_count) {
+      int n = -1;
+      const float bound = k <= kFewSegs / 2 ? bound_of_best(S, G, static_cast<int>(k)) : -CUDART_INF_F;
+      if (bound > -CUDART_INF_F) {
+        const float from = R.infinite ? 0.0f : bound;
+        list_between<NV>(S, G, R, from, CUDART_INF_F, [&](float, int) { return true; });
+        n = list_sorted(S, G);
+      }
+      // (too many: many tokens at the bound)
+      if (n <= 0) {
+        G.sync();
+        n = list_by_count<NV>(S, G, R, h, static_cast<int>(k), least_counted, &cut);
+      }
+      if (n > 0) {
+        mass = cut_list<NV>(S, G, R, h, n, static_cast<int>(k), p, floor, &cut);
+      } else if (n < 0) {
+        const Cut in = {least_counted, kAllIds};
+        if (!select<false, NV>(S, G, R, h, static_cast<u64>(k), in, top, &cut)) cut = in;
+      }
+    }
+    if (by_mass && mass == 0) {
+      const Cut of = tighter(cut, Cut{unit_cut, kAllIds}), in = tighter(cut, floor_cut);
       Cut c;
-      const Cut of = tighter(cut, Cut{unit_cut, kAllIds});
-      mass = cut_by_mass<NV>(S, G, R, h, p, of, in, &c);
+      mass = of.id == kAllIds && in.id == kAllIds ? cut_by_mass<false, NV>(S, G, R, h, p, of, in, &c)
+                                                  : cut_by_mass<true, NV>(S, G, R, h, p, of, in, &c);
       if (mass == 0) {
         const u64 target = fraction_of(p, sum_row<NV>(S, G, R, possible(of)), true);
         G.sync();
-        if (!select<true, NV>(S, G, R, h, target < 1 ? 1 : target, in, top, &c)) c = in;
+        if (!select<true, NV>(S, G, R, h, max(target, static_cast<u64>(1)), in, top, &c)) c = in;
       }
       cut = c;
     }
     cut = tighter(cut, floor_cut);
-    if (mass == 0) {
-      mass = cut.id == kAllIds ? sum_above<NV>(S, G, R, h, cut.value) : sum_row<NV>(S, G, R, possible(cut));
-    }
+    if (mass == 0) mass = cut.id == kAllIds ? sum_above<NV>(S, G, R, h, cut.value) : sum_row<NV>(S, G, R, possible(cut));
+
+    float u = A.u[row];
+    u = u > 0.0f ? fminf(u, 0.99999994f) : 0.0f;
     const int id = locate<NV>(S, G, R, fraction_of(u, mass, false), possible(cut));
-    if (id >= 0 && threadIdx.x == 0) answer(id, R.infinite ? 0.0f : to_f32(z0[id]), mass);
+    if (id >= 0 && threadIdx.x == 0) {
+      const float z = R.infinite ? 0.0f : to_f32(z0[id]);
+      // ln(w / mass), w relative to the largest weight: two terms that are not positive
+      const u64 most = weight(h, S.powers, top);
+      A.ids[row] = id;
+      A.logp[row] = __fdiv_rn(z - top, temperature) - log1pf(static_cast<float>(mass - most) / static_cast<float>(most));
+    }
     G.sync();
   }
 }

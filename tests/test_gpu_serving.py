@@ -603,8 +603,9 @@ def _check_sample(logits, u, r, **kw):
     off = 2.0 ** -32.5 + (w > 0).sum(-1) * (unit / 2) / (total / w.amax(-1))
     assert (u < end + 2 * off).all() and (u >= end - own / total - 2 * off).all()
     want = torch.log(own / total)
-    # the logarithm in 64 bits, of the exact weight and a sum to `off`; rounded to fp32
-    close(logp, want, 2 * off + U * want.abs(), "log probability")
+    # two fp32 terms of one sign and their sum: a difference and a quotient (2 u); the logarithm of 1 + a quotient of two
+    # rounded sums (3 u of the quotient, which is no more of the logarithm, and 2 u of its own); the sum's rounding
+    close(logp, want, 2 * off + 6 * U * want.abs(), "log probability")
     return w, total
 
 
