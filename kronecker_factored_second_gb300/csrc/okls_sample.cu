@@ -9,10 +9,9 @@
 // id (Cut).  The drawn token is the first, in the order of ids, at which the
 // running sum of the kept weights is above u times their sum.
 //
-// Sums are whole numbers.  A weight is rounded to an odd multiple of 2^-(63 -
-// log2 vocab) of the largest (the middle of the interval that it lies in), so a
-// row's sum fits 63 bits and does not depend on the order in which threads add; a
-// running sum past u W is found by exact comparisons.  What decides which token
+// Sums are whole numbers.  A weight is rounded down to a multiple of 2^-(63 -
+// log2 vocab) of the largest, so a row's sum fits 63 bits and does not depend on
+// the order in which threads add; a running sum past u W is found by exact comparisons.  What decides which token
 // is drawn is then the weights' error alone: a hundred thousand tokens have as
 // many borders, and with weights to fp32's 2^-24 one row in a thousand drew a
 // neighbour.  So a weight is formed to about 2^-33:
@@ -53,7 +52,8 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kBinsThread = kBins / kThreads;
-constexpr int kList = 2 * kThreads;  // tokens that are sorted
+constexpr int kList = 1024;  // tokens that are sorted
+constexpr int kEach = kList / kThreads;
 constexpr int kFewSegs = 320;        // segments whose maxima are ranked by counting
 constexpr int kSegs = 1024;      // segments of a CTA's part of a row
 constexpr int kSteps = 2048;     // table entries in an octave
@@ -83,7 +83,7 @@ __device__ const PowerTable g_powers = make_powers();
 // A row's temperature and maximum.
 struct Heat {
   float base;    // taken from a value first: 0, or the maximum where that has many steps (then exact)
-  float least;   // values below this have weight 0
+  float least;   // lower values count as this: their weight is 0
   float ch, cl;  // 2048 log2(e) / T in two words
   int kb;        // bits of the maximum's k + kMagic, 62 bits to the row's unit in the octaves
   float r;       // the maximum's r
@@ -108,8 +108,8 @@ __device__ Heat make_heat(float m, float temperature, int shift) {
   h.cl = __fdiv_rn(rest, temperature);
   const bool far = fabsf(m * h.ch) > 1900.0f * 2048.0f;
   h.base = far ? m : 0.0f;
-  // 70 octaves below the maximum there is nothing left of 62 bits
-  h.least = fmaxf((far ? 0.0f : m) - 70.0f * 2048.0f / h.ch, -3.4e38f);
+  // (64 - shift octaves below the maximum nothing is left of a weight)
+  h.least = fmaxf((far ? 0.0f : m) - (63.9f - static_cast<float>(shift)) * 2048.0f / h.ch, -3.4e38f);
   h.shift = shift;
   h.top = m, h.c = h.ch * (1.0f / 32.0f);
   steps_of(h, m, h.kb, h.r);
@@ -131,8 +131,10 @@ __device__ __forceinline__ u64 weight(const Heat& h, const u64* powers, float z)
   const u64 p = powers[k & (kSteps - 1)];
   u64 w = p + static_cast<u64>(static_cast<long long>(static_cast<int>(p >> 32)) *
                                (__float_as_int(q) - __float_as_int(kMagic)));
-  asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(w), "r"(k >> 11));
-  return w | 1u;
+  // w >> n for n <= 63 (least sees to it), with shifts that stop at 32
+  const uint32_t n = static_cast<uint32_t>(k >> 11), wl = static_cast<uint32_t>(w), wh = static_cast<uint32_t>(w >> 32);
+  const uint32_t low = __funnelshift_rc(wl, wh, n) >> max(static_cast<int>(n) - 32, 0);
+  return (static_cast<u64>(__funnelshift_rc(wh, 0, n)) << 32) | low;
 }
 
 // The bin of a value among 2048, 64 to an octave below the maximum: it does not
@@ -204,8 +206,8 @@ struct Shared {
   };
   u64 seg[kSegs];
   float seg_max[kSegs];
-  u64 warp_sum[kWarps + 1];
-  u64 total, rest;
+  u64 warp_sum[2][kWarps];
+  u64 total, rest;  // of this CTA: what is kept, everything
   float max;
   float warp_max[kWarps];
   int listed, found;
@@ -220,6 +222,7 @@ struct Shared {
 struct Group {  // a cluster, or a CTA alone
   cg::cluster_group c;
   int rank, size;
+  mutable int turn;  // of the two rows of S.warp_sum
   __device__ void sync() const {
     if (size > 1)
       c.sync();
@@ -283,23 +286,55 @@ __device__ __forceinline__ u64 warp_total(u64 v) {
   return v;
 }
 
-// Inclusive scan over the CTA's threads; the sum of all in S.warp_sum[kWarps].
-__device__ u64 cta_scan(Shared& S, u64 v) {
+// Scan over the CTA's threads.  (Two rows of warps' sums in turn: one barrier a scan.)
+struct Scan {
+  u64 run, all;  // up to and with the thread, of all
+};
+__device__ Scan cta_scan(Shared& S, const Group& G, u64 v) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64* sums = S.warp_sum[G.turn ^= 1];
   const u64 own = warp_scan(v, lane);
-  __syncthreads();
-  if (lane == 31) S.warp_sum[warp] = own;
+  if (lane == 31) sums[warp] = own;
   __syncthreads();
   u64 before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    before += w < warp ? S.warp_sum[w] : 0;
-    all += S.warp_sum[w];
+    if (w == warp) before = all;
+    all += sums[w];
   }
+  return {own + before, all};
+}
+// The sum over warps of what each of them has.
+__device__ u64 cta_total(Shared& S, const Group& G, u64 of_warp) {
+  u64* sums = S.warp_sum[G.turn ^= 1];
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = of_warp;
   __syncthreads();
-  if (threadIdx.x == 0) S.warp_sum[kWarps] = all;
-  __syncthreads();
-  return own + before;
+  u64 all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) all += sums[w];
+  return all;
+}
+
+// Inclusive scan over the list's entries, kEach of a thread; returns their sum.
+__device__ __forceinline__ u64 list_scan(Shared& S, const Group& G, const u64 (&w)[kEach], u64 (&run)[kEach]) {
+  u64 sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) sum += w[i];
+  const Scan scan = cta_scan(S, G, sum);
+  u64 at = scan.run - sum;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) run[i] = at += w[i];
+  return scan.all;
+}
+
+// sum += w where z >= least.
+__device__ __forceinline__ void add_from(u64& sum, u64 w, float z, float least) {
+  asm("{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %2, %3;\n\t@p add.u64 %0, %0, %1;\n\t}" : "+l"(sum) : "l"(w), "f"(z), "f"(least));
+}
+// at += n in shared memory where `on`.
+__device__ __forceinline__ void add_shared(bool on, uint32_t at, uint32_t n) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p red.shared.add.u32 [%1], %2;\n\t}" ::"r"(static_cast<int>(on)), "r"(at), "r"(n)
+               : "memory");
 }
 
 // Sum of fn(value, id) over the row; the segments' sums stay in S.seg and the CTA's in S.total.
@@ -321,8 +356,8 @@ __device__ u64 sum_row(Shared& S, const Group& G, const Part<T>& R, Fn fn) {
     if (lane == 0) S.seg[s] = sum;
     mine += sum;
   }
-  cta_scan(S, lane == 0 ? mine : 0);
-  if (threadIdx.x == 0) S.total = S.warp_sum[kWarps];
+  const u64 total = cta_total(S, G, mine);
+  if (threadIdx.x == 0) S.total = total;
   G.sync();
   u64 all = 0;
   for (int r = 0; r < G.size; ++r) all += *G.of(&S.total, r);
@@ -342,16 +377,15 @@ __device__ u64 sum_above(Shared& S, const Group& G, const Part<T>& R, const Heat
       load_finite(R, R.from + (s * NV + v) * 256 + lane * 8, z);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const u64 w = weight(h, S.powers, z[j]);
-        if (z[j] >= least) sum += w;
+        add_from(sum, weight(h, S.powers, z[j]), z[j], least);
       }
     }
     sum = warp_total(sum);
     if (lane == 0) S.seg[s] = sum;
     mine += sum;
   }
-  cta_scan(S, lane == 0 ? mine : 0);
-  if (threadIdx.x == 0) S.total = S.warp_sum[kWarps];
+  const u64 total = cta_total(S, G, mine);
+  if (threadIdx.x == 0) S.total = total;
   G.sync();
   u64 all = 0;
   for (int r = 0; r < G.size; ++r) all += *G.of(&S.total, r);
@@ -452,8 +486,8 @@ __device__ int list_sorted(Shared& S, const Group& G) {
   if (!small || threadIdx.x < 32) {
     for (int size = 2; size <= padded; size <<= 1) {
       for (int stride = size >> 1; stride > 0; stride >>= 1) {
-        const int t = threadIdx.x, i = 2 * t - (t & (stride - 1)), k = i + stride;
-        if (k < padded) {
+        for (int t = threadIdx.x; 2 * t < padded; t += kThreads) {
+          const int i = 2 * t - (t & (stride - 1)), k = i + stride;
           const u64 a = S.list.all[i], b = S.list.all[k];
           if ((a < b) == ((i & size) == 0)) S.list.all[i] = b, S.list.all[k] = a;
         }
@@ -472,7 +506,7 @@ __device__ int list_sorted(Shared& S, const Group& G) {
 // keeps, at which the running sum reaches `target` >= 1: of ones, or of weights
 // (MASS).  False if the sum stays below.  `top` is the row's maximum.
 template <bool MASS, int NV, class T>
-__device__ bool select(Shared& S, const Group& G, const Part<T>& R, const Heat& h, u64 target, const Cut& in, float top,
+__device__ __noinline__ bool select(Shared& S, const Group& G, const Part<T>& R, const Heat& h, u64 target, const Cut& in, float top,
                        Cut* out) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t high = ord_bits(top), low = ord_bits(in.value);
@@ -520,9 +554,9 @@ __device__ bool select(Shared& S, const Group& G, const Part<T>& R, const Heat& 
     }
 #pragma unroll
     for (int i = 0; i < kBinsThread; ++i) sum += mass[i];
-    const u64 run = cta_scan(S, sum);
-    const u64 need = target - above;
-    if (S.warp_sum[kWarps] < need) {
+    const Scan scan = cta_scan(S, G, sum);
+    const u64 run = scan.run, need = target - above;
+    if (scan.all < need) {
       G.sync();
       return false;
     }
@@ -588,17 +622,17 @@ __device__ bool select(Shared& S, const Group& G, const Part<T>& R, const Heat& 
     }
   }
   const int n = list_sorted(S, G);
-  u64 w[2], run[2];
+  u64 w[kEach], run[kEach];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int at = 2 * threadIdx.x + i;
+  for (int i = 0; i < kEach; ++i) {
+    const int at = kEach * threadIdx.x + i;
     w[i] = at >= n ? 0 : MASS ? weight(h, S.powers, list_value(S, at)) : 1;
   }
-  run[1] = cta_scan(S, w[0] + w[1]), run[0] = run[1] - w[1];
+  list_scan(S, G, w, run);
   const u64 need = target - above;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int at = 2 * threadIdx.x + i;
+  for (int i = 0; i < kEach; ++i) {
+    const int at = kEach * threadIdx.x + i;
     if (at < n && run[i] >= need && run[i] - w[i] < need) S.cut = {list_value(S, at), list_id(S, at)};
   }
   __syncthreads();
@@ -645,11 +679,11 @@ __device__ float bound_of_best(Shared& S, const Group& G, int k) {
     at += n;
   }
   __syncthreads();
-  if (threadIdx.x < all) {
-    const float own = maxima[threadIdx.x];
+  for (int at = threadIdx.x; at < all; at += kThreads) {
+    const float own = maxima[at];
     int rank = 0;
 #pragma unroll 8
-    for (int i = 0; i < all; ++i) rank += maxima[i] > own || (maxima[i] == own && i < static_cast<int>(threadIdx.x));
+    for (int i = 0; i < all; ++i) rank += maxima[i] > own || (maxima[i] == own && i < at);
     if (rank == k - 1) S.bound = own;
   }
   __syncthreads();
@@ -659,22 +693,22 @@ __device__ float bound_of_best(Shared& S, const Group& G, int k) {
 // The values at which bins begin: S.high, from which on bins are below `first`,
 // and S.low, from which on they are at most `last`.
 __device__ void bins_to_values(Shared& S, const Heat& h, int first, int last) {
-  if (threadIdx.x < 2) {
-    // the least key whose bin is at most `most`
-    const int most = threadIdx.x == 0 ? first - 1 : last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp < 2) {
+    // the least key whose bin is at most `most`, 32 places a time
+    const int most = warp == 0 ? first - 1 : last;
     uint32_t low = ord_bits(-3.402823466e38f), high = ord_bits(h.top) + 1;
     while (low < high) {
-      const uint32_t mid = low + (high - low) / 2;
-      if (bin_of(h, ord_value(mid)) <= most)
-        high = mid;
-      else
-        low = mid + 1;
+      const uint32_t step = (high - low + 31) / 32, at = low + lane * step;
+      const unsigned reached = __ballot_sync(0xffffffffu, at >= high || at < low || bin_of(h, ord_value(at)) <= most);
+      // (the last place may lie before the end)
+      const int i = reached ? __ffs(reached) - 1 : 32;
+      const uint32_t next = i == 32 || low + i * step < low ? high : min(high, low + i * step);
+      low = i == 0 ? next : low + (i - 1) * step + 1;
+      high = next;
     }
     const float v = low > ord_bits(h.top) ? CUDART_INF_F : ord_value(low);
-    if (threadIdx.x == 0)
-      S.high = v;
-    else
-      S.low = v;
+    if (lane == 0) (warp == 0 ? S.high : S.low) = v;
   }
   __syncthreads();
 }
@@ -683,6 +717,7 @@ __device__ void bins_to_values(Shared& S, const Heat& h, int first, int last) {
 template <bool MASS, int NV, class T, class Keep>
 __device__ void fill_bins(Shared& S, const Group& G, const Part<T>& R, const Heat& h, Keep keep) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t bins = static_cast<uint32_t>(__cvta_generic_to_shared(S.bin.low));
   for (int i = threadIdx.x; i < kBins; i += kThreads) S.bin.low[i] = 0;
   __syncthreads();
   for (int s = warp; s < R.segs; s += kWarps) {
@@ -699,7 +734,7 @@ __device__ void fill_bins(Shared& S, const Group& G, const Part<T>& R, const Hea
           n = bin_weight(h, z[j], b);
         else
           b = bin_of(h, z[j]);
-        if (keep(z[j], q + j - R.shift)) atomicAdd(&S.bin.low[b], n);
+        add_shared(keep(z[j], q + j - R.shift), bins + 4 * b, n);
       }
     }
   }
@@ -721,9 +756,9 @@ __device__ int list_by_count(Shared& S, const Group& G, const Part<T>& R, const 
     sum += count[i];
   }
   if (threadIdx.x == 0) S.border = kBins - 1, S.border_above = 0, S.border_count = kList + 1;
-  const u64 run = cta_scan(S, sum);
-  const u64 need = static_cast<u64>(k), all = S.warp_sum[kWarps];
-  u64 before = run - sum;
+  const Scan scan = cta_scan(S, G, sum);
+  const u64 need = static_cast<u64>(k), all = scan.all;
+  u64 before = scan.run - sum;
 #pragma unroll
   for (int i = 0; i < kBinsThread; ++i) {
     if (before < need && before + count[i] >= need) {
@@ -759,11 +794,11 @@ __device__ int list_by_count(Shared& S, const Group& G, const Part<T>& R, const 
 // The listed tokens e < some, with weights w of this thread's two, join their
 // segments' sums.  Returns their sum; S.total has grown by this CTA's.
 template <int NV, class T>
-__device__ u64 join_segments(Shared& S, const Group& G, const Part<T>& R, int some, const u64 (&w)[2]) {
+__device__ u64 join_segments(Shared& S, const Group& G, const Part<T>& R, int some, const u64 (&w)[kEach]) {
   u64 more = 0, own = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * threadIdx.x + i;
+  for (int i = 0; i < kEach; ++i) {
+    const int e = kEach * threadIdx.x + i;
     if (e >= some || w[i] == 0) continue;
     more += w[i];
     const int s = list_id(S, e) + R.shift - R.from;
@@ -772,11 +807,9 @@ __device__ u64 join_segments(Shared& S, const Group& G, const Part<T>& R, int so
       own += w[i];
     }
   }
-  cta_scan(S, more);
-  const u64 all = S.warp_sum[kWarps];
-  cta_scan(S, own);
+  const u64 all = cta_total(S, G, warp_total(more)), mine = G.size > 1 ? cta_total(S, G, warp_total(own)) : all;
   G.sync();
-  if (threadIdx.x == 0) S.total += S.warp_sum[kWarps];
+  if (threadIdx.x == 0) S.total += mine;
   G.sync();
   return all;
 }
@@ -786,17 +819,19 @@ __device__ u64 join_segments(Shared& S, const Group& G, const Part<T>& R, int so
 template <int NV, class T>
 __device__ u64 cut_list(Shared& S, const Group& G, const Part<T>& R, const Heat& h, int n, int k, float p, float least, Cut* out) {
   n = min(n, k);
-  u64 w[2], run[2];
+  u64 w[kEach], run[kEach];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) w[i] = 2 * static_cast<int>(threadIdx.x) + i < n ? weight(h, S.powers, list_value(S, 2 * threadIdx.x + i)) : 0;
-  run[1] = cta_scan(S, w[0] + w[1]), run[0] = run[1] - w[1];
-  const u64 target = p < 1.0f ? fraction_of(p, S.warp_sum[kWarps], true) : S.warp_sum[kWarps];
+  for (int i = 0; i < kEach; ++i) {
+    const int e = kEach * threadIdx.x + i;
+    w[i] = e < n ? weight(h, S.powers, list_value(S, e)) : 0;
+  }
+  const u64 sum = list_scan(S, G, w, run), target = p < 1.0f ? fraction_of(p, sum, true) : sum;
   for (int i = threadIdx.x; i < R.segs; i += kThreads) S.seg[i] = 0;
   if (threadIdx.x == 0) S.total = 0;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * threadIdx.x + i;
+  for (int i = 0; i < kEach; ++i) {
+    const int e = kEach * threadIdx.x + i;
     if (e >= n) continue;
     const bool stays = e == 0 || (run[i] - w[i] < target && list_value(S, e) >= least);
     const bool next = e + 1 < n && run[i] < target && list_value(S, e + 1) >= least;
@@ -830,8 +865,9 @@ __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const He
     sum += mass[i];
   }
   if (threadIdx.x == 0) S.border = 0, S.border_count = kBins - 1;
-  const u64 run = cta_scan(S, sum), goal = fraction_of(p, S.warp_sum[kWarps], true), margin = S.warp_sum[kWarps] >> 12;
-  u64 at = run - sum;
+  const Scan scan = cta_scan(S, G, sum);
+  const u64 goal = fraction_of(p, scan.all, true), margin = scan.all >> 12;
+  u64 at = scan.run - sum;
 #pragma unroll
   for (int i = 0; i < kBinsThread; ++i) {
     const u64 next = at + mass[i];
@@ -846,7 +882,8 @@ __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const He
 
   // exact masses: of all, of what lies above the border's bins by segments; the border's bins are listed
   list_begin(S);
-  u64 above = 0, rest = 0;
+  const float upper = fmaxf(high, in.value), lower = fmaxf(low, in.value);
+  u64 above = 0, all = 0;
   for (int s = warp; s < R.segs; s += kWarps) {
     u64 part = 0;
 #pragma unroll 1
@@ -859,39 +896,45 @@ __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const He
       for (int j = 0; j < 8; ++j) {
         const int id = q + j - R.shift;
         const u64 w = weight(h, S.powers, z[j]);
-        const bool inside = in_these(z[j], id);
-        const bool upper = inside && z[j] >= high, lists = inside && z[j] >= low && !upper;
-        if (upper) part += w;
-        if (of_these(z[j], id) && !upper && !lists) rest += w;
-        listed |= lists ? 1u << j : 0u;
+        if (TIES) {
+          const bool takes = z[j] >= upper && in_these(z[j], id);
+          if (of_these(z[j], id)) all += w;
+          if (takes) part += w;
+          listed |= z[j] >= lower && !takes ? 1u << j : 0u;
+        } else {
+          // (impossible tokens have weight 0)
+          all += w;
+          add_from(part, w, z[j], upper);
+          listed |= z[j] >= lower && z[j] < upper ? 1u << j : 0u;
+        }
       }
       if (listed != 0) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (listed >> j & 1) list_put(S, z[j], q + j - R.shift);
+          if ((listed >> j & 1) && in_these(z[j], q + j - R.shift)) list_put(S, z[j], q + j - R.shift);
       }
     }
     part = warp_total(part);
     if (lane == 0) S.seg[s] = part;
     above += part;
   }
-  rest = warp_total(rest);
-  cta_scan(S, lane == 0 ? above : 0);
-  if (threadIdx.x == 0) S.total = S.warp_sum[kWarps];
-  cta_scan(S, lane == 0 ? rest : 0);
-  if (threadIdx.x == 0) S.rest = S.warp_sum[kWarps];
+  const u64 total = cta_total(S, G, above), total_all = cta_total(S, G, warp_total(all));
+  if (threadIdx.x == 0) S.total = total, S.rest = total_all;
   const int n = list_sorted(S, G);
-  u64 mass_above = 0, mass_rest = 0;
-  for (int r = 0; r < G.size; ++r) mass_above += *G.of(&S.total, r), mass_rest += *G.of(&S.rest, r);
+  u64 mass_above = 0;
+  all = 0;
+  for (int r = 0; r < G.size; ++r) mass_above += *G.of(&S.total, r), all += *G.of(&S.rest, r);
   if (n < 0) {
     G.sync();
     return 0;
   }
-  u64 w[2], at_run[2];
+  u64 w[kEach], at_run[kEach];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) w[i] = 2 * static_cast<int>(threadIdx.x) + i < n ? weight(h, S.powers, list_value(S, 2 * threadIdx.x + i)) : 0;
-  at_run[1] = cta_scan(S, w[0] + w[1]), at_run[0] = at_run[1] - w[1];
-  const u64 listed = S.warp_sum[kWarps], all = mass_above + listed + mass_rest;
+  for (int i = 0; i < kEach; ++i) {
+    const int e = kEach * threadIdx.x + i;
+    w[i] = e < n ? weight(h, S.powers, list_value(S, e)) : 0;
+  }
+  const u64 listed = list_scan(S, G, w, at_run);
   const u64 target = max(fraction_of(p, all, true), static_cast<u64>(1));
   if (threadIdx.x == 0) S.cut = in, S.found = n;
   __syncthreads();
@@ -900,9 +943,9 @@ __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const He
   const u64 need = target - mass_above;
   if (!wrong && listed >= need) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kEach; ++i) {
       if (at_run[i] >= need && at_run[i] - w[i] < need) {
-        const int e = 2 * threadIdx.x + i;
+        const int e = kEach * threadIdx.x + i;
         S.cut = {list_value(S, e), list_id(S, e)}, S.found = e + 1;
       }
     }
@@ -918,10 +961,10 @@ __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const He
 }
 
 template <class T, int NV>
-__global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs A) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_sample(const SampleArgs A) {
   extern __shared__ unsigned char raw[];
   Shared& S = *reinterpret_cast<Shared*>(raw);
-  Group G = {cg::this_cluster(), 0, 1};
+  Group G = {cg::this_cluster(), 0, 1, 0};
   G.rank = static_cast<int>(G.c.block_rank()), G.size = static_cast<int>(G.c.num_blocks());
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < kSteps; i += kThreads) S.powers[i] = g_powers.v[i];
@@ -1013,9 +1056,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs A) {
     const bool by_count = k > 0 && k < vocab, by_mass = p < 1.0f;
     const Heat h = make_heat(top, temperature, A.shift);
 
-    // no token whose weight is below half a unit is drawn (a mask of the type's lowest value among them)
-    const float unit_cut = fmaxf(top - temperature * (0.69314718f * static_cast<float>(63 - A.shift)), -3.402823466e38f);
-    float floor = unit_cut;
+    float floor = -3.402823466e38f;  // every possible token
     if (least > 0.0f) {
       // the least value is rounded up to fp32, so that comparing values is exact
       if (threadIdx.x == 0) {
@@ -1058,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs A) {
       }
     }
     if (by_mass && mass == 0) {
-      const Cut of = tighter(cut, Cut{unit_cut, kAllIds}), in = tighter(cut, floor_cut);
+      const Cut of = cut, in = tighter(cut, floor_cut);
       Cut c;
       mass = of.id == kAllIds && in.id == kAllIds ? cut_by_mass<false, NV>(S, G, R, h, p, of, in, &c)
                                                   : cut_by_mass<true, NV>(S, G, R, h, p, of, in, &c);
@@ -1115,10 +1156,10 @@ cudaError_t launch_sample(const SampleArgs& args, int dtype, int num_sms, cudaSt
   while ((int64_t(1) << A.shift) < A.vocab) ++A.shift;
   // a cluster for each row while the SMs last and a CTA has 2048 values
   int size = 1;
-  while (size < 8 && A.rows * size * 2 <= num_sms && A.vocab >= size * 4096) size *= 2;
+  while (size < 8 && A.rows * size * 2 <= num_sms && A.vocab >= size * 65536) size *= 2;
   // (what a CTA's segments hold)
   while (lm_div_up(A.vocab + 8, size) > (kSegs - 8) * 1024) size *= 2;
-  const int64_t resident = static_cast<int64_t>(num_sms) * 2 / size;
+  const int64_t resident = static_cast<int64_t>(num_sms) * (1024 / kThreads) / size;
   const int clusters = static_cast<int>(A.rows < resident ? A.rows : resident);
   // segments of 256 values, and of 1024 where that would be more than kFewSegs
   const bool wide = lm_div_up(A.vocab, size) > 65536;
