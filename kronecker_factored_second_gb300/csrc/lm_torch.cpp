@@ -401,25 +401,41 @@ class TensorList {
   py::object seq_;
 };
 
-// Memory that a step writes: [begin, end) of each tensor.
+// Memory that a step writes: [begin, end) of each tensor, kind after kind.
 typedef std::pair<uintptr_t, uintptr_t> Range;
 
-void refuse_overlaps(std::vector<Range>& r) {
-  if (!std::is_sorted(r.begin(), r.end())) std::sort(r.begin(), r.end());
-  for (size_t i = 1; i < r.size(); ++i)
-    REFUSE(r[i].first < r[i - 1].second, "a parameter or a state appears twice, or two of them overlap");
+void refuse_overlaps(std::vector<Range>* kinds, int count) {
+  // usual are a few buffers, each of which its tensors go through upwards
+  bool plain = true;
+  std::vector<Range> all;
+  Range hull[5];
+  int used = 0;
+  for (int k = 0; k < count && plain; ++k) {
+    const std::vector<Range>& r = kinds[k];
+    for (size_t i = 1; i < r.size(); ++i) plain = plain && r[i - 1].second <= r[i].first;
+    if (r.empty()) continue;
+    const Range h = {r.front().first, r.back().second};
+    for (int i = 0; i < used; ++i) plain = plain && (h.second <= hull[i].first || hull[i].second <= h.first);
+    hull[used++] = h;
+  }
+  if (plain) return;
+  for (int k = 0; k < count; ++k) all.insert(all.end(), kinds[k].begin(), kinds[k].end());
+  std::sort(all.begin(), all.end());
+  for (size_t i = 1; i < all.size(); ++i)
+    REFUSE(all[i].first < all[i - 1].second, "a parameter or a state appears twice, or two of them overlap");
 }
 
 // A tensor of a step, as the kernels see it: `count` elements in a row.
-void* flat(const Tensor& t, const char* name, const Tensor& first, int64_t count, bool writes, std::vector<Range>& ranges) {
-  REFUSE(!t.is_cuda(), name, " must be on a CUDA device");
-  same_device(first, t);
-  REFUSE(!t.is_contiguous(), name, " must be contiguous");
-  REFUSE(t.numel() != count, name, " must hold ", count, " values, not ", t.numel());
-  void* p = t.data_ptr();
-  if (writes) {
-    writable(t, name);
-    if (count) ranges.emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + count * t.element_size());
+void* flat(const Tensor& t, const char* name, c10::Device device, int64_t count, std::vector<Range>* ranges) {
+  const c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+  REFUSE(!impl->is_cuda(), name, " must be on a CUDA device");
+  REFUSE(impl->device() != device, "tensors on ", device, " and ", impl->device());
+  REFUSE(!impl->is_contiguous(), name, " must be contiguous");
+  REFUSE(impl->numel() != count, name, " must hold ", count, " values, not ", impl->numel());
+  void* p = const_cast<void*>(impl->data());
+  if (ranges) {
+    if (t.is_inference()) writable(t, name);
+    if (count) ranges->emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + count * impl->itemsize());
   }
   return p;
 }
@@ -427,6 +443,7 @@ void* flat(const Tensor& t, const char* name, const Tensor& first, int64_t count
 void adamw_step(const py::object& params, const py::object& grads, const py::object& avgs, const py::object& sqs,
                 const py::object& avg_scales, const py::object& sq_scales, const py::object& step, const py::object& lr,
                 double beta1, double beta2, double eps, double weight_decay, uint64_t seed) {
+  c10::AutoGradMode no_grad(false);  // an optimizer's step: leaves are written
   const TensorList P(params, "params"), G(grads, "grads"), M(avgs, "exp_avgs"), V(sqs, "exp_avg_sqs");
   const int64_t num = P.size();
   REFUSE(G.size() != num || M.size() != num || V.size() != num, "params, grads, exp_avgs and exp_avg_sqs must be as many");
@@ -464,8 +481,9 @@ void adamw_step(const py::object& params, const py::object& grads, const py::obj
 
   // one call of the C entry for each pair of types
   std::vector<okls_adamw_tensor> lists[4];
-  std::vector<Range> ranges;
-  ranges.reserve(num * (bits8 ? 5 : 3));
+  std::vector<Range> ranges[5];
+  for (auto& r : ranges) r.reserve(num);
+  const c10::Device device = first.device();
   for (auto& l : lists) l.reserve(lists == &l ? num : 0);
   for (int64_t i = 0; i < num; ++i) {
     const Tensor &p = P[i], &g = G[i], &m = M[i], &v = V[i];
@@ -475,21 +493,21 @@ void adamw_step(const py::object& params, const py::object& grads, const py::obj
     const at::ScalarType sd = bits8 ? at::kFloat8_e4m3fn : at::kFloat;
     REFUSE(m.scalar_type() != sd || v.scalar_type() != sd, "exp_avgs and exp_avg_sqs must be ", sd,
            bits8 ? " where scales are given" : "");
-    e.param = flat(p, "a parameter", first, n, true, ranges);
-    e.grad = flat(g, "a gradient", first, n, false, ranges);
-    e.exp_avg = flat(m, "exp_avg", first, n, true, ranges);
-    e.exp_avg_sq = flat(v, "exp_avg_sq", first, n, true, ranges);
+    e.param = flat(p, "a parameter", device, n, &ranges[0]);
+    e.grad = flat(g, "a gradient", device, n, nullptr);
+    e.exp_avg = flat(m, "exp_avg", device, n, &ranges[1]);
+    e.exp_avg_sq = flat(v, "exp_avg_sq", device, n, &ranges[2]);
     if (bits8) {
       const Tensor &ms = (*MS)[i], &vs = (*VS)[i];
       REFUSE(ms.scalar_type() != at::kFloat || vs.scalar_type() != at::kFloat, "scales must be fp32");
       const int64_t groups = (n + kGroup - 1) / kGroup;
-      e.avg_scale = static_cast<float*>(flat(ms, "avg_scale", first, groups, true, ranges));
-      e.sq_scale = static_cast<float*>(flat(vs, "sq_scale", first, groups, true, ranges));
+      e.avg_scale = static_cast<float*>(flat(ms, "avg_scale", device, groups, &ranges[3]));
+      e.sq_scale = static_cast<float*>(flat(vs, "sq_scale", device, groups, &ranges[4]));
     }
     e.count = n, e.id = static_cast<int32_t>(i);
     lists[2 * pd + gd].push_back(e);
   }
-  refuse_overlaps(ranges);
+  refuse_overlaps(ranges, 5);
 
   Call c(first);
   Tensor scalars;

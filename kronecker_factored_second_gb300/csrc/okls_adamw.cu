@@ -201,15 +201,21 @@ __device__ __forceinline__ void state_scales(uint32_t amax_bits, float* mul, flo
 // 8 lanes take a group, 16 consecutive elements each, which are held in
 // registers between the update and the rounding.
 constexpr int kOwn8 = 16;
-constexpr int kChunk8 = kAdamThreads * kOwn8;
+constexpr int kTile8 = kAdamThreads * kOwn8;
+constexpr int kChunk8 = 4 * kTile8;
 template <class P, class G, int N>
 __global__ void __launch_bounds__(kAdamThreads, 3) k_adamw8(const __grid_constant__ AdamwTable<N> T) {
   const int chunk = blockIdx.x, which = find_tensor(T, chunk);
   const AdamwEntry& e = T.t[which];
-  const int64_t i = static_cast<int64_t>(chunk - T.first[which]) * kChunk8 + threadIdx.x * kOwn8;
   const AdamwScalars s = T.s_dev ? *T.s_dev : T.s;
+  const bool aligned = all_aligned(e, 16);
+  const uint32_t low = s.low + static_cast<uint32_t>(e.id);
+  const int64_t begin = static_cast<int64_t>(chunk - T.first[which]) * kChunk8, end = min(begin + kChunk8, e.count);
+#pragma unroll 1
+  for (int64_t tile = begin; tile < end; tile += kTile8) {
+  const int64_t i = tile + threadIdx.x * kOwn8;
   const int64_t left = e.count - i;  // a group's first lane has an element where the group has one
-  const bool vec = left >= kOwn8 && all_aligned(e, 16);
+  const bool vec = left >= kOwn8 && aligned;
   const int64_t group = i / kFp8Group;
   const bool some = group * kFp8Group < e.count;
   P* p = static_cast<P*>(e.p) + i;
@@ -285,7 +291,6 @@ __global__ void __launch_bounds__(kAdamThreads, 3) k_adamw8(const __grid_constan
   float mmul, mscale, vmul, vscale;
   state_scales(am, &mmul, &mscale);
   state_scales(av, &vmul, &vscale);
-  const uint32_t low = s.low + static_cast<uint32_t>(e.id);
   uint32_t wm[4], wv[4];
   Doubt doubt;
 #pragma unroll
@@ -328,6 +333,7 @@ __global__ void __launch_bounds__(kAdamThreads, 3) k_adamw8(const __grid_constan
     }
   }
   if (some && (threadIdx.x & 7) == 0) e.ms[group] = mscale, e.vs[group] = vscale;
+  }
 }
 
 // ------------------------------------------------------ step on the device

@@ -136,6 +136,12 @@ struct Terms<float> {
   }
 };
 
+// Group of a column: pieces of 32 and 64 columns are groups, longer groups are multiples of 128.
+template <int GW>
+__device__ __forceinline__ int group_of(int col, int64_t group) {
+  return GW < 4 ? col / (32 * GW) : group == 128 ? col >> 7 : static_cast<int>((static_cast<uint32_t>(col) >> 7) / static_cast<uint32_t>(group >> 7));
+}
+
 __device__ __forceinline__ uint32_t half_at(const void* p, int64_t i) {
   return __ldg(static_cast<const unsigned short*>(p) + i);
 }
@@ -182,7 +188,7 @@ struct Codes {
         const int64_t first = k0 + l * 32 * GW;
         sz[h][l] = 0;
         if (there && first < A.k) {
-          const int64_t g = GW == 4 ? first / A.group : first / (32 * GW);
+          const int64_t g = group_of<GW>(static_cast<int>(first), A.group);
           sz[h][l] = half_at(A.scale, row[h] * A.lds_row + g * A.lds_group);
           if (ZERO) sz[h][l] |= half_at(A.zero, row[h] * A.ldz_row + g * A.ldz_group) << 16;
         }
@@ -418,12 +424,12 @@ __global__ void __launch_bounds__(Stream<X, NT, GW, ZERO>::kThreads, Stream<X, N
 #pragma unroll
     for (int i = 0; i < kSingles; ++i) {
       const int piece = (i * 32 + lane) / 16, r = row + (lane & 15);
-      const int64_t col = first + (piece % G::kLoads) * 32 * GW;
+      const int col = first + (piece % G::kLoads) * 32 * GW;
       const bool of_zero = ZERO && piece >= G::kLoads;
       single[i] = 0;
       if (r < A.n && col < A.k)
         single[i] = half_at(of_zero ? A.zero : A.scale, r * (of_zero ? A.ldz_row : A.lds_row) +
-                                                            col / A.group * (of_zero ? A.ldz_group : A.lds_group));
+                                                            group_of<GW>(col, A.group) * (of_zero ? A.ldz_group : A.lds_group));
     }
   };
   {
@@ -436,14 +442,17 @@ __global__ void __launch_bounds__(Stream<X, NT, GW, ZERO>::kThreads, Stream<X, N
   const int64_t src_wrap = kMmRows * A.ldq - chunks * (kStreamChunk / 2);
   // chunks that need no look at the matrix's end, nor at groups that are longer than a piece
   const int whole_chunks = static_cast<int>(A.k / kStreamChunk);
-  const int whole_tiles = tidy && (GW < 4 || A.group == 128) ? static_cast<int>(A.n / kMmRows) : 0;
+  const int whole_tiles = GW < 4 || A.group == 128 ? static_cast<int>(A.n / kMmRows) : 0;
   const auto fetch = [&]() {
     put_singles();
     if (load_tile < end_tile) {
       if (load_chunk < whole_chunks && load_tile < whole_tiles) {
         copy16(load_at + put0, src0), copy16(load_at + put1, src0 + 64);
         copy16(load_at + put0 + 128, src1), copy16(load_at + put1 + 128, src1 + 64);
-        copy16_if(lane < 2 * G::kScales, load_at + 2048 + lane * 16, s_src);
+        if (tidy)
+          copy16_if(lane < 2 * G::kScales, load_at + 2048 + lane * 16, s_src);
+        else
+          load_singles(load_at + 2048, load_chunk * kStreamChunk, load_tile * kMmRows);
       } else {
         const int first = load_chunk * kStreamChunk, row = load_tile * kMmRows;
         const int bytes = static_cast<int>((A.k + 1) >> 1) - first / 2 - t * 16;
@@ -453,10 +462,10 @@ __global__ void __launch_bounds__(Stream<X, NT, GW, ZERO>::kThreads, Stream<X, N
         if (!tidy) {
           load_singles(load_at + 2048, first, row);
         } else if (lane < 2 * G::kScales) {
-          const int64_t col = first + s_load * 32 * GW;
+          const int col = first + s_load * 32 * GW;
           const int srow = row + (lane & 1) * 8;
           const void* base = s_zero ? A.zero : A.scale;
-          copy_some(load_at + 2048 + lane * 16, static_cast<const char*>(base) + 2 * static_cast<int64_t>(srow) + col / A.group * s_pitch,
+          copy_some(load_at + 2048 + lane * 16, static_cast<const char*>(base) + 2 * static_cast<int64_t>(srow) + group_of<GW>(col, A.group) * s_pitch,
                     base, col < A.k ? 2 * (static_cast<int>(A.n) - srow) : 0);
         }
       }

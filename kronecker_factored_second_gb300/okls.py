@@ -29,6 +29,7 @@ import ctypes
 import torch
 
 from . import _lib as L
+from . import lm
 
 _DT = {torch.float32: L.OKLS_F32, torch.bfloat16: L.OKLS_BF16}
 
@@ -431,7 +432,6 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1: float =
 
     `step` is the step's number, from 1; or an int64 CUDA tensor with the number of steps done, which
     the call raises by one (what a captured step needs), and then `lr` may be an fp32 CUDA tensor."""
-    from . import lm
     if stream is not None:
         def tensors():
             for group in (params, grads, exp_avgs, exp_avg_sqs, avg_scales or (), sq_scales or (), (step, lr)):
@@ -439,9 +439,8 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1: float =
         with lm._on(stream, *tensors()):
             return adamw_step(params, grads, exp_avgs, exp_avg_sqs, step=step, lr=lr, beta1=beta1, beta2=beta2, eps=eps,
                               weight_decay=weight_decay, avg_scales=avg_scales, sq_scales=sq_scales, seed=seed)
-    with torch.no_grad():
-        lm._n().adamw_step(params, grads, exp_avgs, exp_avg_sqs, avg_scales, sq_scales, step, lr, beta1, beta2, eps,
-                           weight_decay, seed % (1 << 64))
+    lm._n().adamw_step(params, grads, exp_avgs, exp_avg_sqs, avg_scales, sq_scales, step, lr, beta1, beta2, eps, weight_decay,
+                       seed & 0xFFFFFFFFFFFFFFFF)
 
 
 class AdamW(torch.optim.Optimizer):
