@@ -204,7 +204,7 @@ constexpr int kOwn8 = 16;
 constexpr int kTile8 = kAdamThreads * kOwn8;
 constexpr int kChunk8 = 4 * kTile8;
 template <class P, class G, int N>
-__global__ void __launch_bounds__(kAdamThreads, 3) k_adamw8(const __grid_constant__ AdamwTable<N> T) {
+__global__ void __launch_bounds__(kAdamThreads, 4) k_adamw8(const __grid_constant__ AdamwTable<N> T) {
   const int chunk = blockIdx.x, which = find_tensor(T, chunk);
   const AdamwEntry& e = T.t[which];
   const AdamwScalars s = T.s_dev ? *T.s_dev : T.s;

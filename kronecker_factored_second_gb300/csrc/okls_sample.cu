@@ -131,10 +131,16 @@ __device__ __forceinline__ u64 weight(const Heat& h, const u64* powers, float z)
   const u64 p = powers[k & (kSteps - 1)];
   u64 w = p + static_cast<u64>(static_cast<long long>(static_cast<int>(p >> 32)) *
                                (__float_as_int(q) - __float_as_int(kMagic)));
-  // w >> n for n <= 63 (least sees to it), with shifts that stop at 32
+  // w >> n for n <= 63 (least sees to it): shifts that stop at 32, where the
+  // compiler's own looks at which half n reaches
   const uint32_t n = static_cast<uint32_t>(k >> 11), wl = static_cast<uint32_t>(w), wh = static_cast<uint32_t>(w >> 32);
-  const uint32_t low = __funnelshift_rc(wl, wh, n) >> max(static_cast<int>(n) - 32, 0);
-  return (static_cast<u64>(__funnelshift_rc(wh, 0, n)) << 32) | low;
+  uint32_t low, high;
+  asm("shf.r.clamp.b32 %0, %1, %2, %3;" : "=r"(low) : "r"(wl), "r"(wh), "r"(n));
+  asm("shr.u32 %0, %0, %1;" : "+r"(low) : "r"(max(static_cast<int>(n) - 32, 0)));
+  asm("shr.u32 %0, %1, %2;" : "=r"(high) : "r"(wh), "r"(n));
+  u64 r64;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r64) : "r"(low), "r"(high));
+  return r64;
 }
 
 // The bin of a value among 2048, 64 to an octave below the maximum: it does not
@@ -331,12 +337,6 @@ __device__ __forceinline__ u64 list_scan(Shared& S, const Group& G, const u64 (&
 __device__ __forceinline__ void add_from(u64& sum, u64 w, float z, float least) {
   asm("{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %2, %3;\n\t@p add.u64 %0, %0, %1;\n\t}" : "+l"(sum) : "l"(w), "f"(z), "f"(least));
 }
-// at += n in shared memory where `on`.
-__device__ __forceinline__ void add_shared(bool on, uint32_t at, uint32_t n) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p red.shared.add.u32 [%1], %2;\n\t}" ::"r"(static_cast<int>(on)), "r"(at), "r"(n)
-               : "memory");
-}
-
 // Sum of fn(value, id) over the row; the segments' sums stay in S.seg and the CTA's in S.total.
 template <int NV, class T, class Fn>
 __device__ u64 sum_row(Shared& S, const Group& G, const Part<T>& R, Fn fn) {
@@ -734,7 +734,9 @@ __device__ void fill_bins(Shared& S, const Group& G, const Part<T>& R, const Hea
           n = bin_weight(h, z[j], b);
         else
           b = bin_of(h, z[j]);
-        add_shared(keep(z[j], q + j - R.shift), bins + 4 * b, n);
+        // (a word of the lane's behind the bins takes the others: a branch around each addition costs more)
+        b = keep(z[j], q + j - R.shift) ? b : kBins + lane;
+        asm volatile("red.shared.add.u32 [%0], %1;" ::"r"(bins + 4 * b), "r"(n) : "memory");
       }
     }
   }
