@@ -2,10 +2,11 @@
 
 Training: embedding, RMS norms with the residual's addition, 8-bit linear layers (the weights' and activations'
 quantisations and all three products of each), log probabilities and their gradients, and the weight matrices stepped by
-Online KL Shampoo (AdamW for the tables and the norms' weights).  Serving: weights quantised once, the norms write the 8-bit
-inputs of the products, and the best next tokens come back with their log probabilities.
+Online KL Shampoo (AdamW for the tables and the norms' weights, its states in 32 or 8 bits).  Serving: weights quantised
+once, the norms write the 8-bit inputs of the products, and the best next tokens come back with their log probabilities.
+Generation: weights in 4 bits, and tokens drawn with temperature, top-k, top-p and min-p.
 
-    python examples/train_lm.py [--steps 80]
+    python examples/train_lm.py [--steps 80] [--state-bits 32]
 
 The data is synthetic: each token is followed by a fixed successor nine times out of ten, and by any token otherwise, so the
 loss can fall from log(vocab) to about 0.9.
@@ -21,7 +22,7 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from kronecker_factored_second_gb300 import lm  # noqa: E402
-from kronecker_factored_second_gb300.okls import OnlineKLShampoo  # noqa: E402
+from kronecker_factored_second_gb300.okls import AdamW, OnlineKLShampoo  # noqa: E402
 
 
 class TokenModel:
@@ -85,6 +86,38 @@ class Server:
         return lm.token_logprobs(lm.fp8_matmul(r.y, self.out), ids, top_k=top_k)
 
 
+class Generator:
+    """The trained model with its weights in 4 bits, which draws the next tokens of a few sequences."""
+
+    def __init__(self, model, group=64, seed=0):
+        self.m = model
+        q = lambda ws: [lm.int4_quantize(w.detach(), group=group, symmetric=False) for w in ws]  # noqa: E731
+        self.up, self.down, self.out = q(model.up), q(model.down), q([model.out])[0]
+        self.table = model.table.detach().bfloat16()
+        self.norms = [n.detach() for n in model.norms]
+        self.random = torch.Generator(device="cuda")
+        self.random.manual_seed(seed)
+
+    def logits(self, ids):
+        x, res = lm.embedding(self.table, ids, scale=self.m.scale), None
+        for norm, up, down in zip(self.norms, self.up, self.down):
+            r = lm.rms_norm(x, norm, residual=res)
+            res = r.residual
+            x = lm.int4_matmul(torch.nn.functional.silu(lm.int4_matmul(r.y, up)), down)
+        return lm.int4_matmul(lm.rms_norm(x, self.norms[-1], residual=res).y, self.out, out_dtype=torch.float32)
+
+    def generate(self, ids, count, **settings):
+        """`count` tokens after each of `ids` (len(ids) x count), with their log probabilities; settings are lm.sample's."""
+        tokens, scores = [], []
+        for _ in range(count):
+            u = torch.rand(len(ids), generator=self.random, device="cuda")
+            r = lm.sample(self.logits(ids), u, **settings)
+            ids = r.ids
+            tokens.append(ids)
+            scores.append(r.logp)
+        return torch.stack(tokens, 1), torch.stack(scores, 1)
+
+
 def batches(vocab, tokens, seed=1):
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
@@ -98,10 +131,10 @@ def batches(vocab, tokens, seed=1):
         yield torch.where(pad, -1, ids), torch.where(pad, -1, targets), successor
 
 
-def train(steps=80, vocab=512, tokens=4096, log=None):
+def train(steps=80, vocab=512, tokens=4096, log=None, state_bits=32):
     model = TokenModel(vocab)
     shampoo = OnlineKLShampoo(model.matrices(), lr=0.05, weight_decay=0.0)
-    adam = torch.optim.AdamW(model.others(), lr=1e-2, weight_decay=0.0)
+    adam = AdamW(model.others(), lr=1e-2, weight_decay=0.0, state_bits=state_bits)
     data, losses, successor = batches(vocab, tokens), [], None
     for step in range(steps):
         ids, targets, successor = next(data)
@@ -121,14 +154,18 @@ def train(steps=80, vocab=512, tokens=4096, log=None):
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=80)
+    ap.add_argument("--state-bits", type=int, default=32, choices=(8, 32))
     a = ap.parse_args()
-    model, losses, successor = train(a.steps, log=print)
+    model, losses, successor = train(a.steps, log=print, state_bits=a.state_bits)
     print(f"last loss {losses[-1]:.4f}")
     ids = torch.arange(4, device="cuda")
     r = Server(model).next_tokens(ids)
     for i in range(4):
         best = ", ".join(f"{t} ({p:.2f})" for t, p in zip(r.top_ids[i].tolist(), r.top_logp[i].tolist()))
         print(f"after {i} (successor {successor[i].item()}): {best}")
+    tokens, scores = Generator(model).generate(ids, 8, temperature=0.8, top_k=20, top_p=0.95, min_p=0.02)
+    for i in range(4):
+        print(f"from {i}: {tokens[i].tolist()} (log probability {scores[i].sum().item():.2f})")
 
 
 if __name__ == "__main__":

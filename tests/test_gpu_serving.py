@@ -126,10 +126,10 @@ def test_adamw_touches_nothing_else():
             assert torch.equal(x[left], y[left])
 
 
-def _philox(n, ident, t, seed):
-    """The two 16-bit numbers of each of n elements, by the published rounds in whole numbers."""
+def _philox(n, ident, t, seed, first=0):
+    """The two 16-bit numbers of each of n elements, by the published rounds in whole numbers (`first` is even)."""
     s = (seed + t * 0x9E3779B97F4A7C15) % (1 << 64)
-    x = torch.arange((n + 1) // 2, device="cuda")
+    x = torch.arange((n + 1) // 2, device="cuda") + first // 2
     y = torch.full_like(x, (ident + s) % (1 << 32))
     for i in range(5):
         p, q = (x & 0xFFFF) * 0xD256D193, (x >> 16) * 0xD256D193
@@ -749,6 +749,68 @@ def test_sample_refusals():
             f()
 
 
+# ------------------------------------------------------------------ sizes past 32 bits
+def test_adamw_past_32_bits():
+    """A tensor of more than 2^31 elements, both kinds of states: the last elements against the formula."""
+    n, tail = (1 << 31) + 1029, 3000
+    p = torch.ones(n, device="cuda", dtype=BF16)
+    gr = torch.full((n,), 1e-2, device="cuda", dtype=BF16)
+    g = gen(20)
+    for x in (p, gr):
+        x[-tail:] = randn(g, tail, dtype=BF16)
+    old, cut = p[-tail:].clone(), slice(n - tail, n)
+    m, v = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    okls.adamw_step([p], [gr], [m], [v], step=1, **HYPER)
+    zero = torch.zeros(tail, dtype=torch.float64, device="cuda")
+    want = _check_update(p[cut], old, gr[cut], zero, zero, 1, HYPER)
+    close(m[cut], want[0], 4 * U * want[2], "first moment")
+    close(v[cut], want[1], 5 * U * want[1], "second moment")
+    assert (p[1 << 20] == p[0]).item() and (m[: 1 << 20] == m[0]).all()
+    del m, v
+    p[cut] = old
+    m, r = (torch.zeros(n, dtype=torch.uint8, device="cuda").view(E4M3) for _ in range(2))
+    ms, rs = (torch.zeros(-(-n // 128), device="cuda") for _ in range(2))
+    okls.adamw_step([p], [gr], [m], [r], step=1, avg_scales=[ms], sq_scales=[rs], seed=3, **HYPER)
+    wm, wv, mag = _check_update(p[cut], old, gr[cut], zero, zero, 1, HYPER, fast=True)
+    # whole groups at the end
+    at = (n - tail + 127) // 128 * 128
+    skip = at - (n - tail)
+    dm, dv = _philox(n - at, 0, 1, 3, first=at)
+    _check_codes(m[at:], ms[at // 128:], wm[skip:], 5 * U * mag[skip:], dm, False)
+    _check_codes(r[at:], rs[at // 128:], wv[skip:].sqrt(), 8 * U * wv[skip:].sqrt(), dv, True)
+
+
+def test_int4_matmul_past_32_bits():
+    n, k = 140003, 32768  # 2.3 GB of codes
+    g = gen(21)
+    data = torch.randint(0, 256, (n, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = (torch.rand(k // 128, 140008, generator=g, device="cuda") + 0.5).bfloat16()[:, :n].t()
+    w = lm.Int4Tensor(data, s, k)
+    x = randn(g, 1, k, dtype=BF16)
+    y = lm.int4_matmul(x, w)
+    for rows in (slice(0, 50), slice(n - 50, n), slice(131000, 131100)):
+        _check_int4(x, lm.Int4Tensor(data[rows], s[rows], k), y[:, rows], BF16)
+
+
+def test_sample_past_32_bits():
+    rows, vocab = 20000, 131072  # 5.2 GB of logits
+    z = torch.zeros(rows, vocab, device="cuda", dtype=BF16)
+    g = gen(22)
+    some = [0, 1, 16383, 16384, 16385, rows - 1]
+    z[some] = randn(g, len(some), vocab, dtype=BF16, std=3.0)
+    u = torch.rand(rows, generator=g, device="cuda")
+    for kw in (dict(), dict(top_p=0.7), dict(top_k=30)):
+        r = lm.sample(z, u, **kw)
+        one = lm.sample(z[some].contiguous(), u[some], **kw)
+        assert torch.equal(r.ids[some], one.ids) and torch.equal(r.logp[some], one.logp)
+        # rows of equal logits: the id says where u lies (the shortest prefix of at least p of them, or the first k)
+        left = torch.ones(rows, dtype=torch.bool, device="cuda")
+        left[some] = False
+        count = 30 if "top_k" in kw else math.ceil(vocab * float(torch.tensor(kw.get("top_p", 1.0))))
+        want = torch.floor(u.double() * count).int()
+        assert torch.equal(r.ids[left], want[left])
+
+
 # ------------------------------------------------------------------ together
 def test_generation_step_captured_and_on_two_streams():
     """A 4-bit output layer and the sampling of its logits: captured and replayed with new inputs, two graphs of it, and two
@@ -786,3 +848,37 @@ def test_generation_step_captured_and_on_two_streams():
     torch.cuda.synchronize()
     for i, r in enumerate(got):
         assert torch.equal(r.ids, want[i % 4].ids) and torch.equal(r.logp, want[i % 4].logp)
+
+
+@pytest.mark.parametrize("state_bits", [32, 8])
+def test_example_trains_and_generates(state_bits):
+    """The example with AdamW's states in both sizes, and generation from its weights in 4 bits: it runs, and its logits are
+    those of the same weights in fp32."""
+    import importlib.util
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location("train_lm_serving", os.path.join(root, "examples", "train_lm.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    model, losses, _ = example.train(4, vocab=300, tokens=256, state_bits=state_bits)
+    assert all(math.isfinite(x) for x in losses)
+    maker = example.Generator(model)
+    ids = torch.arange(5, device="cuda")
+    z = maker.logits(ids)
+
+    def norm(x, w):
+        return x * torch.rsqrt((x * x).mean(-1, keepdim=True) + 1e-6) * w
+    res = model.table.detach()[ids] * model.scale
+    x = None
+    for n, up, down in zip(maker.norms, maker.up, maker.down):
+        res = res if x is None else res + x
+        x = torch.nn.functional.silu(norm(res, n) @ up.float().t()) @ down.float().t()
+    want = norm(res + x, maker.norms[-1]) @ maker.out.float().t()
+    # some ten roundings to bf16 (2^-8 each) lie between the table and a logit, in sums whose terms they hit at random
+    assert ((z - want).norm() / want.norm()).item() < 10 * 2.0 ** -8
+    tokens, scores = maker.generate(ids, 6, temperature=0.9, top_k=40, top_p=0.9, min_p=0.01)
+    assert tokens.shape == scores.shape == (5, 6) and ((tokens >= 0) & (tokens < 300)).all() and (scores <= 0).all()
+    again, _ = example.Generator(model).generate(ids, 6, temperature=0.9, top_k=40, top_p=0.9, min_p=0.01)
+    assert torch.equal(tokens, again)
+    best, _ = maker.generate(ids, 1, temperature=0.0)
+    assert torch.equal(best[:, 0].long(), z.argmax(-1))
