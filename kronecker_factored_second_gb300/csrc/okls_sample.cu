@@ -57,6 +57,7 @@ constexpr int kEach = kList / kThreads;
 constexpr int kFewSegs = 320;        // segments whose maxima are ranked by counting
 constexpr int kSegs = 1024;      // segments of a CTA's part of a row
 constexpr int kSteps = 2048;     // table entries in an octave
+constexpr float kLowest = -3.402823466e38f;  // the least possible logit
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: added to |x| <= 2^22, leaves x rounded in the low bits
 
 // ------------------------------------------------------------------ weights
@@ -88,7 +89,8 @@ struct Heat {
   int kb;        // bits of the maximum's k + kMagic, 62 bits to the row's unit in the octaves
   float r;       // the maximum's r
   float top, c;  // the maximum, 64 log2(e) / T
-  int shift;     // 62 bits to the row's unit
+  bool zeros;    // a weight is 0 at `least` (a temperature past 1e36 leaves even impossible values one)
+  int shift;     // 62 bits to the row's unit, at least 1
 };
 
 __device__ __forceinline__ void steps_of(const Heat& h, float z, int& kb, float& r) {
@@ -110,6 +112,7 @@ __device__ Heat make_heat(float m, float temperature, int shift) {
   h.base = far ? m : 0.0f;
   // (64 - shift octaves below the maximum nothing is left of a weight)
   h.least = fmaxf((far ? 0.0f : m) - (63.9f - static_cast<float>(shift)) * 2048.0f / h.ch, -3.4e38f);
+  h.zeros = h.least > -3.3e38f;
   h.shift = shift;
   h.top = m, h.c = h.ch * (1.0f / 32.0f);
   steps_of(h, m, h.kb, h.r);
@@ -131,13 +134,11 @@ __device__ __forceinline__ u64 weight(const Heat& h, const u64* powers, float z)
   const u64 p = powers[k & (kSteps - 1)];
   u64 w = p + static_cast<u64>(static_cast<long long>(static_cast<int>(p >> 32)) *
                                (__float_as_int(q) - __float_as_int(kMagic)));
-  // w >> n for n <= 63 (least sees to it): shifts that stop at 32, where the
-  // compiler's own looks at which half n reaches
+  // w >> n for n <= 63 (least sees to it), in funnel shifts: others look at
+  // whether they reach past 31 bits
   const uint32_t n = static_cast<uint32_t>(k >> 11), wl = static_cast<uint32_t>(w), wh = static_cast<uint32_t>(w >> 32);
-  uint32_t low, high;
-  asm("shf.r.clamp.b32 %0, %1, %2, %3;" : "=r"(low) : "r"(wl), "r"(wh), "r"(n));
-  asm("shr.u32 %0, %0, %1;" : "+r"(low) : "r"(max(static_cast<int>(n) - 32, 0)));
-  asm("shr.u32 %0, %1, %2;" : "=r"(high) : "r"(wh), "r"(n));
+  const uint32_t low = __funnelshift_r(__funnelshift_rc(wl, wh, n), 0, static_cast<uint32_t>(max(static_cast<int>(n) - 32, 0)));
+  const uint32_t high = __funnelshift_rc(wh, 0, n);
   u64 r64;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r64) : "r"(low), "r"(high));
   return r64;
@@ -158,21 +159,17 @@ __device__ __forceinline__ uint32_t bin_weight(const Heat& h, float z, int& bin)
   return __float_as_int(w + 8388608.0f) & 0xFFFFu;
 }
 
-// floor(f * w) or ceil for a fraction f in [0, 1).
+// floor(f * w), or ceil, for a normal fraction f in [0, 1).
 __device__ u64 fraction_of(float f, u64 w, bool up) {
-  int e;
-  const u64 mant = static_cast<u64>(ldexpf(frexpf(f, &e), 24));  // f = mant * 2^(e - 24)
-  const int s = 24 - e;
+  const uint32_t bits = __float_as_uint(f), mant = (bits & 0x7FFFFFu) | 0x800000u;  // f = mant * 2^-s
+  const int s = 150 - static_cast<int>(bits >> 23);
+  if (s >= 128) return up && f > 0.0f && w > 0 ? 1 : 0;
   const u64 lo = w * mant, hi = __umul64hi(w, mant);
-  if (mant == 0) return 0;
-  if (s >= 128) return up ? 1 : 0;
   u64 v, rest;
-  if (s >= 64) {
-    v = s == 64 ? hi : hi >> (s - 64);
-    rest = lo | (s == 64 ? 0 : hi << (128 - s));
+  if (s < 64) {
+    v = (hi << (64 - s)) | (lo >> s), rest = lo << (64 - s);
   } else {
-    v = (hi << (64 - s)) | (lo >> s);
-    rest = lo << (64 - s);
+    v = hi >> (s - 64), rest = lo | (hi & ((1ull << (s - 64)) - 1));
   }
   return v + (up && rest != 0);
 }
@@ -368,6 +365,7 @@ __device__ u64 sum_row(Shared& S, const Group& G, const Part<T>& R, Fn fn) {
 template <int NV, class T>
 __device__ u64 sum_above(Shared& S, const Group& G, const Part<T>& R, const Heat& h, float least) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool all_count = least <= kLowest && h.zeros;  // impossible values have weight 0
   u64 mine = 0;
   for (int s = warp; s < R.segs; s += kWarps) {
     u64 sum = 0;
@@ -375,9 +373,12 @@ __device__ u64 sum_above(Shared& S, const Group& G, const Part<T>& R, const Heat
     for (int v = 0; v < NV; ++v) {
       float z[8];
       load_finite(R, R.from + (s * NV + v) * 256 + lane * 8, z);
+      if (all_count) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        add_from(sum, weight(h, S.powers, z[j]), z[j], least);
+        for (int j = 0; j < 8; ++j) sum += weight(h, S.powers, z[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) add_from(sum, weight(h, S.powers, z[j]), z[j], least);
       }
     }
     sum = warp_total(sum);
@@ -697,7 +698,7 @@ __device__ void bins_to_values(Shared& S, const Heat& h, int first, int last) {
   if (warp < 2) {
     // the least key whose bin is at most `most`, 32 places a time
     const int most = warp == 0 ? first - 1 : last;
-    uint32_t low = ord_bits(-3.402823466e38f), high = ord_bits(h.top) + 1;
+    uint32_t low = ord_bits(kLowest), high = ord_bits(h.top) + 1;
     while (low < high) {
       const uint32_t step = (high - low + 31) / 32, at = low + lane * step;
       const unsigned reached = __ballot_sync(0xffffffffu, at >= high || at < low || bin_of(h, ord_value(at)) <= most);
@@ -849,6 +850,8 @@ __device__ u64 cut_list(Shared& S, const Group& G, const Part<T>& R, const Heat&
 // at least p of theirs, and that `in` keeps (tighter than `of`).  Leaves in S.seg
 // and S.total the sums by segments of what is kept, and returns their sum; 0
 // where the border's bins hold too many tokens.
+// Without TIES `of` are all possible tokens (the others have weight 0), `in` those
+// from a value on.
 template <bool TIES, int NV, class T>
 __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const Heat& h, float p, const Cut& of, const Cut& in,
                            Cut* out) {
@@ -857,25 +860,33 @@ __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const He
   const auto in_these = [&](float z, int id) { return TIES ? kept(in, z, id) : z >= in.value; };
   fill_bins<true, NV>(S, G, R, h, of_these);
   // in units of 2^-40 of the largest weight
-  u64 mass[kBinsThread], sum = 0;
-  const int b0 = threadIdx.x * kBinsThread, octave = b0 >> 6;
+  uint32_t mass[kBinsThread];
+  u64 sum = 0;
+  const int b0 = threadIdx.x * kBinsThread, octave = b0 >> 6;  // (a thread's bins lie in one octave)
+  const auto scaled = [octave](u64 n) { return octave < 26 ? n << (26 - octave) : n >> (octave - 26); };
 #pragma unroll
-  for (int i = 0; i < kBinsThread; ++i) {
-    u64 n = 0;
-    for (int r = 0; r < G.size; ++r) n += *G.of(&S.bin.low[b0 + i], r);
-    mass[i] = octave < 26 ? n << (26 - octave) : n >> (octave - 26);
-    sum += mass[i];
+  for (int i = 0; i < kBinsThread; ++i) mass[i] = S.bin.low[b0 + i];
+  for (int r = 1; r < G.size; ++r) {
+    // (a row of 2^17 tokens has 2^31 in a bin at most)
+    const uint32_t* other = G.of(S.bin.low, (G.rank + r) % G.size);
+#pragma unroll
+    for (int i = 0; i < kBinsThread; ++i) mass[i] = min(mass[i], 0x7FFFFFFFu) + min(other[b0 + i], 0x7FFFFFFFu);
   }
+#pragma unroll
+  for (int i = 0; i < kBinsThread; ++i) sum += mass[i];
+  sum = scaled(sum);
   if (threadIdx.x == 0) S.border = 0, S.border_count = kBins - 1;
   const Scan scan = cta_scan(S, G, sum);
   const u64 goal = fraction_of(p, scan.all, true), margin = scan.all >> 12;
   u64 at = scan.run - sum;
+  if (at < goal + margin && scan.run + margin >= goal) {
 #pragma unroll
-  for (int i = 0; i < kBinsThread; ++i) {
-    const u64 next = at + mass[i];
-    if (at + margin < goal && next + margin >= goal) S.border = b0 + i;
-    if (at < goal + margin && next >= goal + margin) S.border_count = b0 + i;
-    at = next;
+    for (int i = 0; i < kBinsThread; ++i) {
+      const u64 next = at + scaled(mass[i]);
+      if (at + margin < goal && next + margin >= goal) S.border = b0 + i;
+      if (at < goal + margin && next >= goal + margin) S.border_count = b0 + i;
+      at = next;
+    }
   }
   __syncthreads();
   bins_to_values(S, h, S.border, S.border_count);
@@ -904,7 +915,6 @@ __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const He
           if (takes) part += w;
           listed |= z[j] >= lower && !takes ? 1u << j : 0u;
         } else {
-          // (impossible tokens have weight 0)
           all += w;
           add_from(part, w, z[j], upper);
           listed |= z[j] >= lower && z[j] < upper ? 1u << j : 0u;
@@ -1058,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_sample(const Samp
     const bool by_count = k > 0 && k < vocab, by_mass = p < 1.0f;
     const Heat h = make_heat(top, temperature, A.shift);
 
-    float floor = -3.402823466e38f;  // every possible token
+    float floor = kLowest;  // every possible token
     if (least > 0.0f) {
       // the least value is rounded up to fp32, so that comparing values is exact
       if (threadIdx.x == 0) {
@@ -1077,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_sample(const Samp
     };
 
     // (the mass of the first k, whatever their weights, is asked for where a cut by mass follows)
-    const float least_counted = by_mass ? -3.402823466e38f : floor;
+    const float least_counted = by_mass ? kLowest : floor;
     Cut cut = {least_counted, kAllIds};
     u64 mass = 0;
     if (by_count) {
@@ -1103,7 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_sample(const Samp
     if (by_mass && mass == 0) {
       const Cut of = cut, in = tighter(cut, floor_cut);
       Cut c;
-      mass = of.id == kAllIds && in.id == kAllIds ? cut_by_mass<false, NV>(S, G, R, h, p, of, in, &c)
+      mass = of.id == kAllIds && in.id == kAllIds && of.value <= kLowest && h.zeros ? cut_by_mass<false, NV>(S, G, R, h, p, of, in, &c)
                                                   : cut_by_mass<true, NV>(S, G, R, h, p, of, in, &c);
       if (mass == 0) {
         const u64 target = fraction_of(p, sum_row<NV>(S, G, R, possible(of)), true);

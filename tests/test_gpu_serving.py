@@ -590,6 +590,7 @@ def _check_sample(logits, u, r, **kw):
     w = _kept(z, **kw)
     total = w.sum(-1)
     ids, logp = r.ids.reshape(-1).long(), r.logp.reshape(-1)
+    assert ((ids >= -1) & (ids < z.shape[1])).all(), "an id outside the vocabulary"
     none = total == 0
     assert torch.equal(ids == -1, none) and (logp[none] == -INF).all()
     some = ~none
@@ -651,6 +652,23 @@ def test_sample_equal_logits(dtype, vocab):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+def test_sample_first_k_end_with_a_run_of_equals(dtype):
+    """The first k are all tokens of the best value, or of the best two: what lies below has no share in the mass."""
+    g = gen(18)
+    rows, vocab = 6, 50000
+    z = randn(g, rows, vocab, std=0.5).clamp(-2, 0.9)
+    z[:3, 7:2007] = 1.0
+    z[3:, 7:1507] = 1.0
+    z[3:, 20000:21000] = 0.95
+    z = z.to(dtype)
+    for k, some in ((2000, slice(0, 3)), (2500, slice(3, 6)), (1500, slice(3, 6)), (1999, slice(0, 3)), (2501, slice(3, 6))):
+        for p in (0.3, 0.9, 1.0):
+            kw = dict(top_k=k, top_p=p, min_p=0.01)
+            u = torch.rand(3, generator=g, device="cuda")
+            _check_sample(z[some], u, lm.sample(z[some], u, **kw), **kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("vocab", [5, 3000, 40000])
 def test_sample_rows_that_are_not_finite(dtype, vocab):
     g = gen(vocab + 1)
@@ -683,6 +701,7 @@ def test_sample_values_of_all_sizes(dtype):
     z[4] -= 1e9
     z[5] *= 1e-3
     z[6] *= 3e5
+    z[7, ::3] = -INF  # (with temperatures past 1e36 as well)
     z = z.to(dtype)
     for kw in SETTINGS + [dict(temperature=t, **f) for t in (2.0 ** -20, 1e-4, 50.0, 1e10, 1e38, INF)
                           for f in (dict(), dict(top_p=0.7), dict(top_k=500, min_p=0.3))]:
