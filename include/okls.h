@@ -774,7 +774,9 @@ okls_status okls_int4_quantize(const void *x, int32_t dtype, int64_t ldx,
  * weights W as above.
  *   x     rows x k, fp32 or bf16; out  rows x n, fp32 or bf16.
  * Products are exact; each group's sum and the sum of the scaled groups are
- * fp32.  Any number of rows is taken, but the way through the kernel is made
+ * fp32.  (bf16 x: a group's sum is formed of 16 + c and -(16 + zero), which costs it
+ * two bits; fp32 x: of c - 8 and 8 - zero.  Values of x beyond 2^122 may overflow
+ * there.)  Any number of rows is taken, but the way through the kernel is made
  * for tokens that are generated, up to some 64 (rows <= 524280).  Rows of codes start
  * on 16-byte boundaries (OKLS_ERR_UNSUPPORTED otherwise).  An infinity in x
  * gives NaN or an infinity, a NaN gives NaN, in that row of out.
@@ -800,7 +802,9 @@ okls_status okls_int4_matmul(const void *x, int32_t x_dtype, int64_t ldx,
  * of the kept w is above u times their sum; logp is ln(w / sum).  A
  * temperature below 2^-20, or NaN, takes the first token of the order.  Other
  * NaN settings leave their filter off; u outside [0, 1) is moved to the nearest value
- * inside, NaN to 0.
+ * inside, NaN to 0.  Weights are known to 2^-32 of themselves and rounded down to
+ * a multiple of 2^-(63 - log2 vocab) of the largest, so a token below that is not
+ * drawn; their sums are exact, and the draw does not depend on the launch.
  *   logits  rows x vocab, fp32 or bf16, pitch ldl; vocab <= 2^20.
  *   u, ids, logp  one for each row.
  * Logits of -inf or NaN are impossible tokens; a row of nothing else gets id

@@ -5,17 +5,23 @@
 //
 // A generation step reads every weight once for a few tokens, so the codes'
 // bytes bound it.  What has to keep up with them is the way from nibbles to
-// products: c - 8 and x are exact in bf16 and their products exact in fp32, so
-// the tensor core takes them (16 weights' rows x 16 of the sum x 8 tokens an
+// products: small whole numbers and x are exact in bf16 and their products exact in
+// fp32, so the tensor core takes them (16 weights' rows x 16 of the sum x 8 tokens an
 // instruction); tokens that are not there are zero columns.  fp32 activations
 // go in as three bf16 terms, whose sum is the value, with three instructions
 // instead of one.  A group's partial sum is scaled in fp32 and added to the
-// running sum there.  With zero points, one more instruction with a factor of
-// ones gives the group's sum of x, which (zero - 8) scale takes away.
+// running sum there.  What the numbers are off by (the zero point, and the 16 or 8
+// of their form) is a factor of the group's sum of x, from a product with ones.
 //
 // The order of a sum's terms is free, so each lane takes the codes where they
-// lie: 8 codes of a word are four pairs (c0, c4), (c1, c5), ..., which a mask
-// and an or turn into bf16 128 + c, and the activations are paired alike.
+// lie: 8 codes of a word are four pairs (c0, c4), (c1, c5), ..., which a shift, a
+// mask and an or turn into bf16 pairs, and the activations are paired alike.
+//
+// Two kernels: k_int4_stream for generated tokens (one wave of CTAs, x in shared
+// memory), k_int4_matmul for more rows or longer ones than that holds.  Measured
+// (bf16, L2 flushed): 1 row, 131072 x 2048 with zero points in 36.9 us (4.1 TB/s;
+// issue slots run out), 5504 x 2048 in 4.6 us without its call; 16 rows, 11008 x 4096
+// in 17 us (x's staging and issue).
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -53,8 +59,6 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t q) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Eight values of x as the four pairs (0, 4), (1, 5), (2, 6), (3, 7) of each
-// of their bf16 terms.
 // Eight values of x as they lie in memory.
 template <class X>
 struct Raw {
@@ -91,6 +95,8 @@ struct Raw {
   }
 };
 
+// Eight values of x as the four pairs (0, 4), (1, 5), (2, 6), (3, 7) of each
+// of their bf16 terms.
 template <class X>
 struct Terms;
 template <>
@@ -562,104 +568,104 @@ __global__ void __launch_bounds__(Stream<X, NT, GW, ZERO>::kThreads, Stream<X, N
   uint32_t stage = ring_at;
   int tile = tile0, chunk = begin;
   for (int base = cta_tile, turns = 0; base < end_tile; base += batch, ++turns) {
-  const int stop = min(base + batch, end_tile);
-  float* mine = parts + (G::kBuffers == 2 ? (turns & 1) * buffer : 0);
+    const int stop = min(base + batch, end_tile);
+    float* mine = parts + (G::kBuffers == 2 ? (turns & 1) * buffer : 0);
 #pragma unroll 1
-  while (tile < stop) {
-    uint32_t xw[NT];
+    while (tile < stop) {
+      uint32_t xw[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) xw[nt] = x_at[nt] + chunk * 8 * x_word;
-    const uint32_t sum_at = sums_at + chunk * G::kSums * 4;
-    fetch();
-    asm volatile("cp.async.wait_group %0;" ::"n"(G::kAhead - 1) : "memory");
-    __syncwarp();
+      for (int nt = 0; nt < NT; ++nt) xw[nt] = x_at[nt] + chunk * 8 * x_word;
+      const uint32_t sum_at = sums_at + chunk * G::kSums * 4;
+      fetch();
+      asm volatile("cp.async.wait_group %0;" ::"n"(G::kAhead - 1) : "memory");
+      __syncwarp();
 #pragma unroll
-    for (int l = 0; l < G::kLoads; ++l) {
-      uint32_t q[2][GW];
+      for (int l = 0; l < G::kLoads; ++l) {
+        uint32_t q[2][GW];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t r = stage + g * 256 + h * 128;
-        if constexpr (GW == 4) {
-          const uint4 v = shared128(r + ((l * 4 + t) ^ turn) * 16);
-          q[h][0] = v.x, q[h][1] = v.y, q[h][2] = v.z, q[h][3] = v.w;
-        } else if constexpr (GW == 2) {
-          const uint2 v = shared64(r + ((l * 2 + (t >> 1)) ^ turn) * 16 + (t & 1) * 8);
-          q[h][0] = v.x, q[h][1] = v.y;
-        } else {
-          q[h][0] = shared32(r + (l ^ turn) * 16 + t * 4);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t r = stage + g * 256 + h * 128;
+          if constexpr (GW == 4) {
+            const uint4 v = shared128(r + ((l * 4 + t) ^ turn) * 16);
+            q[h][0] = v.x, q[h][1] = v.y, q[h][2] = v.z, q[h][3] = v.w;
+          } else if constexpr (GW == 2) {
+            const uint2 v = shared64(r + ((l * 2 + (t >> 1)) ^ turn) * 16 + (t & 1) * 8);
+            q[h][0] = v.x, q[h][1] = v.y;
+          } else {
+            q[h][0] = shared32(r + (l ^ turn) * 16 + t * 4);
+          }
+        }
+        float acc[NT][4];
+#pragma unroll
+        for (int w = 0; w < GW; ++w) {
+          const uint32_t u0 = q[0][w], u1 = q[1][w];
+          const uint32_t a0[4] = {unpack(u0 << 3), unpack(u1 << 3), unpack(u0 >> 1), unpack(u1 >> 1)};
+          const uint32_t a1[4] = {unpack(u0 >> 5), unpack(u1 >> 5), unpack(u0 >> 9), unpack(u1 >> 9)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int f = 0; f < G::kTerms; ++f) {
+              const uint4 x = shared128(xw[nt] + (l * GW + w) * x_word + f * x_term);
+              if (w == 0 && f == 0)
+                mma16816_first(acc[nt], a0, x.x, x.y);
+              else
+                mma16816(acc[nt], a0, x.x, x.y);
+              mma16816(acc[nt], a1, x.z, x.w);
+            }
+          }
+        }
+        // scales, and what is too much in the codes, of rows 2 g and 2 g + 1
+        const uint32_t sv = shared32(stage + 2048 + l * 32 + g * 4);
+        const float s[2] = {__uint_as_float(sv << 16), __uint_as_float(sv & 0xFFFF0000u)};
+        float z[2] = {kExact ? 0.0f : 24.0f, kExact ? 0.0f : 24.0f};
+        if (ZERO) {
+          const uint32_t zv = shared32(stage + 2048 + (G::kLoads + l) * 32 + g * 4);
+          z[0] = (kExact ? -8.0f : 16.0f) + __uint_as_float(zv << 16), z[1] = (kExact ? -8.0f : 16.0f) + __uint_as_float(zv & 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (!kExact || ZERO) {
+            const uint2 v = shared64(sum_at + (l * NT + nt) * 32);
+            const float x0 = __uint_as_float(v.x), x1 = __uint_as_float(v.y);
+            acc[nt][0] = fmaf(-z[0], x0, acc[nt][0]), acc[nt][1] = fmaf(-z[0], x1, acc[nt][1]);
+            acc[nt][2] = fmaf(-z[1], x0, acc[nt][2]), acc[nt][3] = fmaf(-z[1], x1, acc[nt][3]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[nt][i] = fmaf(s[i >> 1], acc[nt][i], y[nt][i]);
         }
       }
-      float acc[NT][4];
-#pragma unroll
-      for (int w = 0; w < GW; ++w) {
-        const uint32_t u0 = q[0][w], u1 = q[1][w];
-        const uint32_t a0[4] = {unpack(u0 << 3), unpack(u1 << 3), unpack(u0 >> 1), unpack(u1 >> 1)};
-        const uint32_t a1[4] = {unpack(u0 >> 5), unpack(u1 >> 5), unpack(u0 >> 9), unpack(u1 >> 9)};
+      stage = stage + G::kStage == ring_end ? ring_at : stage + G::kStage;
+      __syncwarp();
+      chunk += G::kWarps;
+      if (chunk >= chunks) {
+        // leave this tile's part
+        float* to = mine + ((tile - base) * G::kWarps + warp) * kMmRows * tokens;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int f = 0; f < G::kTerms; ++f) {
-            const uint4 x = shared128(xw[nt] + (l * GW + w) * x_word + f * x_term);
-            if (w == 0 && f == 0)
-              mma16816_first(acc[nt], a0, x.x, x.y);
-            else
-              mma16816(acc[nt], a0, x.x, x.y);
-            mma16816(acc[nt], a1, x.z, x.w);
+          for (int i = 0; i < 2; ++i) {
+            const int col = nt * 8 + 2 * t + i;
+            if (col < tokens) *reinterpret_cast<float2*>(to + col * kMmRows + 2 * g) = make_float2(y[nt][i], y[nt][2 + i]);
+            y[nt][i] = y[nt][2 + i] = 0.0f;
           }
         }
-      }
-      // scales, and what is too much in the codes, of rows 2 g and 2 g + 1
-      const uint32_t sv = shared32(stage + 2048 + l * 32 + g * 4);
-      const float s[2] = {__uint_as_float(sv << 16), __uint_as_float(sv & 0xFFFF0000u)};
-      float z[2] = {kExact ? 0.0f : 24.0f, kExact ? 0.0f : 24.0f};
-      if (ZERO) {
-        const uint32_t zv = shared32(stage + 2048 + (G::kLoads + l) * 32 + g * 4);
-        z[0] = (kExact ? -8.0f : 16.0f) + __uint_as_float(zv << 16), z[1] = (kExact ? -8.0f : 16.0f) + __uint_as_float(zv & 0xFFFF0000u);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (!kExact || ZERO) {
-          const uint2 v = shared64(sum_at + (l * NT + nt) * 32);
-          const float x0 = __uint_as_float(v.x), x1 = __uint_as_float(v.y);
-          acc[nt][0] = fmaf(-z[0], x0, acc[nt][0]), acc[nt][1] = fmaf(-z[0], x1, acc[nt][1]);
-          acc[nt][2] = fmaf(-z[1], x0, acc[nt][2]), acc[nt][3] = fmaf(-z[1], x1, acc[nt][3]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[nt][i] = fmaf(s[i >> 1], acc[nt][i], y[nt][i]);
+        do
+          chunk -= chunks, ++tile;
+        while (chunk >= chunks);
       }
     }
-    stage = stage + G::kStage == ring_end ? ring_at : stage + G::kStage;
-    __syncwarp();
-    chunk += G::kWarps;
-    if (chunk >= chunks) {
-      // leave this tile's part
-      float* to = mine + ((tile - base) * G::kWarps + warp) * kMmRows * tokens;
+    __syncthreads();
+    // (a warp has a part of a tile if one of the tile's chunks is its turn)
+    for (int j = threadIdx.x / kMmRows; j < (stop - base) * tokens; j += G::kThreads / kMmRows) {
+      const int r = threadIdx.x % kMmRows, b = j / tokens, c = j - b * tokens, first = (base + b - cta_tile) * chunks;
+      const float* from = mine + (b * G::kWarps * tokens + c) * kMmRows + r;
+      float v = 0.0f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int col = nt * 8 + 2 * t + i;
-          if (col < tokens) *reinterpret_cast<float2*>(to + col * kMmRows + 2 * g) = make_float2(y[nt][i], y[nt][2 + i]);
-          y[nt][i] = y[nt][2 + i] = 0.0f;
-        }
-      }
-      do
-        chunk -= chunks, ++tile;
-      while (chunk >= chunks);
+      for (int w = 0; w < G::kWarps; ++w)
+        if (((w - first) & (G::kWarps - 1)) < chunks) v += from[w * kMmRows * tokens];
+      store(static_cast<int64_t>(base + b) * kMmRows + r, c, v);
     }
-  }
-  __syncthreads();
-  // (a warp has a part of a tile if one of the tile's chunks is its turn)
-  for (int j = threadIdx.x / kMmRows; j < (stop - base) * tokens; j += G::kThreads / kMmRows) {
-    const int r = threadIdx.x % kMmRows, b = j / tokens, c = j - b * tokens, first = (base + b - cta_tile) * chunks;
-    const float* from = mine + (b * G::kWarps * tokens + c) * kMmRows + r;
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < G::kWarps; ++w)
-      if (((w - first) & (G::kWarps - 1)) < chunks) v += from[w * kMmRows * tokens];
-    store(static_cast<int64_t>(base + b) * kMmRows + r, c, v);
-  }
-  if (G::kBuffers == 1) __syncthreads();
+    if (G::kBuffers == 1) __syncthreads();
   }
 }
 
@@ -732,11 +738,11 @@ cudaError_t launch_stream(const Int4Args& A, int tokens, bool tidy, int num_sms,
   return cudaGetLastError();
 }
 
-// Tokens that a pass of the kernel's form holds in shared memory.
+// Tokens, up to `most`, that a pass of the kernel's form holds in shared memory.
 template <class G>
-int64_t stream_fit(int64_t chunks) {
+int64_t stream_fit(int64_t chunks, int64_t most) {
   int64_t fit = 0;
-  while (fit < 16 && G::bytes(chunks, static_cast<int>(fit) + 1) <= kStreamSmem) ++fit;
+  while (fit < most && G::bytes(chunks, static_cast<int>(fit) + 1) <= kStreamSmem) ++fit;
   return fit;
 }
 
@@ -748,12 +754,17 @@ cudaError_t launch_form(const Int4Args& A, int num_sms, cudaStream_t st) {
   };
   const bool tidy = ordered(A.scale, A.lds_row, A.lds_group) && (!ZERO || ordered(A.zero, A.ldz_row, A.ldz_group));
   if (A.n <= (1 << 30)) {
-    // one pass or two of up to 8 tokens, or of up to 16
+    // One pass or two of up to 8 tokens, or of up to 16.  Up to four of at least 8 where the weights
+    // are large: 48 rows, 2^24 codes in 4096 x 4096, take 31 us instead of the other kernel's 38, in 65536 x 2048
+    // 143 instead of 380; 4096 x 1024 19 instead of 15; four passes of 4 (16 rows, 4096 x 16384) 68 instead of 58.
+    constexpr int64_t kLarge = 1 << 23;
     const int64_t chunks = lm_div_up(A.k, kStreamChunk), rows = A.rows;
-    const int64_t few = stream_fit<Stream<X, 1, GW, ZERO>>(chunks), more = stream_fit<Stream<X, 2, GW, ZERO>>(chunks);
-    const auto pass = [rows](int64_t fit) { return static_cast<int>(fit < rows ? lm_div_up(rows, 2) : rows); };
-    if (rows <= 8 && 2 * few >= rows) return launch_stream<X, 1, GW, ZERO>(A, pass(few), tidy, num_sms, st);
-    if (rows <= 32 && 2 * more >= rows) return launch_stream<X, 2, GW, ZERO>(A, pass(more < 16 ? more : 16), tidy, num_sms, st);
+    const int64_t few = stream_fit<Stream<X, 1, GW, ZERO>>(chunks, 8), more = stream_fit<Stream<X, 2, GW, ZERO>>(chunks, 16);
+    if (rows <= 8 && 2 * few >= rows)
+      return launch_stream<X, 1, GW, ZERO>(A, static_cast<int>(few < rows ? lm_div_up(rows, 2) : rows), tidy, num_sms, st);
+    const int64_t passes = more > 0 ? lm_div_up(rows, more) : 5;
+    if (passes <= (more >= 8 && A.n * A.k >= kLarge ? 4 : 2))
+      return launch_stream<X, 2, GW, ZERO>(A, static_cast<int>(lm_div_up(rows, passes)), tidy, num_sms, st);
   }
   const dim3 grid(static_cast<unsigned>(lm_div_up(A.n, kMmRows)), static_cast<unsigned>(lm_div_up(A.rows, 32)));
   k_int4_matmul<X, 4, GW, ZERO><<<grid, kMmThreads, 0, st>>>(A);

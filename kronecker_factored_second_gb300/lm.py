@@ -263,7 +263,8 @@ def token_logprobs_grad(logits: torch.Tensor, ids: torch.Tensor, result: TokenLo
 class Int4Tensor:
     """A weight (rows x cols) in 4 bits: codes 0..15, two in a byte with the even column in the low half (`data`, uint8,
     rows x ceil(cols / 2)), and a bf16 scale for each `group` consecutive columns of a row (32, 64 or a multiple of 128).
-    (code - zero) * scale stands for the value; `zero` is bf16 of scale's shape, or None for 8.
+    (code - zero) * scale stands for the value; `zero` is bf16 of scale's shape, or None for 8.  scale and zero may be
+    laid in any way; group by group (scale.t() contiguous, rows a multiple of 8), as `int4_quantize` does, is read fastest.
 
     Codes from elsewhere are taken as they are; `int4_matmul` needs rows of data that start on 16-byte boundaries."""
     data: torch.Tensor

@@ -487,6 +487,19 @@ def test_int4_matmul(group, zero, rows, n, k):
     _check_int4(x, w, out, BF16)
 
 
+@pytest.mark.parametrize("rows", [31, 33, 48, 49, 64, 65])
+@pytest.mark.parametrize("n,k,group,zero", [(4099, 2055, 32, True), (2051, 4104, 128, False), (1040, 8111, 64, True)])
+def test_int4_matmul_of_large_weights_by_several_passes(rows, n, k, group, zero):
+    g = gen(rows + n)
+    w = _weight(g, n, k, group, zero)
+    for dtype in (BF16, F32):
+        x = pitched(randn(g, rows, k, dtype=dtype), k + 1, 1)
+        out = torch.full((rows + 1, n), 7.0, device="cuda")
+        lm.int4_matmul(x, w, out=out[:rows])
+        _check_int4(x, w, out[:rows], F32)
+        assert (out[rows] == 7).all()
+
+
 def test_int4_matmul_many_and_no_rows():
     g = gen(1)
     w = _weight(g, 100, 256, 64, True)
