@@ -481,7 +481,10 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        capturing = torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
         for g in self.param_groups:
+            if capturing and not g["capturable"]:
+                raise RuntimeError("okls: a captured step needs capturable=True")
             # parameters whose steps have one number go together
             lists = {}
             for p in g["params"]:
@@ -491,6 +494,8 @@ class AdamW(torch.optim.Optimizer):
                     continue
                 st = self.state[p]
                 if not st:
+                    if capturing:
+                        raise RuntimeError("okls: run a step before one is captured, which makes the states")
                     st.update(self._new_state(p, g))
                     if g["capturable"]:
                         st["step"] = lists.setdefault(("new", p.device), torch.zeros(1, dtype=torch.int64, device=p.device))

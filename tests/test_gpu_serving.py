@@ -382,6 +382,28 @@ def test_adamw_optimizer_captured():
         close(p, q, 8 * U * (q.abs() + 1e-2), "captured")
 
 
+def test_adamw_optimizer_refuses_a_capture_that_would_not_count():
+    g = gen(9)
+    p = randn(g, 200).requires_grad_()
+    p.grad = randn(g, 200)
+    host, new = okls.AdamW([p], lr=1e-2), okls.AdamW([p], lr=1e-2, capturable=True)
+    before = p.detach().clone()
+    host.step()
+    moved = p.detach().clone()
+    other, graph = torch.zeros(4, device="cuda"), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        other.add_(1)
+        with pytest.raises(RuntimeError, match="capturable=True"):
+            host.step()  # each replay would be the same step
+        with pytest.raises(RuntimeError, match="before one is captured"):
+            new.step()  # each replay would clear the states
+    graph.replay()
+    assert torch.equal(other, torch.ones(4, device="cuda"))
+    assert torch.equal(p.detach(), moved) and not torch.equal(moved, before)
+    new.step()  # and takes part once they are there
+    assert new.state[p]["step"].item() == 1 and host.state[p]["step"] == 1
+
+
 # -------------------------------------------------------------------- 4 bits
 def _int4_ref(x, group, sym):
     """Codes, scale and zero point by the definition; every step in fp32 is one rounding."""
@@ -511,6 +533,19 @@ def test_int4_matmul_many_and_no_rows():
     assert lm.int4_matmul(x[:, :0], e).abs().max().item() == 0
     none = lm.Int4Tensor(w.data[:0], w.scale[:0], 256, 64)
     assert lm.int4_matmul(x, none).shape == (500, 0)
+
+
+def test_int4_matmul_refuses_an_output_over_its_input():
+    g = gen(9)
+    w = _weight(g, 64, 64, 32, False)
+    buf = randn(g, 6, 64)
+    for x, out in ((buf[:4], buf[:4]), (buf[:4], buf[2:]), (buf[1:5, :], buf[1:5])):
+        with pytest.raises((ValueError, L.OklsError), match="share"):
+            lm.int4_matmul(x, w, out=out)
+    halves = randn(g, 4, 128)  # side by side: no element is shared
+    x = halves[:, :64]
+    _check_int4(x, w, lm.int4_matmul(x, w, out=halves[:, 64:]), F32)
+    _check_int4(buf[:2], w, lm.int4_matmul(buf[:2], w, out=buf[2:4]), F32)
 
 
 def test_int4_matmul_of_its_own_quantisation():
