@@ -1177,7 +1177,8 @@ cudaError_t launch_sample(const SampleArgs& args, int dtype, int num_sms, cudaSt
   while ((int64_t(1) << A.shift) < A.vocab) ++A.shift;
   // more CTAs for a row while the SMs last and a CTA keeps 32768 values: below
   // that the cluster's barriers cost more (one row of 32000 with all filters: 18 us in
-  // one CTA, 23 in eight; of 128256 with top-p: 94 in one, 45 in four, 41 in eight)
+  // one CTA, 23 in eight; of 128256 with top-p: 94 in one, 45 in four, 41 in eight).
+  // Many rows, 1024 of 131072: 234 us with a CTA for a row, 270 with two, 507 with four.
   int size = 1;
   while (size < 8 && A.rows * size * 2 <= num_sms && A.vocab >= size * 32768) size *= 2;
   // (what a CTA's segments hold)
