@@ -162,7 +162,8 @@ __device__ __forceinline__ float round_code(float y, uint32_t random20, Doubt& d
   return __uint_as_float(b & 0xFFF00000u);
 }
 
-// fp32's root of v >= 2^-126, to its last bit but for one in some thousands; 0 for 0.
+// fp32's root of a normal v, to its last bit but for one in some thousands; 0 for 0: a Newton
+// step on the hardware's estimate of the reciprocal root.
 __device__ __forceinline__ float root_of(float v) {
   float y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(v, 1.1754944e-38f)));
@@ -203,6 +204,87 @@ __device__ __forceinline__ void state_scales(uint32_t amax_bits, float* mul, flo
   if (amax_bits >= 0x7F800000u) *scale = CUDART_NAN_F;
 }
 
+// The moments of one element after the step, each product and sum rounded (what a code is must
+// not hang on how a compiler joins them).  The second one's products are rounded up: off by
+// one unit instead of half of one, but a product that is not 0 does not become 0, so a root of 0 is the
+// formula's, and a root below 2^-62 tells of a v that may have left the normal numbers.
+__device__ __forceinline__ float second8(const AdamwScalars& s, float r, float g) {
+  return __fadd_rn(__fmul_ru(s.beta2, __fmul_ru(r, r)), __fmul_ru(__fmul_ru(s.rest2, fabsf(g)), fabsf(g)));
+}
+__device__ __forceinline__ float first8(const AdamwScalars& s, float m, float g) {
+  return __fadd_rn(__fmul_rn(s.beta1, m), __fmul_rn(s.rest1, g));
+}
+__device__ __forceinline__ float update8(const AdamwScalars& s, float p, float m, float r) {
+  return fmaf(-s.rate * m, reciprocal(fmaf(r, s.root, s.eps)), fmaf(-s.decay, p, p));
+}
+
+// Squares leave fp32's range long before the moments do (at beta2 = 0.999 those of gradients below
+// 2^-58 or past 2^69).  A warp that meets one goes through its 32 x 16 elements here, one by one and
+// twice instead of holding them, which the common way is spared.  Where v is no normal number, the
+// root of beta2 r^2 + rest2 g^2 is formed of r and g that a power of two brings into fp32's middle.
+constexpr float kNormal = 0x1p-126f;
+constexpr float kFarRoot = 0x1p-62f;
+constexpr uint32_t kWideRoots = 0x6C800000u;  // 2^90: kFarRoot times 448 / 2^90 is a number, past it it may be 0
+__device__ __forceinline__ bool root_far(const AdamwScalars& s, float r, float g, float& root) {
+  const float v = second8(s, r, g);
+  root = root_of(v);
+  if ((v >= kNormal && v < CUDART_INF_F) || (r == 0.0f && g == 0.0f)) return false;
+  const bool large = v > 1.0f;
+  const float up = large ? 0x1p-65f : 0x1p120f, down = large ? 0x1p65f : 0x1p-120f;
+  r *= up, g *= up;
+  root = __fsqrt_rn(s.beta2 * r * r + s.rest2 * g * g) * down;
+  return true;
+}
+template <class P, class G>
+__device__ __forceinline__ void adamw8_far(const AdamwEntry& e, const AdamwScalars& s, int64_t i, uint32_t low) {
+  const int count = static_cast<int>(max(int64_t(0), min(e.count - i, int64_t(16))));
+  const int64_t group = i / kFp8Group;
+  const bool some = group * kFp8Group < e.count;
+  P* p = static_cast<P*>(e.p) + i;
+  const G* g = static_cast<const G*>(e.g) + i;
+  __nv_fp8_e4m3 *mq = static_cast<__nv_fp8_e4m3*>(e.m) + i, *vq = static_cast<__nv_fp8_e4m3*>(e.v) + i;
+  const float ms = some ? e.ms[group] : 0.0f, vs = some ? e.vs[group] : 0.0f;
+  const auto moments = [&](int j, float& m, float& r) {
+    const float gj = to_f32(g[j]);
+    m = first8(s, __fmul_rn(static_cast<float>(mq[j]), ms), gj);
+    return root_far(s, __fmul_rn(static_cast<float>(vq[j]), vs), gj, r);
+  };
+  float top_m = 0.0f, top_r = 0.0f;
+#pragma unroll 1
+  for (int j = 0; j < count; ++j) {
+    float m, r;
+    const bool far = moments(j, m, r);
+    const float pj = to_f32(p[j]);
+    float a = update8(s, pj, m, r);
+    if (far) {  // (a quarter of both sides where the sum could pass fp32's end)
+      const float part = r > 1.0f ? 0.25f : 1.0f;
+      a = fmaf(-s.rate, __fdiv_rn(part * m, fmaf(part * r, s.root, part * s.eps)), fmaf(-s.decay, pj, pj));
+    }
+    p[j] = from_f32<P>(a);
+    top_m = max_mag(top_m, m), top_r = max_mag(top_r, r);
+  }
+  uint32_t am = __float_as_uint(top_m), av = __float_as_uint(top_r);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+    av = max(av, __shfl_xor_sync(0xffffffffu, av, o));
+  }
+  float mmul, mscale, vmul, vscale;
+  state_scales(am, &mmul, &mscale);
+  state_scales(av, &vmul, &vscale);
+  const float mrest = mul_rest(am, mmul), vrest = mul_rest(av, vmul);
+#pragma unroll 1
+  for (int j = 0; j < count; ++j) {
+    float m, r;
+    moments(j, m, r);
+    const uint2 w = philox(static_cast<uint32_t>((i + j) >> 1), low, s.key);
+    const uint32_t random = (j & 1) ? w.y : w.x;
+    mq[j].__x = static_cast<uint8_t>(e4m3x2(copysignf(round_exact(fabsf(m), mmul, mrest, random & 0xFFFFu, false), m), 0.0f));
+    vq[j].__x = static_cast<uint8_t>(e4m3x2(round_exact(r, vmul, vrest, random >> 16, true), 0.0f));
+  }
+  if (some && (threadIdx.x & 7) == 0) e.ms[group] = mscale, e.vs[group] = vscale;
+}
+
 // 8 lanes take a group, 16 consecutive elements each, which are held in
 // registers between the update and the rounding.
 constexpr int kOwn8 = 16;
@@ -228,6 +310,8 @@ __global__ void __launch_bounds__(kAdamThreads, 4) k_adamw8(const __grid_constan
     uint8_t *mq = static_cast<uint8_t*>(e.m) + i, *vq = static_cast<uint8_t*>(e.v) + i;
 
     float a[kOwn8], m[kOwn8], r[kOwn8];
+    float top_r = 0.0f;  // (elements past the end are zeros: they change no maximum)
+    bool far;
     {
       float b[kOwn8];
       uint4 cm = make_uint4(0, 0, 0, 0), cv = cm;
@@ -261,14 +345,20 @@ __global__ void __launch_bounds__(kAdamThreads, 4) k_adamw8(const __grid_constan
       const uint32_t wm[4] = {cm.x, cm.y, cm.z, cm.w}, wv[4] = {cv.x, cv.y, cv.z, cv.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) codes_to_f32(wm[j], m + 4 * j), codes_to_f32(wv[j], r + 4 * j);
+      uint32_t least = ~0u;  // bits, less one, of the smallest root that is not 0
 #pragma unroll
       for (int j = 0; j < kOwn8; ++j) {
-        // (each product and sum rounded: what a code is must not hang on how a compiler joins them)
-        const float rv = __fmul_rn(r[j], vs), gv = __fmul_rn(__fmul_rn(s.rest2, b[j]), b[j]);
-        m[j] = __fadd_rn(__fmul_rn(s.beta1, __fmul_rn(m[j], ms)), __fmul_rn(s.rest1, b[j]));
-        r[j] = root_of(__fadd_rn(__fmul_rn(s.beta2, __fmul_rn(rv, rv)), gv));
-        a[j] = fmaf(-s.rate * m[j], reciprocal(fmaf(r[j], s.root, s.eps)), fmaf(-s.decay, a[j], a[j]));
+        m[j] = first8(s, __fmul_rn(m[j], ms), b[j]);
+        r[j] = root_of(second8(s, __fmul_rn(r[j], vs), b[j]));
+        a[j] = update8(s, a[j], m[j], r[j]);
+        least = __viaddmin_u32(__float_as_uint(r[j]), 0xFFFFFFFFu, least);
+        top_r = max_mag(top_r, r[j]);
       }
+      far = least < __float_as_uint(kFarRoot) - 1u || !(top_r < CUDART_INF_F);
+    }
+    if (__any_sync(0xffffffffu, far)) {
+      adamw8_far<P, G>(e, s, i, low);
+      continue;
     }
     if (vec) {
       Pack<P> p0, p1;
@@ -283,10 +373,9 @@ __global__ void __launch_bounds__(kAdamThreads, 4) k_adamw8(const __grid_constan
         if (j < left) p[j] = from_f32<P>(a[j]);
     }
 
-    // (elements past the end are zeros: they change no maximum)
-    float top_m = 0.0f, top_r = 0.0f;
+    float top_m = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kOwn8; ++j) top_m = max_mag(top_m, m[j]), top_r = max_mag(top_r, r[j]);
+    for (int j = 0; j < kOwn8; ++j) top_m = max_mag(top_m, m[j]);
     uint32_t am = __float_as_uint(top_m), av = __float_as_uint(top_r);
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) {
@@ -312,7 +401,8 @@ __global__ void __launch_bounds__(kAdamThreads, 4) k_adamw8(const __grid_constan
       wm[j / 4] = e4m3x2(qm[0], qm[1]) | (e4m3x2(qm[2], qm[3]) << 16);
       wv[j / 4] = e4m3x2(qv[0], qv[1]) | (e4m3x2(qv[2], qv[3]) << 16);
     }
-    if (doubt.any()) {
+    // (a root whose share of the group's largest is below fp32's range is no zero, either)
+    if (doubt.any() || av >= kWideRoots) {
       const float mrest = mul_rest(am, mmul), vrest = mul_rest(av, vmul);
 #pragma unroll
       for (int j = 0; j < kOwn8; ++j) {

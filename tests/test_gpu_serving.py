@@ -224,6 +224,56 @@ def test_adamw_8_groups_that_are_not_finite():
     assert torch.equal(p.isnan(), only)
 
 
+@pytest.mark.parametrize("pd,gd", [(F32, F32), (BF16, BF16)])
+@pytest.mark.parametrize("eps", [0.0, 1e-8])
+@pytest.mark.parametrize("low,high", [(-21, -17), (-28, -17), (-29, -1), (18, 24), (30, 38), (-20, 38)])
+def test_adamw_8_moments_whose_squares_leave_fp32(pd, gd, eps, low, high):
+    """Gradients of 10^low to 10^high, each group's and each element's in a place of its own: the moments lie in fp32 where
+    their squares do not.  A root formed in fp32's middle is off by as much as any other: 8 u of itself, as above."""
+    g = gen(30 + high - low)
+    h, n = {**HYPER, "eps": eps}, 1000
+    ps, state = [randn(g, n, dtype=pd)], [[torch.zeros(n, device="cuda").to(E4M3)] for _ in range(2)]
+    scales = [[torch.zeros(-(-n // 128), device="cuda")] for _ in range(2)]
+    value = lambda k: state[k][0].double() * scales[k][0].double().repeat_interleave(128)[:n]  # noqa: E731
+    for t in (1, 2, 3):
+        at = torch.rand(n, generator=g, device="cuda")
+        at[:256] = at[:256].view(2, 128)[:, :1].expand(2, 128).reshape(-1)  # (two groups of one size each)
+        gr = (torch.pow(10.0, (low + (high - low) * at).double()) * torch.sign(randn(g, n)).double()).to(gd)
+        gr[500:520] = 0 if eps and t == 1 else gr[500:520]
+        old = (ps[0].clone(), value(0), value(1).square())
+        okls.adamw_step(ps, [gr], state[0], state[1], step=t, avg_scales=scales[0], sq_scales=scales[1], seed=5, **h)
+        m, v, mag = _check_update(ps[0], *old[:1], gr, *old[1:], t, h, fast=True)
+        dm, dv = _philox(n, 0, t, 5)
+        _check_codes(state[0][0], scales[0][0], m, 5 * U * mag, dm, False)
+        _check_codes(state[1][0], scales[1][0], v.sqrt(), 8 * U * v.sqrt(), dv, True)
+        zero = v == 0
+        assert torch.equal(state[1][0].float() == 0, zero), "a root that is not zero became zero"
+        assert torch.isfinite(ps[0]).all() and torch.isfinite(scales[1][0]).all()
+
+
+def test_adamw_8_ordinary_values_beside_far_ones():
+    """Tensors with and without a far value in the same warp: the others' parameters and codes keep their bits."""
+    g = gen(31)
+    n = 4096
+    p, gr = randn(g, n), randn(g, n, std=1e-2)
+    runs = []
+    for far in (False, True):
+        q, d = p.clone(), gr.clone()
+        if far:
+            d[1030], d[3000] = 1e-21, 1e21
+        state = [torch.zeros(n, device="cuda").to(E4M3) for _ in range(2)]
+        scales = [torch.zeros(n // 128, device="cuda") for _ in range(2)]
+        for t in (1, 2):
+            okls.adamw_step([q], [d], state[:1], state[1:], step=t, avg_scales=scales[:1], sq_scales=scales[1:], **HYPER)
+        runs.append([q, state[0].float(), state[1].float(), *scales])
+    same = torch.ones(n, dtype=torch.bool, device="cuda")
+    same[1030] = False
+    same[3000 // 128 * 128:][:128] = False  # (its group's scale is another)
+    for x, y in zip(*(r[:3] for r in runs)):
+        assert torch.equal(x[same], y[same])
+    assert torch.isfinite(runs[1][0]).all() and runs[1][0][3000] != runs[0][0][3000]
+
+
 def _adamw_set(seed, n=6, bits=32, pd=F32):
     g = gen(seed)
     sizes = [300 + 77 * i for i in range(n)]
