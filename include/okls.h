@@ -778,7 +778,8 @@ okls_status okls_int4_quantize(const void *x, int32_t dtype, int64_t ldx,
  * two bits; fp32 x: of c - 8 and 8 - zero.  Values of x beyond 2^122 may overflow
  * there.)  Any number of rows is taken, but the way through the kernel is made
  * for tokens that are generated, up to some 64 (rows <= 524280).  Rows of codes start
- * on 16-byte boundaries (OKLS_ERR_UNSUPPORTED otherwise).  An infinity in x
+ * on 16-byte boundaries (OKLS_ERR_UNSUPPORTED otherwise).  An out that has an
+ * element in common with x, codes, scale or zero is refused.  An infinity in x
  * gives NaN or an infinity, a NaN gives NaN, in that row of out.
  */
 okls_status okls_int4_matmul(const void *x, int32_t x_dtype, int64_t ldx,

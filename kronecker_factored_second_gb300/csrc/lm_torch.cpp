@@ -5,7 +5,6 @@
 //
 // Wrong tensors raise ValueError; what the C entry refuses raises OklsError.
 #include <ATen/ATen.h>
-#include <ATen/MemoryOverlap.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/GradMode.h>
 #include <c10/core/InferenceMode.h>
@@ -590,9 +589,6 @@ Tensor int4_matmul(const Tensor& x, const Tensor& codes, const Tensor& scale, co
   const bool given = out.has_value();
   if (given) {
     o = plain_matrix(*out, "out", m.rows, n), writable(*out, "out");
-    const auto shared = at::get_overlap_status(*out, x);
-    REFUSE((o.p == m.p && o.p) || shared == at::MemOverlapStatus::Full || shared == at::MemOverlapStatus::Partial,
-           "out must not share memory with x");
   }
   Call c(x);
   if (!out) {

@@ -4,6 +4,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <utility>
 
 #include "okls_host.h"
 #include "okls_internal.h"
@@ -82,6 +83,47 @@ __device__ uint32_t g_taken[kTaken];
 // Reads and clears in one step: bits that a launch on another stream raises
 // meanwhile are read now or stay for the next read.
 __global__ void k_status_take(uint32_t* status, uint32_t* taken) { *taken = atomicExch(status, 0u); }
+
+// Runs of `width` bytes, `pitch` apart in the order of their addresses.
+struct Runs {
+  uintptr_t p;
+  int64_t count, width, pitch;
+};
+Runs runs_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int elem) {
+  return {reinterpret_cast<uintptr_t>(p), rows, cols * elem, ld * elem};
+}
+// Values of `elem` bytes with a pitch in both directions: runs along the one whose
+// neighbours are neighbours, or all that lies between the first and the last.
+Runs runs_of_values(const void* p, int64_t rows, int64_t cols, int64_t ld_row, int64_t ld_col, int elem) {
+  if ((ld_col == 1 || cols == 1) && (ld_row >= cols || rows == 1)) return runs_of(p, rows, cols, ld_row, elem);
+  if ((ld_row == 1 || rows == 1) && (ld_col >= rows || cols == 1)) return runs_of(p, cols, rows, ld_col, elem);
+  return runs_of(p, 1, (rows - 1) * ld_row + (cols - 1) * ld_col + 1, 0, elem);
+}
+
+// Whether two sets of runs have a byte in common.
+bool share_memory(Runs a, Runs b) {
+  if (!a.p || !b.p || a.count <= 0 || b.count <= 0 || a.width <= 0 || b.width <= 0) return false;
+  if (b.p < a.p) std::swap(a, b);
+  if (a.p + (a.count - 1) * a.pitch + a.width <= b.p) return false;
+  if (a.count > 1 && b.count > 1 && a.pitch == b.pitch) {
+    const int64_t off = static_cast<int64_t>(b.p - a.p) % a.pitch;
+    return off < a.width || off + b.width > a.pitch;
+  }
+  const auto next = [](const Runs& r, int64_t i, uintptr_t to) {  // the last run that begins at or before `to`, if that is behind run i
+    const int64_t at = r.count > 1 ? static_cast<int64_t>(to - r.p) / r.pitch : i + 1;
+    return at > i ? at : i + 1;
+  };
+  for (int64_t i = 0, j = 0; i < a.count && j < b.count;) {
+    const uintptr_t pa = a.p + i * a.pitch, pb = b.p + j * b.pitch;
+    if (pa + a.width <= pb)
+      i = next(a, i, pb);
+    else if (pb + b.width <= pa)
+      j = next(b, j, pa);
+    else
+      return true;
+  }
+  return false;
+}
 
 constexpr int64_t kMaxSide = (int64_t(1) << 31) - 2;
 constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
@@ -550,6 +592,14 @@ okls_status okls_int4_matmul(const void* x, int32_t x_dtype, int64_t ldx, const 
   if (k > 0 && (reinterpret_cast<uintptr_t>(codes) % 16 || (n > 1 && ldq % 16)))
     return host_fail(OKLS_ERR_UNSUPPORTED, "%s: codes need 16-byte aligned rows (ldq %lld)", op, static_cast<ll>(ldq));
   if (rows > 65535 * int64_t(8)) return host_fail(OKLS_ERR_UNSUPPORTED, "%s: more than 524280 rows", op);
+  // (blocks store out while others still read)
+  const Runs out_runs = runs_of(out, rows, n, ldo, elem_size(out_dtype));
+  const int64_t groups = lm_div_up(k, group);
+  if (share_memory(out_runs, runs_of(x, rows, k, ldx, elem_size(x_dtype)))) return bad(op, "out must not share memory with x");
+  if (share_memory(out_runs, runs_of(codes, n, lm_div_up(k, 2), ldq, 1)) ||
+      (k > 0 && (share_memory(out_runs, runs_of_values(scale, n, groups, lds_row, lds_group, 2)) ||
+                 share_memory(out_runs, runs_of_values(zero, n, groups, ldz_row, ldz_group, 2)))))
+    return bad(op, "out must not share memory with the weight");
   int sms = 0;
   LM_TRY(host_device_sms(&sms));
   if (k == 0) {

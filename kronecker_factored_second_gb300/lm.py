@@ -313,7 +313,8 @@ def int4_matmul(x: torch.Tensor, w: Int4Tensor, *, out_dtype: torch.dtype | None
     """x w^T in fp32 or bf16 (default: x's type) for the tokens of a generation
     step: x (..., columns of w) fp32 or bf16, up to some 64 rows of it.  More
     rows are right but not fast; a prompt is `fp8_matmul`'s.  With `accumulate`
-    it is added to `out` (rows x rows of w).  No gradient flows through it."""
+    it is added to `out` (rows x rows of w), which has no element in common with x
+    and w.  No gradient flows through it."""
     if stream is not None:
         with _on(stream, x, w.data, w.scale, w.zero, out):
             return int4_matmul(x, w, out_dtype=out_dtype, out=out, accumulate=accumulate)

@@ -598,6 +598,26 @@ def test_int4_matmul_refuses_an_output_over_its_input():
     _check_int4(buf[:2], w, lm.int4_matmul(buf[:2], w, out=buf[2:4]), F32)
 
 
+def test_int4_matmul_refuses_an_output_among_its_input():
+    """Views of one buffer with columns in common, and outputs in the weight; columns beside each other are taken."""
+    g = gen(10)
+    w = _weight(g, 64, 64, 32, True)
+    buf = randn(g, 4, 256)
+    x = buf[:, :64]
+    for out in (buf[:, 32:96], buf[:, 63:127], buf.view(-1)[60:60 + 4 * 128].view(4, 128)[:, :64], buf.view(BF16)[:, 127:191]):
+        with pytest.raises((ValueError, L.OklsError), match="share"):
+            lm.int4_matmul(x, w, out=out)
+    scale = torch.zeros(64 * 64, device="cuda", dtype=BF16)
+    inside = lm.Int4Tensor(w.data, scale.view(64, 64)[:2].t(), 64, 32)
+    with pytest.raises((ValueError, L.OklsError), match="share"):
+        lm.int4_matmul(x, inside, out=scale.view(F32)[32:32 + 256].view(4, 64))
+    left = x.clone()
+    for out in (buf[:, 64:128], buf[:, 192:]):
+        _check_int4(left, w, lm.int4_matmul(x, w, out=out), F32)
+        assert torch.equal(x, left)
+    _check_int4(left, w, lm.int4_matmul(x, w, out=buf.view(BF16)[:, 128:192]), BF16)
+
+
 def test_int4_matmul_of_its_own_quantisation():
     """fp32 activations reach the products with all their digits, also next to each other's extremes."""
     g = gen(2)

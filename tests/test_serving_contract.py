@@ -74,6 +74,40 @@ def test_int4_arguments(lib):
         assert lib.okls_int4_matmul(*[0 if j == i else v for j, v in enumerate(ok)]) == L.OKLS_OK
 
 
+def _bytes(p, rows, cols, ld, size):
+    return {p + (i * ld + j) * size + b for i in range(rows) for j in range(cols) for b in range(size)}
+
+
+def test_int4_refuses_an_output_over_what_it_reads(lib):
+    """Refused exactly where a byte is shared, for pitches alike and not: an output between the rows of x is none of them."""
+    rows, n, k = 3, 6, 32
+    far = [1 << 20, 2 << 20, 3 << 20]  # codes, scale, zero
+
+    def call(x, ldx, out, ldo, od=0, codes=far[0], scale=far[1], ls=(1, 8), zero=far[2], lz=(1, 8), r=rows):
+        return lib.okls_int4_matmul(x, 0, ldx, codes, 16, scale, *ls, zero, *lz, 32, r, n, k, out, od, ldo, 0, None)
+    seen = {True: 0, False: 0}
+    for od in (0, 1):
+        size = 2 if od else 4
+        for ldx in (32, 37, 64):
+            read = _bytes(P, rows, k, ldx, 4)
+            for ldo in (6, 13, 32 * 4 // size, 37 * 4 // size, 64 * 4 // size):
+                for at in list(range(-80, 80, 4)) + list(range(80, 1024, 44)):
+                    shared = bool(read & _bytes(P + at, rows, n, ldo, size))
+                    if not shared and torch.cuda.is_available():
+                        continue  # it would run
+                    seen[shared] += 1
+                    code = call(P, ldx, P + at, ldo, od)
+                    assert (code == BAD and "share" in L.last_error()) == shared, (od, ldx, ldo, at)
+    assert seen[True] > 500 and (seen[False] > 200 or torch.cuda.is_available())
+    for at in (far[0] + 90, far[0] - 68, far[1] + 8, far[2]):  # 6 rows of 16 bytes of codes, 6 scales, 6 zero points
+        assert call(P, 64, at // 4 * 4, 6) == BAD and "weight" in L.last_error()
+    assert call(P, 64, far[1] + 100, 6, ls=(40, 1)) == BAD and call(P, 64, far[2] + 80, 6, lz=(9, 7)) == BAD
+    if not torch.cuda.is_available():
+        for at in (far[0] + 96, far[0] - 72, far[1] + 12):
+            assert call(P, 64, at, 6, r=3) != BAD
+        assert call(P, 64, far[1] + 8, 6, ls=(40, 1), r=1) != BAD and call(P, 64, far[2] + 12, 6, zero=None) != BAD
+
+
 def test_sample_arguments(lib):
     def settings(**kw):
         return ctypes.byref(L.okls_sample_settings(**{**dict(temperature=1.0, top_p=1.0), **kw}))
