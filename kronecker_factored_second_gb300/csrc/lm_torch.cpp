@@ -401,10 +401,11 @@ class TensorList {
   py::object seq_;
 };
 
-// Memory that a step writes: [begin, end) of each tensor, kind after kind.
+// Memory of a step, [begin, end) of each tensor: what it writes, kind after kind, and the gradients, which it
+// only reads (and which may be one and the same).
 typedef std::pair<uintptr_t, uintptr_t> Range;
 
-void refuse_overlaps(std::vector<Range>* kinds, int count) {
+void refuse_overlaps(std::vector<Range>* kinds, int count, const std::vector<Range>& grads) {
   // usual are a few buffers, each of which its tensors go through upwards
   bool plain = true;
   std::vector<Range> all;
@@ -418,25 +419,36 @@ void refuse_overlaps(std::vector<Range>* kinds, int count) {
     for (int i = 0; i < used; ++i) plain = plain && (h.second <= hull[i].first || hull[i].second <= h.first);
     hull[used++] = h;
   }
-  if (plain) return;
-  for (int k = 0; k < count; ++k) all.insert(all.end(), kinds[k].begin(), kinds[k].end());
-  std::sort(all.begin(), all.end());
-  for (size_t i = 1; i < all.size(); ++i)
-    REFUSE(all[i].first < all[i - 1].second, "a parameter or a state appears twice, or two of them overlap");
+  if (!plain) {
+    for (int k = 0; k < count; ++k) all.insert(all.end(), kinds[k].begin(), kinds[k].end());
+    std::sort(all.begin(), all.end());
+    for (size_t i = 1; i < all.size(); ++i)
+      REFUSE(all[i].first < all[i - 1].second, "a parameter or a state appears twice, or two of them overlap");
+    kinds = &all, count = 1;
+  }
+  Range read = {UINTPTR_MAX, 0};
+  for (const Range& g : grads) read = {std::min(read.first, g.first), std::max(read.second, g.second)};
+  for (int k = 0; k < count; ++k) {
+    const std::vector<Range>& r = kinds[k];
+    if (r.empty() || read.second <= r.front().first || r.back().second <= read.first) continue;
+    for (const Range& g : grads) {
+      // the first tensor that ends behind the gradient's begin
+      const auto at = std::upper_bound(r.begin(), r.end(), g.first, [](uintptr_t p, const Range& t) { return p < t.second; });
+      REFUSE(at != r.end() && at->first < g.second, "a gradient overlaps a parameter or a state");
+    }
+  }
 }
 
 // A tensor of a step, as the kernels see it: `count` elements in a row.
-void* flat(const Tensor& t, const char* name, c10::Device device, int64_t count, std::vector<Range>* ranges) {
+void* flat(const Tensor& t, const char* name, c10::Device device, int64_t count, std::vector<Range>& ranges, bool writes = true) {
   const c10::TensorImpl* impl = t.unsafeGetTensorImpl();
   REFUSE(!impl->is_cuda(), name, " must be on a CUDA device");
   REFUSE(impl->device() != device, "tensors on ", device, " and ", impl->device());
   REFUSE(!impl->is_contiguous(), name, " must be contiguous");
   REFUSE(impl->numel() != count, name, " must hold ", count, " values, not ", impl->numel());
   void* p = const_cast<void*>(impl->data());
-  if (ranges) {
-    if (t.is_inference()) writable(t, name);
-    if (count) ranges->emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + count * impl->itemsize());
-  }
+  if (writes && t.is_inference()) writable(t, name);
+  if (count) ranges.emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + count * impl->itemsize());
   return p;
 }
 
@@ -482,7 +494,9 @@ void adamw_step(const py::object& params, const py::object& grads, const py::obj
   // one call of the C entry for each pair of types
   std::vector<okls_adamw_tensor> lists[4];
   std::vector<Range> ranges[5];
+  std::vector<Range> read;
   for (auto& r : ranges) r.reserve(num);
+  read.reserve(num);
   const c10::Device device = first.device();
   for (auto& l : lists) l.reserve(lists == &l ? num : 0);
   for (int64_t i = 0; i < num; ++i) {
@@ -493,21 +507,21 @@ void adamw_step(const py::object& params, const py::object& grads, const py::obj
     const at::ScalarType sd = bits8 ? at::kFloat8_e4m3fn : at::kFloat;
     REFUSE(m.scalar_type() != sd || v.scalar_type() != sd, "exp_avgs and exp_avg_sqs must be ", sd,
            bits8 ? " where scales are given" : "");
-    e.param = flat(p, "a parameter", device, n, &ranges[0]);
-    e.grad = flat(g, "a gradient", device, n, nullptr);
-    e.exp_avg = flat(m, "exp_avg", device, n, &ranges[1]);
-    e.exp_avg_sq = flat(v, "exp_avg_sq", device, n, &ranges[2]);
+    e.param = flat(p, "a parameter", device, n, ranges[0]);
+    e.grad = flat(g, "a gradient", device, n, read, false);
+    e.exp_avg = flat(m, "exp_avg", device, n, ranges[1]);
+    e.exp_avg_sq = flat(v, "exp_avg_sq", device, n, ranges[2]);
     if (bits8) {
       const Tensor &ms = (*MS)[i], &vs = (*VS)[i];
       REFUSE(ms.scalar_type() != at::kFloat || vs.scalar_type() != at::kFloat, "scales must be fp32");
       const int64_t groups = (n + kGroup - 1) / kGroup;
-      e.avg_scale = static_cast<float*>(flat(ms, "avg_scale", device, groups, &ranges[3]));
-      e.sq_scale = static_cast<float*>(flat(vs, "sq_scale", device, groups, &ranges[4]));
+      e.avg_scale = static_cast<float*>(flat(ms, "avg_scale", device, groups, ranges[3]));
+      e.sq_scale = static_cast<float*>(flat(vs, "sq_scale", device, groups, ranges[4]));
     }
     e.count = n, e.id = static_cast<int32_t>(i);
     lists[2 * pd + gd].push_back(e);
   }
-  refuse_overlaps(ranges, 5);
+  refuse_overlaps(ranges, 5, read);
 
   Call c(first);
   Tensor scalars;

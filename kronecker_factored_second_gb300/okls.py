@@ -423,8 +423,8 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1: float =
         m <- beta1 m + (1 - beta1) g,   v <- beta2 v + (1 - beta2) g^2
         p <- p - lr weight_decay p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
 
-    Tensors are contiguous CUDA tensors on one device; params and grads are
-    fp32 or bf16, each on its own.  exp_avgs and exp_avg_sqs are fp32; or, with
+    Tensors are contiguous CUDA tensors on one device that share no memory (but
+    gradients, with one another); params and grads are fp32 or bf16, each on its own.  exp_avgs and exp_avg_sqs are fp32; or, with
     `avg_scales` and `sq_scales` (lists of fp32 tensors, a value for each 128 elements
     of a tensor), e4m3 codes of m and of the root of v, rounded by chance with the mean kept;
     `seed` with the step's number, the tensor's place in the list and the

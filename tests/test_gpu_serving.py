@@ -354,6 +354,42 @@ def test_adamw_refusals():
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_refuses_a_gradient_over_what_it_writes(bits):
+    """Gradients that share memory with a parameter or a state of any tensor of the call, in separate buffers and in one;
+    gradients may be one and the same tensor."""
+    n, dt = 300, F32 if bits == 32 else E4M3
+    for together in (False, True):
+        flat = torch.zeros(40 * n, device="cuda")
+        at = [0]
+
+        def place(count):
+            if not together:
+                return torch.zeros(count, device="cuda")
+            at[0] += count + 20
+            return flat[at[0] - count - 20:at[0] - 20]
+        ps, gs, ms, vs = ([place(n) for _ in range(3)] for _ in range(4))
+        sc = [[place(3) for _ in range(3)] for _ in range(2)] if bits == 8 else [None, None]
+        if bits == 8:
+            ms, vs = ([x.view(E4M3)[:n] for x in y] for y in (ms, vs))
+        kw = dict(step=1, lr=0.1, avg_scales=sc[0], sq_scales=sc[1])
+        written = [ps[0], ps[2], ms[1].view(torch.uint8), vs[0].view(torch.uint8)] + (sc[0][1:2] + sc[1][:1] if bits == 8 else [])
+        for t in written:
+            storage = torch.empty(0, device="cuda").set_(t.untyped_storage())
+            first = t.data_ptr() // 4 * 4 - t.untyped_storage().data_ptr()
+            for off in (0, 4, -4):
+                begin = (first + off) // 4
+                if begin < 0 or begin + n > storage.numel():
+                    continue
+                bad = list(gs)
+                bad[1] = storage[begin:begin + n]
+                with pytest.raises(ValueError, match="gradient overlaps"):
+                    okls.adamw_step(ps, bad, ms, vs, **kw)
+        assert all((x.float() == 0).all() for x in ps + ms + vs)
+        okls.adamw_step(ps, [gs[0], gs[0], gs[0][:n]], ms, vs, **kw)
+        assert dt == ms[0].dtype
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_adamw_captured_step_counts(bits):
     """Replays of a captured step are the steps that follow each other; a captured step with a number of the host is refused."""
     ps, gs, st, sc = _adamw_set(5, bits=bits)
