@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(Stream<X, NT, GW, ZERO>::kThreads, Stream<X, N
           const int srow = row + (lane & 1) * 8;
           const void* base = s_zero ? A.zero : A.scale;
           copy_some(load_at + 2048 + lane * 16, static_cast<const char*>(base) + 2 * static_cast<int64_t>(srow) + group_of<GW>(col, A.group) * s_pitch,
-                    base, col < A.k ? 2 * (static_cast<int>(A.n) - srow) : 0);
+                    base, col < A.k ? 2 * min(static_cast<int>(A.n) - srow, 8) : 0);
         }
       }
       src0 += G::kWarps * kStreamChunk / 2, src1 += G::kWarps * kStreamChunk / 2, s_src += s_turn;

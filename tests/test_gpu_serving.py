@@ -965,6 +965,26 @@ def test_int4_matmul_past_32_bits():
         _check_int4(x, lm.Int4Tensor(data[rows], s[rows], k), y[:, rows], BF16)
 
 
+@pytest.mark.parametrize("zero", [False, True])
+def test_int4_matmul_of_the_most_rows(zero):
+    """2^30 rows of weights, the most that the kernel for generated tokens takes, with sums that end inside a chunk."""
+    n, k = 1 << 30, 31  # 17 GB of codes
+    data = torch.zeros(n, 16, device="cuda", dtype=torch.uint8)
+    scale, z = (torch.ones(1, n, device="cuda", dtype=BF16).t() for _ in range(2))
+    g = gen(23)
+    for rows in (slice(0, 64), slice(n - 64, n)):
+        data[rows] = torch.randint(0, 256, (64, 16), generator=g, device="cuda", dtype=torch.uint8)
+        scale[rows] = torch.rand(64, 1, generator=g, device="cuda").bfloat16() + 0.5
+    w = lm.Int4Tensor(data, scale, k, 32, z if zero else None)
+    x = randn(g, 1, k, dtype=BF16)
+    y = lm.int4_matmul(x, w, out_dtype=F32)
+    for rows in (slice(0, 64), slice(n - 64, n), slice(1 << 29, (1 << 29) + 64)):
+        part = lm.Int4Tensor(data[rows], scale[rows], k, 32, w.zero[rows] if zero else None)
+        _check_int4(x, part, y[:, rows], F32)
+        assert (y[:, rows] != 0).all()
+    assert (y[:, 64:n - 64] == y[0, 64]).all()
+
+
 def test_sample_past_32_bits():
     rows, vocab = 20000, 131072  # 5.2 GB of logits
     z = torch.zeros(rows, vocab, device="cuda", dtype=BF16)
