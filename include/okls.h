@@ -731,7 +731,7 @@ typedef struct okls_adamw_config {
 } okls_adamw_config;
 
 /* `tensors` and `config` are host memory and free again when the call
- * returns.  scalars_dev: NULL, and the step's number is `step`; or what
+ * returns; all of them are checked before the first tensor is stepped.  scalars_dev: NULL, and the step's number is `step`; or what
  * okls_adamw_clock wrote in this step (`step` and the config's values are not
  * used then). */
 okls_status okls_adamw_step(const okls_adamw_tensor *tensors, int64_t num,

@@ -446,7 +446,9 @@ void* flat(const Tensor& t, const char* name, c10::Device device, int64_t count,
   REFUSE(impl->device() != device, "tensors on ", device, " and ", impl->device());
   REFUSE(!impl->is_contiguous(), name, " must be contiguous");
   REFUSE(impl->numel() != count, name, " must hold ", count, " values, not ", impl->numel());
+  REFUSE(count > (int64_t(1) << 33), name, " must hold 2^33 values at most, not ", count);
   void* p = const_cast<void*>(impl->data());
+  REFUSE(reinterpret_cast<uintptr_t>(p) % impl->itemsize() != 0, name, " is not aligned to its elements");
   if (writes && t.is_inference()) writable(t, name);
   if (count) ranges.emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + count * impl->itemsize());
   return p;
@@ -531,7 +533,7 @@ void adamw_step(const py::object& params, const py::object& grads, const py::obj
     REFUSE(c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None,
            "a captured step needs its number on the device (step as a tensor), or every replay would be the same step");
   }
-  // everything is checked before anything is written
+  // the settings, too, are checked before anything is written
   for (int k = 0; k < 4; ++k) {
     if (lists[k].empty() && k > 0) continue;
     check(okls_adamw_step(nullptr, 0, k / 2, k % 2, bits8 ? OKLS_E4M3 : OKLS_F32, &cfg, counted ? 1 : number, ptr_of(scalars),

@@ -519,27 +519,33 @@ okls_status okls_adamw_step(const okls_adamw_tensor* tensors, int64_t num, int32
   LM_TRY(check_mat(op, "scalars_dev", scalars_dev ? scalars_dev : tensors, 1, scalars_dev ? 1 : 0, 1, 16));
   const bool bits8 = state_dtype == OKLS_E4M3;
   const int se = bits8 ? 1 : 4;
+  bool some = false;
+  for (int64_t i = 0; i < num; ++i) {  // all of them, before the first launch
+    const okls_adamw_tensor& t = tensors[i];
+    if (t.count < 0 || t.count > (int64_t(1) << 33)) return bad(op, "a tensor's count must be in [0, 2^33]");
+    if (t.count == 0) continue;
+    LM_TRY(check_mat(op, "param", t.param, 1, t.count, t.count, elem_size(param_dtype)));
+    LM_TRY(check_mat(op, "grad", t.grad, 1, t.count, t.count, elem_size(grad_dtype)));
+    LM_TRY(check_mat(op, "exp_avg", t.exp_avg, 1, t.count, t.count, se));
+    LM_TRY(check_mat(op, "exp_avg_sq", t.exp_avg_sq, 1, t.count, t.count, se));
+    if (bits8) {
+      LM_TRY(check_mat(op, "avg_scale", t.avg_scale, 1, 1, 1, 4));
+      LM_TRY(check_mat(op, "sq_scale", t.sq_scale, 1, 1, 1, 4));
+    }
+    some = true;
+  }
+  if (!some) return OKLS_OK;
   int sms = 0;
+  LM_TRY(host_device_sms(&sms));
   const AdamwScalars s = adamw_scalars(adamw_hyper(config), scalars_dev ? 1 : step);
   AdamwEntry e[kAdamwTable];
   for (int64_t i = 0; i < num;) {
     int k = 0;
     for (; i < num && k < kAdamwTable; ++i) {
       const okls_adamw_tensor& t = tensors[i];
-      if (t.count < 0 || t.count > (int64_t(1) << 33)) return bad(op, "a tensor's count must be in [0, 2^33]");
-      if (t.count == 0) continue;
-      LM_TRY(check_mat(op, "param", t.param, 1, t.count, t.count, elem_size(param_dtype)));
-      LM_TRY(check_mat(op, "grad", t.grad, 1, t.count, t.count, elem_size(grad_dtype)));
-      LM_TRY(check_mat(op, "exp_avg", t.exp_avg, 1, t.count, t.count, se));
-      LM_TRY(check_mat(op, "exp_avg_sq", t.exp_avg_sq, 1, t.count, t.count, se));
-      if (bits8) {
-        LM_TRY(check_mat(op, "avg_scale", t.avg_scale, 1, 1, 1, 4));
-        LM_TRY(check_mat(op, "sq_scale", t.sq_scale, 1, 1, 1, 4));
-      }
-      e[k++] = {t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.avg_scale, t.sq_scale, t.count, t.id};
+      if (t.count != 0) e[k++] = {t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.avg_scale, t.sq_scale, t.count, t.id};
     }
     if (k == 0) break;
-    if (sms == 0) LM_TRY(host_device_sms(&sms));
     LM_TRY(launched(op, launch_adamw(e, k, param_dtype, grad_dtype, bits8, s, static_cast<const AdamwScalars*>(scalars_dev),
                                      static_cast<cudaStream_t>(stream))));
   }

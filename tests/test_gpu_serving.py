@@ -389,6 +389,21 @@ def test_adamw_refuses_a_gradient_over_what_it_writes(bits):
         assert dt == ms[0].dtype
 
 
+def test_adamw_refuses_too_long_a_tensor_before_it_counts():
+    """A tensor past 2^33 elements, of other types than the first: neither the counter nor the first tensor moves."""
+    n = (1 << 33) + 1
+    ps, gs, st, sc = _adamw_set(10, n=1, bits=8)
+    before = ps[0].clone()
+    big = [torch.empty(n, device="cuda", dtype=BF16) for _ in range(2)]
+    states = [torch.empty(n, device="cuda", dtype=torch.uint8).view(E4M3) for _ in range(2)]
+    scales = [torch.empty(-(-n // 128), device="cuda") for _ in range(2)]
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+    with pytest.raises((ValueError, L.OklsError), match="2\\^33"):
+        okls.adamw_step(ps + big[:1], gs + big[1:], st[0] + states[:1], st[1] + states[1:], step=step, lr=0.1,
+                        avg_scales=sc[0] + scales[:1], sq_scales=sc[1] + scales[1:])
+    assert step.item() == 0 and torch.equal(ps[0], before)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_adamw_captured_step_counts(bits):
     """Replays of a captured step are the steps that follow each other; a captured step with a number of the host is refused."""

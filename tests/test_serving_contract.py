@@ -59,6 +59,18 @@ def test_adamw_arguments(lib):
             lib.okls_adamw_clock)
 
 
+def test_adamw_checks_every_tensor_before_the_first_launch(lib):
+    """A wrong tensor behind those of the first launch is refused before the device is asked for anything."""
+    config = ctypes.byref(L.okls_adamw_config(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, weight_decay=0.1))
+    for num in (2, 401, 1000):
+        for wrong in (dict(count=(1 << 33) + 1), dict(param=None), dict(grad=P + 1)):
+            good = dict(param=P, grad=P, exp_avg=P, exp_avg_sq=P, count=5)
+            if torch.cuda.is_available():
+                good["count"] = 0  # (they would be stepped if the last one were not looked at)
+            t = (L.okls_adamw_tensor * num)(*[L.okls_adamw_tensor(**good)] * (num - 1), L.okls_adamw_tensor(**{**good, "count": 5, **wrong}))
+            assert lib.okls_adamw_step(t, num, 0, 0, 0, config, 1, None, None) == BAD, (num, wrong, L.last_error())
+
+
 def test_int4_arguments(lib):
     ok = [P, 0, 64, 10, 64, 32, P, 32, P, 1, 16, None, 0, 0, None]
     refused(ok, [({0: None}, BAD), ({1: 2}, BAD), ({2: 63}, BAD), ({3: -1}, BAD), ({4: 1 << 31}, BAD), ({5: 16}, BAD),
