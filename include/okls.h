@@ -710,7 +710,9 @@ okls_status okls_token_logprobs_grad_rest(
  * for sqrt(v)) of the word of element i in Philox-2x32 with five rounds:
  * counter (i / 2, id + low word of s), key the high word of s = seed + t *
  * 0x9E3779B97F4A7C15 (mod 2^64), first word of the result for even i, second
- * for odd.  A sqrt(v) that is not zero keeps at least the smallest code.
+ * for odd.  A sqrt(v) that is not zero keeps at least the smallest code.  Tensors
+ * that are stepped by several calls with one step number get numbers of their
+ * own from ids or upper words of the seed of their own.
  * Tensors of one call have one set of types; they do not overlap.  A gradient
  * that is not finite reaches p, m and v.
  */

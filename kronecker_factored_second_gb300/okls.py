@@ -428,7 +428,8 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1: float =
     `avg_scales` and `sq_scales` (lists of fp32 tensors, a value for each 128 elements
     of a tensor), e4m3 codes of m and of the root of v, rounded by chance with the mean kept;
     `seed` with the step's number, the tensor's place in the list and the
-    element decides the chances.  The update uses the moments before that rounding.
+    element decides the chances (of seeds that differ by d < 2^32, tensor i + d of the smaller
+    has those of tensor i).  The update uses the moments before that rounding.
 
     `step` is the step's number, from 1; or an int64 CUDA tensor with the number of steps done, which
     the call raises by one (what a captured step needs), and then `lr` may be an fp32 CUDA tensor."""
@@ -449,7 +450,8 @@ class AdamW(torch.optim.Optimizer):
     norms, biases), or all of it.
 
     `state_bits` 8 keeps the moments as e4m3 codes with a scale for each 128
-    elements, rounded by chance (see `adamw_step`); `seed` decides the chances.
+    elements, rounded by chance (see `adamw_step`); `seed` decides the chances, which every
+    parameter has of its own.
     `capturable` keeps the steps' numbers on the device, for a step that is
     captured into a CUDA graph (run one outside of it first, which makes the
     states); lr may then be an fp32 CUDA tensor.  Every parameter of a
@@ -482,12 +484,13 @@ class AdamW(torch.optim.Optimizer):
             with torch.enable_grad():
                 loss = closure()
         capturing = torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
+        count = 0  # parameters of the groups before this one
         for g in self.param_groups:
             if capturing and not g["capturable"]:
                 raise RuntimeError("okls: a captured step needs capturable=True")
             # parameters whose steps have one number go together
             lists = {}
-            for p in g["params"]:
+            for place, p in enumerate(g["params"], count):
                 if p.grad is None:
                     if g["capturable"] and self.state[p]:
                         raise RuntimeError("okls: every parameter of a capturable group needs a gradient at each step")
@@ -500,20 +503,21 @@ class AdamW(torch.optim.Optimizer):
                     if g["capturable"]:
                         st["step"] = lists.setdefault(("new", p.device), torch.zeros(1, dtype=torch.int64, device=p.device))
                 key = id(st["step"]) if g["capturable"] else (st["step"] + 1, p.device)
-                lists.setdefault(key, []).append((p, st))
+                lists.setdefault(key, []).append((p, st, place))
+            count += len(g["params"])
             for key, items in lists.items():
                 if not isinstance(items, list):
                     continue
                 number = items[0][1]["step"] if g["capturable"] else key[0]
                 names = ("exp_avg", "exp_avg_sq") + (("avg_scale", "sq_scale") if g["state_bits"] == 8 else ())
-                m, v, *scales = ([st[n] for _, st in items] for n in names)
+                m, v, *scales = ([st[n] for _, st, _ in items] for n in names)
                 beta1, beta2 = g["betas"]
-                adamw_step([p for p, _ in items], [p.grad.contiguous() for p, _ in items], m, v, step=number, lr=g["lr"],
+                adamw_step([p for p, *_ in items], [p.grad.contiguous() for p, *_ in items], m, v, step=number, lr=g["lr"],
                            beta1=beta1, beta2=beta2, eps=g["eps"], weight_decay=g["weight_decay"],
                            avg_scales=scales[0] if scales else None, sq_scales=scales[1] if scales else None,
-                           seed=g["seed"])
+                           seed=g["seed"] + (items[0][2] << 32))  # a key of the call's own
                 if not g["capturable"]:
-                    for _, st in items:
+                    for _, st, _ in items:
                         st["step"] = number
         return loss
 

@@ -261,6 +261,37 @@ def test_optimizer_steps_like_torch(on_cpu, capturable):
             own.step()
 
 
+@pytest.mark.parametrize("capturable", [False, True])
+def test_tensors_of_a_step_have_chances_of_their_own(monkeypatch, capturable):
+    """The counter's second word and the key of the random numbers differ between any two tensors of a step, whatever groups
+    and numbers of steps they are in; a single group's are those of adamw_step with the optimizer's seed."""
+    import types
+    seen = []
+
+    def step(params, grads, ms, vs, mscales, vscales, step, lr, b1, b2, eps, wd, seed):
+        if isinstance(step, torch.Tensor):
+            step += 1
+            step = step.item()
+        s = (seed + step * 0x9E3779B97F4A7C15) % (1 << 64)
+        seen.extend((s >> 32, (i + s) % (1 << 32)) for i in range(len(params)))
+    monkeypatch.setattr(lm, "_n", lambda: types.SimpleNamespace(adamw_step=step))
+    for seed in (0, 7, (1 << 64) - 1, -1):
+        p = _params(9)
+        opt = okls.AdamW([dict(params=p[:4]), dict(params=p[4:6]), dict(params=p[6:], lr=0.5)], state_bits=8, seed=seed,
+                         capturable=capturable)
+        for t, skip in enumerate([(1, 5), (), (1, 4) if not capturable else ()]):
+            _set_grads(p, t, skip)
+            seen.clear()
+            opt.step()
+            assert len(set(seen)) == len(seen) == 9 - len(skip)
+        alone = okls.AdamW(_params(3), state_bits=8, seed=seed)
+        _set_grads(alone.param_groups[0]["params"], 0)
+        seen.clear()
+        alone.step()
+        s = (seed + 0x9E3779B97F4A7C15) % (1 << 64)
+        assert seen == [(s >> 32, (i + s) % (1 << 32)) for i in range(3)]
+
+
 def test_a_refused_step_is_not_counted(on_cpu):
     p = _params(1)
     opt = okls.AdamW(p)
