@@ -681,6 +681,50 @@ def test_int4_matmul_of_its_own_quantisation():
         _check_int4(x, w, lm.int4_matmul(x, w), F32)
 
 
+def _whole_weight(g, n, k, group, zero):
+    """Scales are powers of two, zero points whole: (code - zero) * scale has no rounding anywhere."""
+    w = _weight(g, n, k, group, zero)
+    w.scale.copy_(torch.exp2(torch.randint(0, 3, w.scale.shape, generator=g, device="cuda").float()))
+    if zero:
+        w.zero.copy_(torch.randint(0, 16, w.zero.shape, generator=g, device="cuda"))
+    return w
+
+
+@pytest.mark.parametrize("group,zero", [(32, True), (32, False), (64, True), (64, False), (128, True), (128, False), (256, True)])
+@pytest.mark.parametrize("rows,n,k", [(1, 40, 31), (1, 2003, 2048), (3, 33, 32768), (8, 100, 4097), (16, 4100, 2055), (16, 48, 8192),
+                                      (33, 47, 4097), (64, 1040, 8111), (70, 31, 1000), (130, 64, 16384)])
+def test_int4_matmul_of_whole_numbers(group, zero, rows, n, k):
+    """Whole x of at most 2: the sums of 31 * 2 * 4 for each of k terms stay below 2^24, so that every order of the additions
+    is exact and a term that is missing or counted twice shows."""
+    assert 31 * 2 * 4 * k < 1 << 24
+    g = gen(rows * 7 + k)
+    w = _whole_weight(g, n, k, group, zero)
+    x = torch.randint(1, 3, (rows, k), generator=g, device="cuda") * (2 * torch.randint(0, 2, (rows, k), generator=g, device="cuda") - 1)
+    want = x.double() @ w.float().double().t()
+    for dtype in (BF16, F32):
+        got = lm.int4_matmul(x.to(dtype), w, out_dtype=F32)
+        assert torch.equal(got.double(), want)
+        assert torch.equal(lm.int4_matmul(x.to(dtype), w, out=got, accumulate=True).double(), 2 * want)
+
+
+@pytest.mark.parametrize("group,zero", [(32, True), (64, False), (128, True), (256, False)])
+@pytest.mark.parametrize("rows", [8, 16, 70])
+def test_int4_matmul_of_one_column_at_a_time(group, zero, rows):
+    """Each row of x has one value, in every column in turn: three bf16 terms of fp32 x (1, 2^-9 and 2^-19 of it) times a code
+    less a zero point fill 24 bits, so the output is the weight's column times that value, exactly."""
+    g = gen(40 + rows)
+    n, k = 37, 600
+    w = _whole_weight(g, n, k, group, zero)
+    v = w.float().double().t()
+    for dtype, value in ((F32, 1 + 2.0 ** -9 + 2.0 ** -19), (BF16, 1 + 2.0 ** -7)):
+        for first in range(0, k, rows):
+            at = torch.arange(first, min(first + rows, k), device="cuda")
+            x = torch.zeros(rows, k, device="cuda", dtype=dtype)
+            x[torch.arange(at.numel(), device="cuda"), at] = value
+            got = lm.int4_matmul(x, w, out_dtype=F32)
+            assert torch.equal(got[:at.numel()].double(), v[at] * value) and (got[at.numel():] == 0).all()
+
+
 def test_int4_matmul_not_finite():
     g = gen(3)
     for dtype in (BF16, F32):
