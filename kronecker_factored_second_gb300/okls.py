@@ -496,12 +496,16 @@ class AdamW(torch.optim.Optimizer):
                         raise RuntimeError("okls: every parameter of a capturable group needs a gradient at each step")
                     continue
                 st = self.state[p]
+                made = not st or (g["capturable"] and not isinstance(st["step"], torch.Tensor))
+                if made and capturing:
+                    raise RuntimeError("okls: run a step before one is captured, which makes the states")
                 if not st:
-                    if capturing:
-                        raise RuntimeError("okls: run a step before one is captured, which makes the states")
                     st.update(self._new_state(p, g))
-                    if g["capturable"]:
-                        st["step"] = lists.setdefault(("new", p.device), torch.zeros(1, dtype=torch.int64, device=p.device))
+                if made and g["capturable"]:
+                    counter = torch.full((1,), st["step"], dtype=torch.int64, device=p.device)
+                    st["step"] = lists.setdefault(("counter", st["step"], p.device), counter)
+                elif not g["capturable"] and isinstance(st["step"], torch.Tensor):
+                    st["step"] = int(st["step"])
                 key = id(st["step"]) if g["capturable"] else (st["step"] + 1, p.device)
                 lists.setdefault(key, []).append((p, st, place))
             count += len(g["params"])

@@ -332,6 +332,26 @@ def test_optimizer_state_round_trip(on_cpu, bits, capturable):
         assert torch.equal(p, q)
 
 
+@pytest.mark.parametrize("first", [False, True])
+def test_steps_are_counted_on_when_capturable_changes(on_cpu, first):
+    """A group that is made capturable after some steps (or no longer is) goes on with its next number, its tensors together."""
+    a, b = _params(), _params()
+    own, ref = okls.AdamW(a, lr=0.1, capturable=first), torch.optim.AdamW(b, lr=0.1, weight_decay=0.01)
+    for t in range(6):
+        for ps in (a, b):
+            _set_grads(ps, t)
+        on_cpu.clear()
+        own.step(), ref.step()
+        assert on_cpu == [4]
+        for p in a:
+            n = own.state[p]["step"]
+            assert int(n) == t + 1 and isinstance(n, torch.Tensor) == own.param_groups[0]["capturable"]
+        if t in (1, 3):
+            own.param_groups[0]["capturable"] = not own.param_groups[0]["capturable"]
+    for x, y in zip(a, b):
+        assert torch.allclose(x, y, rtol=1e-5, atol=1e-6)
+
+
 def test_optimizer_refuses_settings():
     p = _params(1)
     for kw in (dict(state_bits=16), dict(betas=(1.0, 0.9)), dict(eps=-1.0), dict(weight_decay=-0.1), dict(lr=torch.tensor(0.1))):
