@@ -484,7 +484,7 @@ class AdamW(torch.optim.Optimizer):
             with torch.enable_grad():
                 loss = closure()
         capturing = torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
-        count = 0  # parameters of the groups before this one
+        count, calls = 0, []  # parameters of the groups before this one; groups whose step is not refused
         for g in self.param_groups:
             if capturing and not g["capturable"]:
                 raise RuntimeError("okls: a captured step needs capturable=True")
@@ -509,6 +509,8 @@ class AdamW(torch.optim.Optimizer):
                 key = id(st["step"]) if g["capturable"] else (st["step"] + 1, p.device)
                 lists.setdefault(key, []).append((p, st, place))
             count += len(g["params"])
+            calls.append((g, lists))
+        for g, lists in calls:
             for key, items in lists.items():
                 if not isinstance(items, list):
                     continue

@@ -352,6 +352,18 @@ def test_steps_are_counted_on_when_capturable_changes(on_cpu, first):
         assert torch.allclose(x, y, rtol=1e-5, atol=1e-6)
 
 
+def test_a_group_that_is_refused_keeps_the_others_from_stepping(on_cpu):
+    p = _params()
+    opt = okls.AdamW([dict(params=p[:2]), dict(params=p[2:], capturable=True)])
+    _set_grads(p, 0)
+    opt.step()
+    _set_grads(p, 1, (3,))
+    before = [x.detach().clone() for x in p]
+    with pytest.raises(RuntimeError, match="gradient"):
+        opt.step()
+    assert all(torch.equal(x, y) for x, y in zip(p, before)) and opt.state[p[0]]["step"] == 1
+
+
 def test_optimizer_refuses_settings():
     p = _params(1)
     for kw in (dict(state_bits=16), dict(betas=(1.0, 0.9)), dict(eps=-1.0), dict(weight_decay=-0.1), dict(lr=torch.tensor(0.1))):
