@@ -1063,6 +1063,27 @@ def test_sample_past_32_bits():
         assert torch.equal(r.ids[left], want[left])
 
 
+@pytest.mark.parametrize("vocab", [1 << 20, 1040001])
+def test_sample_of_more_equals_than_a_bin_counts(vocab):
+    """Rows of so many equal logits, each in one or two blocks, that a bin's 32-bit sum of their weights wraps around (2^18
+    tokens of the largest weight): all equal, two values, and a run of equals below a few better ones."""
+    g = gen(24)
+    rows = 96  # (more would give a row more blocks)
+    z = torch.zeros(rows, vocab, device="cuda", dtype=BF16)
+    z[1, ::2] = -1.0
+    z[2] = -2.0
+    z[2, 1000:1040] = 1.0
+    z[3, : 1 << 18] = 0.5
+    z[4, : (1 << 18) + 1] = 0.5
+    z[5] = randn(g, vocab, dtype=BF16).clamp(max=0.0)  # half of them are the best
+    some = list(range(6)) + [rows - 1]
+    for kw in (dict(top_p=0.3), dict(top_p=0.9), dict(top_p=0.5, temperature=0.7), dict(top_k=400000), dict(top_k=700001, top_p=0.6),
+               dict(top_p=0.95, min_p=0.2), dict()):
+        u = torch.rand(rows, generator=g, device="cuda")
+        r = lm.sample(z, u, **kw)
+        _check_sample(z[some], u[some], lm.TokenSample(r.ids[some], r.logp[some]), **kw)
+
+
 # ------------------------------------------------------------------ together
 def test_generation_step_captured_and_on_two_streams():
     """A 4-bit output layer and the sampling of its logits: captured and replayed with new inputs, two graphs of it, and two
