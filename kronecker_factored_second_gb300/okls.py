@@ -486,44 +486,51 @@ class AdamW(torch.optim.Optimizer):
         capturing = torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
         count, calls = 0, []  # parameters of the groups before this one; groups whose step is not refused
         for g in self.param_groups:
-            if capturing and not g["capturable"]:
+            capturable = g["capturable"]
+            if capturing and not capturable:
                 raise RuntimeError("okls: a captured step needs capturable=True")
-            # parameters whose steps have one number go together
-            lists = {}
+            # parameters whose steps have one number go together: number -> parameters, gradients, states, first one's place
+            lists, counters = {}, {}
+            kind = torch.Tensor if capturable else int
             for place, p in enumerate(g["params"], count):
-                if p.grad is None:
-                    if g["capturable"] and self.state[p]:
+                grad, st = p.grad, self.state[p]
+                if grad is None:
+                    if capturable and st:
                         raise RuntimeError("okls: every parameter of a capturable group needs a gradient at each step")
                     continue
-                st = self.state[p]
-                made = not st or (g["capturable"] and not isinstance(st["step"], torch.Tensor))
-                if made and capturing:
-                    raise RuntimeError("okls: run a step before one is captured, which makes the states")
-                if not st:
-                    st.update(self._new_state(p, g))
-                if made and g["capturable"]:
-                    counter = torch.full((1,), st["step"], dtype=torch.int64, device=p.device)
-                    st["step"] = lists.setdefault(("counter", st["step"], p.device), counter)
-                elif not g["capturable"] and isinstance(st["step"], torch.Tensor):
-                    st["step"] = int(st["step"])
-                key = id(st["step"]) if g["capturable"] else (st["step"] + 1, p.device)
-                lists.setdefault(key, []).append((p, st, place))
+                number = st["step"] if st else None
+                if type(number) is not kind:
+                    if capturing:
+                        raise RuntimeError("okls: run a step before one is captured, which makes the states")
+                    if not st:
+                        st.update(self._new_state(p, g))
+                    number = int(st["step"])
+                    if capturable:
+                        where = number, p.device
+                        if where not in counters:
+                            counters[where] = torch.full((1,), number, dtype=torch.int64, device=p.device)
+                        number = counters[where]
+                    st["step"] = number
+                key = id(number) if capturable else (number + 1, p.device)
+                if key not in lists:
+                    lists[key] = [], [], [], place
+                ps, gs, sts, _ = lists[key]
+                ps.append(p)
+                gs.append(grad.contiguous())
+                sts.append(st)
             count += len(g["params"])
             calls.append((g, lists))
         for g, lists in calls:
-            for key, items in lists.items():
-                if not isinstance(items, list):
-                    continue
-                number = items[0][1]["step"] if g["capturable"] else key[0]
-                names = ("exp_avg", "exp_avg_sq") + (("avg_scale", "sq_scale") if g["state_bits"] == 8 else ())
-                m, v, *scales = ([st[n] for _, st, _ in items] for n in names)
-                beta1, beta2 = g["betas"]
-                adamw_step([p for p, *_ in items], [p.grad.contiguous() for p, *_ in items], m, v, step=number, lr=g["lr"],
-                           beta1=beta1, beta2=beta2, eps=g["eps"], weight_decay=g["weight_decay"],
-                           avg_scales=scales[0] if scales else None, sq_scales=scales[1] if scales else None,
-                           seed=g["seed"] + (items[0][2] << 32))  # a key of the call's own
+            names = ("exp_avg", "exp_avg_sq") + (("avg_scale", "sq_scale") if g["state_bits"] == 8 else ())
+            beta1, beta2 = g["betas"]
+            for key, (ps, gs, sts, place) in lists.items():
+                number = sts[0]["step"] if g["capturable"] else key[0]
+                m, v, *scales = ([st[n] for st in sts] for n in names)
+                adamw_step(ps, gs, m, v, step=number, lr=g["lr"], beta1=beta1, beta2=beta2, eps=g["eps"],
+                           weight_decay=g["weight_decay"], avg_scales=scales[0] if scales else None,
+                           sq_scales=scales[1] if scales else None, seed=g["seed"] + (place << 32))  # a key of the call's own
                 if not g["capturable"]:
-                    for _, st, _ in items:
+                    for st in sts:
                         st["step"] = number
         return loss
 
