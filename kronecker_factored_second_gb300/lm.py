@@ -291,7 +291,7 @@ class Int4Tensor:
 
     def float(self) -> torch.Tensor:
         """The values in fp32."""
-        c = torch.stack((self.data & 15, self.data >> 4), 2).view(self.data.shape[0], -1)[:, : self.cols].float()
+        c = torch.stack((self.data & 15, self.data >> 4), 2).flatten(1)[:, : self.cols].float()
 
         def spread(t):
             return t.float().repeat_interleave(self.group, 1)[:, : self.cols]

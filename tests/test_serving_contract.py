@@ -157,6 +157,14 @@ def test_int4_tensor_checks_and_values():
             lm.Int4Tensor(**{**dict(data=codes, scale=s, cols=100, group=32, zero=z), **bad})
 
 
+def test_int4_tensor_without_rows_or_columns():
+    for rows, cols in ((0, 100), (0, 0), (5, 0)):
+        groups = -(-cols // 32)
+        w = lm.Int4Tensor(torch.zeros(rows, -(-cols // 2), dtype=torch.uint8), torch.ones(rows, groups).bfloat16(), cols, 32,
+                          torch.ones(rows, groups).bfloat16())
+        assert w.float().shape == w.shape == (rows, cols)
+
+
 class _Lent:
     """Stands for a CUDA tensor: remembers the streams that were told of it."""
     is_cuda = True
