@@ -205,11 +205,9 @@ __device__ __forceinline__ void state_scales(uint32_t amax_bits, float* mul, flo
 }
 
 // The moments of one element after the step, each product and sum rounded (what a code is must
-// not hang on how a compiler joins them).  The second one's products are rounded up: off by
-// one unit instead of half of one, but a product that is not 0 does not become 0, so a root of 0 is the
-// formula's, and a root below 2^-62 tells of a v that may have left the normal numbers.
+// not hang on how a compiler joins them).
 __device__ __forceinline__ float second8(const AdamwScalars& s, float r, float g) {
-  return __fadd_rn(__fmul_ru(s.beta2, __fmul_ru(r, r)), __fmul_ru(__fmul_ru(s.rest2, fabsf(g)), fabsf(g)));
+  return __fadd_rn(__fmul_rn(s.beta2, __fmul_rn(r, r)), __fmul_rn(__fmul_rn(s.rest2, g), g));
 }
 __device__ __forceinline__ float first8(const AdamwScalars& s, float m, float g) {
   return __fadd_rn(__fmul_rn(s.beta1, m), __fmul_rn(s.rest1, g));
@@ -285,6 +283,22 @@ __device__ __forceinline__ void adamw8_far(const AdamwEntry& e, const AdamwScala
   if (some && (threadIdx.x & 7) == 0) e.ms[group] = mscale, e.vs[group] = vscale;
 }
 
+// Whether 16 elements from a 16-byte boundary are all 0.
+template <class G>
+__device__ __forceinline__ bool no_values(const G* g) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(G)); ++i) {
+    const uint4 u = reinterpret_cast<const uint4*>(g)[i];
+    any |= u.x | u.y | u.z | u.w;
+  }
+  return (any & (sizeof(G) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0;
+}
+__device__ __forceinline__ bool no_codes(const uint8_t* q) {
+  const uint4 u = *reinterpret_cast<const uint4*>(q);
+  return ((u.x | u.y | u.z | u.w) & 0x7F7F7F7Fu) == 0;
+}
+
 // 8 lanes take a group, 16 consecutive elements each, which are held in
 // registers between the update and the rounding.
 constexpr int kOwn8 = 16;
@@ -345,16 +359,23 @@ __global__ void __launch_bounds__(kAdamThreads, 4) k_adamw8(const __grid_constan
       const uint32_t wm[4] = {cm.x, cm.y, cm.z, cm.w}, wv[4] = {cv.x, cv.y, cv.z, cv.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) codes_to_f32(wm[j], m + 4 * j), codes_to_f32(wv[j], r + 4 * j);
-      uint32_t least = ~0u;  // bits, less one, of the smallest root that is not 0
+      uint32_t least = ~0u;  // bits of the smallest root
 #pragma unroll
       for (int j = 0; j < kOwn8; ++j) {
         m[j] = first8(s, __fmul_rn(m[j], ms), b[j]);
         r[j] = root_of(second8(s, __fmul_rn(r[j], vs), b[j]));
         a[j] = update8(s, a[j], m[j], r[j]);
-        least = __viaddmin_u32(__float_as_uint(r[j]), 0xFFFFFFFFu, least);
+        least = min(least, __float_as_uint(r[j]));
         top_r = max_mag(top_r, r[j]);
       }
-      far = least < __float_as_uint(kFarRoot) - 1u || !(top_r < CUDART_INF_F);
+      // an infinite v (its root came out as NaN), or a small one that is not the 0 of an element without gradient and
+      // code (usual are lanes of nothing but those: rows of a table whose tokens did not occur)
+      far = !(top_r < CUDART_INF_F);
+      if (least < __float_as_uint(kFarRoot) && !(vec && no_values(g) && no_codes(vq))) {
+#pragma unroll
+        for (int j = 0; j < kOwn8; ++j)
+          if (j < left && r[j] < kFarRoot) far = far || to_f32(g[j]) != 0.0f || (vq[j] & 0x7F) != 0;
+      }
     }
     if (__any_sync(0xffffffffu, far)) {
       adamw8_far<P, G>(e, s, i, low);
