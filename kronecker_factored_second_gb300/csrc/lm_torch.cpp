@@ -448,7 +448,7 @@ void* flat(const Tensor& t, const char* name, c10::Device device, int64_t count,
   REFUSE(impl->numel() != count, name, " must hold ", count, " values, not ", impl->numel());
   REFUSE(count > (int64_t(1) << 33), name, " must hold 2^33 values at most, not ", count);
   void* p = const_cast<void*>(impl->data());
-  REFUSE(reinterpret_cast<uintptr_t>(p) % impl->itemsize() != 0, name, " is not aligned to its elements");
+  REFUSE((reinterpret_cast<uintptr_t>(p) & (impl->itemsize() - 1)) != 0, name, " is not aligned to its elements");
   if (writes && t.is_inference()) writable(t, name);
   if (count) ranges.emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + count * impl->itemsize());
   return p;
