@@ -23,9 +23,11 @@
 // reproducible and does not depend on the launch's shape.
 //
 // Measured (L2 flushed): 131M fp32 elements with 32-bit moments in 529 us (6.9
-// TB/s: memory), bf16 ones with 8-bit moments in 335 us (4.0 TB/s: some 72
-// instructions an element fill the issue slots; with one tile instead of four for
-// a CTA 380); 49 tensors of 2048 in 10.5 us (9.3 of them the call's work on the host).
+// TB/s: memory), bf16 ones with 8-bit moments in 339 us (3.9 TB/s: some 75
+// instructions an element take three of four issue slots, and most ready warps wait for
+// their turn; with one tile instead of four for a CTA 380; 64 registers a thread, past
+// which 64 to 80 bytes are spilled); 49 tensors of 2048 in 10.3 us (8.6 of them the
+// call's work on the host).
 #include <math_constants.h>
 
 #include "okls_lm.cuh"

@@ -19,9 +19,11 @@
 //
 // Two kernels: k_int4_stream for generated tokens (one wave of CTAs, x in shared
 // memory), k_int4_matmul for more rows or longer ones than that holds.  Measured
-// (bf16, L2 flushed): 1 row, 131072 x 2048 with zero points in 36.9 us (4.1 TB/s;
-// issue slots run out), 5504 x 2048 in 4.6 us without its call; 16 rows, 11008 x 4096
-// in 17 us (x's staging and issue).
+// (bf16, L2 flushed): 1 row, 131072 x 2048 with zero points in 36.9 us (4.1 TB/s; 2.6 of
+// four instructions a clock from 14 warps an SM, which wait for results of their own and for the
+// tensor pipe's turn, hardly for memory), 5504 x 2048 in 4.6 us without its call; 16 rows,
+// 11008 x 4096 in 18 us (1.6 a clock: x's staging and its barrier, then the same waits and
+// x's reads from shared memory).
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kMmThreads) k_int4_matmul(const Int4Args A) {
 // and their scales, and leaves its part of a tile's sums in shared memory; every few
 // tiles the CTA adds the parts up, in the warps' order.
 //
-// Issue slots are what runs short, so the codes' way is two instructions a
+// Instructions cost more than bytes here, so the codes' way is two of them a
 // pair: a shift brings a nibble to the fraction's upper bits, a mask and an or
 // make it bf16 16 + c.  The 16 + zero too many are taken away with the sum of x.
 // (That costs a sum two bits, which fp32 activations are given back: there 24 is

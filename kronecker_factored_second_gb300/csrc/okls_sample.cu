@@ -41,9 +41,11 @@
 //
 // Measured (L2 flushed): 512 rows of 128257 fp32 with top-p in 258 us (1.0 TB/s),
 // 1024 rows of 131072 bf16 without a filter in 213 to 238 us (39 instructions a
-// token; look-ups in the table meet banks twice), both bound by issue slots; one
-// row of 32000 in 18 us without its call, a chain of barriers and scans; 256 rows
-// of 32000 with settings of their own in 68 us, the chain of the slowest row.
+// token): 2.2 and 2.3 of four instructions a clock, with 29 of 64 warps an SM, a third of whose
+// waiting is for logits from memory or L2; one row of 32000 in 18 us without its call
+// (16 warps that wait for barriers, for code that is not in the instruction cache and for memory);
+// 256 rows of 32000 with settings of their own in 66 to 78 us, the chain of the slowest row.
+// At 64 registers a thread some 300 bytes are spilled, in the rare paths and around them.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -876,7 +878,8 @@ __device__ u64 cut_by_mass(Shared& S, const Group& G, const Part<T>& R, const He
 #pragma unroll
   for (int i = 0; i < kBinsThread; ++i) mass[i] = S.bin.low[b0 + i];
   for (int r = 1; r < G.size; ++r) {
-    // (a row of 2^17 tokens has 2^31 in a bin at most)
+    // (Not past 32 bits here.  A CTA's own sum wraps around past 2^18 tokens of the largest weight: the exact masses
+    // below then find the border to be wrong, or too many tokens at it, and `select` takes over.)
     const uint32_t* other = G.of(S.bin.low, (G.rank + r) % G.size);
 #pragma unroll
     for (int i = 0; i < kBinsThread; ++i) mass[i] = min(mass[i], 0x7FFFFFFFu) + min(other[b0 + i], 0x7FFFFFFFu);
@@ -1177,7 +1180,7 @@ cudaError_t launch_sample(const SampleArgs& args, int dtype, int num_sms, cudaSt
   while ((int64_t(1) << A.shift) < A.vocab) ++A.shift;
   // more CTAs for a row while the SMs last and a CTA keeps 32768 values: below
   // that the cluster's barriers cost more (one row of 32000 with all filters: 18 us in
-  // one CTA, 23 in eight; of 128256 with top-p: 94 in one, 45 in four, 41 in eight).
+  // one CTA, 23 in eight; of 128256 with top-p: 94 in one, 45 in the four that it gets, 41 in eight).
   // Many rows, 1024 of 131072: 234 us with a CTA for a row, 270 with two, 507 with four.
   int size = 1;
   while (size < 8 && A.rows * size * 2 <= num_sms && A.vocab >= size * 32768) size *= 2;
